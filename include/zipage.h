@@ -283,6 +283,176 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
                                    const zp_params* params, void* workspace, size_t workspace_bytes,
                                    int64_t stall_limit_ns, zp_stream stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators around the cache: rotary positions, an 8-bit form of the pool, and attention with
+ * a sliding window.
+ *
+ * They share these conventions, on top of the ones at the top of this file:
+ *   - Workspaces are zeroed once before their first use (the Python binding's new_workspace
+ *     does) and then belong to one call in flight at a time.  A call leaves the parts that the
+ *     next one expects zeroed as it found them, so calls of any of these operators may follow
+ *     one another on a stream, and captured graphs may share a workspace if they are replayed
+ *     one after the other.
+ *   - The error word at the start of the workspace is sticky: a call writes it only when it
+ *     finds an error, and it keeps the first one until zp_read_error() reads and clears it.
+ *     One read can so cover all layers of a step.
+ *   - params.scale is finite and above 0 where a call uses it.
+ *   - A zp_rows describes bf16 rows [tokens][heads][head_dim] whose last dimension is
+ *     contiguous; strides are in elements.  Any strides are accepted; rows whose base address
+ *     and strides are multiples of 16 bytes are moved with wide loads and stores.
+ * --------------------------------------------------------------------------------------- */
+typedef struct zp_rows {
+  void* data;             /* device, bf16; NULL only where the call says so */
+  int64_t token_stride;
+  int64_t head_stride;
+} zp_rows;
+
+/* How the angles of far positions are scaled.  f_i = theta^(-2i / rotary_dim), i < rotary_dim/2,
+ * is the unscaled angle per position of pair i. */
+enum {
+  ZP_ROPE_NONE = 0,
+  ZP_ROPE_LINEAR = 1,     /* f_i / factor */
+  ZP_ROPE_BASE = 2,       /* theta * factor^(rotary_dim / (rotary_dim - 2)) in place of theta */
+  ZP_ROPE_YARN = 3,       /* f_i for pairs that turn at least `high` times over original_len
+                             positions, f_i / factor for those below `low` turns, a linear ramp
+                             over the pair index between; cos and sin times 0.1 ln(factor) + 1 */
+  ZP_ROPE_WAVELENGTH = 4  /* the same ends, blended between by (turns - low) / (high - low) */
+};
+
+typedef struct zp_rope_config {
+  int32_t head_dim;       /* even, 2 .. 512 */
+  int32_t rotary_dim;     /* the first rotary_dim values of a head are rotated: even,
+                             2 .. min(head_dim, 256); the others pass through */
+  int32_t interleaved;    /* 1: pair i is (x[2i], x[2i+1]); 0: (x[i], x[i + rotary_dim/2]) */
+  int32_t scaling;        /* ZP_ROPE_* */
+  double theta;           /* > 1 */
+  double factor;          /* >= 1; ignored with ZP_ROPE_NONE */
+  int32_t original_len;   /* > 0 for ZP_ROPE_YARN and ZP_ROPE_WAVELENGTH */
+  double low, high;       /* 0 < low < high, for the same two */
+  double mscale;          /* factor on cos and sin; 0: the scaling's own (1, or the one above) */
+} zp_rope_config;
+
+/* What zp_rope_apply needs, filled by zp_rope_init and passed with every call.  Angles are held
+ * as turns per position in units of 2^-64, so that position * angle wraps exactly. */
+typedef struct zp_rope {
+  int32_t head_dim, rotary_dim, interleaved;
+  float mscale;
+  uint64_t turns[128];
+} zp_rope;
+
+/* Host only. */
+zp_status zp_rope_init(const zp_rope_config* config, zp_rope* out);
+
+/* Rotary positions of the queries and keys of T tokens in one launch:
+ *   (y_a, y_b) = mscale * (x_a cos - x_b sin, x_b cos + x_a sin),  angle = positions[t] * f_i,
+ * computed in fp32 and rounded to bf16 once.
+ *   q, k            rows [T][num_q_heads] and [T][num_kv_heads]; either may be NULL (or have no
+ *                   heads).
+ *   q_out, k_out    where the results go: the same rows (in place) or others that do not overlap
+ *                   them.  In place, values past rotary_dim are not touched.
+ *   positions       device int32 [T], any value (negative angles turn backwards).
+ * Returns ZP_OK once queued.  No workspace. */
+zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const zp_rows* q_out, int32_t num_q_heads,
+                        const zp_rows* k, const zp_rows* k_out, int32_t num_kv_heads, const int32_t* positions,
+                        int32_t T, zp_stream stream);
+
+/* The 8-bit pool: E4M3 codes in the bf16 pool's layout, [num_layers][num_blocks][2]
+ * [num_kv_heads][block_size][head_dim], and one fp32 scale per (layer, block, K|V, head); a value
+ * is code * scale.  zp_kv8_append and zp_kv8_pack_blocks write scales that are powers of two: the
+ * smallest 2^e >= amax / 448, e >= -126, over the finite values of the block's tokens (0 for a
+ * block of zeros).  With such a scale dividing by it is exact, so a code is off by E4M3's own
+ * rounding only, reading back to bf16 is exact, and a scale that grows later keeps every code
+ * that stays in E4M3's normal range.  Values that are not finite are stored as E4M3's NaN.
+ * zp_kv8_unpack_blocks and zp_kv8_decode_attn take any finite scales. */
+typedef struct zp_kv8_pool {
+  void* codes;            /* device, 16-byte aligned */
+  float* scales;          /* device [num_layers][num_blocks][2][num_kv_heads] */
+  int64_t num_blocks;
+} zp_kv8_pool;
+
+/* Quantises new keys and values of one layer as they enter the cache.
+ *   k, v            rows [T][num_kv_heads][head_dim] of the new tokens of all requests, request
+ *                   after request.
+ *   token_start     device int32 [B + 1], 0 = token_start[0] <= ... <= token_start[B] = T: request r
+ *                   owns rows token_start[r] .. token_start[r + 1] - 1 (none is fine).
+ *   cached          device int32 [B], tokens in request r's cache before the call: its new tokens
+ *                   take positions cached[r], cached[r] + 1, ...
+ *   block_tables    device int32 [B][max_blocks]; only the entries of blocks that receive tokens
+ *                   are read.  A block that receives tokens belongs to one request (shared
+ *                   prefix blocks are full, and never appended to).
+ * A block whose first token is new starts with a scale of its own.  In a part-full block the
+ * scale is the larger of the old one and the one the new tokens need; if that is larger, the
+ * codes already there are brought to it (rounded once more).  Rows behind the last token are not
+ * written.
+ *   workspace       device, >= 256 bytes, 256-byte aligned.
+ * A request whose entries of token_start or cached are out of range, or that would pass
+ * max_blocks, is skipped; so is a block with an id outside the pool: ZP_ERR_BAD_TABLE.  If
+ * token_start decreases anywhere, which requests are written is undefined (nothing outside their
+ * blocks is).  head_dim 64 or 128, block_size 16 or 32. */
+zp_status zp_kv8_append(const zp_kv8_pool* pool, int32_t layer, const zp_rows* k, const zp_rows* v, int32_t T,
+                        const int32_t* token_start, const int32_t* cached, int32_t B, const int32_t* block_tables,
+                        int32_t max_blocks, const zp_params* params, void* workspace, size_t workspace_bytes,
+                        zp_stream stream);
+
+/* Whole blocks between the bf16 pool that the compression pass works on and the 8-bit pool, for
+ * layers [layer_begin, layer_begin + layer_count) (count 0: all, then begin must be 0):
+ *   pack    block src_ids[i] of `pool`  -> block dst_ids[i] of `kv8`;
+ *   unpack  block src_ids[i] of `kv8` -> block dst_ids[i] of `pool`, bf16(code * scale).
+ *   src_ids, dst_ids  device int32 [n]; dst_ids are distinct.
+ *   fill        pack only: device int32 [n] or NULL, tokens in each block (0 .. block_size; NULL:
+ *               all are full).  Rows past them are neither read nor written.
+ *   workspace   device, >= 256 bytes, 256-byte aligned.
+ * An id outside its pool, or a bad fill: that block is skipped, ZP_ERR_BAD_TABLE. */
+zp_status zp_kv8_pack_blocks(const zp_kv_pool* pool, const int32_t* src_ids, const int32_t* fill,
+                             const zp_kv8_pool* kv8, const int32_t* dst_ids, int32_t n, int32_t layer_begin,
+                             int32_t layer_count, const zp_params* params, void* workspace, size_t workspace_bytes,
+                             zp_stream stream);
+zp_status zp_kv8_unpack_blocks(const zp_kv8_pool* kv8, const int32_t* src_ids, const zp_kv_pool* pool,
+                               const int32_t* dst_ids, int32_t n, int32_t layer_begin, int32_t layer_count,
+                               const zp_params* params, void* workspace, size_t workspace_bytes, zp_stream stream);
+
+/* Paged decode attention over the 8-bit pool: zp_paged_decode_attn's operation on code * scale,
+ * optionally with a window.  Request r's one query is at position L - 1, L = seq_lens[r]:
+ *   out[r][qh] = softmax_t(params.scale * <q[r][qh], k_t>) . v_t over t < L with
+ *   t >= L - window or t < sinks   (window 0: every t < L).
+ *   q, out        rows [B][H_q][head_dim].
+ *   seq_lens      device int32 [B], 0 <= L <= max_blocks * b.  0 (a padded row): zeros are written.
+ *   workspace     >= zp_kv8_decode_workspace_size() bytes, 256-byte aligned.
+ * A bad seq_len or block id: that row (request and kv head) is not written, ZP_ERR_BAD_TABLE.
+ * Only table entries of visible blocks are read.  head_dim 64 or 128, block_size 16 or 32, up to
+ * 16 query heads per kv head. */
+zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables,
+                             const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window, int32_t sinks,
+                             const zp_rows* out, const zp_params* params, void* workspace, size_t workspace_bytes,
+                             zp_stream stream);
+
+size_t zp_kv8_decode_workspace_size(const zp_params* params, int32_t B, int32_t max_blocks);
+
+/* Attention with a sliding window and a few first tokens that stay visible, over the bf16 pool,
+ * for one to many new tokens per request (decode, verification of drafts, chunked prefill).  The
+ * new tokens' keys and values are already in the pool.  Query i of request r's n is at position
+ * p = seq_lens[r] - n + i and sees
+ *   t <= p with t > p - window or t < sinks   (window 0: every t <= p).
+ *   q, out        rows [T][H_q][head_dim], request after request.
+ *   q_start       device int32 [B + 1], as token_start of zp_kv8_append.  Rows of q and out
+ *                 outside q_start's range are neither read nor written.
+ *   max_q         the most new tokens of a request of this call (an upper bound is fine; a request
+ *                 above it is skipped: ZP_ERR_BAD_TABLE).
+ *   seq_lens      device int32 [B], tokens in the cache, the new ones included: n <= L <=
+ *                 max_blocks * b.
+ *   workspace     >= zp_paged_window_workspace_size() bytes, 256-byte aligned.
+ * A bad length, q_start or block id: the rows concerned are not written, ZP_ERR_BAD_TABLE.
+ * ZP_ERR_TIMEOUT (a wait inside the kernel gave up) as for zp_compress: the output is undefined.
+ * Keys and values that a row does not see do not reach it, whatever they hold.  head_dim 64 or
+ * 128, block_size 16 or 32, up to 16 query heads per kv head. */
+zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                               int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                               int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                               const zp_params* params, void* workspace, size_t workspace_bytes, zp_stream stream);
+
+size_t zp_paged_window_workspace_size(const zp_params* params, int32_t T, int32_t B, int32_t max_q,
+                                      int32_t max_blocks, int32_t window, int32_t sinks);
+
 /* Synchronises `stream`, copies the error word at the start of `workspace` to *out_status and
  * clears it.  Returns ZP_ERR_CUDA if the copy fails. */
 zp_status zp_read_error(void* workspace, zp_stream stream, zp_status* out_status);

@@ -1,0 +1,122 @@
+// zp_attn.cpp — the entry points of decode attention over the 8-bit pool and of attention with a
+// sliding window: argument checks, workspace, and the choice of the kernel.
+#include <climits>
+#include <cmath>
+
+#include "zp_attn.h"
+
+namespace zp {
+namespace {
+
+zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_rows* q, const zp_rows* out,
+                const int32_t* tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
+                int32_t sinks) {
+  if (!p || B < 0 || max_blocks < 1 || window < 0 || sinks < 0 || num_blocks <= 0) return ZP_ERR_INVALID_ARG;
+  if (layer < 0 || layer >= p->num_layers) return ZP_ERR_INVALID_ARG;
+  if (p->num_kv_heads <= 0 || p->num_q_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return ZP_ERR_INVALID_ARG;
+  if (!(p->scale > 0.0f) || !std::isfinite(p->scale)) return ZP_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return ZP_ERR_UNSUPPORTED;
+  if (p->block_size != 16 && p->block_size != 32) return ZP_ERR_UNSUPPORTED;
+  if (p->num_q_heads / p->num_kv_heads > 16 || B > 65535 || p->num_kv_heads > 65535) return ZP_ERR_UNSUPPORTED;
+  // positions are 32-bit numbers
+  if (static_cast<int64_t>(max_blocks) * p->block_size > INT_MAX) return ZP_ERR_UNSUPPORTED;
+  if (B == 0) return ZP_OK;
+  if (!q || !out || !q->data || !out->data || !aligned(q->data, 2) || !aligned(out->data, 2)) return ZP_ERR_INVALID_ARG;
+  if (!tables || !seq_lens) return ZP_ERR_INVALID_ARG;
+  return ZP_OK;
+}
+
+AttnArgs args_of(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_rows* q, const zp_rows* out,
+                 const int32_t* tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
+                 int32_t sinks) {
+  AttnArgs a{};
+  a.num_blocks = num_blocks;
+  a.q = static_cast<const uint16_t*>(q->data);
+  a.out = static_cast<uint16_t*>(out->data);
+  a.q_ts = q->token_stride, a.q_hs = q->head_stride;
+  a.o_ts = out->token_stride, a.o_hs = out->head_stride;
+  a.tables = tables;
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.layer = layer;
+  a.max_blocks = max_blocks;
+  a.Hkv = p->num_kv_heads;
+  a.G = p->num_q_heads / p->num_kv_heads;
+  a.b = p->block_size;
+  a.window = window;
+  a.sinks = sinks;
+  a.sl2 = p->scale * 1.4426950408889634f;
+  return a;
+}
+
+bool sizes_ok(const zp_params* p, int32_t B, int32_t max_blocks) {
+  return p && B >= 0 && max_blocks >= 1 && p->num_kv_heads > 0 && p->num_q_heads > 0 &&
+         p->num_q_heads % p->num_kv_heads == 0 && p->head_dim > 0 && p->block_size > 0;
+}
+
+}  // namespace
+}  // namespace zp
+
+using namespace zp;
+
+extern "C" size_t zp_kv8_decode_workspace_size(const zp_params* p, int32_t B, int32_t max_blocks) {
+  if (!sizes_ok(p, B, max_blocks)) return 0;
+  return split_bytes(p, B, 1, static_cast<int64_t>(max_blocks) * p->block_size);
+}
+
+extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
+                                        const int32_t* block_tables, const int32_t* seq_lens, int32_t B,
+                                        int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                        const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_kv8_decode_attn");
+  if (!pool || !pool->codes || !pool->scales) return ZP_ERR_INVALID_ARG;
+  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  if (s != ZP_OK) return s;
+  if (!aligned(pool->codes, 16) || !aligned(pool->scales, 4)) return ZP_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < zp_kv8_decode_workspace_size(p, B, max_blocks))
+    return ZP_ERR_INVALID_ARG;
+  if (B == 0) return ZP_OK;
+  AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  a.pool = static_cast<const uint8_t*>(pool->codes);
+  a.scales = pool->scales;
+  a.T = B;
+  a.max_q = 1;
+  const SplitPlan plan = split_plan(p, B, 1, static_cast<int64_t>(max_blocks) * p->block_size, window, sinks);
+  return split_launch(a, true, p->head_dim, plan, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q,
+                                                 int32_t max_blocks, int32_t window, int32_t sinks) {
+  if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
+  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows) return 256;
+  return split_bytes(p, B, max_q, static_cast<int64_t>(max_blocks) * p->block_size);
+}
+
+extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                          int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                          int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                          const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_paged_window_attn");
+  if (!pool || !pool->base || T < 0 || max_q < 1) return ZP_ERR_INVALID_ARG;
+  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  if (s != ZP_OK) return s;
+  if (!aligned(pool->base, 16) || (B > 0 && !q_start)) return ZP_ERR_INVALID_ARG;
+  // (layer, block) is one coordinate of the tensor map
+  if (static_cast<int64_t>(p->num_layers) * pool->num_blocks > INT_MAX) return ZP_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks))
+    return ZP_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return ZP_OK;
+  AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  a.pool = static_cast<const uint8_t*>(pool->base);
+  a.q_start = q_start;
+  a.T = T;
+  a.max_q = max_q < T ? max_q : T;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
+    a.max_q = max_q;
+    const SplitPlan plan = split_plan(p, B, max_q, static_cast<int64_t>(max_blocks) * p->block_size, window, sinks);
+    return split_launch(a, false, p->head_dim, plan, workspace, st);
+  }
+  return tile_launch(a, pool, p, workspace, st);
+}

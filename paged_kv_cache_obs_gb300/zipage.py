@@ -64,6 +64,33 @@ class zp_debug(ctypes.Structure):
                 ("score", ctypes.c_void_p), ("keep", ctypes.c_void_p)]
 
 
+class zp_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+ZP_ROPE_NONE = 0
+ZP_ROPE_LINEAR = 1
+ZP_ROPE_BASE = 2
+ZP_ROPE_YARN = 3
+ZP_ROPE_WAVELENGTH = 4
+
+
+class zp_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_int32), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("mscale", ctypes.c_double)]
+
+
+class zp_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+class zp_kv8_pool(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -95,6 +122,21 @@ _sig("zp_test_decode_stalled", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _P, _P, 
 _sig("zp_redundancy_all_pairs", _I32, [ctypes.POINTER(zp_kv_pool), _P, ctypes.POINTER(zp_seq_meta),
                                        ctypes.POINTER(zp_params), _P, _P, _SZ, _P])
 _sig("zp_redundancy_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32])
+_ROWS = ctypes.POINTER(zp_rows)
+_sig("zp_rope_init", _I32, [ctypes.POINTER(zp_rope_config), ctypes.POINTER(zp_rope)])
+_sig("zp_rope_apply", _I32, [ctypes.POINTER(zp_rope), _ROWS, _ROWS, _I32, _ROWS, _ROWS, _I32, _P, _I32, _P])
+_sig("zp_kv8_append", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _ROWS, _I32, _P, _P, _I32, _P, _I32,
+                             ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_kv8_pack_blocks", _I32, [ctypes.POINTER(zp_kv_pool), _P, _P, ctypes.POINTER(zp_kv8_pool), _P, _I32, _I32, _I32,
+                                  ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_kv8_unpack_blocks", _I32, [ctypes.POINTER(zp_kv8_pool), _P, ctypes.POINTER(zp_kv_pool), _P, _I32, _I32, _I32,
+                                    ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_kv8_decode_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32])
+_sig("zp_kv8_decode_attn", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, _P, _I32, _I32, _I32, _I32, _ROWS,
+                                  ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_paged_window_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32, _I32, _I32, _I32, _I32])
+_sig("zp_paged_window_attn", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
+                                    _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _P])
 _sig("zp_read_error", _I32, [_P, _P, _I32P])
 _sig("zp_alloc_create", _I32, [_I64, ctypes.POINTER(_P)])
 _sig("zp_alloc_destroy", None, [_P])
@@ -286,6 +328,113 @@ def zp_paged_decode_attn_static(pool, layer: int, q, block_tables, seq_lens, out
                                          q.shape[0], block_tables.shape[1], _ptr(out),
                                          ctypes.byref(make_params(params)), _ptr(dev_status), _stream(stream))
     _check("zp_paged_decode_attn_static", st)
+
+
+# ------------------------------------------------------------------ rotary positions ---------
+
+def _rows(t):
+    """bf16 rows [tokens, heads, head_dim] with any token and head strides."""
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError("the last dimension of rows must be contiguous")
+    return zp_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _params(params):
+    """A dict, or what make_params made of it (which a caller may keep)."""
+    return params if isinstance(params, zp_params) else make_params(params)
+
+
+def _nbytes(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+def zp_rope_init(head_dim: int, rotary_dim: int, theta: float, interleaved: bool = False,
+                 scaling: int = ZP_ROPE_NONE, factor: float = 1.0, original_len: int = 0, low: float = 1.0,
+                 high: float = 4.0, mscale: float = 0.0) -> zp_rope:
+    """The handle of zp_rope_apply (host only; see zp_rope_config in include/zipage.h)."""
+    cfg = zp_rope_config(head_dim, rotary_dim, int(interleaved), scaling, theta, factor, original_len, low, high, mscale)
+    rope = zp_rope()
+    _check("zp_rope_init", lib.zp_rope_init(ctypes.byref(cfg), ctypes.byref(rope)))
+    return rope
+
+
+def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Rotates q [T, H_q, d] and k [T, H_kv, d] (either may be None), in place or into q_out, k_out."""
+    rq, rk = (None if t is None else _rows(t) for t in (q, k))
+    oq = None if q is None else (rq if q_out is None else _rows(q_out))
+    ok = None if k is None else (rk if k_out is None else _rows(k_out))
+    st = lib.zp_rope_apply(ctypes.byref(rope), rq, oq, 0 if q is None else q.shape[1], rk, ok,
+                           0 if k is None else k.shape[1], _ptr(positions), positions.shape[0], _stream(stream))
+    _check("zp_rope_apply", st)
+
+
+# ------------------------------------------------------------------ 8-bit cache --------------
+
+def _kv8(codes, scales):
+    return zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1])
+
+
+def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_tables, params, workspace, stream=None):
+    """Quantises the new keys and values k, v [T, H_kv, d] of one layer into the 8-bit pool: codes
+    (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
+    token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
+    st = lib.zp_kv8_append(_kv8(codes, scales), layer, _rows(k), _rows(v), k.shape[0], _ptr(token_start), _ptr(cached),
+                           cached.shape[0], _ptr(block_tables), block_tables.shape[1], _params(params),
+                           _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check("zp_kv8_append", st)
+
+
+def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace, fill=None, layers: tuple | None = None,
+                       stream=None):
+    """Blocks src_ids of the bf16 pool into blocks dst_ids of the 8-bit pool.  fill: optional device
+    int32 [n] of tokens per block; layers: optional (layer_begin, layer_count)."""
+    lb, lc = layers if layers is not None else (0, 0)
+    st = lib.zp_kv8_pack_blocks(zp_kv_pool(pool.data_ptr(), pool.shape[1]), _ptr(src_ids), _ptr(fill),
+                                _kv8(codes, scales), _ptr(dst_ids), src_ids.shape[0], lb, lc, _params(params),
+                                _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check("zp_kv8_pack_blocks", st)
+
+
+def zp_kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, params, workspace, layers: tuple | None = None,
+                         stream=None):
+    """Blocks src_ids of the 8-bit pool into blocks dst_ids of the bf16 pool."""
+    lb, lc = layers if layers is not None else (0, 0)
+    st = lib.zp_kv8_unpack_blocks(_kv8(codes, scales), _ptr(src_ids), zp_kv_pool(pool.data_ptr(), pool.shape[1]),
+                                  _ptr(dst_ids), src_ids.shape[0], lb, lc, _params(params), _ptr(workspace),
+                                  _nbytes(workspace), _stream(stream))
+    _check("zp_kv8_unpack_blocks", st)
+
+
+def zp_kv8_decode_workspace_size(params, B: int, max_blocks: int) -> int:
+    return lib.zp_kv8_decode_workspace_size(_params(params), B, max_blocks)
+
+
+def zp_kv8_decode_attn(codes, scales, layer: int, q, block_tables, seq_lens, out, params, workspace, window: int = 0,
+                       sinks: int = 0, stream=None):
+    """Decode attention over the 8-bit pool: q, out bf16 [B, H_q, d]; a request sees its last
+    `window` tokens and the first `sinks` (window 0: all)."""
+    st = lib.zp_kv8_decode_attn(_kv8(codes, scales), layer, _rows(q), _ptr(block_tables), _ptr(seq_lens), q.shape[0],
+                                block_tables.shape[1], window, sinks, _rows(out), _params(params), _ptr(workspace),
+                                _nbytes(workspace), _stream(stream))
+    _check("zp_kv8_decode_attn", st)
+
+
+# ------------------------------------------------------------------ windowed attention -------
+
+def zp_paged_window_workspace_size(params, T: int, B: int, max_q: int, max_blocks: int, window: int, sinks: int) -> int:
+    return lib.zp_paged_window_workspace_size(_params(params), T, B, max_q, max_blocks, window, sinks)
+
+
+def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, out, params, workspace, window: int,
+                         sinks: int, max_q: int, stream=None):
+    """Attention of the new tokens q [T, H_q, d] (request r: rows q_start[r] .. q_start[r + 1] - 1, its
+    last tokens in the cache) over the bf16 pool, with a window and `sinks` first tokens that stay
+    visible.  max_q: the most new tokens of a request."""
+    st = lib.zp_paged_window_attn(zp_kv_pool(pool.data_ptr(), pool.shape[1]), layer, _rows(q), _ptr(q_start), q.shape[0],
+                                  max_q, _ptr(block_tables), _ptr(seq_lens), seq_lens.shape[0], block_tables.shape[1],
+                                  window, sinks, _rows(out), _params(params), _ptr(workspace), _nbytes(workspace),
+                                  _stream(stream))
+    _check("zp_paged_window_attn", st)
 
 
 def zp_read_error(workspace, stream=None) -> int:
