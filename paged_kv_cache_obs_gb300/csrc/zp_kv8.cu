@@ -46,12 +46,18 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// Largest finite magnitude of two bf16 values, as its 15 bits, against `m`; inf and NaN are left out.
+// Largest magnitude of bf16 pairs, as two 15-bit patterns (which order like the values); inf and
+// NaN come out as 0x7F80 and above.
 __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) {
-  const uint32_t a = x & 0x7FFFu, b = (x >> 16) & 0x7FFFu;
-  if (a < 0x7F80u) m = max(m, a);
-  if (b < 0x7F80u) m = max(m, b);
-  return m;
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7FFF7FFFu));
+  return r;
+}
+// The same over the finite values only.
+__device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t x) {
+  if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+  if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+  return amax2(m, x);
 }
 
 // The scale of a tile whose largest finite magnitude has the bf16 bits `m`: with
@@ -64,18 +70,43 @@ __device__ __forceinline__ float scale_of(uint32_t m) {
 }
 __device__ __forceinline__ float inverse(float s) { return s > 0.0f ? 1.0f / s : 0.0f; }  // exact for powers of two
 
-// Two bf16 values to two codes; infinities become NaN (E4M3 has none).
+// Two bf16 values to two codes.  ODD: some value of the tile is not finite; infinities become NaN
+// (E4M3 has none).
+template <bool ODD>
 __device__ __forceinline__ uint32_t enc_pair(uint32_t x, float inv) {
   uint32_t c = enc2(lo_f(x) * inv, hi_f(x) * inv);
-  if ((x & 0x7F80u) == 0x7F80u) c |= 0x7Fu;
-  if ((x & 0x7F800000u) == 0x7F800000u) c |= 0x7F00u;
+  if (ODD && (x & 0x7F80u) == 0x7F80u) c |= 0x7Fu;
+  if (ODD && (x & 0x7F800000u) == 0x7F800000u) c |= 0x7F00u;
   return c;
 }
+template <bool ODD>
 __device__ __forceinline__ uint2 enc8(const uint4& x, float inv) {
-  return make_uint2(enc_pair(x.x, inv) | enc_pair(x.y, inv) << 16, enc_pair(x.z, inv) | enc_pair(x.w, inv) << 16);
+  return make_uint2(enc_pair<ODD>(x.x, inv) | enc_pair<ODD>(x.y, inv) << 16,
+                    enc_pair<ODD>(x.z, inv) | enc_pair<ODD>(x.w, inv) << 16);
 }
 
-__device__ __forceinline__ uint32_t warp_max(uint32_t m) { return __reduce_max_sync(0xffffffffu, m); }
+__device__ __forceinline__ uint32_t warp_max(uint32_t m) {
+  return __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+}
+
+// The tile's largest finite magnitude (bf16 bits) over the warp's registers; `odd`: some value is
+// not finite.  Two instructions a pair of values, and a second look only for tiles that need it.
+template <int NL>
+__device__ __forceinline__ uint32_t tile_amax(const uint4 (&w)[NL], bool& odd) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int l = 0; l < NL; ++l) m = amax2(amax2(amax2(amax2(m, w[l].x), w[l].y), w[l].z), w[l].w);
+  m = warp_max(m);
+  odd = m >= 0x7F80u;
+  if (odd) {
+    m = 0;
+#pragma unroll
+    for (int l = 0; l < NL; ++l)
+      m = amax2_finite(amax2_finite(amax2_finite(amax2_finite(m, w[l].x), w[l].y), w[l].z), w[l].w);
+    m = warp_max(m);
+  }
+  return m;
+}
 
 // ---- append -------------------------------------------------------------------------------
 
@@ -103,53 +134,63 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
   }
 }
 
-// Work is laid out over slots: request r of B owns the slots from token_start[r] / b + 2 r on, as
-// many as (blocks that its tokens can touch) or more, so a warp finds its request by searching
-// token_start alone and the host needs no per-request sizes: T / b + 2 B slots in all.  Grid (slot,
-// group of kWarpsQ tiles); a warp takes one (K|V, head) tile of the slot's block.
+// Work is laid out over slots, one touched block each.  Slot r < B is the first block that
+// request r's tokens touch, so a decode step needs no search.  Behind them request r owns the slots
+// B + token_start[r] / b + r on for its further blocks: at most token_start[r + 1] / b -
+// token_start[r] / b + 1 of them, since tokens that start anywhere in a block touch at most
+// n / b + 1 blocks after it.  A warp there finds its request by searching token_start, 32 probes at
+// a time, and the host needs no per-request sizes: T / b + 2 B slots in all.  Grid (slot, group
+// of kWarpsQ tiles); a warp takes one (K|V, head) tile of the slot's block.
 template <int D, int BS, bool VEC>
 __global__ void __launch_bounds__(kThreadsQ) append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;                 // lanes per row (8 values each)
   constexpr int RPL = 32 / LPR;              // rows per load of the warp
   constexpr int NL = BS / RPL;               // loads per tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t u = blockIdx.x;
   const int tile = blockIdx.y * kWarpsQ + warp;
 
-  if (blockIdx.x == 0 && blockIdx.y == 0) {  // token_start as a whole, once
-    bool bad = false;
-    for (int r = threadIdx.x; r < a.B; r += kThreadsQ) bad |= a.token_start[r] > a.token_start[r + 1];
-    if (threadIdx.x == 0) bad |= a.token_start[0] != 0 || a.token_start[a.B] != a.T;
-    if (bad) record(a.err, ZP_ERR_BAD_TABLE);
+  int r = static_cast<int>(blockIdx.x);
+  int s0, s1, j = 0;
+  int64_t c;
+  if (r < a.B) {
+    s0 = a.token_start[r];
+    s1 = a.token_start[r + 1];
+    c = a.cached[r];
+    // token_start as a whole: each request looks at its own step, the first at both ends
+    if (blockIdx.y == 0 && threadIdx.x == 0 &&
+        (s1 < s0 || (r == 0 && (s0 != 0 || a.token_start[a.B] != a.T))))
+      record(a.err, ZP_ERR_BAD_TABLE);
+  } else {
+    // the last request whose first further slot is <= u
+    const int64_t u = static_cast<int64_t>(blockIdx.x) - a.B;
+    int lo = 0, hi = a.B, last;
+    while (true) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      int si = -1, ei = 0, ci = 0;
+      if (i < hi) {
+        si = a.token_start[i];
+        ei = a.token_start[i + 1];
+        ci = a.cached[i];
+      }
+      const uint32_t vote = __ballot_sync(0xffffffffu, si >= 0 && static_cast<int64_t>(si / BS) + i <= u);
+      if (vote == 0) return;  // only when token_start[0] is not 0
+      last = 31 - __clz(vote);
+      lo += last * step;
+      hi = min(hi, lo + step);
+      if (step == 1) {
+        s0 = __shfl_sync(0xffffffffu, si, last);
+        s1 = __shfl_sync(0xffffffffu, ei, last);
+        c = __shfl_sync(0xffffffffu, ci, last);
+        break;
+      }
+    }
+    r = lo;
+    j = static_cast<int>(u - (s0 / BS + r)) + 1;
   }
   if (tile >= 2 * a.Hkv) return;
-
-  // the last request whose first slot is <= u, 32 probes at a time
-  int lo = 0, hi = a.B;
-  int s0 = 0;
-  while (true) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    int s = 0;
-    bool at = false;
-    if (i < hi) {
-      s = a.token_start[i];
-      at = s >= 0 && static_cast<int64_t>(s / BS) + 2 * static_cast<int64_t>(i) <= u;
-    }
-    const uint32_t vote = __ballot_sync(0xffffffffu, at);
-    if (vote == 0) return;  // only when token_start[0] is not 0
-    const int last = 31 - __clz(vote);
-    s0 = __shfl_sync(0xffffffffu, s, last);
-    lo += last * step;
-    hi = min(hi, lo + step);
-    if (step == 1) break;
-  }
-  const int r = lo;
-  const int64_t j = u - (s0 / BS + 2 * static_cast<int64_t>(r));
-  const int s1 = a.token_start[r + 1];
-  const int64_t c = a.cached[r];
   const int64_t n = static_cast<int64_t>(s1) - s0;
   if (n <= 0) return;
-  if (s1 > a.T || c < 0 || c + n > static_cast<int64_t>(a.max_blocks) * BS) {
+  if (s0 < 0 || s1 > a.T || c < 0 || c + n > static_cast<int64_t>(a.max_blocks) * BS) {
     if (j == 0 && tile == 0 && lane == 0) record(a.err, ZP_ERR_BAD_TABLE);
     return;
   }
@@ -157,31 +198,27 @@ __global__ void __launch_bounds__(kThreadsQ) append_kernel(const AppendArgs a) {
   const int64_t p0 = max(c, blk * BS), p1 = min(c + n, (blk + 1) * BS);  // this block's new tokens
   if (p0 >= p1) return;
   const int64_t phys = a.tables[static_cast<int64_t>(r) * a.max_blocks + blk];
-  if (phys < 0 || phys >= a.num_blocks) {
-    if (tile == 0 && lane == 0) record(a.err, ZP_ERR_BAD_TABLE);
-    return;
-  }
   const int kv = tile / a.Hkv, h = tile - kv * a.Hkv;
   const int first = static_cast<int>(p0 - blk * BS), end = static_cast<int>(p1 - blk * BS);  // rows [first, end)
-  const int64_t t = ((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 + kv) * a.Hkv + h;
-  uint8_t* const codes = a.codes + t * (BS * D) + lane * 8;  // + 256 per load
-  const uint16_t* const x = (kv ? a.x[1] : a.x[0]) + (s0 + (p0 - c)) * (kv ? a.ts[1] : a.ts[0]) +
-                            h * (kv ? a.hs[1] : a.hs[0]) + (lane % LPR) * 8;
   const int64_t ts = kv ? a.ts[1] : a.ts[0];
-  const float old = first > 0 ? a.scales[t] : 0.0f;
+  const uint16_t* const x = (kv ? a.x[1] : a.x[0]) + (s0 + (p0 - c)) * ts + h * (kv ? a.hs[1] : a.hs[0]) + (lane % LPR) * 8;
   const int row = lane / LPR;
-
-  uint4 w[NL];
-  uint32_t m = 0;
+  uint4 w[NL];  // on their way while the block's id is
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
     const int rr = l * RPL + row;
     w[l] = make_uint4(0, 0, 0, 0);
     if (rr >= first && rr < end) w[l] = load8<VEC>(x + (rr - first) * ts);
   }
-#pragma unroll
-  for (int l = 0; l < NL; ++l) m = amax2(amax2(amax2(amax2(m, w[l].x), w[l].y), w[l].z), w[l].w);
-  const float s = fmaxf(old, scale_of(warp_max(m))), inv = inverse(s);
+  if (phys < 0 || phys >= a.num_blocks) {
+    if (tile == 0 && lane == 0) record(a.err, ZP_ERR_BAD_TABLE);
+    return;
+  }
+  const int64_t t = ((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 + kv) * a.Hkv + h;
+  uint8_t* const codes = a.codes + t * (BS * D) + lane * 8;  // + 256 per load
+  const float old = first > 0 ? a.scales[t] : 0.0f;
+  bool odd;
+  const float s = fmaxf(old, scale_of(tile_amax(w, odd))), inv = inverse(s);
   if (first > 0 && s > old) {  // the rows already there, brought to the larger scale
     const float ratio = old * inv;
 #pragma unroll
@@ -200,7 +237,8 @@ __global__ void __launch_bounds__(kThreadsQ) append_kernel(const AppendArgs a) {
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
     const int rr = l * RPL + row;
-    if (rr >= first && rr < end) *reinterpret_cast<uint2*>(codes + l * 256) = enc8(w[l], inv);
+    if (rr >= first && rr < end)
+      *reinterpret_cast<uint2*>(codes + l * 256) = odd ? enc8<true>(w[l], inv) : enc8<false>(w[l], inv);
   }
   if (lane == 0 && (first == 0 || s > old)) a.scales[t] = s;
 }
@@ -248,15 +286,13 @@ __global__ void __launch_bounds__(kThreadsQ) pack_kernel(const BlockArgs a) {
   uint2* const codes = reinterpret_cast<uint2*>(a.dst + dst * (BS * D)) + lane;
   const int nv = fill * D;  // values of the block's tokens come first
   uint4 w[NL];
-  uint32_t m = 0;
 #pragma unroll
   for (int l = 0; l < NL; ++l) w[l] = (l * 256 + lane * 8 < nv) ? x[l * 32] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int l = 0; l < NL; ++l) m = amax2(amax2(amax2(amax2(m, w[l].x), w[l].y), w[l].z), w[l].w);
-  const float s = scale_of(warp_max(m)), inv = inverse(s);
+  bool odd;
+  const float s = scale_of(tile_amax(w, odd)), inv = inverse(s);
 #pragma unroll
   for (int l = 0; l < NL; ++l)
-    if (l * 256 + lane * 8 < nv) codes[l * 32] = enc8(w[l], inv);
+    if (l * 256 + lane * 8 < nv) codes[l * 32] = odd ? enc8<true>(w[l], inv) : enc8<false>(w[l], inv);
   if (lane == 0) a.scales[dst] = s;
 }
 
