@@ -288,14 +288,13 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
  * a sliding window.
  *
  * They share these conventions, on top of the ones at the top of this file:
- *   - Workspaces are zeroed once before their first use (the Python binding's new_workspace
- *     does) and then belong to one call in flight at a time.  A call leaves the parts that the
- *     next one expects zeroed as it found them, so calls of any of these operators may follow
- *     one another on a stream, and captured graphs may share a workspace if they are replayed
- *     one after the other.
- *   - The error word at the start of the workspace is sticky: a call writes it only when it
- *     finds an error, and it keeps the first one until zp_read_error() reads and clears it.
- *     One read can so cover all layers of a step.
+ *   - A workspace belongs to one call in flight at a time; calls of any of these operators may
+ *     follow one another on a stream with the same one, and captured graphs may share one if they
+ *     are replayed one after the other.
+ *   - The error word at the start of the workspace is sticky: zero it once (the Python binding's
+ *     new_workspace does).  A call writes it only when it finds an error, and it keeps the first one
+ *     until zp_read_error() reads and clears it, so one read can cover all layers of a step.
+ *     Nothing else in a workspace has to hold any value.
  *   - params.scale is finite and above 0 where a call uses it.
  *   - A zp_rows describes bf16 rows [tokens][heads][head_dim] whose last dimension is
  *     contiguous; strides are in elements.  Any strides are accepted; rows whose base address

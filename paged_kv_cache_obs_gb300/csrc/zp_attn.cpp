@@ -13,6 +13,8 @@ zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_
                 int32_t sinks) {
   if (!p || B < 0 || max_blocks < 1 || window < 0 || sinks < 0 || num_blocks <= 0) return ZP_ERR_INVALID_ARG;
   if (layer < 0 || layer >= p->num_layers) return ZP_ERR_INVALID_ARG;
+  // (layer, block) is one 32-bit coordinate of the tensor map
+  if (num_blocks > INT_MAX / p->num_layers) return ZP_ERR_UNSUPPORTED;
   if (p->num_kv_heads <= 0 || p->num_q_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return ZP_ERR_INVALID_ARG;
   if (!(p->scale > 0.0f) || !std::isfinite(p->scale)) return ZP_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return ZP_ERR_UNSUPPORTED;
@@ -61,7 +63,7 @@ using namespace zp;
 
 extern "C" size_t zp_kv8_decode_workspace_size(const zp_params* p, int32_t B, int32_t max_blocks) {
   if (!sizes_ok(p, B, max_blocks)) return 0;
-  return split_bytes(p, B, 1, static_cast<int64_t>(max_blocks) * p->block_size);
+  return split_plan(p, true, B, 1, max_blocks, 0, 0).bytes;
 }
 
 extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
@@ -81,15 +83,15 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
   a.scales = pool->scales;
   a.T = B;
   a.max_q = 1;
-  const SplitPlan plan = split_plan(p, B, 1, static_cast<int64_t>(max_blocks) * p->block_size, window, sinks);
-  return split_launch(a, true, p->head_dim, plan, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return split_launch(a, p, true, split_plan(p, true, B, 1, max_blocks, window, sinks), workspace,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q,
                                                  int32_t max_blocks, int32_t window, int32_t sinks) {
   if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
   if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows) return 256;
-  return split_bytes(p, B, max_q, static_cast<int64_t>(max_blocks) * p->block_size);
+  return split_plan(p, false, B, max_q, max_blocks, window, sinks).bytes;
 }
 
 extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
@@ -98,15 +100,14 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
                                           const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
   zp::NvtxRange nvtx_range("zp_paged_window_attn");
   if (!pool || !pool->base || T < 0 || max_q < 1) return ZP_ERR_INVALID_ARG;
+  if (T == 0) B = 0;  // nothing to do, and q and out may be empty
   const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
   if (!aligned(pool->base, 16) || (B > 0 && !q_start)) return ZP_ERR_INVALID_ARG;
-  // (layer, block) is one coordinate of the tensor map
-  if (static_cast<int64_t>(p->num_layers) * pool->num_blocks > INT_MAX) return ZP_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks))
     return ZP_ERR_INVALID_ARG;
-  if (B == 0 || T == 0) return ZP_OK;
+  if (B == 0) return ZP_OK;
   AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
   a.pool = static_cast<const uint8_t*>(pool->base);
   a.q_start = q_start;
@@ -115,8 +116,7 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
     a.max_q = max_q;
-    const SplitPlan plan = split_plan(p, B, max_q, static_cast<int64_t>(max_blocks) * p->block_size, window, sinks);
-    return split_launch(a, false, p->head_dim, plan, workspace, st);
+    return split_launch(a, p, false, split_plan(p, false, B, max_q, max_blocks, window, sinks), workspace, st);
   }
   return tile_launch(a, pool, p, workspace, st);
 }

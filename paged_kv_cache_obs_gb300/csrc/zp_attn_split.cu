@@ -4,12 +4,13 @@
 //
 //   out[row] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale <q_row, k_t>) over the t that the row sees
 //
-// The work is bound by the bytes of K and V; every byte is read once, straight from HBM into the
-// registers from which the warp-level MMAs take it, with no shared memory on the way:
+// The work is bound by the bytes of K and V.  Every warp streams its tiles of 16 tokens through a
+// ring of its own (TMA, one box each for K and V, completing on the stage's mbarrier) and multiplies
+// with the warp-level MMAs, whose operands come from plain 16-byte shared loads:
 //   - S^T = K Q^T with the 16 tokens of a tile as the MMA's 16 rows and the query rows as its 8
-//     columns.  The order of the contraction is free as long as K and Q agree, so a lane loads 16
+//     columns.  The order of the contraction is free as long as K and Q agree, so a lane takes 16
 //     contiguous bytes of a key and uses each 4 (or 8) of them in one k-step.
-//   - O^T = V^T P^T with the values' dims as rows and tokens as the contraction.  A lane loads
+//   - O^T = V^T P^T with the values' dims as rows and tokens as the contraction.  A lane takes
 //     contiguous dims of the 4 tokens that its A fragment holds; a byte permutation pairs two
 //     tokens of a dim in a register.  Which dim a row of the product stands for is free too.
 //   - P goes from the accumulator layout (a lane holds tokens) to the operand layout (a lane holds
@@ -23,12 +24,15 @@
 // more than 8 (in log2), so that P stays below 2^8 and most tiles need one vote in place of
 // reductions and rescaling.
 //
-// Grid (split, kv head, request), 4 warps a CTA; a split is a range of the request's visible
-// 16-token tiles.  With more than one split the CTA that finishes a row last merges the partials in
-// the order of the splits, so results do not depend on the order in which CTAs run.
+// Grid (split, kv head, request), 4 warps a CTA; a row's visible 16-token tiles are dealt evenly
+// over its splits.  Up to 8 splits are one thread-block cluster, which joins its sums through
+// distributed shared memory; with more, each cluster leaves one part, and a second kernel joins
+// the parts.  Both join in the order of the splits, so results do not depend on the order in which
+// CTAs run, and nothing in the workspace has to be zero.
 #include "zp_attn.h"
 
 #include <algorithm>
+#include <climits>
 
 #include "zp_ptx.cuh"
 
@@ -38,8 +42,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                    // tokens
-constexpr int kMaxTps = 32 * kWarps;         // a lane holds the block id of each of its warp's tiles
 constexpr float kLazy = 8.0f;
+constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -69,29 +73,53 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-template <bool F16>
+// c (16x8 fp32) = or += a (16x16) * b (16x8), f16 or bf16
+template <bool F16, bool ADD = true>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
+  const float z[4] = {ADD ? c[0] : 0.0f, ADD ? c[1] : 0.0f, ADD ? c[2] : 0.0f, ADD ? c[3] : 0.0f};
   if (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
 }
 
-// The pool is read once: loads that skip L1.
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Token of a tile that stands in row (and, for V, contraction index) k of the products.  With
+// 128-byte rows under the 128-byte swizzle this order lets the 16-byte loads of K (rows 2i and
+// 2i+1 together) and of V (rows 0, 2, 4, 6 or 1, 3, 5, 7 together) touch every bank once.
+__device__ __forceinline__ int token_at(int k) { return k ^ ((k & 1) << 2); }
+
+// Byte offset of 16-byte chunk `ch` of row `row` of a tile of 16 rows of RB bytes, as the TMA
+// stores it: 128-byte swizzle, rows above 128 bytes as two halves; 64-byte swizzle for 64.
+template <int RB>
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
+  if constexpr (RB == 64) return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+  return (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
 }
 
 // What a (request, kv head) sees.
@@ -126,11 +154,23 @@ __device__ __forceinline__ bool span_of(const AttnArgs& a, int r, Span& s, bool&
   return true;
 }
 
-__device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int h, int row, int dim, const float (&v)[4]) {
-  if (row >= a.G * s.n) return;
+// v and l += another part's sums, brought from its maximum to M.  A part without a maximum has sums of
+// 0, or NaN if every logit was.
+__device__ __forceinline__ void join(float (&v)[4], float& l, float4 y, float yl, float ym, float M) {
+  const float w = ym == -INFINITY ? 1.0f : ex2(ym - M);
+  l = fmaf(yl, w, l);
+  v[0] = fmaf(y.x, w, v[0]);
+  v[1] = fmaf(y.y, w, v[1]);
+  v[2] = fmaf(y.z, w, v[2]);
+  v[3] = fmaf(y.w, w, v[3]);
+}
+
+// Four dims of an output row: sums over the sum of weights (0 where nothing is seen).
+__device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int h, int row, int dim, const float (&v)[4], float l) {
   const int i = row / a.G, g = row - i * a.G;
   uint16_t* const o = a.out + (s.q0 + i) * a.o_ts + (h * a.G + g) * a.o_hs + dim;
-  const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
   if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
   } else {
@@ -142,51 +182,132 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int
 }
 
 template <bool FP8, int D, int NT>
-__global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int ES = FP8 ? 1 : 2;              // bytes per value
-  constexpr int ROWS = 8 * NT;
-  constexpr int KC = D * ES / 64;              // 16-byte chunks of a key that a lane holds
+struct Shape {
+  static constexpr int ES = FP8 ? 1 : 2;                  // bytes per value
+  static constexpr int RB = D * ES;                       // bytes of a row
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int TILE = kTile * RB;                 // bytes of K (or V) of a tile
+  static constexpr int SUB = RB <= 64 ? 2 : 1;            // tiles that a warp takes at a time
+  static constexpr int STAGES = 2;
+  static constexpr int STAGE = SUB * 2 * TILE;            // [tile][K|V]
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int ACC = kWarps * ROWS * D * 4;       // the warps' sums, in the ring's place
+  static constexpr int SMEM = (RING > ACC ? RING : ACC) + 1024;
+  // CTAs of an SM: what shared memory and, with 16 rows, registers hold
+  static constexpr int CTAS = NT == 2 ? (D == 128 ? 2 : 3) : RB <= 128 ? 4 : 3;
+};
+
+// Where 16-byte chunk `ch` of a row's sums stands: spread so that neither the warps' writes nor the
+// joining reads meet in a bank.
+template <bool FP8>
+__device__ __forceinline__ int acc_at(int row, int ch) {
+  const int c = (row >> 1) & 3;
+  return ch ^ (FP8 ? c : (c & 1) | (c & 2) << 1);
+}
+
+template <bool FP8, int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
+  using Sh = Shape<FP8, D, NT>;
+  constexpr int ROWS = Sh::ROWS, RB = Sh::RB, STAGES = Sh::STAGES, TILE = Sh::TILE, SUB = Sh::SUB;
+  constexpr int KC = RB / 64;                  // 16-byte chunks of a key that a lane holds
   constexpr int KS = D / 16;                   // k-steps of S
   constexpr int MT = D / 16;                   // 16-dim row tiles of O^T
-  constexpr int VW = D * ES / 32;              // words of a value row that a lane holds: 2, 4 or 8
-  __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-  __shared__ __align__(16) float sm_acc[kWarps][ROWS][D];
-  __shared__ int sm_last;
+  constexpr int VW = RB / 32;                  // words of a value row that a lane holds: 2, 4 or 8
+  __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS], cta_m[ROWS], cta_l[ROWS];
+  __shared__ __align__(8) uint64_t full[kWarps][STAGES];
+  __shared__ int sm_bad;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
+  const int bshift = a.b == 2 * kTile ? 1 : 0;  // tiles per block, as a shift
+  const int32_t* const table = a.tables + static_cast<int64_t>(r) * a.max_blocks;
+  const int first = split * kWarps + warp;  // the warp's first group of SUB tiles
+  // Without a window the warp's tiles do not depend on the row's length, and their block ids are on
+  // their way together with it.
+  const bool early = a.window == 0;
+  int early_id = 0;
+  if (early) {
+    const int64_t blk = ((first + static_cast<int64_t>(lane / SUB) * (a.splits * kWarps)) * SUB + lane % SUB) >> bshift;
+    if (blk < a.max_blocks) early_id = table[blk];
+  }
   Span s;
   bool bad;
-  if (!span_of(a, r, s, bad)) {
+  if (!span_of(a, r, s, bad)) {  // the same for every CTA of the cluster
     if (bad && split == 0 && h == 0 && tid == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
     return;
   }
-  const int ns = max(1, (s.tiles + a.tps - 1) / a.tps);
-  if (split >= ns) return;
-  const int tile0 = split * a.tps, tile1 = min(s.tiles, tile0 + a.tps);
-  const int cnt = max(0, (tile1 - tile0 - warp + kWarps - 1) / kWarps);  // tiles of this warp
+  // the row's tiles are dealt out one by one to the warps of its splits
+  const int stride = a.splits * kWarps;
+  const int groups = (s.tiles + SUB - 1) / SUB;
+  const int todo = max(0, (groups - first + stride - 1) / stride);  // groups of SUB tiles of this warp
 
-  // lane i: block id (and scales) of the warp's i-th tile
-  const int tpb = a.b / kTile;
-  int my_phys = 0, my_tile = 0;
-  float my_ks = 0.0f, my_vs = 0.0f;
-  bool my_bad = false;
-  const int64_t layer_base = static_cast<int64_t>(a.layer) * a.num_blocks;
-  if (lane < cnt) {
-    const int li = tile0 + warp + kWarps * lane;
-    my_tile = li < s.sink_tiles ? li : s.win_tile + li - s.sink_tiles;
-    my_phys = a.tables[static_cast<int64_t>(r) * a.max_blocks + my_tile / tpb];
-    my_bad = my_phys < 0 || my_phys >= a.num_blocks;
-    if (FP8 && !my_bad) {
-      const float* sc = a.scales + (layer_base + my_phys) * 2 * a.Hkv + h;
-      my_ks = sc[0];
-      my_vs = sc[a.Hkv];
-    }
+  if (tid == 0) sm_bad = 0;
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
   }
-  const bool cta_bad = __syncthreads_or(my_bad);
-  if (cta_bad && tid == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
-  const int todo = cta_bad ? 0 : cnt;
+  if (tid == 0) prefetch_tensormap(&tm);
+  __syncthreads();
+
+  // Lane i holds the block id (and scales) of tile i of the warp's list, 32 tiles at a time, and the
+  // next 32 besides.  An id outside the pool is reported, and block 0 read in its place.
+  constexpr int BATCH = 32 / SUB;  // groups whose ids a warp holds
+  const int64_t layer_base = static_cast<int64_t>(a.layer) * a.num_blocks;
+  const auto tile_of = [&](int i, int sub) {  // tile of the cache; past the list's end: >= 2^30
+    const int li = (first + stride * i) * SUB + sub;
+    return li < s.sink_tiles ? li : li < s.tiles ? s.win_tile + li - s.sink_tiles : 1 << 30;
+  };
+  int phys[2] = {0, 0};
+  float kscale[2] = {0.0f, 0.0f}, vscale[2] = {0.0f, 0.0f};
+  bool bad_id = false;
+  const auto load_ids = [&](int n) {
+    const int tile = tile_of(n * BATCH + lane / SUB, lane % SUB);
+    int id = 0;
+    if (tile < 1 << 30) id = (early && n == 0) ? early_id : table[tile >> bshift];
+    const bool out = id < 0 || id >= a.num_blocks;
+    bad_id |= out;
+    id = out ? 0 : id;
+    if (n & 1) phys[1] = id;
+    else phys[0] = id;
+  };
+  const auto load_scales = [&](int n) {
+    if (!FP8) return;
+    const float* const sc = a.scales + (layer_base + ((n & 1) ? phys[1] : phys[0])) * 2 * a.Hkv + h;
+    const float x = sc[0], y = sc[a.Hkv];
+    if (n & 1) kscale[1] = x, vscale[1] = y;
+    else kscale[0] = x, vscale[0] = y;
+  };
+  uint8_t* const my_ring = ring + warp * (STAGES * Sh::STAGE);
+  // The pool is the tensor {d, 2 Hkv b rows, layers * blocks}: K rows of head h start at h b, V rows
+  // at (Hkv + h) b.
+  const auto issue = [&](int i, int st) {
+    int id[SUB];
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub)
+      id[sub] = __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? phys[1] : phys[0], (i % BATCH) * SUB + sub);
+    if (lane == 0) {
+      uint64_t* const bar = &full[warp][st];
+      const bool all = tile_of(i, SUB - 1) < 1 << 30;  // the list's last group may be short
+      mbar_arrive_expect_tx(bar, (all ? SUB : 1) * 2 * TILE);
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) {
+        if (sub > 0 && !all) break;
+        uint8_t* const k = my_ring + st * Sh::STAGE + sub * 2 * TILE;
+        const int row = h * a.b + (tile_of(i, sub) & ((1 << bshift) - 1)) * kTile;
+#pragma unroll
+        for (int hd = 0; hd < (RB > 128 ? 2 : 1); ++hd) {
+          tma_load_3d(k + hd * kTile * 128, &tm, bar, hd * 64, row, static_cast<int>(layer_base) + id[sub]);
+          tma_load_3d(k + TILE + hd * kTile * 128, &tm, bar, hd * 64, a.Hkv * a.b + row, static_cast<int>(layer_base) + id[sub]);
+        }
+      }
+    }
+  };
+  load_ids(0);
+  for (int i = 0; i < STAGES && i < todo; ++i) issue(i, i);
+  load_scales(0);
 
   // queries as B fragments: column (row of the output) nt*8 + g
   uint32_t qb[NT][KS][2];
@@ -197,16 +318,27 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     const bool have = row < a.G * s.n;
     const int i = have ? row / a.G : 0, gi = have ? row - i * a.G : 0;
     const uint16_t* const q = a.q + (s.q0 + i) * a.q_ts + (h * a.G + gi) * a.q_hs;
-    // two values at dim e of the row (e even); queries may start at any 2-byte address
-    const auto two = [&](int e) {
-      return have ? static_cast<uint32_t>(q[e]) | static_cast<uint32_t>(q[e + 1]) << 16 : 0u;
-    };
+    // the lane's 16-byte chunk c + 4j of a key holds 4 k-steps (E4M3) or 2 (bf16)
+    if (!have) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      // 16-byte chunk c + 4j of a key: FP8 holds 4 k-steps, bf16 holds 2
-      const int e = FP8 ? 16 * (c + 4 * (ks >> 2)) + 4 * (ks & 3) : 8 * (c + 4 * (ks >> 1)) + 4 * (ks & 1);
-      qb[nt][ks][0] = two(e);
-      qb[nt][ks][1] = two(e + 2);
+      for (int ks = 0; ks < KS; ++ks) qb[nt][ks][0] = qb[nt][ks][1] = 0;
+    } else if ((reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+#pragma unroll
+      for (int v = 0; v < KS / 2; ++v) {  // 8 values
+        const int e = FP8 ? 16 * (c + 4 * (v >> 1)) + 8 * (v & 1) : 8 * (c + 4 * v);
+        const uint4 x = *reinterpret_cast<const uint4*>(q + e);
+        qb[nt][2 * v][0] = x.x;
+        qb[nt][2 * v][1] = x.y;
+        qb[nt][2 * v + 1][0] = x.z;
+        qb[nt][2 * v + 1][1] = x.w;
+      }
+    } else {  // queries may start at any 2-byte address
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int e = FP8 ? 16 * (c + 4 * (ks >> 2)) + 4 * (ks & 3) : 8 * (c + 4 * (ks >> 1)) + 4 * (ks & 1);
+        qb[nt][ks][0] = static_cast<uint32_t>(q[e]) | static_cast<uint32_t>(q[e + 1]) << 16;
+        qb[nt][ks][1] = static_cast<uint32_t>(q[e + 2]) | static_cast<uint32_t>(q[e + 3]) << 16;
+      }
     }
     float mult = 1.0f;
     if (FP8) {
@@ -240,117 +372,91 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     for (int mt = 0; mt < MT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
   }
 
-  // K: rows g and g + 8 of the tile; V: tokens 2c, 2c+1, 2c+8, 2c+9
-  uint4 kr[2][KC];
-  uint32_t vr[4][VW];
-  const int64_t head_bytes = static_cast<int64_t>(a.b) * D * ES;
-  const auto tile_ptr = [&](int i) {
-    const int phys = __shfl_sync(0xffffffffu, my_phys, i), tile = __shfl_sync(0xffffffffu, my_tile, i);
-    return a.pool + ((layer_base + phys) * 2 * a.Hkv + h) * head_bytes + (tile % tpb) * (kTile * D * ES);
-  };
-  const auto load_k = [&](const uint8_t* p) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int j = 0; j < KC; ++j) kr[half][j] = ldg16(p + (g + 8 * half) * (D * ES) + (c + 4 * j) * 16);
-  };
-  const auto load_v = [&](const uint8_t* p) {
-    p += a.Hkv * head_bytes;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint8_t* const row = p + (2 * c + (t & 1) + 8 * (t >> 1)) * (D * ES);
-      if constexpr (VW == 2) {
-        const uint2 x = ldg8(row + g * 8);
-        vr[t][0] = x.x;
-        vr[t][1] = x.y;
-      } else {
-#pragma unroll
-        for (int j = 0; j < VW / 4; ++j) {
-          const uint4 x = ldg16(row + (g + 8 * j) * 16);
-          vr[t][4 * j] = x.x;
-          vr[t][4 * j + 1] = x.y;
-          vr[t][4 * j + 2] = x.z;
-          vr[t][4 * j + 3] = x.w;
-        }
-      }
-    }
-  };
-  const uint8_t* cur = nullptr;
-  if (todo > 0) {
-    cur = tile_ptr(0);
-    load_k(cur);
-    load_v(cur);
-  }
   const int p_last = s.p0 + s.n - 1;
-  for (int i = 0; i < todo; ++i) {
-    const int t0 = __shfl_sync(0xffffffffu, my_tile, i) * kTile;
-    const float ks_scale = FP8 ? __shfl_sync(0xffffffffu, my_ks, i) : 1.0f;
-    const float vs_scale = FP8 ? __shfl_sync(0xffffffffu, my_vs, i) : 1.0f;
-    const bool more = i + 1 < todo;
-    const uint8_t* const next = more ? tile_ptr(i + 1) : nullptr;
+  float vref = 0.0f, vinv = 0.0f;  // FP8: V scale that o is in units of, and its inverse
+  bool ok = true;
+  int i = 0;
+  uint32_t phase = 0;  // of the ring's current round
+  for (; i < todo; ++i) {
+    const int st = i & (STAGES - 1);
+    if (i % BATCH == 0 && i + BATCH < todo) load_ids(i / BATCH + 1);
+    if (i % BATCH == BATCH / 4 && i - BATCH / 4 + BATCH < todo) load_scales(i / BATCH + 1);
+    float ks[SUB], vs[SUB];
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) {
+      const int src = (i % BATCH) * SUB + sub;
+      ks[sub] = FP8 ? __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? kscale[1] : kscale[0], src) : 1.0f;
+      vs[sub] = FP8 ? __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? vscale[1] : vscale[0], src) : 1.0f;
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][st], phase, kWaitNs));
+    if (!ok) break;
+    if (st == STAGES - 1) phase ^= 1;
+    const uint32_t buf = smem_u32(my_ring + st * Sh::STAGE);
 
-    float x[NT][4];
+    // S^T, tokens of rows g and g + 8 of each tile's product
+    float x[SUB][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+    for (int sub = 0; sub < SUB; ++sub) {
 #pragma unroll
-    for (int j = 0; j < KC; ++j) {
-      const uint32_t w0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
-      const uint32_t w1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
-      if constexpr (FP8) {
+      for (int j = 0; j < KC; ++j) {
+        const uint4 k0 = lds16(buf + sub * 2 * TILE + chunk_at<RB>(token_at(g), c + 4 * j));
+        const uint4 k1 = lds16(buf + sub * 2 * TILE + chunk_at<RB>(token_at(g) + 8, c + 4 * j));
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < (FP8 ? 4 : 2); ++w) {
           uint32_t a0, a1, a2, a3;
-          dec4(w0[w], a0, a2);
-          dec4(w1[w], a1, a3);
+          if constexpr (FP8) {
+            dec4(w0[w], a0, a2);
+            dec4(w1[w], a1, a3);
+          } else {
+            a0 = w0[2 * w], a1 = w1[2 * w], a2 = w0[2 * w + 1], a3 = w1[2 * w + 1];
+          }
+          const int kstep = (FP8 ? 4 : 2) * j + w;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<true>(x[nt], a0, a1, a2, a3, qb[nt][4 * j + w][0], qb[nt][4 * j + w][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (kstep == 0) mma<FP8, false>(x[sub][nt], a0, a1, a2, a3, qb[nt][kstep][0], qb[nt][kstep][1]);
+            else mma<FP8>(x[sub][nt], a0, a1, a2, a3, qb[nt][kstep][0], qb[nt][kstep][1]);
+          }
         }
-      } else {
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma<false>(x[nt], w0[2 * w], w1[2 * w], w0[2 * w + 1], w1[2 * w + 1], qb[nt][2 * j + w][0], qb[nt][2 * j + w][1]);
       }
     }
-    if (more) load_k(next);
-
+    // tokens seen by every row, or row by row
+    bool full_sub[SUB], none[SUB];
+    int t0[SUB];
+    bool raise = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] *= qs[nt][e & 1] * ks_scale;
-    // tokens t0 .. t0 + 15: seen by every row, or row by row
-    const bool full = t0 + kTile - 1 <= s.p0 && (a.window == 0 || t0 > p_last - a.window || t0 + kTile <= a.sinks);
-    if (!full) {
+    for (int sub = 0; sub < SUB; ++sub) {
+      const int tile = tile_of(i, sub);
+      none[sub] = sub > 0 && tile >= 1 << 30;  // past the list's end: above every position
+      t0[sub] = none[sub] ? INT_MAX - kTile : tile * kTile;
+      full_sub[sub] = !none[sub] && t0[sub] + kTile - 1 <= s.p0 &&
+                      (a.window == 0 || t0[sub] > p_last - a.window || t0[sub] + kTile <= a.sinks);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = nt * 8 + 2 * c + (e & 1), t = t0 + g + (e >> 1) * 8;
-          const int p = s.p0 + min(row / a.G, s.n - 1);
-          if (!(t <= p && (a.window == 0 || t > p - a.window || t < a.sinks))) x[nt][e] = -INFINITY;
-        }
-      // values that no row sees: zero times anything must be zero
+        for (int e = 0; e < 4; ++e) x[sub][nt][e] *= FP8 ? qs[nt][e & 1] * ks[sub] : qs[nt][e & 1];
+      if (!full_sub[sub]) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int tt = t0 + 2 * c + (t & 1) + 8 * (t >> 1);
-        if (!(tt <= p_last && (a.window == 0 || tt > s.p0 - a.window || tt < a.sinks))) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int w = 0; w < VW; ++w) vr[t][w] = 0;
-        }
+          for (int e = 0; e < 4; ++e) {
+            const int row = nt * 8 + 2 * c + (e & 1), t = t0[sub] + token_at(g) + (e >> 1) * 8;
+            const int p = s.p0 + min(row / a.G, s.n - 1);
+            if (!(t <= p && (a.window == 0 || t > p - a.window || t < a.sinks))) x[sub][nt][e] = -INFINITY;
+          }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) raise |= fmaxf(x[sub][nt][e], x[sub][nt][e + 2]) > m[nt][e] + kLazy;
     }
-    bool raise = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) raise |= fmaxf(x[nt][e], x[nt][e + 2]) > m[nt][e] + kLazy;
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(x[nt][e], x[nt][e + 2]);
+          float mx = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
+          if (SUB > 1) mx = fmaxf(mx, fmaxf(x[SUB - 1][nt][e], x[SUB - 1][nt][e + 2]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -366,94 +472,169 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
           }
         }
     }
-    uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-        x[nt][e] = ex2(x[nt][e] - ref);
-        l[nt][e & 1] += x[nt][e];
-      }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (FP8) {
-          ph[nt][e] = transpose8(pack_f16(x[nt][2 * e], x[nt][2 * e + 1]));
-        } else {
-          const uint32_t hi = pack_bf16(x[nt][2 * e], x[nt][2 * e + 1]);
-          ph[nt][e] = transpose8(hi);
-          pl[nt][e] = transpose8(pack_bf16(x[nt][2 * e] - lo_f(hi), x[nt][2 * e + 1] - hi_f(hi)));
+        for (int sub = 0; sub < SUB; ++sub) {
+          x[sub][nt][e] = ex2(x[sub][nt][e] - ref);
+          l[nt][e & 1] += x[sub][nt][e];
         }
       }
-    }
-    bool redo = false;
-    if (!FP8 && !full && s.n > 1) {
-      // a value that some rows see and others do not must not reach the others as 0 * inf
-      bool odd = false;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int sub = 0; sub < SUB; ++sub) {
+      if (none[sub]) continue;
+      const uint32_t vbuf = buf + sub * 2 * TILE + TILE;
+      // V of contraction indices 2c, 2c+1, 2c+8, 2c+9
+      uint32_t vr[4][VW];
 #pragma unroll
-        for (int w = 0; w < VW; ++w)
-          odd |= (vr[t][w] & 0x7F80u) == 0x7F80u || (vr[t][w] & 0x7F800000u) == 0x7F800000u;
-      redo = __any_sync(0xffffffffu, odd);
-    }
-    if (!FP8 && redo) {
-      // plain products, token by token, for the rows that see it
-      for (int tt = 0; tt < kTile; ++tt) {
-        const uint8_t* const row = cur + a.Hkv * head_bytes + tt * (D * ES);
+      for (int t = 0; t < 4; ++t) {
+        const int row = token_at(2 * c + (t & 1)) + 8 * (t >> 1);
+        if constexpr (VW == 2) {
+          const uint2 y = lds8(vbuf + chunk_at<RB>(row, g >> 1) + (g & 1) * 8);
+          vr[t][0] = y.x;
+          vr[t][1] = y.y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < VW / 4; ++j) {
+            const uint4 y = lds16(vbuf + chunk_at<RB>(row, g + 8 * j));
+            vr[t][4 * j] = y.x;
+            vr[t][4 * j + 1] = y.y;
+            vr[t][4 * j + 2] = y.z;
+            vr[t][4 * j + 3] = y.w;
+          }
+        }
+      }
+      bool redo = false;
+      if (!full_sub[sub]) {
+        // values that no row sees: zero times anything must be zero
+        bool odd = false;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int tt = t0[sub] + token_at(2 * c + (t & 1)) + 8 * (t >> 1);
+          const bool any = tt <= p_last && (a.window == 0 || tt > s.p0 - a.window || tt < a.sinks);
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            if (!any) vr[t][w] = 0;
+            if (!FP8) odd |= (vr[t][w] & 0x7F80u) == 0x7F80u || (vr[t][w] & 0x7F800000u) == 0x7F800000u;
+          }
+        }
+        // a value that some rows see and others do not must not reach the others as 0 * inf
+        if (!FP8 && s.n > 1) redo = __any_sync(0xffffffffu, odd);
+      }
+      if constexpr (FP8) {
+        // o is in units of vref, which follows the tiles' V scales: P times their ratio is what
+        // meets the codes.  A ratio above 64 raises vref; one below 1/64 would cost P its small
+        // values (f16 has 2^-24), so such a tile's product is made by itself and scaled in fp32.
+        if (fabsf(vs[sub]) > 64.0f * vref) {
+          const float next = fmaxf(fabsf(vs[sub]), 1.17549435e-38f), corr = vref / next;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][mt][e] *= corr;
+          vref = next;
+          vinv = 1.0f / next;
+        }
+        const float ratio = vs[sub] * vinv;
+        const bool small = fabsf(ratio) < 0.015625f;
+        const float pm = small ? 1.0f : ratio;
+        uint32_t ph[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ph[nt][e] = transpose8(pack_f16(x[sub][nt][2 * e] * pm, x[sub][nt][2 * e + 1] * pm));
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t l01 = __byte_perm(vr[0][w], vr[1][w], 0x5140), h01 = __byte_perm(vr[0][w], vr[1][w], 0x7362);
+          const uint32_t l23 = __byte_perm(vr[2][w], vr[3][w], 0x5140), h23 = __byte_perm(vr[2][w], vr[3][w], 0x7362);
+          uint32_t f[8];
+          dec4(l01, f[0], f[1]);
+          dec4(l23, f[2], f[3]);
+          dec4(h01, f[4], f[5]);
+          dec4(h23, f[6], f[7]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (!small) {
+                mma<true>(o[nt][2 * w + k], f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], ph[nt][0], ph[nt][1]);
+              } else {
+                float y[4];
+                mma<true, false>(y, f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], ph[nt][0], ph[nt][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][2 * w + k][e] = fmaf(y[e], ratio, o[nt][2 * w + k][e]);
+              }
+            }
+        }
+      } else if (redo) {
+        // plain products, token by token, for the rows that see it
+        for (int k = 0; k < kTile; ++k) {
+          const int tt = token_at(k);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float pa = __shfl_sync(0xffffffffu, x[sub][nt][e], (k & 7) * 4 + c);
+              const float pb = __shfl_sync(0xffffffffu, x[sub][nt][e + 2], (k & 7) * 4 + c);
+              const float pt = k < 8 ? pa : pb;
+              const int p = s.p0 + min((nt * 8 + 2 * c + e) / a.G, s.n - 1), t = t0[sub] + tt;
+              if (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks)) {
+#pragma unroll
+                for (int j = 0; j < VW / 4; ++j) {
+                  const uint4 v = lds16(vbuf + chunk_at<RB>(tt, g + 8 * j));
+                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int mt = 0; mt < 4; ++mt) {
+                    o[nt][4 * j + mt][e] += pt * lo_f(w[mt]);
+                    o[nt][4 * j + mt][e + 2] += pt * hi_f(w[mt]);
+                  }
+                }
+              }
+            }
+        }
+      } else {
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float pa = __shfl_sync(0xffffffffu, x[nt][e], (tt & 7) * 4 + c);
-            const float pb = __shfl_sync(0xffffffffu, x[nt][e + 2], (tt & 7) * 4 + c);
-            const float pt = tt < 8 ? pa : pb;
-            const int p = s.p0 + min((nt * 8 + 2 * c + e) / a.G, s.n - 1), t = t0 + tt;
-            if (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks)) {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(row + (g + 8 * (mt >> 2)) * 16 + (mt & 3) * 4);
-                o[nt][mt][e] += pt * lo_f(w);
-                o[nt][mt][e + 2] += pt * hi_f(w);
-              }
-            }
+            const uint32_t hi = pack_bf16(x[sub][nt][2 * e], x[sub][nt][2 * e + 1]);
+            ph[nt][e] = transpose8(hi);
+            pl[nt][e] = transpose8(pack_bf16(x[sub][nt][2 * e] - lo_f(hi), x[sub][nt][2 * e + 1] - hi_f(hi)));
           }
-      }
-    } else if constexpr (FP8) {
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t l01 = __byte_perm(vr[0][w], vr[1][w], 0x5140), h01 = __byte_perm(vr[0][w], vr[1][w], 0x7362);
-        const uint32_t l23 = __byte_perm(vr[2][w], vr[3][w], 0x5140), h23 = __byte_perm(vr[2][w], vr[3][w], 0x7362);
-        uint32_t f[8];
-        dec4(l01, f[0], f[1]);
-        dec4(l23, f[2], f[3]);
-        dec4(h01, f[4], f[5]);
-        dec4(h23, f[6], f[7]);
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t a0 = __byte_perm(vr[0][w], vr[1][w], 0x5410), a1 = __byte_perm(vr[0][w], vr[1][w], 0x7632);
+          const uint32_t a2 = __byte_perm(vr[2][w], vr[3][w], 0x5410), a3 = __byte_perm(vr[2][w], vr[3][w], 0x7632);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma<true>(y, f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], ph[nt][0], ph[nt][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][2 * w + k][e] = fmaf(y[e], vs_scale, o[nt][2 * w + k][e]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<false>(o[nt][w], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+            mma<false>(o[nt][w], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
           }
-      }
-    } else {
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t a0 = __byte_perm(vr[0][w], vr[1][w], 0x5410), a1 = __byte_perm(vr[0][w], vr[1][w], 0x7632);
-        const uint32_t a2 = __byte_perm(vr[2][w], vr[3][w], 0x5410), a3 = __byte_perm(vr[2][w], vr[3][w], 0x7632);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma<false>(o[nt][w], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-          mma<false>(o[nt][w], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
         }
       }
     }
-    if (more) load_v(next);
-    cur = next;
+    __syncwarp();  // every lane has read the stage
+    if (i + STAGES < todo) issue(i + STAGES, st);
   }
+  if (!ok) {
+    // copies still in flight after a failed wait land (bounded) before the ring is used again
+    for (int k = i; k < min(todo, i + STAGES); ++k) {
+      mbar_wait_bounded(&full[warp][k & (STAGES - 1)], phase, kWaitNs);
+      if ((k & (STAGES - 1)) == STAGES - 1) phase ^= 1;
+    }
+    if (lane == 0) atomicCAS(a.err, 0, ZP_ERR_TIMEOUT);
+  }
+  if (__any_sync(0xffffffffu, bad_id) && lane == 0) {
+    atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
+    sm_bad = 1;
+  }
+  __syncthreads();  // the ring is free
+  float* const sm_acc = reinterpret_cast<float*>(ring);  // [warp][row][dim]
 
   // the warps' sums, then the CTA's; lane (g, c) holds columns 2c, 2c+1 of its dims
 #pragma unroll
@@ -469,147 +650,176 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
         sm_m[warp][row] = m[nt][e];
         sm_l[warp][row] = sum;
       }
+      const float unit = FP8 ? vref : 1.0f;
+      float4* const dst = reinterpret_cast<float4*>(sm_acc) + (warp * ROWS + row) * (D / 4);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        // FP8: dims (D/8) g + 2 mt, +1;  bf16: dims 8 (g + 8 (mt / 4)) + 2 (mt % 4), +1
+      for (int mt = 0; mt < MT; mt += 2) {
+        // FP8: dims (D/8) g + 2 mt .. + 3;  bf16: dims 8 (g + 8 (mt / 4)) + 2 (mt % 4) .. + 3
         const int dim = FP8 ? (D / 8) * g + 2 * mt : 8 * (g + 8 * (mt >> 2)) + 2 * (mt & 3);
-        *reinterpret_cast<float2*>(&sm_acc[warp][row][dim]) = make_float2(o[nt][mt][e], o[nt][mt][e + 2]);
+        dst[acc_at<FP8>(row, dim / 4)] = make_float4(o[nt][mt][e] * unit, o[nt][mt][e + 2] * unit, o[nt][mt + 1][e] * unit,
+                                                     o[nt][mt + 1][e + 2] * unit);
       }
     }
   __syncthreads();
-  const int rows = a.G * s.n;
-  const int64_t unit = static_cast<int64_t>(r) * a.Hkv + h;
-  float* const part = a.part + unit * a.max_splits * ROWS * (D + 2);  // [split][row][D sums, max, sum]
-  for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
+  // the CTA's sums (in the first warp's place), then the cluster's: CTA k of the cluster joins every
+  // CLth group of 128 vectors, in the order of the CTAs
+  const int rows = a.G * s.n, vecs = rows * (D / 4);
+  const bool cta_bad = sm_bad != 0;
+  for (int idx = tid; idx < vecs; idx += kThreads) {
     const int row = idx / (D / 4), dim = (idx % (D / 4)) * 4;
     float M = -INFINITY, Ls = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][row]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = sm_m[w][row];
-      // a warp without a maximum has sums of 0, or NaN if every logit was
-      const float cw = mw == -INFINITY ? 1.0f : ex2(mw - M);
-      const float4 y = *reinterpret_cast<const float4*>(&sm_acc[w][row][dim]);
-      Ls += sm_l[w][row] * cw;
-      v[0] += y.x * cw;
-      v[1] += y.y * cw;
-      v[2] += y.z * cw;
-      v[3] += y.w * cw;
+    for (int w = 0; w < kWarps; ++w)
+      join(v, Ls, reinterpret_cast<const float4*>(sm_acc)[(w * ROWS + row) * (D / 4) + acc_at<FP8>(row, dim / 4)], sm_l[w][row],
+           sm_m[w][row], M);
+    reinterpret_cast<float4*>(sm_acc)[row * (D / 4) + acc_at<FP8>(row, dim / 4)] = make_float4(v[0], v[1], v[2], v[3]);
+    if (dim == 0) {
+      cta_m[row] = cta_bad ? NAN : M;  // a maximum is never NaN: marks a bad block id
+      cta_l[row] = Ls;
     }
-    if (ns == 1) {
-      if (cta_bad) continue;
-      const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= inv;
-      store_row4(a, s, h, row, dim, v);
+  }
+  const uint32_t cl = cluster_nctarank(), rank = cluster_ctarank();
+  const int parts = a.splits / static_cast<int>(cl);
+  if (cl > 1) cluster_sync();
+  else __syncthreads();
+  const int64_t unit = static_cast<int64_t>(r) * a.Hkv + h;
+  for (int idx = static_cast<int>(rank) * kThreads + tid; idx < vecs; idx += static_cast<int>(cl) * kThreads) {
+    const int row = idx / (D / 4), dim = (idx % (D / 4)) * 4;
+    float M = -INFINITY, Ls = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    bool skip = false;
+    for (uint32_t k = 0; k < cl; ++k) {
+      const float mk = ld_cluster_f1(mapa(smem_u32(&cta_m[row]), k));
+      skip |= isnan(mk);
+      M = fmaxf(M, mk);
+    }
+    for (uint32_t k = 0; k < cl; ++k)
+      join(v, Ls, ld_cluster_f4(mapa(smem_u32(&sm_acc[row * D + acc_at<FP8>(row, dim / 4) * 4]), k)), ld_cluster_f1(mapa(smem_u32(&cta_l[row]), k)),
+           ld_cluster_f1(mapa(smem_u32(&cta_m[row]), k)), M);
+    if (parts == 1) {
+      if (!skip) store_row4(a, s, h, row, dim, v, Ls);
     } else {
-      float* const p = part + (static_cast<int64_t>(split) * ROWS + row) * (D + 2);
-      *reinterpret_cast<float2*>(p + dim) = make_float2(v[0], v[1]);
-      *reinterpret_cast<float2*>(p + dim + 2) = make_float2(v[2], v[3]);
+      float* const p = a.part + ((unit * parts + split / static_cast<int>(cl)) * ROWS + row) * (D + 4);
+      *reinterpret_cast<float4*>(p + dim) = make_float4(v[0], v[1], v[2], v[3]);
       if (dim == 0) {
-        p[D] = cta_bad ? NAN : M;  // a maximum is never NaN: marks a split with a bad block id
+        p[D] = skip ? NAN : M;
         p[D + 1] = Ls;
       }
     }
   }
-  if (ns == 1) return;
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t before = atomicAdd(&a.done[unit], 1u);
-    sm_last = before == static_cast<uint32_t>(ns - 1);
-    if (sm_last) a.done[unit] = 0;  // as the next call expects it
+  if (cl > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+// Joins the parts of a row: one warp a row, in the order of the parts.
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttnArgs a, int parts, int ROWS) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's writes are visible
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int row = static_cast<int>(w % ROWS), h = static_cast<int>(w / ROWS % a.Hkv);
+  const int64_t r = w / ROWS / a.Hkv;
+  if (r >= a.B) return;
+  Span s;
+  bool bad;
+  if (!span_of(a, static_cast<int>(r), s, bad) || row >= a.G * s.n) return;
+  const float* const p = a.part + ((r * a.Hkv + h) * parts * ROWS + row) * (D + 4);
+  const int64_t step = static_cast<int64_t>(ROWS) * (D + 4);
+  float M = -INFINITY;
+  bool skip = false;
+  for (int k = lane; k < parts; k += 32) {
+    const float mk = p[k * step + D];
+    skip |= isnan(mk);
+    M = fmaxf(M, mk);
   }
-  __syncthreads();
-  if (!sm_last) return;
-  __threadfence();
-  for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
-    const int row = idx / (D / 4), dim = (idx % (D / 4)) * 4;
-    const float* const p = part + static_cast<int64_t>(row) * (D + 2);
-    const int64_t step = static_cast<int64_t>(ROWS) * (D + 2);
-    float M = -INFINITY, Ls = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool skip = false;
-    for (int k = 0; k < ns; ++k) {
-      const float mk = __ldcg(p + k * step + D);
-      skip |= isnan(mk);
-      M = fmaxf(M, mk);
-    }
-    if (skip) continue;
-    for (int k = 0; k < ns; ++k) {
-      const float mk = __ldcg(p + k * step + D);
-      const float ck = mk == -INFINITY ? 1.0f : ex2(mk - M);
-      const float2 y0 = __ldcg(reinterpret_cast<const float2*>(p + k * step + dim));
-      const float2 y1 = __ldcg(reinterpret_cast<const float2*>(p + k * step + dim + 2));
-      Ls += __ldcg(p + k * step + D + 1) * ck;
-      v[0] += y0.x * ck;
-      v[1] += y0.y * ck;
-      v[2] += y1.x * ck;
-      v[3] += y1.y * ck;
-    }
-    const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+  if (__any_sync(0xffffffffu, skip)) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= inv;
-    store_row4(a, s, h, row, dim, v);
-  }
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  if (lane * 4 >= D) return;
+  float Ls = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k)
+    join(v, Ls, *reinterpret_cast<const float4*>(p + k * step + lane * 4), p[k * step + D + 1], p[k * step + D], M);
+  store_row4(a, s, h, row, lane * 4, v, Ls);
 }
 
 template <bool FP8, int D, int NT>
-cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
-  split_kernel<FP8, D, NT><<<dim3(a.max_splits, a.Hkv, a.B), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch(const CUtensorMap& tm, const AttnArgs& a, const SplitPlan& plan, cudaStream_t st) {
+  constexpr int smem = Shape<FP8, D, NT>::SMEM;
+  static PerDeviceInit attrs;
+  cudaError_t e = attrs.run(
+      [] { return cudaFuncSetAttribute(split_kernel<FP8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.gridDim = dim3(plan.splits, a.Hkv, a.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = plan.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  e = cudaLaunchKernelEx(&cfg, split_kernel<FP8, D, NT>, tm, a);
+  if (e != cudaSuccess || plan.splits == plan.cluster) return e;
+  // launched while the split kernel still runs; it waits for it on the device
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.B) * a.Hkv * plan.rows + kWarps - 1) / kWarps));
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, plan.splits / plan.cluster, plan.rows);
 }
 
 template <bool FP8>
-cudaError_t dispatch(const AttnArgs& a, int d, int rows, cudaStream_t st) {
-  if (d == 128) return rows == 8 ? launch<FP8, 128, 1>(a, st) : launch<FP8, 128, 2>(a, st);
-  return rows == 8 ? launch<FP8, 64, 1>(a, st) : launch<FP8, 64, 2>(a, st);
+cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const SplitPlan& plan, cudaStream_t st) {
+  if (d == 128) return plan.rows == 8 ? launch<FP8, 128, 1>(tm, a, plan, st) : launch<FP8, 128, 2>(tm, a, plan, st);
+  return plan.rows == 8 ? launch<FP8, 64, 1>(tm, a, plan, st) : launch<FP8, 64, 2>(tm, a, plan, st);
 }
 
 }  // namespace
 
-// CTAs that a launch aims at; a split is at least two tiles per warp and at most what lanes hold.
-constexpr int64_t kTargetCtas = 152 * 6;
-constexpr int kMinTps = 2 * kWarps;
-
-SplitPlan split_plan(const zp_params* p, int B, int max_q, int64_t max_tokens, int window, int sinks) {
+// How many CTAs share a (request, kv head): what one wave of CTAs allows, each with two tiles per
+// warp at least.  A wave counts 7/8 of the CTAs that fit the SMs, since clusters of 8 do not fill
+// every GPC: a 131072-token request of 4 kv heads takes 35 us with 16 clusters a head (512 CTAs) and
+// 47 us with 19 (608).  Batches that fill a wave by themselves are not split: every further CTA
+// costs about 5 us of an SM's slot in latencies (224 requests of 1 to 2048 tokens, 8 kv heads: 90 us
+// unsplit, 106 us with 2, 139 us with 4), while 4 requests of 100 to 500 tokens take 6.9 us with 4
+// splits and 10.3 us unsplit.
+SplitPlan split_plan(const zp_params* p, bool fp8, int B, int max_q, int max_blocks, int window, int sinks) {
+  constexpr int64_t kSms = 152;
   SplitPlan s{};
-  const int G = p->num_q_heads / p->num_kv_heads;
-  s.rows = G * max_q <= 8 ? 8 : 16;
-  int64_t tiles = (max_tokens + kTile - 1) / kTile;
+  s.rows = p->num_q_heads / p->num_kv_heads * max_q <= 8 ? 8 : 16;
+  int64_t tiles = (static_cast<int64_t>(max_blocks) * p->block_size + kTile - 1) / kTile;
   if (window > 0) {
     const int64_t seen = (static_cast<int64_t>(window) + max_q - 1 + kTile - 1) / kTile + 1 +
                          (static_cast<int64_t>(sinks) + kTile - 1) / kTile;
     tiles = std::min(tiles, seen);
   }
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
-  const int64_t want = (kTargetCtas + units - 1) / units;
-  const int64_t even = ((tiles + want - 1) / want + kWarps - 1) / kWarps * kWarps;
-  s.tps = static_cast<int>(std::min<int64_t>(std::max<int64_t>(even, kMinTps), kMaxTps));
-  s.splits = static_cast<int>(std::max<int64_t>(1, (tiles + s.tps - 1) / s.tps));
+  const int64_t wave = kSms * (s.rows == 16 ? 2 : fp8 ? 4 : 3) * 7 / 8;
+  const int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
+  s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
+  s.splits = n >= 8 ? static_cast<int>(n / 8 * 8) : s.cluster;
+  const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
+  s.bytes = 256;
+  if (parts > 1) s.bytes += static_cast<size_t>(units) * parts * s.rows * (p->head_dim + 4) * sizeof(float);
   return s;
 }
 
-size_t split_bytes(const zp_params* p, int B, int max_q, int64_t max_tokens) {
-  const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
-  const int64_t tiles = (max_tokens + kTile - 1) / kTile;
-  // the most splits that split_plan gives to `tiles` or fewer
-  const int64_t splits = std::min((tiles + kMinTps - 1) / kMinTps,
-                                  std::max((kTargetCtas + units - 1) / units, (tiles + kMaxTps - 1) / kMaxTps));
-  const int rows = p->num_q_heads / p->num_kv_heads * max_q <= 8 ? 8 : 16;
-  size_t bytes = 256 + (static_cast<size_t>(units) * 4 + 255) / 256 * 256;
-  if (splits > 1) bytes += static_cast<size_t>(units) * splits * rows * (p->head_dim + 2) * sizeof(float);
-  return bytes;
-}
-
-zp_status split_launch(AttnArgs a, bool fp8, int head_dim, const SplitPlan& plan, void* workspace, cudaStream_t st) {
+zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  a.tps = plan.tps;
-  a.max_splits = plan.splits;
+  a.splits = plan.splits;
   a.err = reinterpret_cast<int32_t*>(ws);
-  a.done = reinterpret_cast<uint32_t*>(ws + 256);
-  a.part = reinterpret_cast<float*>(ws + 256 + (static_cast<size_t>(a.B) * a.Hkv * 4 + 255) / 256 * 256);
-  const cudaError_t e = fp8 ? dispatch<true>(a, head_dim, plan.rows, st) : dispatch<false>(a, head_dim, plan.rows, st);
+  a.part = reinterpret_cast<float*>(ws + 256);
+  const int d = p->head_dim;
+  const uint64_t rows = static_cast<uint64_t>(2) * a.Hkv * a.b, blocks = static_cast<uint64_t>(p->num_layers) * a.num_blocks;
+  CUtensorMap tm;
+  // box: 16 rows of one (block, K or V, head), all of an 8-bit row or 64 columns of a bf16 one
+  const bool ok = fp8 ? encode_tmap_3d_u8(&tm, a.pool, d, rows, blocks, d, rows * d, d, kTile, 1, d)
+                      : encode_tmap_3d_bf16(&tm, a.pool, d, rows, blocks, static_cast<uint64_t>(d) * 2, rows * d * 2, 64, kTile, 1);
+  if (!ok) return ZP_ERR_CUDA;
+  const cudaError_t e = fp8 ? dispatch<true>(tm, a, d, plan, st) : dispatch<false>(tm, a, d, plan, st);
   return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 

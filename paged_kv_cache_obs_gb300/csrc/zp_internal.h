@@ -18,6 +18,10 @@ bool encode_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64
                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
                          uint32_t box2);
 
+// The same for bytes; `swizzle` is 64 or 128 (bytes), the inner box extent or more.
+bool encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1_bytes,
+                       uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2, int swizzle);
+
 // Number of SMs of the current device (cached per device).
 int num_sms();
 

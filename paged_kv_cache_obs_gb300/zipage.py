@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -330,22 +331,58 @@ def zp_paged_decode_attn_static(pool, layer: int, q, block_tables, seq_lens, out
     _check("zp_paged_decode_attn_static", st)
 
 
-# ------------------------------------------------------------------ rotary positions ---------
+# ------------------------------------------------------------------ per-step operators -------
+#
+# These run once per layer and step, so their marshalling is kept short: structs are packed into
+# bytes (which a void pointer argument takes), and the current stream is read as a number.
+
+def _fast(name, args):
+    f = lib[name]  # a function object of its own: the one in `lib` keeps its typed pointers
+    f.restype = _I32
+    f.argtypes = args
+    return f
+
+
+_rope_apply = _fast("zp_rope_apply", [_P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P])
+_kv8_append = _fast("zp_kv8_append", [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P])
+_kv8_decode_attn = _fast("zp_kv8_decode_attn", [_P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _SZ, _P])
+_paged_window_attn = _fast("zp_paged_window_attn", [_P, _I32, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
+                                                    _P, _SZ, _P])
+_pack_rows = struct.Struct("Nqq").pack     # zp_rows
+_pack_kv8 = struct.Struct("NNq").pack      # zp_kv8_pool
+_pack_pool = struct.Struct("Nq").pack      # zp_kv_pool
+_addr = ctypes.addressof
+
 
 def _rows(t):
-    """bf16 rows [tokens, heads, head_dim] with any token and head strides."""
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    """bf16 rows [tokens, heads, head_dim] with any token and head strides, as a zp_rows."""
+    return zp_rows.from_buffer_copy(_row_bytes(t))
+
+
+def _row_bytes(t):
+    ts, hs, es = t.stride()
+    if es != 1:
         raise ValueError("the last dimension of rows must be contiguous")
-    return zp_rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return _pack_rows(t.data_ptr(), ts, hs)
+
+
+def _stream_of(t, stream):
+    """The stream to launch on: the given one, or the current one of the tensor's device, which has to
+    be the current device (the library launches there)."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+# the current stream's handle without building a Stream object
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _params(params):
     """A dict, or what make_params made of it (which a caller may keep)."""
     return params if isinstance(params, zp_params) else make_params(params)
-
-
-def _nbytes(workspace):
-    return workspace.numel() * workspace.element_size()
 
 
 def zp_rope_init(head_dim: int, rotary_dim: int, theta: float, interleaved: bool = False,
@@ -360,28 +397,34 @@ def zp_rope_init(head_dim: int, rotary_dim: int, theta: float, interleaved: bool
 
 def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream=None):
     """Rotates q [T, H_q, d] and k [T, H_kv, d] (either may be None), in place or into q_out, k_out."""
-    rq, rk = (None if t is None else _rows(t) for t in (q, k))
-    oq = None if q is None else (rq if q_out is None else _rows(q_out))
-    ok = None if k is None else (rk if k_out is None else _rows(k_out))
-    st = lib.zp_rope_apply(ctypes.byref(rope), rq, oq, 0 if q is None else q.shape[1], rk, ok,
-                           0 if k is None else k.shape[1], _ptr(positions), positions.shape[0], _stream(stream))
-    _check("zp_rope_apply", st)
+    rq = oq = rk = ok = None
+    hq = hk = 0
+    if q is not None:
+        rq, hq = _row_bytes(q), q.size(1)
+        oq = rq if q_out is None else _row_bytes(q_out)
+    if k is not None:
+        rk, hk = _row_bytes(k), k.size(1)
+        ok = rk if k_out is None else _row_bytes(k_out)
+    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, positions.data_ptr(), positions.size(0),
+                     _stream_of(positions, stream))
+    if st:
+        _check("zp_rope_apply", st)
 
 
-# ------------------------------------------------------------------ 8-bit cache --------------
-
-def _kv8(codes, scales):
-    return zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1])
+def _kv8_bytes(codes, scales):
+    return _pack_kv8(codes.data_ptr(), scales.data_ptr(), codes.size(1))
 
 
 def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_tables, params, workspace, stream=None):
     """Quantises the new keys and values k, v [T, H_kv, d] of one layer into the 8-bit pool: codes
     (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
     token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
-    st = lib.zp_kv8_append(_kv8(codes, scales), layer, _rows(k), _rows(v), k.shape[0], _ptr(token_start), _ptr(cached),
-                           cached.shape[0], _ptr(block_tables), block_tables.shape[1], _params(params),
-                           _ptr(workspace), _nbytes(workspace), _stream(stream))
-    _check("zp_kv8_append", st)
+    p = _params(params)
+    st = _kv8_append(_kv8_bytes(codes, scales), layer, _row_bytes(k), _row_bytes(v), k.size(0), token_start.data_ptr(),
+                     cached.data_ptr(), cached.size(0), block_tables.data_ptr(), block_tables.size(1), _addr(p),
+                     workspace.data_ptr(), workspace.nbytes, _stream_of(codes, stream))
+    if st:
+        _check("zp_kv8_append", st)
 
 
 def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace, fill=None, layers: tuple | None = None,
@@ -390,8 +433,9 @@ def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace,
     int32 [n] of tokens per block; layers: optional (layer_begin, layer_count)."""
     lb, lc = layers if layers is not None else (0, 0)
     st = lib.zp_kv8_pack_blocks(zp_kv_pool(pool.data_ptr(), pool.shape[1]), _ptr(src_ids), _ptr(fill),
-                                _kv8(codes, scales), _ptr(dst_ids), src_ids.shape[0], lb, lc, _params(params),
-                                _ptr(workspace), _nbytes(workspace), _stream(stream))
+                                zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1]), _ptr(dst_ids),
+                                src_ids.shape[0], lb, lc, _params(params), _ptr(workspace), workspace.nbytes,
+                                _stream_of(codes, stream))
     _check("zp_kv8_pack_blocks", st)
 
 
@@ -399,9 +443,9 @@ def zp_kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, params, workspac
                          stream=None):
     """Blocks src_ids of the 8-bit pool into blocks dst_ids of the bf16 pool."""
     lb, lc = layers if layers is not None else (0, 0)
-    st = lib.zp_kv8_unpack_blocks(_kv8(codes, scales), _ptr(src_ids), zp_kv_pool(pool.data_ptr(), pool.shape[1]),
-                                  _ptr(dst_ids), src_ids.shape[0], lb, lc, _params(params), _ptr(workspace),
-                                  _nbytes(workspace), _stream(stream))
+    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1]), _ptr(src_ids),
+                                  zp_kv_pool(pool.data_ptr(), pool.shape[1]), _ptr(dst_ids), src_ids.shape[0], lb, lc,
+                                  _params(params), _ptr(workspace), workspace.nbytes, _stream_of(codes, stream))
     _check("zp_kv8_unpack_blocks", st)
 
 
@@ -413,13 +457,13 @@ def zp_kv8_decode_attn(codes, scales, layer: int, q, block_tables, seq_lens, out
                        sinks: int = 0, stream=None):
     """Decode attention over the 8-bit pool: q, out bf16 [B, H_q, d]; a request sees its last
     `window` tokens and the first `sinks` (window 0: all)."""
-    st = lib.zp_kv8_decode_attn(_kv8(codes, scales), layer, _rows(q), _ptr(block_tables), _ptr(seq_lens), q.shape[0],
-                                block_tables.shape[1], window, sinks, _rows(out), _params(params), _ptr(workspace),
-                                _nbytes(workspace), _stream(stream))
-    _check("zp_kv8_decode_attn", st)
+    p = _params(params)
+    st = _kv8_decode_attn(_kv8_bytes(codes, scales), layer, _row_bytes(q), block_tables.data_ptr(), seq_lens.data_ptr(),
+                          q.size(0), block_tables.size(1), window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(),
+                          workspace.nbytes, _stream_of(codes, stream))
+    if st:
+        _check("zp_kv8_decode_attn", st)
 
-
-# ------------------------------------------------------------------ windowed attention -------
 
 def zp_paged_window_workspace_size(params, T: int, B: int, max_q: int, max_blocks: int, window: int, sinks: int) -> int:
     return lib.zp_paged_window_workspace_size(_params(params), T, B, max_q, max_blocks, window, sinks)
@@ -430,11 +474,13 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
     """Attention of the new tokens q [T, H_q, d] (request r: rows q_start[r] .. q_start[r + 1] - 1, its
     last tokens in the cache) over the bf16 pool, with a window and `sinks` first tokens that stay
     visible.  max_q: the most new tokens of a request."""
-    st = lib.zp_paged_window_attn(zp_kv_pool(pool.data_ptr(), pool.shape[1]), layer, _rows(q), _ptr(q_start), q.shape[0],
-                                  max_q, _ptr(block_tables), _ptr(seq_lens), seq_lens.shape[0], block_tables.shape[1],
-                                  window, sinks, _rows(out), _params(params), _ptr(workspace), _nbytes(workspace),
-                                  _stream(stream))
-    _check("zp_paged_window_attn", st)
+    p = _params(params)
+    st = _paged_window_attn(_pack_pool(pool.data_ptr(), pool.size(1)), layer, _row_bytes(q), q_start.data_ptr(), q.size(0),
+                            max_q, block_tables.data_ptr(), seq_lens.data_ptr(), seq_lens.size(0), block_tables.size(1),
+                            window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(), workspace.nbytes,
+                            _stream_of(pool, stream))
+    if st:
+        _check("zp_paged_window_attn", st)
 
 
 def zp_read_error(workspace, stream=None) -> int:

@@ -53,7 +53,7 @@ def test_kv8_decode_refuses(zp):
     rows = zp._rows(x)
 
     def call(pool=zp.zp_kv8_pool(base, base, 4), layer=0, q=rows, tables=base, seq=base, B=2, mb=2, window=0, sinks=0, out=rows,
-             params=zp.make_params(p), ws=base, nb=512):
+             params=zp.make_params(p), ws=base, nb=1 << 40):
         return zp.lib.zp_kv8_decode_attn(pool, layer, q, tables, seq, B, mb, window, sinks, out, params, ws, nb, None)
 
     _refusals(zp, call, base, x, p)
@@ -62,7 +62,7 @@ def test_kv8_decode_refuses(zp):
                  zp.zp_kv8_pool(base + 8, base, 4), zp.zp_kv8_pool(base, base + 1, 4)):
         assert call(pool=pool) == bad
     assert call(B=0, q=None, out=None, tables=None, seq=None) == zp.ZP_OK
-    assert call(nb=zp.zp_kv8_decode_workspace_size(p, 2, 64) - 1, mb=64) == bad
+    assert call(mb=4096, B=1, nb=zp.zp_kv8_decode_workspace_size(p, 1, 4096) - 1) == bad
 
 
 def test_window_refuses(zp):
@@ -70,7 +70,7 @@ def test_window_refuses(zp):
     rows = zp._rows(x)
 
     def call(pool=zp.zp_kv_pool(base, 4), layer=0, q=rows, start=base, T=2, max_q=1, tables=base, seq=base, B=2, mb=2, window=4,
-             sinks=1, out=rows, params=zp.make_params(p), ws=base, nb=512):
+             sinks=1, out=rows, params=zp.make_params(p), ws=base, nb=1 << 40):
         return zp.lib.zp_paged_window_attn(pool, layer, q, start, T, max_q, tables, seq, B, mb, window, sinks, out, params, ws, nb, None)
 
     _refusals(zp, call, base, x, p)
@@ -80,16 +80,18 @@ def test_window_refuses(zp):
         assert call(**kw) == bad, kw
     assert call(pool=zp.zp_kv_pool(base, 1 << 31)) == zp.ZP_ERR_UNSUPPORTED
     assert call(B=0, q=None, out=None, tables=None, seq=None, start=None) == zp.ZP_OK
-    assert call(T=0) == zp.ZP_OK
+    assert call(T=0) == zp.ZP_OK and call(T=0, q=zp.zp_rows(None, 0, 0), out=zp.zp_rows(None, 0, 0)) == zp.ZP_OK
 
 
 def test_workspace_sizes(zp):
     p = _params(32, 8, 128, 16)
-    # one split: the header and the counters alone; more: partials, never fewer for longer caches
-    assert zp.zp_kv8_decode_workspace_size(p, 1, 1) == 512
-    sizes = [zp.zp_kv8_decode_workspace_size(p, 3, mb) for mb in range(1, 3000, 7)]
-    assert sizes == sorted(sizes)
-    assert zp.zp_kv8_decode_workspace_size(p, 256, 8192) < 1 << 31
+    # a batch that is not split, or whose splits are one cluster, needs the header alone; few long
+    # requests need parts, never fewer for longer caches, and a window never more than none
+    assert zp.zp_kv8_decode_workspace_size(p, 256, 8192) == 256 and zp.zp_kv8_decode_workspace_size(p, 1, 1) == 256
+    sizes = [zp.zp_kv8_decode_workspace_size(p, 1, mb) for mb in range(1, 3000, 7)]
+    assert sizes == sorted(sizes) and 256 < sizes[-1] < 16 << 20
+    for w in (1, 100, 5000, 10 ** 6):
+        assert zp.zp_paged_window_workspace_size(p, 2, 1, 2, 4096, w, 9) <= zp.zp_paged_window_workspace_size(p, 2, 1, 2, 4096, 0, 0)
     assert zp.zp_kv8_decode_workspace_size(p, -1, 4) == 0 and zp.zp_paged_window_workspace_size(p, 4, 1, 0, 4, 1, 1) == 0
 
 
