@@ -20,8 +20,8 @@ zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_
   if (p->head_dim != 64 && p->head_dim != 128) return ZP_ERR_UNSUPPORTED;
   if (p->block_size != 16 && p->block_size != 32) return ZP_ERR_UNSUPPORTED;
   if (p->num_q_heads / p->num_kv_heads > 16 || B > 65535 || p->num_kv_heads > 65535) return ZP_ERR_UNSUPPORTED;
-  // positions are 32-bit numbers
-  if (static_cast<int64_t>(max_blocks) * p->block_size > INT_MAX) return ZP_ERR_UNSUPPORTED;
+  // differences of three positions fit 32 bits
+  if (static_cast<int64_t>(max_blocks) * p->block_size > (1 << 30)) return ZP_ERR_UNSUPPORTED;
   if (B == 0) return ZP_OK;
   if (!q || !out || !q->data || !out->data || !aligned(q->data, 2) || !aligned(out->data, 2)) return ZP_ERR_INVALID_ARG;
   if (!tables || !seq_lens) return ZP_ERR_INVALID_ARG;
@@ -45,8 +45,10 @@ AttnArgs args_of(const zp_params* p, int32_t layer, int64_t num_blocks, const zp
   a.Hkv = p->num_kv_heads;
   a.G = p->num_q_heads / p->num_kv_heads;
   a.b = p->block_size;
-  a.window = window;
-  a.sinks = sinks;
+  // a window or first tokens past the longest cache see what all of it would
+  const int most = max_blocks * p->block_size;
+  a.window = window >= most ? 0 : window;
+  a.sinks = sinks < most ? sinks : most;
   a.sl2 = p->scale * 1.4426950408889634f;
   return a;
 }
@@ -90,7 +92,8 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
 extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q,
                                                  int32_t max_blocks, int32_t window, int32_t sinks) {
   if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
-  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows) return 256;
+  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
+    return tile_plan(p, T, B, max_q, max_blocks, window, sinks).bytes;
   return split_plan(p, false, B, max_q, max_blocks, window, sinks).bytes;
 }
 
@@ -112,11 +115,10 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   a.pool = static_cast<const uint8_t*>(pool->base);
   a.q_start = q_start;
   a.T = T;
-  a.max_q = max_q < T ? max_q : T;
+  a.max_q = max_q;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
-    a.max_q = max_q;
     return split_launch(a, p, false, split_plan(p, false, B, max_q, max_blocks, window, sinks), workspace, st);
   }
-  return tile_launch(a, pool, p, workspace, st);
+  return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks), workspace, st);
 }

@@ -18,7 +18,7 @@ struct AttnArgs {
   int32_t* err;
   float* part;             // [B][Hkv][parts][rows][d + 4]: sums, maximum, sum of weights
   int T, B, layer, max_blocks, Hkv, G, b, max_q, window, sinks;
-  int splits;              // CTAs of a (request, kv head)
+  int splits;              // CTAs that share a row's tokens
   float sl2;               // scale * log2(e)
 };
 
@@ -37,7 +37,16 @@ SplitPlan split_plan(const zp_params* p, bool fp8, int B, int max_q, int max_blo
 // Launches the split kernel (and the one that joins its parts).
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st);
 
-// Launches the tiled kernel (rows above kMaxSplitRows); of the workspace it uses the error word.
-zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, void* workspace, cudaStream_t st);
+// How a call of the tiled kernel is cut: items (2 x 128 rows) of a request and kv head, CTAs that
+// share an item's tiles, items in all.
+struct TilePlan {
+  int nx, splits;
+  int64_t items;
+  size_t bytes;
+};
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks);
+
+// Launches the tiled kernel (rows above kMaxSplitRows), and the one that joins the parts.
+zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
 
 }  // namespace zp

@@ -1,28 +1,35 @@
 // zp_attn_tile.cu — attention of many query rows with a sliding window and first tokens that stay
 // visible, over the paged bf16 pool, on the 5th-generation tensor cores; sm_103a.
 //
-// A CTA holds 2 tiles of 128 query rows of one (request, kv head) — 128 / G queries times the G
+// An item is 2 tiles of 128 query rows of one (request, kv head) — 128 / G queries times the G
 // heads of the group, so K and V are read once for the whole group — and walks the 128-token
 // tiles of the cache that any of its rows sees: first the blocks with always-visible first
-// tokens, then the window's.  Blocks between the two are never loaded.
+// tokens, then the window's.  Blocks between the two are never loaded.  A resident CTA per SM takes
+// every 152nd item.  Where a call has fewer items than SMs, the tiles of an item are shared by
+// several CTAs, whose sums a second kernel joins.
 //
 // Roles: a producer warp brings K and V through the block table (one TMA box per block and
-// 64-column half, 128-byte swizzle, two-stage rings); an MMA warp issues S = Q K^T and
-// O += P V with tcgen05; two groups of four warps (thread = row, one group per query tile) turn
-// S into P.  S, P and O stay in TMEM: P (bf16) overwrites S and is the A operand of the second
+// 64-column half, 128-byte swizzle, two-stage rings); a warp brings the next item's queries as soon
+// as the last product that reads them is done; an MMA warp issues S = Q K^T and O += P V with
+// tcgen05; two groups of four warps (thread = row, one group per query tile) turn S into P.  S, P
+// and O stay in TMEM (all 512 columns): P (bf16) overwrites S and is the A operand of the second
 // product, V its B operand with the dims contiguous.  While one tile's group works on its
-// softmax, the tensor core multiplies for the other tile.
+// softmax, the tensor core multiplies for the other tile; the next item's first products start
+// while the last sums are still being written out.
 //
 // The running maximum is kept lazily (raised only when a logit passes it by more than 8 in
 // log2), so O is rescaled in TMEM rarely.  Sums and maxima are fp32; P is rounded to bf16 (off by
-// at most 2^-9 of itself), as the second product's operand type asks.
+// at most 2^-8 of itself), as the second product's operand type asks.
 //
 // A tile in which some row does not see some token ("mixed": the diagonal, the window's edge, the
 // first tokens, the list's end) takes the masked path.  There the softmax groups also look V over in
 // shared memory: tokens that no row sees are zeroed, and if a value that only some rows see is not
-// finite, the CTA's rows are computed again by a plain loop, so that 0 * inf never reaches a row
+// finite, the item's rows are computed again by a plain loop, so that 0 * inf never reaches a row
 // that does not see it.
 #include "zp_attn.h"
+
+#include <algorithm>
+#include <climits>
 
 #include "zp_ptx.cuh"
 
@@ -32,21 +39,24 @@ namespace {
 constexpr int kRows = 128;            // rows of a query tile = TMEM lanes
 constexpr int kKeys = 128;            // tokens of a KV tile
 constexpr int kStages = 2;
-constexpr int kProdWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kThreads = 384;         // two softmax groups, and a group of the other roles
+constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
+constexpr int kFlags = 8;             // items that roles can be apart, and more
 
 template <int D>
 struct __align__(1024) TileSmem {
   uint8_t q[2][D / 64][kRows * 128];         // [tile][64-column half][row][128 B], 128-byte swizzle
   uint8_t k[kStages][D / 64][kKeys * 128];
   uint8_t v[kStages][D / 64][kKeys * 128];
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], v_clean, drain;
+  uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], v_clean, drain;
   uint32_t tmem;
-  int abort, redo;
+  int abort;
+  int bad[kFlags], redo[kFlags];             // the last item (counted from 1) that a block id or a value marked
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -119,15 +129,93 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What a CTA walks.
-struct Walk {
+// Two fp32 values in a register pair, and what Blackwell does with both at once.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair2(float x) { return pair(__float_as_uint(x), __float_as_uint(x)); }
+
+// The lowest n bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// An item: which, and what it walks.
+struct Item {
+  int r, h, split;
   int L, n, q0, p0;        // tokens, queries, first row of q, position of the request's first query
-  int i0, queries;         // first query of the CTA, how many
-  int sink_blocks, win_block, blocks, tiles;
+  int i0, queries;         // first query of the item, how many
+  int p_first, p_last;     // positions of its first and last query
+  int sink_blocks, win_block, blocks;
+  int j0, j1;              // its tiles of the list
+  bool two;                // the second query tile has rows
 };
 
+// What an item needs from memory, loaded one item ahead.
+struct Raw {
+  int L, q0, q1;
+};
+__device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items, int per_request) {
+  Raw raw{0, 0, 0};
+  if (item < items) {
+    const int r = item / per_request;
+    raw.L = a.seq_lens[r];
+    raw.q0 = a.q_start[r];
+    raw.q1 = a.q_start[r + 1];
+  }
+  return raw;
+}
+
+// Items in order of request, kv head, queries from the last (which see the most) to the first,
+// and part of the tiles.  False: nothing to do (`bad`: the request is reported).
+__device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, const Raw& raw, Item& w, bool& bad) {
+  const int qpt = kRows / a.G;  // queries per tile
+  w.split = item % a.splits;
+  item /= a.splits;
+  const int x = item % nx;
+  item /= nx;
+  w.h = item % a.Hkv;
+  w.r = item / a.Hkv;
+  w.L = raw.L;
+  w.q0 = raw.q0;
+  const int64_t n = static_cast<int64_t>(raw.q1) - raw.q0;
+  bad = w.q0 < 0 || n < 0 || n > a.max_q || w.q0 + n > a.T;
+  bad = bad || (n > 0 && (w.L < n || w.L > static_cast<int64_t>(a.max_blocks) * a.b));
+  if (bad) return false;
+  w.n = static_cast<int>(n);
+  w.i0 = (nx - 1 - x) * 2 * qpt;
+  if (w.i0 >= w.n) return false;
+  w.queries = min(2 * qpt, w.n - w.i0);
+  w.p0 = w.L - w.n;
+  w.p_first = w.p0 + w.i0;
+  w.p_last = w.p_first + w.queries - 1;
+  const int bs = a.b == 16 ? 4 : 5;
+  const int first = a.window == 0 ? 0 : max(0, w.p_first - a.window + 1);
+  w.win_block = first >> bs;
+  w.sink_blocks = static_cast<int>(min((static_cast<int64_t>(min(a.sinks, w.L)) + a.b - 1) >> bs, static_cast<int64_t>(w.win_block)));
+  w.blocks = w.sink_blocks + (w.p_last >> bs) + 1 - w.win_block;
+  const int tiles = static_cast<int>((static_cast<int64_t>(w.blocks) * a.b + kKeys - 1) / kKeys);
+  w.j0 = static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits);
+  w.j1 = static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits);
+  w.two = w.queries > qpt;
+  return true;
+}
+
 // Token of column `col` of list tile j.
-__device__ __forceinline__ int token_of(const AttnArgs& a, const Walk& w, int j, int col) {
+__device__ __forceinline__ int token_of(const AttnArgs& a, const Item& w, int j, int col) {
   const int e = j * kKeys + col, sink = w.sink_blocks * a.b;
   return e < sink ? e : w.win_block * a.b + e - sink;
 }
@@ -136,28 +224,61 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int t) {
   return t <= p && (a.window == 0 || t > p - a.window || t < a.sinks);
 }
 
-// Rows of the CTA by plain loops: one warp per row, a lane per token for the logits and a lane per
-// dims for the sums.  For the rare inputs that the tiles cannot take.
+// Some row of the item does not see some token of list tile j.
+__device__ __forceinline__ bool mixed_tile(const AttnArgs& a, const Item& w, int j) {
+  const int t_lo = token_of(a, w, j, 0), t_hi = token_of(a, w, j, kKeys - 1);
+  return !(t_hi - t_lo == kKeys - 1 && (j + 1) * kKeys <= w.blocks * a.b && t_hi <= w.p_first &&
+           (a.window == 0 || t_lo > w.p_last - a.window || t_hi < a.sinks));
+}
+
+// The columns c0 .. c0 + 31 of a run of tokens base + col that position p sees, as bits.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, int p, int base, int c0) {
+  const uint32_t upto = low_bits(p - base - c0 + 1);
+  if (a.window == 0) return upto;
+  // t > p - window, or t < sinks
+  const uint32_t gone = low_bits(p - a.window - base - c0 + 1), kept = low_bits(a.sinks - base - c0);
+  return upto & (~gone | kept);
+}
+
+// Where a row's results go: the output, or its part of a split item.
+struct Sink {
+  uint16_t* out;   // NULL: no such row
+  float* part;     // D sums, maximum, sum of weights
+};
 template <int D>
-__device__ __noinline__ void rows_plainly(const AttnArgs& a, const Walk& w, int r, int h, int warp, int lane) {
+__device__ __forceinline__ Sink sink_of(const AttnArgs& a, const Item& w, int i, int g, bool have) {
+  Sink s{nullptr, nullptr};
+  if (!have) return s;
+  const int64_t t = w.q0 + w.i0 + i, head = w.h * a.G + g;
+  s.out = a.out + t * a.o_ts + head * a.o_hs;
+  if (a.splits > 1) s.part = a.part + ((static_cast<int64_t>(w.split) * a.T + t) * (a.Hkv * a.G) + head) * (D + 4);
+  return s;
+}
+
+// Rows of one query tile by plain loops: one warp per row, a lane per token for the logits and a lane
+// per dims for the sums.  For the rare inputs that the tiles cannot take.
+template <int D>
+__device__ __noinline__ void rows_plainly(const AttnArgs& a, const Item& w, int t, int warp, int lane) {
   constexpr int DL = D / 32;
-  const int64_t tile_bytes = static_cast<int64_t>(a.b) * D;  // values of a (block, K|V, head)
+  const int qpt = kRows / a.G;
+  const int64_t tile_values = static_cast<int64_t>(a.b) * D;  // of a (block, K|V, head)
   const uint16_t* const pool = reinterpret_cast<const uint16_t*>(a.pool);
-  for (int rr = warp; rr < w.queries * a.G; rr += 8) {
-    const int i = w.i0 + rr / a.G, g = rr % a.G, p = w.p0 + i;
-    const uint16_t* const q = a.q + (w.q0 + i) * a.q_ts + (h * a.G + g) * a.q_hs;
+  for (int rr = warp; rr < qpt * a.G; rr += 4) {
+    const int i = t * qpt + rr / a.G, g = rr % a.G, p = w.p_first + i;
+    if (i >= w.queries) break;
+    const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs;
     float m = -INFINITY, l = 0.0f, o[DL];
 #pragma unroll
     for (int e = 0; e < DL; ++e) o[e] = 0.0f;
-    for (int j = 0; j < w.tiles; ++j)
+    for (int j = w.j0; j < w.j1; ++j)
       for (int c0 = 0; c0 < kKeys; c0 += 32) {
-        const int e = j * kKeys + c0 + lane, t = token_of(a, w, j, c0 + lane);
-        const bool on = e < w.blocks * a.b && sees(a, p, t);
+        const int e = j * kKeys + c0 + lane, tok = token_of(a, w, j, c0 + lane);
+        const bool on = e < w.blocks * a.b && sees(a, p, tok);
         float x = -INFINITY;
         const uint16_t* kv = nullptr;
         if (on) {
-          const int64_t phys = a.tables[static_cast<int64_t>(r) * a.max_blocks + t / a.b];
-          kv = pool + (((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 * a.Hkv + h) * tile_bytes) + (t % a.b) * D;
+          const int64_t phys = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + tok / a.b];
+          kv = pool + (((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 * a.Hkv + w.h) * tile_values) + (tok % a.b) * D;
           x = 0.0f;
           for (int dd = 0; dd < D; ++dd) x = fmaf(lo_f(q[dd]), lo_f(kv[dd]), x);
           x *= a.sl2;
@@ -179,63 +300,47 @@ __device__ __noinline__ void rows_plainly(const AttnArgs& a, const Walk& w, int 
           vote &= vote - 1;
           const float ps = __shfl_sync(0xffffffffu, pt, src);
           const uint16_t* const vt = reinterpret_cast<const uint16_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kv), src)) + a.Hkv * tile_bytes;
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kv), src)) + a.Hkv * tile_values;
           l += ps;
 #pragma unroll
           for (int e2 = 0; e2 < DL; ++e2) o[e2] = fmaf(ps, lo_f(vt[lane * DL + e2]), o[e2]);
         }
       }
-    uint16_t* const out = a.out + (w.q0 + i) * a.o_ts + (h * a.G + g) * a.o_hs;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const Sink s = sink_of<D>(a, w, i, g, true);
+    if (s.part) {
 #pragma unroll
-    for (int e = 0; e < DL; e += 2) {
-      const uint32_t y = pack_bf16(o[e] * inv, o[e + 1] * inv);
-      out[lane * DL + e] = static_cast<uint16_t>(y);
-      out[lane * DL + e + 1] = static_cast<uint16_t>(y >> 16);
+      for (int e = 0; e < DL; ++e) s.part[lane * DL + e] = o[e];
+      if (lane == 0) {
+        s.part[D] = m;
+        s.part[D + 1] = l;
+      }
+    } else {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int e = 0; e < DL; e += 2) {
+        const uint32_t y = pack_bf16(o[e] * inv, o[e + 1] * inv);
+        s.out[lane * DL + e] = static_cast<uint16_t>(y);
+        s.out[lane * DL + e + 1] = static_cast<uint16_t>(y >> 16);
+      }
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
+// Q_TMA: the queries' rows are aligned and come by TMA (one box per tile and 64-column half: the
+// group's heads of 128 / G tokens, which is the order of the tile's rows); else by plain loads.
+template <int D, bool Q_TMA>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tq,
+                                                           const __grid_constant__ AttnArgs a, int nx, int items) {
   constexpr int NH = D / 64;
   extern __shared__ uint8_t dyn[];
   TileSmem<D>& s = *reinterpret_cast<TileSmem<D>*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, r = blockIdx.z;
-  const int qpt = kRows / a.G;  // queries per tile
+  const int qpt = kRows / a.G, per_request = nx * a.Hkv * a.splits;
+  const int step = static_cast<int>(gridDim.x);
 
-  Walk w;
-  w.L = a.seq_lens[r];
-  w.q0 = a.q_start[r];
-  const int64_t n64 = static_cast<int64_t>(a.q_start[r + 1]) - w.q0;
-  bool bad = w.q0 < 0 || n64 < 0 || n64 > a.max_q || w.q0 + n64 > a.T;
-  bad = bad || (n64 > 0 && (w.L < n64 || w.L > static_cast<int64_t>(a.max_blocks) * a.b));
-  if (bad) {
-    if (blockIdx.x == 0 && h == 0 && tid == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
-    return;
-  }
-  w.n = static_cast<int>(n64);
-  w.i0 = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) * 2 * qpt;  // the last queries see the most
-  if (w.i0 >= w.n) return;
-  w.queries = min(2 * qpt, w.n - w.i0);
-  w.p0 = w.L - w.n;
-  const int p_first = w.p0 + w.i0, p_last = p_first + w.queries - 1;
-  const int first = a.window == 0 ? 0 : max(0, p_first - a.window + 1);
-  w.win_block = first / a.b;
-  w.sink_blocks = min((min(a.sinks, w.L) + a.b - 1) / a.b, w.win_block);
-  w.blocks = w.sink_blocks + p_last / a.b + 1 - w.win_block;
-  w.tiles = (w.blocks * a.b + kKeys - 1) / kKeys;
-  const bool two = w.queries > qpt;  // the second tile has rows
-
-  bool bad_id = false;
-  for (int e = tid; e < w.blocks; e += kThreads) {
-    const int blk = e < w.sink_blocks ? e : w.win_block + e - w.sink_blocks;
-    const int id = a.tables[static_cast<int64_t>(r) * a.max_blocks + blk];
-    bad_id |= id < 0 || id >= a.num_blocks;
-  }
   if (tid == 0) {
-    mbar_init(&s.q_full, two ? 8 : 4);
+    mbar_init(&s.q_full, Q_TMA ? 1 : 32);
+    mbar_init(&s.q_empty, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], 1);
@@ -246,107 +351,184 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
       mbar_init(&s.o_full[i], 1);
+      mbar_init(&s.o_empty[i], 4);
     }
-    mbar_init(&s.v_clean, two ? 8 : 4);
+    mbar_init(&s.v_clean, 8);
     mbar_init(&s.drain, 1);
     s.abort = 0;
-    s.redo = 0;
+    for (int i = 0; i < kFlags; ++i) s.bad[i] = s.redo[i] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm);
+    if (Q_TMA) prefetch_tensormap(&tq);
   }
-  if (__syncthreads_or(bad_id)) {
-    if (tid == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
-    return;
-  }
+  // rows of the query tiles that no query fills stay zero
+  for (int i = tid; i < static_cast<int>(sizeof(s.q) / 16); i += kThreads)
+    reinterpret_cast<uint4*>(&s.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == kMmaWarp) tmem_alloc(&s.tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = s.tmem;
   volatile int* const abort = &s.abort;
-  const int bpt = kKeys / a.b;  // blocks per tile
-  // some row of the CTA does not see some token of list tile j
-  const auto mixed_tile = [&](int j) {
-    const int t_lo = token_of(a, w, j, 0), t_hi = token_of(a, w, j, kKeys - 1);
-    return !(t_hi - t_lo == kKeys - 1 && (j + 1) * kKeys <= w.blocks * a.b && t_hi <= p_first &&
-             (a.window == 0 || t_lo > p_last - a.window || t_hi < a.sinks));
-  };
+
+  // registers follow the roles: 2 x 128 x 208 + 128 x 88 of the 384 x 168 that the launch gave
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  Item w;
+  bool bad;
+  Raw raw = load_raw(a, blockIdx.x, items, per_request);
+  int count = 0;       // items with work so far
+  uint32_t tiles = 0;  // KV tiles of the items before
 
   if (warp == kProdWarp) {
-    int issued = 0;  // 2 j + 1 after K of tile j, 2 j + 2 after its V
-    for (int j = 0; j < w.tiles; ++j) {
-      const int st = j % kStages;
-      const uint32_t ph = (j / kStages) & 1;
-      const int nb = min(bpt, w.blocks - j * bpt);
-      int z = 0;
-      if (lane < nb) {
-        const int e = j * bpt + lane, blk = e < w.sink_blocks ? e : w.win_block + e - w.sink_blocks;
-        z = a.layer * static_cast<int>(a.num_blocks) + a.tables[static_cast<int64_t>(r) * a.max_blocks + blk];
+    const int bpt = kKeys / a.b;  // blocks per tile
+    bool go = true;
+    uint32_t done = 0;            // tiles whose K and V were issued
+    int half = 0;                 // and whether K of the next one was
+    for (int item = blockIdx.x; go && item < items; item += step) {
+      const Raw now = raw;
+      raw = load_raw(a, item + step, items, per_request);
+      if (!take_item(a, item, nx, now, w, bad)) {
+        if (bad && lane == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
+        continue;
       }
-      bool go = true;
-      for (int kv = 0; kv < 2 && go; ++kv) {
-        uint64_t* const full = kv ? &s.v_full[st] : &s.k_full[st];
-        if (lane == 0) {
-          if (j >= kStages) go = wait(kv ? &s.v_empty[st] : &s.k_empty[st], ph ^ 1, abort);
-          if (go) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb * a.b * D * 2));
+      ++count;
+      const int32_t* const table = a.tables + static_cast<int64_t>(w.r) * a.max_blocks;
+      const auto id_of = [&](int j) {  // block id that the lane loads for tile j
+        const int e = j * bpt + lane;
+        if (lane >= bpt || e >= w.blocks || j >= w.j1) return 0;
+        return table[e < w.sink_blocks ? e : w.win_block + e - w.sink_blocks];
+      };
+      int id = id_of(w.j0);
+      for (int j = w.j0; go && j < w.j1; ++j, ++done) {
+        const uint32_t st = done % kStages, ph = (done / kStages) & 1;
+        const int nb = min(bpt, w.blocks - j * bpt);
+        // an id outside the pool: the item's rows are not written, and block 0 is read in its place
+        const bool out = id < 0 || id >= a.num_blocks;
+        if (__any_sync(0xffffffffu, out) && lane == 0) {
+          *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) = count;
+          atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
         }
-        go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) break;
-        if (lane < nb)
+        const int z = a.layer * static_cast<int>(a.num_blocks) + (out ? 0 : id);
+        id = id_of(j + 1);
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* const full = kv ? &s.v_full[st] : &s.k_full[st];
+          if (lane == 0) {
+            if (done >= kStages) go = wait(kv ? &s.v_empty[st] : &s.k_empty[st], ph ^ 1, abort);
+            if (go) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb * a.b * D * 2));
+          }
+          go = __shfl_sync(0xffffffffu, go, 0);
+          if (!go) break;
+          if (lane < nb)
 #pragma unroll
-          for (int hd = 0; hd < NH; ++hd)
-            tma_load_3d((kv ? s.v[st][hd] : s.k[st][hd]) + lane * a.b * 128, &tm, full, hd * 64, (kv * a.Hkv + h) * a.b, z);
-        __syncwarp();
-        issued = 2 * j + kv + 1;
+            for (int hd = 0; hd < NH; ++hd)
+              tma_load_3d((kv ? s.v[st][hd] : s.k[st][hd]) + lane * a.b * 128, &tm, full, hd * 64, (kv * a.Hkv + w.h) * a.b, z);
+          __syncwarp();
+          half = kv == 0;
+        }
+        if (!go) break;
       }
-      if (!go) break;
     }
     // copies still in flight after a give-up land before the shared memory is released
-    if (lane == 0 && *abort)
-      for (int x = max(0, issued - 2 * kStages); x < issued; ++x) {
-        const int j = x >> 1;
-        mbar_wait_bounded((x & 1) ? &s.v_full[j % kStages] : &s.k_full[j % kStages], (j / kStages) & 1, kWaitNs);
+    if (lane == 0 && *abort) {
+      for (uint32_t x = done > kStages ? done - kStages : 0; x < done; ++x) {
+        mbar_wait_bounded(&s.k_full[x % kStages], (x / kStages) & 1, kWaitNs);
+        mbar_wait_bounded(&s.v_full[x % kStages], (x / kStages) & 1, kWaitNs);
       }
+      if (half) mbar_wait_bounded(&s.k_full[done % kStages], (done / kStages) & 1, kWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == kQWarp) {
+    bool go = true;
+    for (int item = blockIdx.x; go && item < items; item += step) {
+      const Raw now = raw;
+      raw = load_raw(a, item + step, items, per_request);
+      if (!take_item(a, item, nx, now, w, bad)) continue;
+      ++count;
+      if (lane == 0 && count > 1) go = wait(&s.q_empty, count & 1, abort);  // completion count - 1
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) break;
+      if constexpr (Q_TMA) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&s.q_full, static_cast<uint32_t>((w.two ? 2 : 1) * qpt * a.G * D * 2));
+          for (int t = 0; t < (w.two ? 2 : 1); ++t)
+            for (int hd = 0; hd < NH; ++hd) tma_load_3d(s.q[t][hd], &tq, &s.q_full, hd * 64, w.h * a.G, w.q0 + w.i0 + t * qpt);
+        }
+      } else {
+        for (int rr = lane; rr < min(w.queries, 2 * qpt) * a.G; rr += 32) {
+          const int i = rr / a.G, g = rr - i * a.G, t = i >= qpt, row = (i - t * qpt) * a.G + g;
+          const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs;
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = static_cast<uint32_t>(q[c * 8 + 2 * e]) | static_cast<uint32_t>(q[c * 8 + 2 * e + 1]) << 16;
+            *reinterpret_cast<uint4*>(&s.q[t][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&s.q_full);
+      }
+      __syncwarp();
+    }
+    if (Q_TMA && lane == 0 && *abort && count > 0) mbar_wait_bounded(&s.q_full, (count - 1) & 1, kWaitNs);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
       const uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kTransposeB;
-      const int nt = two ? 2 : 1;
-      const auto issue_s = [&](int t, int st) {
+      const auto issue_s = [&](int t, uint32_t st) {
+#pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_bf16(tbase + t * kKeys, smem_desc_sw128(smem_u32(&s.q[t][kk >> 2][(kk & 3) * 32])),
                    smem_desc_sw128(smem_u32(&s.k[st][kk >> 2][(kk & 3) * 32])), idesc_s, kk > 0);
         mma_commit(&s.s_full[t]);
       };
-      bool ok = wait(&s.q_full, 0, abort) && wait(&s.k_full[0], 0, abort);
-      if (ok) {
+      bool ok = true;
+      uint32_t cleaned = 0, p_seen[2] = {0, 0}, o_used[2] = {0, 0};
+      for (int item = blockIdx.x; ok && item < items; item += step) {
+        const Raw now = raw;
+        raw = load_raw(a, item + step, items, per_request);
+        if (!take_item(a, item, nx, now, w, bad)) continue;
+        const int nt = w.two ? 2 : 1;
+        ok = wait(&s.q_full, count & 1, abort);
+        ++count;
+        if (ok && w.j0 < w.j1) ok = wait(&s.k_full[tiles % kStages], (tiles / kStages) & 1, abort);
+        if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) issue_s(t, 0);
-        mma_commit(&s.k_empty[0]);
-      }
-      uint32_t cleaned = 0;  // mixed tiles so far
-      for (int j = 0; ok && j < w.tiles; ++j) {
-        const int st = j % kStages, nst = (j + 1) % kStages;
-        const bool more = j + 1 < w.tiles;
-        ok = wait(&s.v_full[st], (j / kStages) & 1, abort);
-        if (ok && mixed_tile(j)) ok = wait(&s.v_clean, cleaned++ & 1, abort);
-        for (int t = 0; ok && t < nt; ++t) {
-          ok = wait(&s.p_full[t], j & 1, abort);
-          if (!ok) break;
-          tc_fence_after();
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_bf16_ts(tbase + 256 + t * 128, tbase + t * kKeys + kk * 8,
-                        smem_desc_mn_sw128(smem_u32(&s.v[st][0][kk * 16 * 128]), kKeys * 128), idesc_o, j > 0 || kk > 0);
-          if (t == nt - 1) mma_commit(&s.v_empty[st]);
-          if (more) {
-            if (t == 0) ok = wait(&s.k_full[nst], ((j + 1) / kStages) & 1, abort);
+        if (w.j0 < w.j1) {
+          for (int t = 0; t < nt; ++t) issue_s(t, tiles % kStages);
+          mma_commit(&s.k_empty[tiles % kStages]);
+        }
+        if (w.j1 - w.j0 <= 1) mma_commit(&s.q_empty);
+        for (int j = w.j0; ok && j < w.j1; ++j, ++tiles) {
+          const uint32_t st = tiles % kStages, nst = (tiles + 1) % kStages;
+          const bool more = j + 1 < w.j1;
+          ok = wait(&s.v_full[st], (tiles / kStages) & 1, abort);
+          if (ok && mixed_tile(a, w, j)) ok = wait(&s.v_clean, cleaned++ & 1, abort);
+          for (int t = 0; ok && t < nt; ++t) {
+            ok = wait(&s.p_full[t], p_seen[t]++ & 1, abort);
+            if (ok && j == w.j0 && o_used[t]++ > 0) ok = wait(&s.o_empty[t], o_used[t] & 1, abort);
             if (!ok) break;
             tc_fence_after();
-            issue_s(t, nst);
-            if (t == nt - 1) mma_commit(&s.k_empty[nst]);
-          } else {
-            mma_commit(&s.o_full[t]);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_bf16_ts(tbase + 256 + t * 128, tbase + t * kKeys + kk * 8,
+                          smem_desc_mn_sw128(smem_u32(&s.v[st][0][kk * 16 * 128]), kKeys * 128), idesc_o, j > w.j0 || kk > 0);
+            if (t == nt - 1) mma_commit(&s.v_empty[st]);
+            if (more) {
+              if (t == 0) ok = wait(&s.k_full[nst], ((tiles + 1) / kStages) & 1, abort);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t, nst);
+              if (t == nt - 1) {
+                mma_commit(&s.k_empty[nst]);
+                if (j + 2 == w.j1) mma_commit(&s.q_empty);  // no further product reads the queries
+              }
+            } else {
+              mma_commit(&s.o_full[t]);
+            }
           }
         }
       }
@@ -357,48 +539,36 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    Item w;
+    bool bad;
+    Raw raw = load_raw(a, blockIdx.x, items, per_request);
+    int count = 0;
+    uint32_t tiles = 0;
     const int t = warp >> 2, row = tid & 127;
-    const int group = two ? 256 : 128;  // threads of the softmax groups
-    if (t == 0 || two) {
-      // the row's query into the swizzled tile; rows past the queries are zero
-      const int qi = row / a.G, gi = row - qi * a.G;
-      const int i = t * qpt + qi;  // query of the CTA
+    const int qi = row / a.G, gi = row - qi * a.G;
+    const int i = t * qpt + qi;  // query of the item
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tbase + lanes + t * kKeys, to = tbase + lanes + 256 + t * 128;
+    const uint64_t sl2x2 = pair2(a.sl2);
+    uint32_t s_seen = 0, o_seen = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += step) {
+      const Raw now = raw;
+      raw = load_raw(a, item + step, items, per_request);
+      if (!take_item(a, item, nx, now, w, bad)) continue;
+      ++count;
+      const uint32_t tile_base = tiles;
+      tiles += static_cast<uint32_t>(w.j1 - w.j0);
+      if (t == 1 && !w.two) continue;
       const bool have = qi < qpt && i < w.queries;
-      const int p = p_first + min(i, w.queries - 1);
-      {
-        const uint16_t* const q = have ? a.q + (w.q0 + w.i0 + i) * a.q_ts + (h * a.G + gi) * a.q_hs : a.q;
-        const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (have) {
-            if (vec) {
-              x = *reinterpret_cast<const uint4*>(q + c * 8);
-            } else {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = static_cast<uint32_t>(q[c * 8 + 2 * e]) | static_cast<uint32_t>(q[c * 8 + 2 * e + 1]) << 16;
-              x = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(&s.q[t][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = x;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.q_full);
-
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tbase + lanes + t * kKeys, to = tbase + lanes + 256 + t * 128;
+      const int p = w.p_first + min(i, w.queries - 1);
       float m = -INFINITY, l = 0.0f;
-      bool ok = true;
-      for (int j = 0; j < w.tiles; ++j) {
-        const int st = j % kStages;
-        const bool mixed = mixed_tile(j);
-        ok = wait(&s.s_full[t], j & 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int j = w.j0; j < w.j1; ++j) {
+        const uint32_t tile = tile_base + static_cast<uint32_t>(j - w.j0), st = tile % kStages;
+        ok = __all_sync(0xffffffffu, wait(&s.s_full[t], s_seen++ & 1, abort));
         if (!ok) break;
         tc_fence_after();
         uint32_t x[4][32];
@@ -408,25 +578,28 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_ld_dep(x[1]);
         tmem_ld_dep(x[2]);
         tmem_ld_dep(x[3]);
-        if (mixed) {
-          const int left = w.blocks * a.b - j * kKeys;  // columns that the list has
+        if (mixed_tile(a, w, j)) {
+          const int left = w.blocks * a.b - j * kKeys;           // columns that the list has
+          const int cut = w.sink_blocks * a.b - j * kKeys;       // columns of the first tokens' blocks
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t in_sink = low_bits(cut - c * 32);
+            const uint32_t bits = low_bits(left - c * 32) & ((seen_bits(a, p, j * kKeys, c * 32) & in_sink) |
+                                                             (seen_bits(a, p, w.win_block * a.b - cut, c * 32) & ~in_sink));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int col = c * 32 + e;
-              if (!(col < left && sees(a, p, token_of(a, w, j, col)))) x[c][e] = __float_as_uint(-INFINITY);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1)) x[c][e] = __float_as_uint(-INFINITY);
+          }
           // V: see the head of this file
-          ok = wait(&s.v_full[st], (j / kStages) & 1, abort);
+          ok = wait(&s.v_full[st], (tile / kStages) & 1, abort);
           bool odd = false;
           if (ok)
-            for (int y = (t * 128 + row); y < kKeys * (D / 8); y += group) {
+            for (int y = t * 128 + row; y < kKeys * (D / 8); y += w.two ? 256 : 128) {
               const int col = y / (D / 8), c = y % (D / 8);
               uint4* const at = reinterpret_cast<uint4*>(&s.v[st][c >> 3][col * 128 + (((c & 7) ^ (col & 7)) << 4)]);
               const int tk = token_of(a, w, j, col);
-              // the span of positions that see the token contains some row's
-              const bool any = col < left && tk <= p_last && (a.window == 0 || tk > p_first - a.window || tk < a.sinks);
+              // the positions from the item's first to its last that see the token
+              const bool any = col < left && tk <= w.p_last && (a.window == 0 || tk > w.p_first - a.window || tk < a.sinks);
               if (!any) {
                 *at = make_uint4(0, 0, 0, 0);
               } else {
@@ -436,21 +609,24 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 for (int e = 0; e < 4; ++e) odd |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
               }
             }
-          if (odd) s.redo = 1;
+          if (odd) *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) = count;
           fence_proxy_async_smem();
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) mbar_arrive(&s.v_clean);
+          if (lane == 0) {
+            mbar_arrive(&s.v_clean);
+            if (!w.two) mbar_arrive(&s.v_clean);  // for the other group
+          }
         }
-        float mx = -INFINITY;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int e = 0; e < 32; ++e)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[c][e]));
-        mx *= a.sl2;
-        if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-          const float mn = fmaxf(m, mx), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
-          if (j > 0) {  // O of the tiles so far, complete since s_full follows their products
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          const float mn = fmaxf(m, top), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
+          if (j > w.j0) {  // O of the tiles so far, complete since s_full follows their products
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -464,56 +640,82 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           l *= corr;
           m = mn;
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t ref = pair2(m == -INFINITY ? 0.0f : -m);
+        uint64_t sum[2] = {0, 0};  // pairs of +0
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const uint32_t (&src)[32] = x[2 * c + (e >> 4)];
-            const float y0 = ex2(fmaf(__uint_as_float(src[(2 * e) & 31]), a.sl2, -ref));
-            const float y1 = ex2(fmaf(__uint_as_float(src[(2 * e + 1) & 31]), a.sl2, -ref));
-            sum[e & 3] += y0 + y1;
+            float y0, y1;
+            unpair(fma2(pair(src[(2 * e) & 31], src[(2 * e + 1) & 31]), sl2x2, ref), y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(y0), __float_as_uint(y1)));
             pk[e] = pack_bf16(y0, y1);
           }
           tmem_st32(ts + c * 32, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float a0, a1;
+        unpair(add2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[t]);
       }
-      if (ok) ok = wait(&s.o_full[t], 0, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
+      if (!ok) break;
+      const bool empty = w.j0 == w.j1;  // a part without tiles
+      if (!empty) {
+        ok = __all_sync(0xffffffffu, wait(&s.o_full[t], o_seen++ & 1, abort));
+        if (!ok) break;
         tc_fence_after();
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* const out = have ? a.out + (w.q0 + w.i0 + i) * a.o_ts + (h * a.G + gi) * a.o_hs : a.out;
-        const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+      }
+      const Sink to_row = sink_of<D>(a, w, i, gi, have);
+      const bool marked = *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) == count;
+      const bool again = *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) == count;
+      const bool write = have && !marked && !again;
+      if (to_row.part && (write || marked || empty)) {
+        to_row.part[D] = marked ? NAN : m;  // a maximum is never NaN: marks a part with a bad block id
+        to_row.part[D + 1] = l;
+      }
+      if (!empty) {
+        const float inv = to_row.part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+        const bool vec = (reinterpret_cast<uintptr_t>(to_row.out) & 15) == 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32_issue(to + c * 32, o);
           tmem_wait_ld(o);
-          if (have) {
-            uint32_t y[16];
+          if (c == D / 32 - 1) {  // the next item may use O
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.o_empty[t]);
+          }
+          if (!write) continue;
+          if (to_row.part) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-            if (vec) {
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            continue;
+          }
+          uint32_t y[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-            } else {
+          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (vec) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                out[c * 32 + 2 * e] = static_cast<uint16_t>(y[e]);
-                out[c * 32 + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
-              }
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(to_row.out + c * 32 + e * 8) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              to_row.out[c * 32 + 2 * e] = static_cast<uint16_t>(y[e]);
+              to_row.out[c * 32 + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
             }
           }
         }
+        if (again && !marked) rows_plainly<D>(a, w, t, warp & 3, lane);
       }
     }
   }
@@ -521,36 +723,128 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __syncthreads();
   if (tid == 0 && s.abort) atomicCAS(a.err, 0, ZP_ERR_TIMEOUT);
   if (warp == kMmaWarp) tmem_dealloc(tbase, kTmemCols);
-  if (s.redo && !s.abort && warp < 8) rows_plainly<D>(a, w, r, h, warp, lane);
+}
+
+// Joins the parts of split items: one warp a row (token, head), in the order of the parts.
+template <int D>
+__global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ AttnArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete and visible
+  const int lane = threadIdx.x & 31, heads = a.Hkv * a.G;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t t = w / heads;
+  if (t >= a.T) return;
+  const int head = static_cast<int>(w - t * heads);
+  // the request of row t: rows of none, and of requests that were skipped, have no parts
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int64_t q0 = a.q_start[lo], n = a.q_start[lo + 1] - q0, L = a.seq_lens[lo];
+  if (q0 < 0 || t < q0 || t >= q0 + n || n > a.max_q || q0 + n > a.T || L < n || L > static_cast<int64_t>(a.max_blocks) * a.b) return;
+  const float* const p = a.part + w * (D + 4);
+  const int64_t step = static_cast<int64_t>(a.T) * heads * (D + 4);
+  float M = -INFINITY;
+  bool skip = false;
+  for (int k = 0; k < a.splits; ++k) {
+    const float mk = p[k * step + D];
+    skip |= isnan(mk);
+    M = fmaxf(M, mk);
+  }
+  if (skip || lane * 4 >= D) return;
+  float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = 0; k < a.splits; ++k) {
+    const float mk = p[k * step + D], lk = p[k * step + D + 1];
+    if (mk == -INFINITY && lk == 0.0f) continue;  // a part that saw nothing; its sums may be unset
+    const float c = mk == -INFINITY ? 1.0f : ex2(mk - M);
+    const float4 y = *reinterpret_cast<const float4*>(p + k * step + lane * 4);
+    l = fmaf(lk, c, l);
+    v[0] = fmaf(y.x, c, v[0]);
+    v[1] = fmaf(y.y, c, v[1]);
+    v[2] = fmaf(y.z, c, v[2]);
+    v[3] = fmaf(y.w, c, v[3]);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* const out = a.out + t * a.o_ts + head * a.o_hs + lane * 4;
+  const uint32_t y0 = pack_bf16(v[0] * inv, v[1] * inv), y1 = pack_bf16(v[2] * inv, v[3] * inv);
+  out[0] = static_cast<uint16_t>(y0);
+  out[1] = static_cast<uint16_t>(y0 >> 16);
+  out[2] = static_cast<uint16_t>(y1);
+  out[3] = static_cast<uint16_t>(y1 >> 16);
 }
 
 static_assert(sizeof(TileSmem<128>) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
-template <int D>
-cudaError_t launch(const CUtensorMap& tm, const AttnArgs& a, cudaStream_t st) {
+template <int D, bool Q_TMA>
+cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs& a, int nx, int items, cudaStream_t st) {
   constexpr int bytes = sizeof(TileSmem<D>) + 1024;
   static PerDeviceInit attrs;
-  const cudaError_t e = attrs.run(
-      [] { return cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  cudaError_t e = attrs.run(
+      [] { return cudaFuncSetAttribute(tile_kernel<D, Q_TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
   if (e != cudaSuccess) return e;
-  const int per_cta = 2 * (kRows / a.G);
-  tile_kernel<D><<<dim3((a.max_q + per_cta - 1) / per_cta, a.Hkv, a.B), kThreads, bytes, st>>>(tm, a);
-  return cudaGetLastError();
+  tile_kernel<D, Q_TMA><<<std::min(items, kSms), kThreads, bytes, st>>>(tm, tq, a, nx, items);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.splits == 1) return e;
+  // launched while the tiles still run; it waits for them on the device
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) * a.Hkv * a.G + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, tile_join_kernel<D>, a);
+}
+
+// Items of a call at most.
+int64_t items_of(const zp_params* p, int B, int max_q, int& nx) {
+  const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
+  nx = (max_q + per_item - 1) / per_item;
+  return static_cast<int64_t>(nx) * p->num_kv_heads * B;
 }
 
 }  // namespace
 
-zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, void* workspace, cudaStream_t st) {
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks) {
+  TilePlan plan{};
+  const int64_t items = items_of(p, B, max_q, plan.nx);
+  int64_t tokens = static_cast<int64_t>(max_blocks) * p->block_size;
+  const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
+  if (window > 0) tokens = std::min(tokens, static_cast<int64_t>(window) + per_item + sinks + 2 * p->block_size);
+  const int64_t tiles = (tokens + kKeys - 1) / kKeys;
+  // a part has four tiles at least: below that its sums cost more than the tiles
+  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(items, 1), tiles / 4)));
+  plan.items = items * plan.splits;
+  plan.bytes = 256;
+  if (plan.splits > 1) plan.bytes += static_cast<size_t>(plan.splits) * T * p->num_q_heads * (p->head_dim + 4) * sizeof(float);
+  return plan;
+}
+
+zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st) {
+  if (plan.items > INT_MAX / 2) return ZP_ERR_UNSUPPORTED;
   a.err = static_cast<int32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.splits = plan.splits;
   const int d = p->head_dim;
-  CUtensorMap tm;
+  CUtensorMap tm, tq{};
   // the pool as {d, 2*Hkv*b rows per (layer, block), layers*num_blocks}; box = one block's b rows
   // of one (K or V, head), 64 columns
   if (!encode_tmap_3d_bf16(&tm, pool->base, d, static_cast<uint64_t>(2) * a.Hkv * a.b,
                            static_cast<uint64_t>(p->num_layers) * pool->num_blocks, static_cast<uint64_t>(d) * 2,
                            static_cast<uint64_t>(2) * a.Hkv * a.b * d * 2, 64, a.b, 1))
     return ZP_ERR_CUDA;
-  const cudaError_t e = d == 128 ? launch<128>(tm, a, st) : launch<64>(tm, a, st);
+  // the queries as {d, heads, T}; rows behind the last token come as zeros
+  const bool q_tma = aligned(a.q, 16) && a.q_ts > 0 && a.q_hs > 0 && a.q_ts % 8 == 0 && a.q_hs % 8 == 0 &&
+                     encode_tmap_3d_bf16(&tq, a.q, d, static_cast<uint64_t>(a.Hkv) * a.G, a.T, static_cast<uint64_t>(a.q_hs) * 2,
+                                         static_cast<uint64_t>(a.q_ts) * 2, 64, a.G, kRows / a.G);
+  const int items = static_cast<int>(plan.items);
+  cudaError_t e;
+  if (d == 128) e = q_tma ? launch<128, true>(tm, tq, a, plan.nx, items, st) : launch<128, false>(tm, tq, a, plan.nx, items, st);
+  else e = q_tma ? launch<64, true>(tm, tq, a, plan.nx, items, st) : launch<64, false>(tm, tq, a, plan.nx, items, st);
   return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
