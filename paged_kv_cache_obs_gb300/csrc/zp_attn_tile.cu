@@ -91,6 +91,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], issued by a single thread.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -161,6 +168,7 @@ struct Item {
   int p_first, p_last;     // positions of its first and last query
   int sink_blocks, win_block, blocks;
   int j0, j1;              // its tiles of the list
+  int c0, c1, c2;          // tiles below c0 and from c1 to c2 - 1 are seen whole by every row; the others are mixed
   bool two;                // the second query tile has rows
 };
 
@@ -168,10 +176,10 @@ struct Item {
 struct Raw {
   int L, q0, q1;
 };
-__device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items, int per_request) {
+__device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items) {
   Raw raw{0, 0, 0};
   if (item < items) {
-    const int r = item / per_request;
+    const int r = item / (a.splits * a.Hkv) % a.B;
     raw.L = a.seq_lens[r];
     raw.q0 = a.q_start[r];
     raw.q1 = a.q_start[r + 1];
@@ -179,16 +187,16 @@ __device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items, 
   return raw;
 }
 
-// Items in order of request, kv head, queries from the last (which see the most) to the first,
+// Items in order of queries from the last (which see the most) to the first, request, kv head,
 // and part of the tiles.  False: nothing to do (`bad`: the request is reported).
 __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, const Raw& raw, Item& w, bool& bad) {
   const int qpt = kRows / a.G;  // queries per tile
   w.split = item % a.splits;
   item /= a.splits;
-  const int x = item % nx;
-  item /= nx;
   w.h = item % a.Hkv;
-  w.r = item / a.Hkv;
+  item /= a.Hkv;
+  w.r = item % a.B;
+  const int x = item / a.B;
   w.L = raw.L;
   w.q0 = raw.q0;
   const int64_t n = static_cast<int64_t>(raw.q1) - raw.q0;
@@ -211,6 +219,12 @@ __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, c
   w.j0 = static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits);
   w.j1 = static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits);
   w.two = w.queries > qpt;
+  // runs of the list: first tokens' blocks, where column e is token e, and the window's, where it is
+  // token e + shift; one run where the two meet
+  const int sink = w.sink_blocks == w.win_block ? 0 : w.sink_blocks << bs, shift = sink ? (w.win_block << bs) - sink : 0;
+  w.c0 = min(min(sink, a.sinks), w.p_first + 1) / kKeys;
+  w.c1 = (max(sink, a.window == 0 ? 0 : w.p_last - a.window + 1 - shift) + kKeys - 1) / kKeys;
+  w.c2 = min(w.p_first + 1 - shift, w.blocks << bs) / kKeys;
   return true;
 }
 
@@ -225,11 +239,7 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int t) {
 }
 
 // Some row of the item does not see some token of list tile j.
-__device__ __forceinline__ bool mixed_tile(const AttnArgs& a, const Item& w, int j) {
-  const int t_lo = token_of(a, w, j, 0), t_hi = token_of(a, w, j, kKeys - 1);
-  return !(t_hi - t_lo == kKeys - 1 && (j + 1) * kKeys <= w.blocks * a.b && t_hi <= w.p_first &&
-           (a.window == 0 || t_lo > w.p_last - a.window || t_hi < a.sinks));
-}
+__device__ __forceinline__ bool mixed_tile(const Item& w, int j) { return j >= w.c0 && (j < w.c1 || j >= w.c2); }
 
 // The columns c0 .. c0 + 31 of a run of tokens base + col that position p sees, as bits.
 __device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, int p, int base, int c0) {
@@ -335,8 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   extern __shared__ uint8_t dyn[];
   TileSmem<D>& s = *reinterpret_cast<TileSmem<D>*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qpt = kRows / a.G, per_request = nx * a.Hkv * a.splits;
+  const int qpt = kRows / a.G;
+  // The CTA's items: the grid takes a run of gridDim.x items in one direction, the next in the other,
+  // so that the sums of what its CTAs get come near one another (items get lighter along the list).
   const int step = static_cast<int>(gridDim.x);
+  const auto next_item = [&](int item) {
+    const int in = item % step;
+    return item - in + step + (step - 1 - in);
+  };
 
   if (tid == 0) {
     mbar_init(&s.q_full, Q_TMA ? 1 : 32);
@@ -377,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   Item w;
   bool bad;
-  Raw raw = load_raw(a, blockIdx.x, items, per_request);
+  Raw raw = load_raw(a, blockIdx.x, items);
   int count = 0;       // items with work so far
   uint32_t tiles = 0;  // KV tiles of the items before
 
@@ -386,9 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     bool go = true;
     uint32_t done = 0;            // tiles whose K and V were issued
     int half = 0;                 // and whether K of the next one was
-    for (int item = blockIdx.x; go && item < items; item += step) {
+    for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
       const Raw now = raw;
-      raw = load_raw(a, item + step, items, per_request);
+      raw = load_raw(a, next_item(item), items);
       if (!take_item(a, item, nx, now, w, bad)) {
         if (bad && lane == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
         continue;
@@ -441,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     __syncwarp();
   } else if (warp == kQWarp) {
     bool go = true;
-    for (int item = blockIdx.x; go && item < items; item += step) {
+    for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
       const Raw now = raw;
-      raw = load_raw(a, item + step, items, per_request);
+      raw = load_raw(a, next_item(item), items);
       if (!take_item(a, item, nx, now, w, bad)) continue;
       ++count;
       if (lane == 0 && count > 1) go = wait(&s.q_empty, count & 1, abort);  // completion count - 1
@@ -475,68 +491,102 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     if (Q_TMA && lane == 0 && *abort && count > 0) mbar_wait_bounded(&s.q_full, (count - 1) & 1, kWaitNs);
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-      const uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kTransposeB;
-      const auto issue_s = [&](int t, uint32_t st) {
+    // The whole warp walks, and one thread of it issues: addresses and descriptors that the compiler
+    // knows to be the warp's own stay in uniform registers, where the products take them from.
+    // (Issued by a thread of a divergent warp, each product cost 95 cycles in place of its 64.)
+    // Descriptors are made once; a step along the contraction adds to their start address (in
+    // units of 16 bytes).
+    static_assert(kStages == 2, "descriptors below");
+    const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+    const uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kTransposeB;
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint64_t qd0 = smem_desc_sw128(smem_u32(s.q[0])), qd1 = smem_desc_sw128(smem_u32(s.q[1]));
+    const uint64_t kd0 = smem_desc_sw128(smem_u32(s.k[0])), kd1 = smem_desc_sw128(smem_u32(s.k[1]));
+    const uint64_t vd0 = smem_desc_mn_sw128(smem_u32(s.v[0]), kKeys * 128), vd1 = smem_desc_mn_sw128(smem_u32(s.v[1]), kKeys * 128);
+    const bool one = elect_one();
+    const auto issue_s = [&](int t, uint32_t st) {
+      const uint64_t qd = t ? qd1 : qd0, kd = st ? kd1 : kd0;
+      const uint32_t d = tb + t * kKeys;
+      if (one) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(tbase + t * kKeys, smem_desc_sw128(smem_u32(&s.q[t][kk >> 2][(kk & 3) * 32])),
-                   smem_desc_sw128(smem_u32(&s.k[st][kk >> 2][(kk & 3) * 32])), idesc_s, kk > 0);
-        mma_commit(&s.s_full[t]);
-      };
-      bool ok = true;
-      uint32_t cleaned = 0, p_seen[2] = {0, 0}, o_used[2] = {0, 0};
-      for (int item = blockIdx.x; ok && item < items; item += step) {
-        const Raw now = raw;
-        raw = load_raw(a, item + step, items, per_request);
-        if (!take_item(a, item, nx, now, w, bad)) continue;
-        const int nt = w.two ? 2 : 1;
-        ok = wait(&s.q_full, count & 1, abort);
-        ++count;
-        if (ok && w.j0 < w.j1) ok = wait(&s.k_full[tiles % kStages], (tiles / kStages) & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        if (w.j0 < w.j1) {
-          for (int t = 0; t < nt; ++t) issue_s(t, tiles % kStages);
-          mma_commit(&s.k_empty[tiles % kStages]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          constexpr int kHalf = kRows * 128 / 16;  // from one 64-column half to the next
+          const int at = (kk >> 2) * kHalf + (kk & 3) * 2;
+          mma_bf16(d, qd + at, kd + at, idesc_s, kk > 0);
         }
-        if (w.j1 - w.j0 <= 1) mma_commit(&s.q_empty);
-        for (int j = w.j0; ok && j < w.j1; ++j, ++tiles) {
-          const uint32_t st = tiles % kStages, nst = (tiles + 1) % kStages;
-          const bool more = j + 1 < w.j1;
-          ok = wait(&s.v_full[st], (tiles / kStages) & 1, abort);
-          if (ok && mixed_tile(a, w, j)) ok = wait(&s.v_clean, cleaned++ & 1, abort);
-          for (int t = 0; ok && t < nt; ++t) {
-            ok = wait(&s.p_full[t], p_seen[t]++ & 1, abort);
-            if (ok && j == w.j0 && o_used[t]++ > 0) ok = wait(&s.o_empty[t], o_used[t] & 1, abort);
+        mma_commit(&s.s_full[t]);
+      }
+      __syncwarp();
+    };
+    const auto issue_o = [&](int t, uint32_t st, bool add) {
+      const uint64_t vd = st ? vd1 : vd0;
+      const uint32_t d = tb + 256 + t * 128, p = tb + t * kKeys;
+      if (one) {
+        mma_bf16_ts(d, p, vd, idesc_o, add);
+#pragma unroll
+        for (int kk = 1; kk < kKeys / 16; ++kk) mma_bf16_ts(d, p + kk * 8, vd + kk * 128, idesc_o, 1);
+      }
+      __syncwarp();
+    };
+    const auto commit = [&](uint64_t* bar) {
+      if (one) mma_commit(bar);
+      __syncwarp();
+    };
+    // the warp's answer: every lane waits
+    const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, abort)) != 0; };
+    bool ok = true;
+    uint32_t cleaned = 0, p_seen[2] = {0, 0}, o_used[2] = {0, 0};
+    for (int item = blockIdx.x; ok && item < items; item = next_item(item)) {
+      const Raw now = raw;
+      raw = load_raw(a, next_item(item), items);
+      if (!take_item(a, item, nx, now, w, bad)) continue;
+      const int n = __shfl_sync(0xffffffffu, w.j1 - w.j0, 0);
+      const bool two = __shfl_sync(0xffffffffu, static_cast<int>(w.two), 0) != 0;
+      ok = wait_all(&s.q_full, count & 1);
+      ++count;
+      uint32_t st = __shfl_sync(0xffffffffu, tiles & 1, 0);
+      if (ok && n > 0) ok = wait_all(&s.k_full[st], (tiles >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (n > 0) {
+        issue_s(0, st);
+        if (two) issue_s(1, st);
+        commit(&s.k_empty[st]);
+      }
+      if (n <= 1) commit(&s.q_empty);
+      for (int j = 0; ok && j < n; ++j, ++tiles, st ^= 1) {
+        const bool more = j + 1 < n;
+        ok = wait_all(&s.v_full[st], (tiles >> 1) & 1);
+        if (ok && mixed_tile(w, w.j0 + j)) ok = wait_all(&s.v_clean, cleaned++ & 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (t == 1 && !two)) break;
+          const bool last = t == 1 || !two;
+          ok = wait_all(&s.p_full[t], p_seen[t]++ & 1);
+          if (ok && j == 0 && o_used[t]++ > 0) ok = wait_all(&s.o_empty[t], o_used[t] & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(t, st, j > 0);
+          if (last) commit(&s.v_empty[st]);
+          if (more) {
+            if (t == 0) ok = wait_all(&s.k_full[st ^ 1], ((tiles + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_bf16_ts(tbase + 256 + t * 128, tbase + t * kKeys + kk * 8,
-                          smem_desc_mn_sw128(smem_u32(&s.v[st][0][kk * 16 * 128]), kKeys * 128), idesc_o, j > w.j0 || kk > 0);
-            if (t == nt - 1) mma_commit(&s.v_empty[st]);
-            if (more) {
-              if (t == 0) ok = wait(&s.k_full[nst], ((tiles + 1) / kStages) & 1, abort);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(t, nst);
-              if (t == nt - 1) {
-                mma_commit(&s.k_empty[nst]);
-                if (j + 2 == w.j1) mma_commit(&s.q_empty);  // no further product reads the queries
-              }
-            } else {
-              mma_commit(&s.o_full[t]);
+            issue_s(t, st ^ 1);
+            if (last) {
+              commit(&s.k_empty[st ^ 1]);
+              if (j + 2 == n) commit(&s.q_empty);  // no further product reads the queries
             }
+          } else {
+            commit(&s.o_full[t]);
           }
         }
       }
-      // products still in flight after a give-up complete before TMEM is released
-      if (!ok) {
-        mma_commit(&s.drain);
-        mbar_wait_bounded(&s.drain, 0, kWaitNs);
-      }
+    }
+    // products still in flight after a give-up complete before TMEM is released
+    if (!ok) {
+      commit(&s.drain);
+      mbar_wait_bounded(&s.drain, 0, kWaitNs);
     }
     __syncwarp();
   }
@@ -544,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     Item w;
     bool bad;
-    Raw raw = load_raw(a, blockIdx.x, items, per_request);
+    Raw raw = load_raw(a, blockIdx.x, items);
     int count = 0;
     uint32_t tiles = 0;
     const int t = warp >> 2, row = tid & 127;
@@ -555,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint64_t sl2x2 = pair2(a.sl2);
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += step) {
+    for (int item = blockIdx.x; ok && item < items; item = next_item(item)) {
       const Raw now = raw;
-      raw = load_raw(a, item + step, items, per_request);
+      raw = load_raw(a, next_item(item), items);
       if (!take_item(a, item, nx, now, w, bad)) continue;
       ++count;
       const uint32_t tile_base = tiles;
@@ -578,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_ld_dep(x[1]);
         tmem_ld_dep(x[2]);
         tmem_ld_dep(x[3]);
-        if (mixed_tile(a, w, j)) {
+        if (mixed_tile(w, j)) {
           const int left = w.blocks * a.b - j * kKeys;           // columns that the list has
           const int cut = w.sink_blocks * a.b - j * kKeys;       // columns of the first tokens' blocks
 #pragma unroll
