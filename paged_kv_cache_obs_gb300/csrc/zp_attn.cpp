@@ -14,7 +14,7 @@ zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_
   if (!p || B < 0 || max_blocks < 1 || window < 0 || sinks < 0 || num_blocks <= 0) return ZP_ERR_INVALID_ARG;
   if (layer < 0 || layer >= p->num_layers) return ZP_ERR_INVALID_ARG;
   // (layer, block) is one 32-bit coordinate of the tensor map
-  if (num_blocks > INT_MAX / p->num_layers) return ZP_ERR_UNSUPPORTED;
+  if (num_blocks >= INT_MAX / p->num_layers) return ZP_ERR_UNSUPPORTED;
   if (p->num_kv_heads <= 0 || p->num_q_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return ZP_ERR_INVALID_ARG;
   if (!(p->scale > 0.0f) || !std::isfinite(p->scale)) return ZP_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return ZP_ERR_UNSUPPORTED;
@@ -41,6 +41,7 @@ AttnArgs args_of(const zp_params* p, int32_t layer, int64_t num_blocks, const zp
   a.seq_lens = seq_lens;
   a.B = B;
   a.layer = layer;
+  a.layers = p->num_layers;
   a.max_blocks = max_blocks;
   a.Hkv = p->num_kv_heads;
   a.G = p->num_q_heads / p->num_kv_heads;

@@ -17,7 +17,7 @@ struct AttnArgs {
   const int32_t *tables, *seq_lens;
   int32_t* err;
   float* part;             // [B][Hkv][parts][rows][d + 4]: sums, maximum, sum of weights
-  int T, B, layer, max_blocks, Hkv, G, b, max_q, window, sinks;
+  int T, B, layer, layers, max_blocks, Hkv, G, b, max_q, window, sinks;
   int splits;              // CTAs that share a row's tokens
   float sl2;               // scale * log2(e)
 };

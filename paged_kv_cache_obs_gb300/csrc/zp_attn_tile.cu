@@ -39,7 +39,7 @@ namespace {
 constexpr int kRows = 128;            // rows of a query tile = TMEM lanes
 constexpr int kKeys = 128;            // tokens of a KV tile
 constexpr int kStages = 2;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kKWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;         // two softmax groups, and a group of the other roles
 constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -47,15 +47,31 @@ constexpr float kLazy = 8.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
 constexpr int kFlags = 8;             // items that roles can be apart, and more
 
+// An item: which, and what it walks.
+struct Item {
+  int r, h, split;         // r < 0: there are no more
+  int L, n, q0, p0;        // tokens, queries, first row of q, position of the request's first query
+  int i0, queries;         // first query of the item, how many
+  int p_first, p_last;     // positions of its first and last query
+  int sink_blocks, win_block, blocks;
+  int j0, j1;              // its tiles of the list
+  int c0, c1, c2;          // tiles below c0 and from c1 to c2 - 1 are seen whole by every row; the others are mixed
+  bool two;                // the second query tile has rows
+};
+
+constexpr int kItems = 4;             // ring of items that the MMA warp hands to the softmax groups
+
 template <int D>
 struct __align__(1024) TileSmem {
   uint8_t q[2][D / 64][kRows * 128];         // [tile][64-column half][row][128 B], 128-byte swizzle
   uint8_t k[kStages][D / 64][kKeys * 128];
   uint8_t v[kStages][D / 64][kKeys * 128];
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], v_clean, drain;
+  uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems];
   uint32_t tmem;
   int abort;
+  Item items[kItems];
   int bad[kFlags], redo[kFlags];             // the last item (counted from 1) that a block id or a value marked
 };
 
@@ -89,6 +105,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       return false;
     }
   }
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // True in one lane of the (whole) warp.
@@ -160,18 +189,6 @@ __device__ __forceinline__ uint64_t pair2(float x) { return pair(__float_as_uint
 // The lowest n bits, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
-// An item: which, and what it walks.
-struct Item {
-  int r, h, split;
-  int L, n, q0, p0;        // tokens, queries, first row of q, position of the request's first query
-  int i0, queries;         // first query of the item, how many
-  int p_first, p_last;     // positions of its first and last query
-  int sink_blocks, win_block, blocks;
-  int j0, j1;              // its tiles of the list
-  int c0, c1, c2;          // tiles below c0 and from c1 to c2 - 1 are seen whole by every row; the others are mixed
-  bool two;                // the second query tile has rows
-};
-
 // What an item needs from memory, loaded one item ahead.
 struct Raw {
   int L, q0, q1;
@@ -179,7 +196,7 @@ struct Raw {
 __device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items) {
   Raw raw{0, 0, 0};
   if (item < items) {
-    const int r = item / (a.splits * a.Hkv) % a.B;
+    const int r = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(a.splits * a.Hkv) % static_cast<uint32_t>(a.B));
     raw.L = a.seq_lens[r];
     raw.q0 = a.q_start[r];
     raw.q1 = a.q_start[r + 1];
@@ -191,12 +208,16 @@ __device__ __forceinline__ Raw load_raw(const AttnArgs& a, int item, int items) 
 // and part of the tiles.  False: nothing to do (`bad`: the request is reported).
 __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, const Raw& raw, Item& w, bool& bad) {
   const int qpt = kRows / a.G;  // queries per tile
-  w.split = item % a.splits;
-  item /= a.splits;
-  w.h = item % a.Hkv;
-  item /= a.Hkv;
-  w.r = item % a.B;
-  const int x = item / a.B;
+  uint32_t u = static_cast<uint32_t>(item);
+  w.split = 0;
+  if (a.splits > 1) {
+    w.split = static_cast<int>(u % static_cast<uint32_t>(a.splits));
+    u /= static_cast<uint32_t>(a.splits);
+  }
+  w.h = static_cast<int>(u % static_cast<uint32_t>(a.Hkv));
+  u /= static_cast<uint32_t>(a.Hkv);
+  w.r = static_cast<int>(u % static_cast<uint32_t>(a.B));
+  const int x = static_cast<int>(u / static_cast<uint32_t>(a.B));
   w.L = raw.L;
   w.q0 = raw.q0;
   const int64_t n = static_cast<int64_t>(raw.q1) - raw.q0;
@@ -213,11 +234,15 @@ __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, c
   const int bs = a.b == 16 ? 4 : 5;
   const int first = a.window == 0 ? 0 : max(0, w.p_first - a.window + 1);
   w.win_block = first >> bs;
-  w.sink_blocks = static_cast<int>(min((static_cast<int64_t>(min(a.sinks, w.L)) + a.b - 1) >> bs, static_cast<int64_t>(w.win_block)));
+  w.sink_blocks = min((min(a.sinks, w.L) + a.b - 1) >> bs, w.win_block);
   w.blocks = w.sink_blocks + (w.p_last >> bs) + 1 - w.win_block;
-  const int tiles = static_cast<int>((static_cast<int64_t>(w.blocks) * a.b + kKeys - 1) / kKeys);
-  w.j0 = static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits);
-  w.j1 = static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits);
+  const int tiles = ((w.blocks << bs) + kKeys - 1) / kKeys;  // at most 2^23, and 152 splits
+  w.j0 = 0;
+  w.j1 = tiles;
+  if (a.splits > 1) {
+    w.j0 = static_cast<int>(static_cast<uint32_t>(tiles) * w.split / static_cast<uint32_t>(a.splits));
+    w.j1 = static_cast<int>(static_cast<uint32_t>(tiles) * (w.split + 1) / static_cast<uint32_t>(a.splits));
+  }
   w.two = w.queries > qpt;
   // runs of the list: first tokens' blocks, where column e is token e, and the window's, where it is
   // token e + shift; one run where the two meet
@@ -242,12 +267,19 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int t) {
 __device__ __forceinline__ bool mixed_tile(const Item& w, int j) { return j >= w.c0 && (j < w.c1 || j >= w.c2); }
 
 // The columns c0 .. c0 + 31 of a run of tokens base + col that position p sees, as bits.
-__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, int p, int base, int c0) {
+__device__ __forceinline__ uint32_t run_bits(const AttnArgs& a, int p, int base, int c0) {
   const uint32_t upto = low_bits(p - base - c0 + 1);
   if (a.window == 0) return upto;
   // t > p - window, or t < sinks
   const uint32_t gone = low_bits(p - a.window - base - c0 + 1), kept = low_bits(a.sinks - base - c0);
   return upto & (~gone | kept);
+}
+// The same of list tile j, which may join the first tokens' run and the window's.
+__device__ __forceinline__ uint32_t tile_bits(const AttnArgs& a, const Item& w, int j, int p, int c0) {
+  const int cut = w.sink_blocks * a.b - j * kKeys, left = w.blocks * a.b - j * kKeys;  // columns of the first run, of the list
+  const uint32_t in_sink = low_bits(cut - c0);
+  return low_bits(left - c0) & ((run_bits(a, p, j * kKeys, c0) & in_sink) |
+                                (run_bits(a, p, w.win_block * a.b - cut, c0) & ~in_sink));
 }
 
 // Where a row's results go: the output, or its part of a split item.
@@ -336,6 +368,46 @@ __device__ __noinline__ void rows_plainly(const AttnArgs& a, const Item& w, int 
   }
 }
 
+// Looks V of mixed tile j over in shared memory (one warp): tokens that no row sees are zeroed; true (in
+// some lane) if a value that only some rows see is not finite.  8 tokens at a time, which are tokens
+// of one block; a lane holds 16-byte chunk lane % (D / 8) of every (256 / D)th of them.
+template <int D>
+__device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int j, uint8_t* v, int lane) {
+  constexpr int kPer = 256 / D, kLoads = 8 / kPer;
+  const int ch = lane % (D / 8), sub = lane / (D / 8);
+  uint8_t* at[kLoads];
+#pragma unroll
+  for (int y = 0; y < kLoads; ++y) {
+    const int col = y * kPer + sub;
+    at[y] = v + (ch >> 3) * (kKeys * 128) + col * 128 + (((ch & 7) ^ col) << 4);
+  }
+  // lane g < 16: whether the g-th 8 tokens need a look (blocks past the list's end are zeros)
+  const int t0 = token_of(a, w, j, (lane & 15) * 8);
+  const bool whole = t0 + 7 <= w.p_first && (a.window == 0 || t0 > w.p_last - a.window || t0 + 7 < a.sinks);
+  const bool listed = j * kKeys + (lane & 15) * 8 < w.blocks * a.b;
+  uint32_t todo = __ballot_sync(0xffffffffu, listed && !whole) & 0xFFFFu;
+  uint32_t top = 0;
+  while (todo) {
+    const int g = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int tk = __shfl_sync(0xffffffffu, t0, g) + sub;
+    uint4 x[kLoads];
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) x[y] = *reinterpret_cast<const uint4*>(at[y] + g * 1024);
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int t = tk + y * kPer;
+      if (t <= w.p_last && (a.window == 0 || t > w.p_first - a.window || t < a.sinks)) {
+        top = max_u16x2(max_u16x2(top, x[y].x & 0x7FFF7FFFu), x[y].y & 0x7FFF7FFFu);
+        top = max_u16x2(max_u16x2(top, x[y].z & 0x7FFF7FFFu), x[y].w & 0x7FFF7FFFu);
+      } else {
+        *reinterpret_cast<uint4*>(at[y] + g * 1024) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  return (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+}
+
 // Q_TMA: the queries' rows are aligned and come by TMA (one box per tile and 64-column half: the
 // group's heads of 128 / G tokens, which is the order of the tile's rows); else by plain loads.
 template <int D, bool Q_TMA>
@@ -357,11 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   if (tid == 0) {
     mbar_init(&s.q_full, Q_TMA ? 1 : 32);
     mbar_init(&s.q_empty, 1);
+    mbar_init(&s.drain, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], 1);
       mbar_init(&s.v_full[i], 1);
       mbar_init(&s.v_empty[i], 1);
+      mbar_init(&s.v_mixed[i], 1);
+      mbar_init(&s.v_clean[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
@@ -369,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(&s.o_full[i], 1);
       mbar_init(&s.o_empty[i], 4);
     }
-    mbar_init(&s.v_clean, 8);
-    mbar_init(&s.drain, 1);
+    for (int i = 0; i < kItems; ++i) mbar_init(&s.item_full[i], 1);
     s.abort = 0;
     for (int i = 0; i < kFlags; ++i) s.bad[i] = s.redo[i] = 0;
     fence_mbar_init();
@@ -388,20 +462,26 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const uint32_t tbase = s.tmem;
   volatile int* const abort = &s.abort;
 
-  // registers follow the roles: 2 x 128 x 208 + 128 x 88 of the 384 x 168 that the launch gave
+  // registers follow the roles: 2 x 128 x 200 + 128 x 104 of the 384 x 168 that the launch gave
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   Item w;
   bool bad;
   Raw raw = load_raw(a, blockIdx.x, items);
   int count = 0;       // items with work so far
   uint32_t tiles = 0;  // KV tiles of the items before
 
-  if (warp == kProdWarp) {
+  if (warp == kKWarp || warp == kVWarp) {
+    // One warp each: K of the next tile is wanted a product earlier than its V, and in one warp it
+    // waited behind the V before it.
+    const int kv = warp == kVWarp;
+    uint64_t* const empties = kv ? s.v_empty : s.k_empty;
     const int bpt = kKeys / a.b;  // blocks per tile
     bool go = true;
-    uint32_t done = 0;            // tiles whose K and V were issued
-    int half = 0;                 // and whether K of the next one was
+    uint32_t done = 0;            // tiles issued
+    int q_loads = 0;              // items whose queries were
+    uint64_t* last[kStages] = {};  // barrier of each stage's last tile, and how often each was used
+    uint32_t used_full = 0, used_mixed = 0, last_parity = 0;  // bits by stage
     for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
       const Raw now = raw;
       raw = load_raw(a, next_item(item), items);
@@ -416,6 +496,38 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (lane >= bpt || e >= w.blocks || j >= w.j1) return 0;
         return table[e < w.sink_blocks ? e : w.win_block + e - w.sink_blocks];
       };
+      // K's warp brings the item's queries too, once the last product that reads the ones before is
+      // done; behind the first K, whose stage is free earlier.  (In the warp that looks V over they came
+      // up to 3 us late.)
+      const auto load_q = [&] {
+        if (lane == 0 && count > 1) go = wait(&s.q_empty, count & 1, abort);  // completion count - 1
+        go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) return;
+        q_loads = count;
+        if constexpr (Q_TMA) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&s.q_full, static_cast<uint32_t>((w.two ? 2 : 1) * qpt * a.G * D * 2));
+            for (int t = 0; t < (w.two ? 2 : 1); ++t)
+              for (int hd = 0; hd < NH; ++hd) tma_load_3d(s.q[t][hd], &tq, &s.q_full, hd * 64, w.h * a.G, w.q0 + w.i0 + t * qpt);
+          }
+        } else {
+          for (int rr = lane; rr < w.queries * a.G; rr += 32) {
+            const int i = rr / a.G, g = rr - i * a.G, t = i >= qpt, row = (i - t * qpt) * a.G + g;
+            const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs;
+            for (int c = 0; c < D / 8; ++c) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[e] = static_cast<uint32_t>(q[c * 8 + 2 * e]) | static_cast<uint32_t>(q[c * 8 + 2 * e + 1]) << 16;
+              *reinterpret_cast<uint4*>(&s.q[t][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&s.q_full);
+        }
+        __syncwarp();
+      };
+      if (!kv && w.j0 == w.j1) load_q();  // a part without tiles
       int id = id_of(w.j0);
       for (int j = w.j0; go && j < w.j1; ++j, ++done) {
         const uint32_t st = done % kStages, ph = (done / kStages) & 1;
@@ -426,69 +538,60 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) = count;
           atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
         }
-        const int z = a.layer * static_cast<int>(a.num_blocks) + (out ? 0 : id);
+        // blocks past the list's end have a coordinate past the tensor's: they come as zeros
+        const int z = lane < nb ? a.layer * static_cast<int>(a.num_blocks) + (out ? 0 : id) : a.layers * static_cast<int>(a.num_blocks);
         id = id_of(j + 1);
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* const full = kv ? &s.v_full[st] : &s.k_full[st];
-          if (lane == 0) {
-            if (done >= kStages) go = wait(kv ? &s.v_empty[st] : &s.k_empty[st], ph ^ 1, abort);
-            if (go) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb * a.b * D * 2));
-          }
-          go = __shfl_sync(0xffffffffu, go, 0);
-          if (!go) break;
-          if (lane < nb)
-#pragma unroll
-            for (int hd = 0; hd < NH; ++hd)
-              tma_load_3d((kv ? s.v[st][hd] : s.k[st][hd]) + lane * a.b * 128, &tm, full, hd * 64, (kv * a.Hkv + w.h) * a.b, z);
-          __syncwarp();
-          half = kv == 0;
+        uint64_t* full = kv ? &s.v_full[st] : &s.k_full[st];
+        uint32_t* used = &used_full;
+        if (kv && mixed_tile(w, j)) {
+          full = &s.v_mixed[st];
+          used = &used_mixed;
         }
+        if (lane == 0) {
+          if (done >= kStages) go = wait(&empties[st], ph ^ 1, abort);
+          if (go) mbar_arrive_expect_tx(full, kKeys * D * 2);
+        }
+        go = __shfl_sync(0xffffffffu, go, 0);
         if (!go) break;
+        if (lane < bpt)
+#pragma unroll
+          for (int hd = 0; hd < NH; ++hd)
+            tma_load_3d((kv ? s.v[st][hd] : s.k[st][hd]) + lane * a.b * 128, &tm, full, hd * 64, (kv * a.Hkv + w.h) * a.b, z);
+        if (!kv && j == w.j0) load_q();
+        last[st] = full;
+        last_parity = (last_parity & ~(1u << st)) | (*used & (1u << st));
+        *used ^= 1u << st;
+        __syncwarp();
       }
     }
     // copies still in flight after a give-up land before the shared memory is released
-    if (lane == 0 && *abort) {
-      for (uint32_t x = done > kStages ? done - kStages : 0; x < done; ++x) {
-        mbar_wait_bounded(&s.k_full[x % kStages], (x / kStages) & 1, kWaitNs);
-        mbar_wait_bounded(&s.v_full[x % kStages], (x / kStages) & 1, kWaitNs);
-      }
-      if (half) mbar_wait_bounded(&s.k_full[done % kStages], (done / kStages) & 1, kWaitNs);
-    }
+    if (lane == 0 && *abort)
+      for (int st = 0; st < kStages; ++st)
+        if (last[st]) mbar_wait_bounded(last[st], (last_parity >> st) & 1, kWaitNs);
+    if (Q_TMA && lane == 0 && *abort && q_loads > 0) mbar_wait_bounded(&s.q_full, (q_loads - 1) & 1, kWaitNs);
     __syncwarp();
-  } else if (warp == kQWarp) {
+  } else if (warp == kCleanWarp) {
+    // V of the mixed tiles: see the head of this file
     bool go = true;
+    uint32_t seen_mixed = 0;  // phases by stage
     for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
       const Raw now = raw;
       raw = load_raw(a, next_item(item), items);
       if (!take_item(a, item, nx, now, w, bad)) continue;
       ++count;
-      if (lane == 0 && count > 1) go = wait(&s.q_empty, count & 1, abort);  // completion count - 1
-      go = __shfl_sync(0xffffffffu, go, 0);
-      if (!go) break;
-      if constexpr (Q_TMA) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&s.q_full, static_cast<uint32_t>((w.two ? 2 : 1) * qpt * a.G * D * 2));
-          for (int t = 0; t < (w.two ? 2 : 1); ++t)
-            for (int hd = 0; hd < NH; ++hd) tma_load_3d(s.q[t][hd], &tq, &s.q_full, hd * 64, w.h * a.G, w.q0 + w.i0 + t * qpt);
-        }
-      } else {
-        for (int rr = lane; rr < min(w.queries, 2 * qpt) * a.G; rr += 32) {
-          const int i = rr / a.G, g = rr - i * a.G, t = i >= qpt, row = (i - t * qpt) * a.G + g;
-          const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs;
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = static_cast<uint32_t>(q[c * 8 + 2 * e]) | static_cast<uint32_t>(q[c * 8 + 2 * e + 1]) << 16;
-            *reinterpret_cast<uint4*>(&s.q[t][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
+      for (int j = w.j0; j < w.j1; ++j) {
+        if (!mixed_tile(w, j)) continue;
+        const uint32_t st = (tiles + static_cast<uint32_t>(j - w.j0)) % kStages;
+        go = __all_sync(0xffffffffu, wait(&s.v_mixed[st], (seen_mixed >> st) & 1, abort));
+        if (!go) break;
+        seen_mixed ^= 1u << st;
+        if (look_over<D>(a, w, j, s.v[st][0], lane)) *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) = count;
         fence_proxy_async_smem();
-        mbar_arrive(&s.q_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.v_clean[st]);
       }
-      __syncwarp();
+      tiles += static_cast<uint32_t>(w.j1 - w.j0);
     }
-    if (Q_TMA && lane == 0 && *abort && count > 0) mbar_wait_bounded(&s.q_full, (count - 1) & 1, kWaitNs);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // The whole warp walks, and one thread of it issues: addresses and descriptors that the compiler
@@ -535,13 +638,39 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     // the warp's answer: every lane waits
     const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, abort)) != 0; };
     bool ok = true;
-    uint32_t cleaned = 0, p_seen[2] = {0, 0}, o_used[2] = {0, 0};
-    for (int item = blockIdx.x; ok && item < items; item = next_item(item)) {
-      const Raw now = raw;
-      raw = load_raw(a, next_item(item), items);
-      if (!take_item(a, item, nx, now, w, bad)) continue;
-      const int n = __shfl_sync(0xffffffffu, w.j1 - w.j0, 0);
-      const bool two = __shfl_sync(0xffffffffu, static_cast<int>(w.two), 0) != 0;
+    uint32_t seen_clean = 0, seen_full = 0;  // phases by stage
+    uint32_t p_seen[2] = {0, 0}, o_used[2] = {0, 0};
+    // the next item with work, one item ahead of its products; the softmax groups take it from here
+    int item = blockIdx.x;
+    int n_next = 0, c0_next = 0, c1_next = 0, c2_next = 0;
+    bool two_next = false;
+    const auto publish = [&](int k) {  // the k-th (from 0)
+      Item next;
+      next.two = false;
+      next.j0 = next.c0 = next.c1 = next.c2 = 0;
+      bool have = false;
+      while (!have && item < items) {
+        const Raw now = raw;
+        const int cur = item;
+        item = next_item(item);
+        raw = load_raw(a, item, items);
+        have = take_item(a, cur, nx, now, next, bad);
+      }
+      if (!have) next.r = -1;
+      if (one) {
+        s.items[k % kItems] = next;
+        mbar_arrive(&s.item_full[k % kItems]);
+      }
+      __syncwarp();
+      // what the products need of it: tiles (-1: no more items), and which of them are mixed
+      n_next = __shfl_sync(0xffffffffu, have ? next.j1 - next.j0 : -1, 0);
+      two_next = __shfl_sync(0xffffffffu, static_cast<int>(next.two), 0) != 0;
+      c0_next = next.c0 - next.j0, c1_next = next.c1 - next.j0, c2_next = next.c2 - next.j0;
+    };
+    publish(0);
+    while (ok && n_next >= 0) {
+      const int n = n_next, c0 = c0_next, c1 = c1_next, c2 = c2_next;
+      const bool two = two_next;
       ok = wait_all(&s.q_full, count & 1);
       ++count;
       uint32_t st = __shfl_sync(0xffffffffu, tiles & 1, 0);
@@ -554,10 +683,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         commit(&s.k_empty[st]);
       }
       if (n <= 1) commit(&s.q_empty);
+      publish(count);  // while the softmax groups have their first tile
       for (int j = 0; ok && j < n; ++j, ++tiles, st ^= 1) {
         const bool more = j + 1 < n;
-        ok = wait_all(&s.v_full[st], (tiles >> 1) & 1);
-        if (ok && mixed_tile(w, w.j0 + j)) ok = wait_all(&s.v_clean, cleaned++ & 1);
+        if (j >= c0 && (j < c1 || j >= c2)) {
+          ok = wait_all(&s.v_clean[st], (seen_clean >> st) & 1);
+          seen_clean ^= 1u << st;
+        } else {
+          ok = wait_all(&s.v_full[st], (seen_full >> st) & 1);
+          seen_full ^= 1u << st;
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || (t == 1 && !two)) break;
@@ -591,12 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    Item w;
-    bool bad;
-    Raw raw = load_raw(a, blockIdx.x, items);
-    int count = 0;
-    uint32_t tiles = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    int count = 0;  // items so far
     const int t = warp >> 2, row = tid & 127;
     const int qi = row / a.G, gi = row - qi * a.G;
     const int i = t * qpt + qi;  // query of the item
@@ -605,19 +736,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint64_t sl2x2 = pair2(a.sl2);
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item = next_item(item)) {
-      const Raw now = raw;
-      raw = load_raw(a, next_item(item), items);
-      if (!take_item(a, item, nx, now, w, bad)) continue;
+    while (true) {
+      ok = __all_sync(0xffffffffu, wait(&s.item_full[count % kItems], (count / kItems) & 1, abort));
+      if (!ok) break;
+      const Item& w = s.items[count % kItems];  // stays until the group is two items further
+      if (w.r < 0) break;
       ++count;
-      const uint32_t tile_base = tiles;
-      tiles += static_cast<uint32_t>(w.j1 - w.j0);
       if (t == 1 && !w.two) continue;
       const bool have = qi < qpt && i < w.queries;
       const int p = w.p_first + min(i, w.queries - 1);
       float m = -INFINITY, l = 0.0f;
       for (int j = w.j0; j < w.j1; ++j) {
-        const uint32_t tile = tile_base + static_cast<uint32_t>(j - w.j0), st = tile % kStages;
         ok = __all_sync(0xffffffffu, wait(&s.s_full[t], s_seen++ & 1, abort));
         if (!ok) break;
         tc_fence_after();
@@ -629,43 +758,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_ld_dep(x[2]);
         tmem_ld_dep(x[3]);
         if (mixed_tile(w, j)) {
-          const int left = w.blocks * a.b - j * kKeys;           // columns that the list has
-          const int cut = w.sink_blocks * a.b - j * kKeys;       // columns of the first tokens' blocks
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t in_sink = low_bits(cut - c * 32);
-            const uint32_t bits = low_bits(left - c * 32) & ((seen_bits(a, p, j * kKeys, c * 32) & in_sink) |
-                                                             (seen_bits(a, p, w.win_block * a.b - cut, c * 32) & ~in_sink));
+            const uint32_t bits = tile_bits(a, w, j, p, c * 32);
+            // a warp's rows are a few queries, so most of its 32-column pieces are whole
+            if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) continue;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(bits >> e & 1)) x[c][e] = __float_as_uint(-INFINITY);
-          }
-          // V: see the head of this file
-          ok = wait(&s.v_full[st], (tile / kStages) & 1, abort);
-          bool odd = false;
-          if (ok)
-            for (int y = t * 128 + row; y < kKeys * (D / 8); y += w.two ? 256 : 128) {
-              const int col = y / (D / 8), c = y % (D / 8);
-              uint4* const at = reinterpret_cast<uint4*>(&s.v[st][c >> 3][col * 128 + (((c & 7) ^ (col & 7)) << 4)]);
-              const int tk = token_of(a, w, j, col);
-              // the positions from the item's first to its last that see the token
-              const bool any = col < left && tk <= w.p_last && (a.window == 0 || tk > w.p_first - a.window || tk < a.sinks);
-              if (!any) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 v = *at;
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
-              }
-            }
-          if (odd) *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) = count;
-          fence_proxy_async_smem();
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive(&s.v_clean);
-            if (!w.two) mbar_arrive(&s.v_clean);  // for the other group
           }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -707,13 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
           tmem_st32(ts + c * 32, pk);
         }
-        float a0, a1;
-        unpair(add2(sum[0], sum[1]), a0, a1);
-        l += a0 + a1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[t]);
+        float a0, a1;
+        unpair(add2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
       }
       if (!ok) break;
       const bool empty = w.j0 == w.j1;  // a part without tiles
@@ -732,40 +832,46 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (!empty) {
         const float inv = to_row.part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-        const bool vec = (reinterpret_cast<uintptr_t>(to_row.out) & 15) == 0;
+        const uint32_t align = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to_row.out));
+        uint32_t o[D / 32][32];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32_issue(to + c * 32, o);
-          tmem_wait_ld(o);
-          if (c == D / 32 - 1) {  // the next item may use O
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.o_empty[t]);
-          }
-          if (!write) continue;
-          if (to_row.part) {
+        for (int c = 0; c < D / 32; ++c) tmem_ld32_issue(to + c * 32, o[c]);
+        tmem_wait_ld(o[0]);
+#pragma unroll
+        for (int c = 1; c < D / 32; ++c) tmem_ld_dep(o[c]);
+        tc_fence_before();  // the next item may use O
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_empty[t]);
+        if (write && to_row.part) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            continue;
-          }
-          uint32_t y[16];
+              reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]);
+        } else if (write) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (vec) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t y[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(to_row.out + c * 32 + e * 8) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          } else {
+            for (int e = 0; e < 16; ++e)
+              y[e] = pack_bf16(__uint_as_float(o[c][2 * e]) * inv, __uint_as_float(o[c][2 * e + 1]) * inv);
+            if ((align & 31) == 0) {
+              st_global_32(to_row.out + c * 32, y);
+              st_global_32(to_row.out + c * 32 + 16, y + 8);
+            } else if ((align & 15) == 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              to_row.out[c * 32 + 2 * e] = static_cast<uint16_t>(y[e]);
-              to_row.out[c * 32 + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(to_row.out + c * 32 + e * 8) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                to_row.out[c * 32 + 2 * e] = static_cast<uint16_t>(y[e]);
+                to_row.out[c * 32 + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
+              }
             }
           }
         }
-        if (again && !marked) rows_plainly<D>(a, w, t, warp & 3, lane);
+        if (again && !marked) rows_plainly<D>(a, s.items[(count - 1) % kItems], t, warp & 3, lane);
       }
     }
   }
