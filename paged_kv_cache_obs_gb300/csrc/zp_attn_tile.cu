@@ -43,7 +43,7 @@ constexpr int kKWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;         // two softmax groups, and a group of the other roles
 constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLazy = 8.0f;
+constexpr float kLazy = 24.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
 constexpr int kFlags = 8;             // items that roles can be apart, and more
 
