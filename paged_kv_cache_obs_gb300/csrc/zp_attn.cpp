@@ -66,7 +66,7 @@ using namespace zp;
 
 extern "C" size_t zp_kv8_decode_workspace_size(const zp_params* p, int32_t B, int32_t max_blocks) {
   if (!sizes_ok(p, B, max_blocks)) return 0;
-  return split_plan(p, true, B, 1, max_blocks, 0, 0).bytes;
+  return split_plan(p, B, 1, max_blocks, 0, 0).bytes;
 }
 
 extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
@@ -86,7 +86,7 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
   a.scales = pool->scales;
   a.T = B;
   a.max_q = 1;
-  return split_launch(a, p, true, split_plan(p, true, B, 1, max_blocks, window, sinks), workspace,
+  return split_launch(a, p, true, split_plan(p, B, 1, max_blocks, window, sinks), workspace,
                       reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -95,7 +95,7 @@ extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, 
   if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
   if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
     return tile_plan(p, T, B, max_q, max_blocks, window, sinks).bytes;
-  return split_plan(p, false, B, max_q, max_blocks, window, sinks).bytes;
+  return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
 }
 
 extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
@@ -119,7 +119,7 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   a.max_q = max_q;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
-    return split_launch(a, p, false, split_plan(p, false, B, max_q, max_blocks, window, sinks), workspace, st);
+    return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks), workspace, st);
   }
   return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks), workspace, st);
 }

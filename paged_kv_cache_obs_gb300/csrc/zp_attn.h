@@ -32,7 +32,7 @@ struct SplitPlan {
   int splits, cluster;
   size_t bytes;
 };
-SplitPlan split_plan(const zp_params* p, bool fp8, int B, int max_q, int max_blocks, int window, int sinks);
+SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks);
 
 // Launches the split kernel (and the one that joins its parts).
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st);

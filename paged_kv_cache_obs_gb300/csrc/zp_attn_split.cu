@@ -188,13 +188,18 @@ struct Shape {
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = kTile * RB;                 // bytes of K (or V) of a tile
   static constexpr int SUB = RB <= 64 ? 2 : 1;            // tiles that a warp takes at a time
-  static constexpr int STAGES = 2;
-  static constexpr int STAGE = SUB * 2 * TILE;            // [tile][K|V]
-  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int HALF = SUB * TILE;                 // K or V of what a warp takes at a time
+  // A warp's ring has slots of K and V together (one wait for both); but rows of 256 bytes in three
+  // slots of K or V, which leaves room for a fourth CTA on the SM (64 requests with a window of 1024:
+  // 50 -> 44 us; with E4M3 rows the further waits cost 5 %).
+  static constexpr bool JOINT = RB < 256 || NT == 2;
+  static constexpr int SLOTS = JOINT ? 2 : 3;
+  static constexpr int SLOT = (JOINT ? 2 : 1) * HALF;
+  static constexpr int RING = kWarps * SLOTS * SLOT;
   static constexpr int ACC = kWarps * ROWS * D * 4;       // the warps' sums, in the ring's place
   static constexpr int SMEM = (RING > ACC ? RING : ACC) + 1024;
   // CTAs of an SM: what shared memory and, with 16 rows, registers hold
-  static constexpr int CTAS = NT == 2 ? (D == 128 ? 2 : 3) : RB <= 128 ? 4 : 3;
+  static constexpr int CTAS = NT == 2 ? (D == 128 ? 2 : 3) : 4;
 };
 
 // Where 16-byte chunk `ch` of a row's sums stands: spread so that neither the warps' writes nor the
@@ -208,13 +213,13 @@ __device__ __forceinline__ int acc_at(int row, int ch) {
 template <bool FP8, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<FP8, D, NT>;
-  constexpr int ROWS = Sh::ROWS, RB = Sh::RB, STAGES = Sh::STAGES, TILE = Sh::TILE, SUB = Sh::SUB;
+  constexpr int ROWS = Sh::ROWS, RB = Sh::RB, SLOTS = Sh::SLOTS, TILE = Sh::TILE, SUB = Sh::SUB;
   constexpr int KC = RB / 64;                  // 16-byte chunks of a key that a lane holds
   constexpr int KS = D / 16;                   // k-steps of S
   constexpr int MT = D / 16;                   // 16-dim row tiles of O^T
   constexpr int VW = RB / 32;                  // words of a value row that a lane holds: 2, 4 or 8
   __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS], cta_m[ROWS], cta_l[ROWS];
-  __shared__ __align__(8) uint64_t full[kWarps][STAGES];
+  __shared__ __align__(8) uint64_t full[kWarps][SLOTS];
   __shared__ int sm_bad;
   extern __shared__ uint8_t dyn[];
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 
   if (tid == 0) sm_bad = 0;
   if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+    for (int i = 0; i < SLOTS; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
   if (tid == 0) prefetch_tensormap(&tm);
@@ -280,33 +285,37 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
     if (n & 1) kscale[1] = x, vscale[1] = y;
     else kscale[0] = x, vscale[0] = y;
   };
-  uint8_t* const my_ring = ring + warp * (STAGES * Sh::STAGE);
+  uint8_t* const my_ring = ring + warp * (SLOTS * Sh::SLOT);
   // The pool is the tensor {d, 2 Hkv b rows, layers * blocks}: K rows of head h start at h b, V rows
   // at (Hkv + h) b.
-  const auto issue = [&](int i, int st) {
+  // What fills slot after slot: fill n is group n, or K (n even) or V of group n / 2.
+  constexpr int FILLS = Sh::JOINT ? 1 : 2;  // of a group
+  const auto issue = [&](int n, int slot) {
+    const int i = n / FILLS;
     int id[SUB];
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub)
       id[sub] = __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? phys[1] : phys[0], (i % BATCH) * SUB + sub);
     if (lane == 0) {
-      uint64_t* const bar = &full[warp][st];
-      const bool all = tile_of(i, SUB - 1) < 1 << 30;  // the list's last group may be short
-      mbar_arrive_expect_tx(bar, (all ? SUB : 1) * 2 * TILE);
+      uint64_t* const bar = &full[warp][slot];
+      const bool all = SUB == 1 || tile_of(i, SUB - 1) < 1 << 30;  // the list's last group may be short
+      mbar_arrive_expect_tx(bar, (all ? SUB : 1) * (2 / FILLS) * TILE);
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub) {
         if (sub > 0 && !all) break;
-        uint8_t* const k = my_ring + st * Sh::STAGE + sub * 2 * TILE;
-        const int row = h * a.b + (tile_of(i, sub) & ((1 << bshift) - 1)) * kTile;
+        const int row = h * a.b + (bshift ? (tile_of(i, sub) & 1) * kTile : 0), z = static_cast<int>(layer_base) + id[sub];
 #pragma unroll
-        for (int hd = 0; hd < (RB > 128 ? 2 : 1); ++hd) {
-          tma_load_3d(k + hd * kTile * 128, &tm, bar, hd * 64, row, static_cast<int>(layer_base) + id[sub]);
-          tma_load_3d(k + TILE + hd * kTile * 128, &tm, bar, hd * 64, a.Hkv * a.b + row, static_cast<int>(layer_base) + id[sub]);
+        for (int kv = 0; kv < 2 / FILLS; ++kv) {
+          uint8_t* const to = my_ring + slot * Sh::SLOT + kv * Sh::HALF + sub * TILE;
+          const int r0 = (Sh::JOINT ? kv : n & 1) ? a.Hkv * a.b + row : row;
+#pragma unroll
+          for (int hd = 0; hd < (RB > 128 ? 2 : 1); ++hd) tma_load_3d(to + hd * kTile * 128, &tm, bar, hd * 64, r0, z);
         }
       }
     }
   };
   load_ids(0);
-  for (int i = 0; i < STAGES && i < todo; ++i) issue(i, i);
+  for (int n = 0; n < SLOTS && n < FILLS * todo; ++n) issue(n, n);
   load_scales(0);
 
   // queries as B fragments: column (row of the output) nt*8 + g
@@ -375,10 +384,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   const int p_last = s.p0 + s.n - 1;
   float vref = 0.0f, vinv = 0.0f;  // FP8: V scale that o is in units of, and its inverse
   bool ok = true;
-  int i = 0;
-  uint32_t phase = 0;  // of the ring's current round
-  for (; i < todo; ++i) {
-    const int st = i & (STAGES - 1);
+  int fill = 0, slot = 0;  // the fill that comes next, and its slot
+  uint32_t phase = 0;      // of the ring's current round
+  // waits for it, and what follows its last use
+  const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][slot], phase, kWaitNs)) != 0; };
+  const auto used = [&] {
+    __syncwarp();  // every lane has read it
+    if (fill + SLOTS < FILLS * todo) issue(fill + SLOTS, slot);
+    ++fill;
+    if (++slot == SLOTS) slot = 0, phase ^= 1;
+  };
+  for (int i = 0; i < todo; ++i) {
     if (i % BATCH == 0 && i + BATCH < todo) load_ids(i / BATCH + 1);
     if (i % BATCH == BATCH / 4 && i - BATCH / 4 + BATCH < todo) load_scales(i / BATCH + 1);
     float ks[SUB], vs[SUB];
@@ -388,10 +404,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
       ks[sub] = FP8 ? __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? kscale[1] : kscale[0], src) : 1.0f;
       vs[sub] = FP8 ? __shfl_sync(0xffffffffu, ((i / BATCH) & 1) ? vscale[1] : vscale[0], src) : 1.0f;
     }
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][st], phase, kWaitNs));
+    ok = arrived();
     if (!ok) break;
-    if (st == STAGES - 1) phase ^= 1;
-    const uint32_t buf = smem_u32(my_ring + st * Sh::STAGE);
+    const uint32_t kbuf = smem_u32(my_ring + slot * Sh::SLOT);
 
     // S^T, tokens of rows g and g + 8 of each tile's product
     float x[SUB][NT][4];
@@ -399,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
     for (int sub = 0; sub < SUB; ++sub) {
 #pragma unroll
       for (int j = 0; j < KC; ++j) {
-        const uint4 k0 = lds16(buf + sub * 2 * TILE + chunk_at<RB>(token_at(g), c + 4 * j));
-        const uint4 k1 = lds16(buf + sub * 2 * TILE + chunk_at<RB>(token_at(g) + 8, c + 4 * j));
+        const uint4 k0 = lds16(kbuf + sub * TILE + chunk_at<RB>(token_at(g), c + 4 * j));
+        const uint4 k1 = lds16(kbuf + sub * TILE + chunk_at<RB>(token_at(g) + 8, c + 4 * j));
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int w = 0; w < (FP8 ? 4 : 2); ++w) {
@@ -420,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         }
       }
     }
+    if constexpr (!Sh::JOINT) used();
     // tokens seen by every row, or row by row
     bool full_sub[SUB], none[SUB];
     int t0[SUB];
@@ -483,10 +499,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           l[nt][e & 1] += x[sub][nt][e];
         }
       }
+    if constexpr (!Sh::JOINT) {
+      ok = arrived();
+      if (!ok) break;
+    }
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub) {
       if (none[sub]) continue;
-      const uint32_t vbuf = buf + sub * 2 * TILE + TILE;
+      const uint32_t vbuf = smem_u32(my_ring + slot * Sh::SLOT + (Sh::JOINT ? Sh::HALF : 0)) + sub * TILE;
       // V of contraction indices 2c, 2c+1, 2c+8, 2c+9
       uint32_t vr[4][VW];
 #pragma unroll
@@ -618,14 +638,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
-    if (i + STAGES < todo) issue(i + STAGES, st);
+    used();
   }
   if (!ok) {
     // copies still in flight after a failed wait land (bounded) before the ring is used again
-    for (int k = i; k < min(todo, i + STAGES); ++k) {
-      mbar_wait_bounded(&full[warp][k & (STAGES - 1)], phase, kWaitNs);
-      if ((k & (STAGES - 1)) == STAGES - 1) phase ^= 1;
+    for (int n = fill; n < min(FILLS * todo, fill + SLOTS); ++n) {
+      mbar_wait_bounded(&full[warp][slot], phase, kWaitNs);
+      if (++slot == SLOTS) slot = 0, phase ^= 1;
     }
     if (lane == 0) atomicCAS(a.err, 0, ZP_ERR_TIMEOUT);
   }
@@ -786,7 +805,7 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // costs about 5 us of an SM's slot in latencies (224 requests of 1 to 2048 tokens, 8 kv heads: 90 us
 // unsplit, 106 us with 2, 139 us with 4), while 4 requests of 100 to 500 tokens take 6.9 us with 4
 // splits and 10.3 us unsplit.
-SplitPlan split_plan(const zp_params* p, bool fp8, int B, int max_q, int max_blocks, int window, int sinks) {
+SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks) {
   constexpr int64_t kSms = 152;
   SplitPlan s{};
   s.rows = p->num_q_heads / p->num_kv_heads * max_q <= 8 ? 8 : 16;
@@ -797,7 +816,7 @@ SplitPlan split_plan(const zp_params* p, bool fp8, int B, int max_q, int max_blo
     tiles = std::min(tiles, seen);
   }
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
-  const int64_t wave = kSms * (s.rows == 16 ? 2 : fp8 ? 4 : 3) * 7 / 8;
+  const int64_t wave = kSms * (s.rows == 16 ? 2 : 4) * 7 / 8;
   const int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
   s.splits = n >= 8 ? static_cast<int>(n / 8 * 8) : s.cluster;
