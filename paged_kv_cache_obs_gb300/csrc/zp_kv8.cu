@@ -16,7 +16,7 @@
 namespace zp {
 namespace {
 
-constexpr int kWarpsQ = 8;
+constexpr int kWarpsQ = 4;
 constexpr int kThreadsQ = kWarpsQ * 32;
 
 __device__ __forceinline__ void record(int32_t* err, int code) { atomicCAS(err, 0, code); }
@@ -141,8 +141,10 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
 // n / b + 1 blocks after it.  A warp there finds its request by searching token_start, 32 probes at
 // a time, and the host needs no per-request sizes: T / b + 2 B slots in all.  Grid (slot, group
 // of kWarpsQ tiles); a warp takes one (K|V, head) tile of the slot's block.
+// Registers are held to 10 CTAs an SM (5 with 32 x 128 tiles): the chains of dependent loads need the
+// warps (8200 prompt tokens: 10.7 us so, 11.6 with the compiler's choice of 64 registers).
 template <int D, int BS, bool VEC>
-__global__ void __launch_bounds__(kThreadsQ) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreadsQ, BS * D == 4096 ? 5 : 10) append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;                 // lanes per row (8 values each)
   constexpr int RPL = 32 / LPR;              // rows per load of the warp
   constexpr int NL = BS / RPL;               // loads per tile
@@ -296,24 +298,38 @@ __global__ void __launch_bounds__(kThreadsQ) pack_kernel(const BlockArgs a) {
   if (lane == 0) a.scales[dst] = s;
 }
 
-template <int D, int BS>
+// WIDE: the bf16 pool stands on 32-byte boundaries, and a lane writes its 16 values at once.
+template <int D, int BS, bool WIDE>
 __global__ void __launch_bounds__(kThreadsQ) unpack_kernel(const BlockArgs a) {
-  constexpr int NL = BS * D / 256;
+  constexpr int NL = BS * D / 512;  // loads of 16 codes a lane
   const int lane = threadIdx.x & 31;
   int64_t src, dst;
   int fill;
   if (!take_tile(a, static_cast<int64_t>(blockIdx.x) * kWarpsQ + (threadIdx.x >> 5), BS, src, dst, fill)) return;
-  const uint2* const codes = reinterpret_cast<const uint2*>(a.src + src * (BS * D)) + lane;
-  uint4* const y = reinterpret_cast<uint4*>(a.dst + dst * (BS * D * 2)) + lane;
-  uint2 w[NL];
+  const uint4* const codes = reinterpret_cast<const uint4*>(a.src + src * (BS * D)) + lane;
+  uint8_t* const y = a.dst + dst * (BS * D * 2) + lane * 32;
+  uint4 w[NL];
 #pragma unroll
   for (int l = 0; l < NL; ++l) w[l] = codes[l * 32];
   const float s = a.scales[src];
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
-    const float2 e0 = dec2(w[l].x & 0xFFFFu), e1 = dec2(w[l].x >> 16), e2 = dec2(w[l].y & 0xFFFFu), e3 = dec2(w[l].y >> 16);
-    y[l * 32] = make_uint4(pack2(e0.x * s, e0.y * s), pack2(e1.x * s, e1.y * s), pack2(e2.x * s, e2.y * s),
-                           pack2(e3.x * s, e3.y * s));
+    const uint32_t c[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 lo = dec2(c[e] & 0xFFFFu), hi = dec2(c[e] >> 16);
+      v[2 * e] = pack2(lo.x * s, lo.y * s);
+      v[2 * e + 1] = pack2(hi.x * s, hi.y * s);
+    }
+    if constexpr (WIDE) {
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + l * 1024), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+    } else {
+      *reinterpret_cast<uint4*>(y + l * 1024) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(y + l * 1024 + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
@@ -342,7 +358,8 @@ void launch_append(const AppendArgs& a, bool vec, dim3 grid, cudaStream_t st) {
 template <int D, int BS>
 void launch_blocks(const BlockArgs& a, bool pack, unsigned grid, cudaStream_t st) {
   if (pack) pack_kernel<D, BS><<<grid, kThreadsQ, 0, st>>>(a);
-  else unpack_kernel<D, BS><<<grid, kThreadsQ, 0, st>>>(a);
+  else if (aligned(a.dst, 32)) unpack_kernel<D, BS, true><<<grid, kThreadsQ, 0, st>>>(a);
+  else unpack_kernel<D, BS, false><<<grid, kThreadsQ, 0, st>>>(a);
 }
 
 zp_status convert(const zp_kv_pool* pool, const zp_kv8_pool* kv8, bool pack, const int32_t* src_ids, const int32_t* fill,
