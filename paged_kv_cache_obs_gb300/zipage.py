@@ -361,17 +361,38 @@ def _rows(t):
 
 def _row_bytes(t):
     ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError("the last dimension of rows must be contiguous")
+    if es != 1 or t.dtype is not torch.bfloat16:
+        raise ValueError("rows are bf16 and their last dimension is contiguous")
     return _pack_rows(t.data_ptr(), ts, hs)
+
+
+def _i32(t):
+    """Address of a device int32 array."""
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError("tables, lengths, positions and block ids are contiguous int32 tensors")
+    return t.data_ptr()
+
+
+def _pool(pool):
+    """(address, number of blocks) of a bf16 pool."""
+    if pool.dtype is not torch.bfloat16 or not pool.is_contiguous():
+        raise ValueError("the pool is a contiguous bf16 tensor")
+    return pool.data_ptr(), pool.size(1)
+
+
+def _kv8(codes, scales):
+    """(address of the codes, address of the scales, number of blocks) of an 8-bit pool."""
+    if codes.element_size() != 1 or scales.dtype is not torch.float32 or not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes are one byte a value and scales fp32, both contiguous")
+    return codes.data_ptr(), scales.data_ptr(), codes.size(1)
 
 
 def _stream_of(t, stream):
     """The stream to launch on: the given one, or the current one of the tensor's device, which has to
     be the current device (the library launches there)."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors have to be on the current CUDA device")
     return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
@@ -405,14 +426,10 @@ def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream
     if k is not None:
         rk, hk = _row_bytes(k), k.size(1)
         ok = rk if k_out is None else _row_bytes(k_out)
-    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, positions.data_ptr(), positions.size(0),
+    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, _i32(positions), positions.size(0),
                      _stream_of(positions, stream))
     if st:
         _check("zp_rope_apply", st)
-
-
-def _kv8_bytes(codes, scales):
-    return _pack_kv8(codes.data_ptr(), scales.data_ptr(), codes.size(1))
 
 
 def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_tables, params, workspace, stream=None):
@@ -420,8 +437,8 @@ def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_ta
     (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
     token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
     p = _params(params)
-    st = _kv8_append(_kv8_bytes(codes, scales), layer, _row_bytes(k), _row_bytes(v), k.size(0), token_start.data_ptr(),
-                     cached.data_ptr(), cached.size(0), block_tables.data_ptr(), block_tables.size(1), _addr(p),
+    st = _kv8_append(_pack_kv8(*_kv8(codes, scales)), layer, _row_bytes(k), _row_bytes(v), k.size(0), _i32(token_start),
+                     _i32(cached), cached.size(0), _i32(block_tables), block_tables.size(1), _addr(p),
                      workspace.data_ptr(), workspace.nbytes, _stream_of(codes, stream))
     if st:
         _check("zp_kv8_append", st)
@@ -432,10 +449,9 @@ def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace,
     """Blocks src_ids of the bf16 pool into blocks dst_ids of the 8-bit pool.  fill: optional device
     int32 [n] of tokens per block; layers: optional (layer_begin, layer_count)."""
     lb, lc = layers if layers is not None else (0, 0)
-    st = lib.zp_kv8_pack_blocks(zp_kv_pool(pool.data_ptr(), pool.shape[1]), _ptr(src_ids), _ptr(fill),
-                                zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1]), _ptr(dst_ids),
-                                src_ids.shape[0], lb, lc, _params(params), _ptr(workspace), workspace.nbytes,
-                                _stream_of(codes, stream))
+    st = lib.zp_kv8_pack_blocks(zp_kv_pool(*_pool(pool)), _i32(src_ids), None if fill is None else _i32(fill),
+                                zp_kv8_pool(*_kv8(codes, scales)), _i32(dst_ids), src_ids.size(0), lb, lc, _params(params),
+                                workspace.data_ptr(), workspace.nbytes, _stream_of(codes, stream))
     _check("zp_kv8_pack_blocks", st)
 
 
@@ -443,9 +459,9 @@ def zp_kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, params, workspac
                          stream=None):
     """Blocks src_ids of the 8-bit pool into blocks dst_ids of the bf16 pool."""
     lb, lc = layers if layers is not None else (0, 0)
-    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1]), _ptr(src_ids),
-                                  zp_kv_pool(pool.data_ptr(), pool.shape[1]), _ptr(dst_ids), src_ids.shape[0], lb, lc,
-                                  _params(params), _ptr(workspace), workspace.nbytes, _stream_of(codes, stream))
+    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(*_kv8(codes, scales)), _i32(src_ids), zp_kv_pool(*_pool(pool)),
+                                  _i32(dst_ids), src_ids.size(0), lb, lc, _params(params), workspace.data_ptr(),
+                                  workspace.nbytes, _stream_of(codes, stream))
     _check("zp_kv8_unpack_blocks", st)
 
 
@@ -458,7 +474,7 @@ def zp_kv8_decode_attn(codes, scales, layer: int, q, block_tables, seq_lens, out
     """Decode attention over the 8-bit pool: q, out bf16 [B, H_q, d]; a request sees its last
     `window` tokens and the first `sinks` (window 0: all)."""
     p = _params(params)
-    st = _kv8_decode_attn(_kv8_bytes(codes, scales), layer, _row_bytes(q), block_tables.data_ptr(), seq_lens.data_ptr(),
+    st = _kv8_decode_attn(_pack_kv8(*_kv8(codes, scales)), layer, _row_bytes(q), _i32(block_tables), _i32(seq_lens),
                           q.size(0), block_tables.size(1), window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(),
                           workspace.nbytes, _stream_of(codes, stream))
     if st:
@@ -475,8 +491,8 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
     last tokens in the cache) over the bf16 pool, with a window and `sinks` first tokens that stay
     visible.  max_q: the most new tokens of a request."""
     p = _params(params)
-    st = _paged_window_attn(_pack_pool(pool.data_ptr(), pool.size(1)), layer, _row_bytes(q), q_start.data_ptr(), q.size(0),
-                            max_q, block_tables.data_ptr(), seq_lens.data_ptr(), seq_lens.size(0), block_tables.size(1),
+    st = _paged_window_attn(_pack_pool(*_pool(pool)), layer, _row_bytes(q), _i32(q_start), q.size(0), max_q,
+                            _i32(block_tables), _i32(seq_lens), seq_lens.size(0), block_tables.size(1),
                             window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(), workspace.nbytes,
                             _stream_of(pool, stream))
     if st:

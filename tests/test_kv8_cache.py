@@ -92,6 +92,31 @@ def test_block_conversion_refuses(zp, pack):
     assert call(n=0, src=None, dst=None) == zp.ZP_OK
 
 
+def test_binding_refuses_what_it_would_misread(zp):
+    """Types, layouts and places of tensors that the library could not tell from good ones."""
+    bf = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    i32, i64 = torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)
+    pool = torch.zeros((1, 4, 2, 2, 16, 64), dtype=torch.bfloat16)
+    codes, scales = torch.zeros(pool.shape, dtype=torch.uint8), torch.zeros((1, 4, 2, 2))
+    tables, ws = torch.zeros((4, 6), dtype=torch.int32), torch.zeros(1024, dtype=torch.uint8)
+    p = _params(2, 64, 16)
+    rope = zp.zp_rope_init(64, 64, 1e4)
+    for call in (lambda: zp.zp_rope_apply(rope, bf.half(), None, i32), lambda: zp.zp_rope_apply(rope, bf, None, i64),
+                 lambda: zp.zp_rope_apply(rope, bf, None, i32),    # not on a CUDA device
+                 lambda: zp.zp_kv8_append(pool, scales, 0, bf, bf, i32, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales.half(), 0, bf, bf, i32, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32, i32, tables[:, :3], p, ws),
+                 lambda: zp.zp_kv8_append(codes.transpose(2, 3), scales, 0, bf, bf, i32, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_decode_attn(codes, scales, 0, bf, tables, i64, bf, p, ws),
+                 lambda: zp.zp_kv8_decode_attn(codes, scales, 0, bf, tables, i32, bf.float(), p, ws),
+                 lambda: zp.zp_paged_window_attn(codes, 0, bf, i32, tables, i32, bf, p, ws, 4, 1, 1),
+                 lambda: zp.zp_paged_window_attn(pool, 0, bf, i32, tables.t(), i32, bf, p, ws, 4, 1, 1),
+                 lambda: zp.zp_kv8_pack_blocks(pool, i64, codes, scales, i32, p, ws),
+                 lambda: zp.zp_kv8_unpack_blocks(codes, scales, i32, pool.float(), i32, p, ws)):
+        with pytest.raises(ValueError):
+            call()
+
+
 # ------------------------------------------------------------------ append (GPU) --------------
 
 class _Cache:
@@ -301,6 +326,28 @@ def test_pack_and_unpack_blocks(zp, Hkv, d, b):
     exact = val.float().to(torch.bfloat16)
     want[1:, dst] = exact[1:][:, src]
     assert torch.equal(out.cpu().nan_to_num(9.0), want.nan_to_num(9.0)) and zp.zp_read_error(ws) == 0
+
+
+@pytest.mark.gpu
+def test_unpack_to_a_pool_off_a_32_byte_boundary(zp):
+    # (and the same bits on one: 32-byte stores)
+    p = _params(2, 64, 16, 2)
+    rng = np.random.default_rng(2)
+    shape = (2, 4, 2, 2, 16, 64)
+    codes = torch.from_numpy(rng.integers(0, 255, shape).astype(np.uint8)).cuda()
+    scales = torch.full((2, 4, 2, 2), 0.25, device="cuda")
+    ids = torch.arange(4, dtype=torch.int32, device="cuda")
+    n = codes.numel()
+    buf = torch.full((n + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    outs = []
+    for off in (16, 8):
+        out = buf[off:off + n].view(shape)
+        zp.zp_kv8_unpack_blocks(codes, scales, ids, out, ids, p, zp.new_workspace(256))
+        assert bool((buf[:off] == 7).all()) and bool((buf[off + n:] == 7).all())
+        outs.append(out.clone())
+        buf.fill_(7.0)
+    want = torch.from_numpy(S.e4m3_decode(codes.cpu().numpy()) * 0.25).to(torch.bfloat16)
+    assert torch.equal(outs[0].nan_to_num(9.0), outs[1].nan_to_num(9.0)) and torch.equal(outs[0].cpu().nan_to_num(9.0), want.nan_to_num(9.0))
 
 
 @pytest.mark.gpu
