@@ -1,5 +1,6 @@
 // zp_attn.cpp — the entry points of decode attention over the 8-bit pool and of attention with a
 // sliding window: argument checks, workspace, and the choice of the kernel.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -7,6 +8,8 @@
 
 namespace zp {
 namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_rows* q, const zp_rows* out,
                 const int32_t* tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
@@ -16,7 +19,7 @@ zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_
   // (layer, block) is one 32-bit coordinate of the tensor map
   if (num_blocks >= INT_MAX / p->num_layers) return ZP_ERR_UNSUPPORTED;
   if (p->num_kv_heads <= 0 || p->num_q_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return ZP_ERR_INVALID_ARG;
-  if (!(p->scale > 0.0f) || !std::isfinite(p->scale)) return ZP_ERR_INVALID_ARG;
+  if (!(p->scale > 0.0f) || !std::isfinite(p->scale * kLog2e)) return ZP_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return ZP_ERR_UNSUPPORTED;
   if (p->block_size != 16 && p->block_size != 32) return ZP_ERR_UNSUPPORTED;
   if (p->num_q_heads / p->num_kv_heads > 16 || B > 65535 || p->num_kv_heads > 65535) return ZP_ERR_UNSUPPORTED;
@@ -50,13 +53,13 @@ AttnArgs args_of(const zp_params* p, int32_t layer, int64_t num_blocks, const zp
   const int most = max_blocks * p->block_size;
   a.window = window >= most ? 0 : window;
   a.sinks = sinks < most ? sinks : most;
-  a.sl2 = p->scale * 1.4426950408889634f;
+  a.sl2 = p->scale * kLog2e;
   return a;
 }
 
 bool sizes_ok(const zp_params* p, int32_t B, int32_t max_blocks) {
   return p && B >= 0 && max_blocks >= 1 && p->num_kv_heads > 0 && p->num_q_heads > 0 &&
-         p->num_q_heads % p->num_kv_heads == 0 && p->head_dim > 0 && p->block_size > 0;
+         p->num_q_heads % p->num_kv_heads == 0 && p->num_q_heads / p->num_kv_heads <= 16 && p->head_dim > 0 && p->block_size > 0;
 }
 
 }  // namespace
@@ -116,7 +119,8 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   a.pool = static_cast<const uint8_t*>(pool->base);
   a.q_start = q_start;
   a.T = T;
-  a.max_q = max_q;
+  // a request of more tokens than its blocks hold is refused by its length in any case
+  a.max_q = std::min(max_q, max_blocks * p->block_size);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
     return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks), workspace, st);

@@ -17,7 +17,7 @@
 // softmax, the tensor core multiplies for the other tile; the next item's first products start
 // while the last sums are still being written out.
 //
-// The running maximum is kept lazily (raised only when a logit passes it by more than 8 in
+// The running maximum is kept lazily (raised only when a logit passes it by more than 24 in
 // log2), so O is rescaled in TMEM rarely.  Sums and maxima are fp32; P is rounded to bf16 (off by
 // at most 2^-8 of itself), as the second product's operand type asks.
 //
@@ -45,7 +45,7 @@ constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLazy = 24.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
-constexpr int kFlags = 8;             // items that roles can be apart, and more
+constexpr int kFlags = 8;             // items: K's warp is at most 6 ahead of a softmax group (the ring's 3, 2 stages, one)
 
 // An item: which, and what it walks.
 struct Item {
@@ -59,7 +59,10 @@ struct Item {
   bool two;                // the second query tile has rows
 };
 
-constexpr int kItems = 4;             // ring of items that the MMA warp hands to the softmax groups
+// Ring of items that the MMA warp hands to the softmax groups.  A slot is taken again when both groups
+// are done with its item: the second group has no part in items of one query tile, so nothing else
+// would keep the others from running away from it while it writes a long item out.
+constexpr int kItems = 4;
 
 template <int D>
 struct __align__(1024) TileSmem {
@@ -68,7 +71,7 @@ struct __align__(1024) TileSmem {
   uint8_t v[kStages][D / 64][kKeys * 128];
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems], item_empty[kItems];
   uint32_t tmem;
   int abort;
   Item items[kItems];
@@ -444,7 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(&s.o_full[i], 1);
       mbar_init(&s.o_empty[i], 4);
     }
-    for (int i = 0; i < kItems; ++i) mbar_init(&s.item_full[i], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&s.item_full[i], 1);
+      mbar_init(&s.item_empty[i], 8);
+    }
     s.abort = 0;
     for (int i = 0; i < kFlags; ++i) s.bad[i] = s.redo[i] = 0;
     fence_mbar_init();
@@ -657,6 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         have = take_item(a, cur, nx, now, next, bad);
       }
       if (!have) next.r = -1;
+      if (k >= kItems) ok = wait_all(&s.item_empty[k % kItems], (k / kItems - 1) & 1);
+      if (!ok) return;
       if (one) {
         s.items[k % kItems] = next;
         mbar_arrive(&s.item_full[k % kItems]);
@@ -718,11 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
       }
     }
-    // products still in flight after a give-up complete before TMEM is released
-    if (!ok) {
-      commit(&s.drain);
-      mbar_wait_bounded(&s.drain, 0, kWaitNs);
-    }
+    // products still in flight after a give-up, of whichever role, complete before TMEM is released
+    commit(&s.drain);
+    mbar_wait_bounded(&s.drain, 0, kWaitNs);
     __syncwarp();
   }
   } else {
@@ -739,10 +745,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     while (true) {
       ok = __all_sync(0xffffffffu, wait(&s.item_full[count % kItems], (count / kItems) & 1, abort));
       if (!ok) break;
-      const Item& w = s.items[count % kItems];  // stays until the group is two items further
+      const Item& w = s.items[count % kItems];  // stays until every warp has let go of it
+      uint64_t* const let_go = &s.item_empty[count % kItems];
       if (w.r < 0) break;
       ++count;
-      if (t == 1 && !w.two) continue;
+      if (t == 1 && !w.two) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(let_go);
+        continue;
+      }
       const bool have = qi < qpt && i < w.queries;
       const int p = w.p_first + min(i, w.queries - 1);
       float m = -INFINITY, l = 0.0f;
@@ -873,6 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         if (again && !marked) rows_plainly<D>(a, s.items[(count - 1) % kItems], t, warp & 3, lane);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(let_go);
     }
   }
   tc_fence_before();
@@ -956,25 +969,24 @@ cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs&
   return cudaLaunchKernelEx(&cfg, tile_join_kernel<D>, a);
 }
 
-// Items of a call at most.
-int64_t items_of(const zp_params* p, int B, int max_q, int& nx) {
-  const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
-  nx = (max_q + per_item - 1) / per_item;
-  return static_cast<int64_t>(nx) * p->num_kv_heads * B;
-}
-
 }  // namespace
 
 TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks) {
   TilePlan plan{};
-  const int64_t items = items_of(p, B, max_q, plan.nx);
   int64_t tokens = static_cast<int64_t>(max_blocks) * p->block_size;
   const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
+  const auto items_of = [&](int64_t n) { return (n + per_item - 1) / per_item; };  // of a request and head with n queries
+  // max_q may be a loose bound: no request has more queries than the call, or than its blocks hold.
+  // Splits follow the bound alone, so that a workspace for many rows is enough for fewer.
+  const int64_t most = std::min<int64_t>(max_q, tokens), heads = static_cast<int64_t>(p->num_kv_heads) * B;
+  const int64_t items = items_of(most) * heads;
+  const int64_t nx = items_of(std::min<int64_t>(most, std::max(T, 1)));
   if (window > 0) tokens = std::min(tokens, static_cast<int64_t>(window) + per_item + sinks + 2 * p->block_size);
   const int64_t tiles = (tokens + kKeys - 1) / kKeys;
   // a part has four tiles at least: below that its sums cost more than the tiles
   plan.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(items, 1), tiles / 4)));
-  plan.items = items * plan.splits;
+  plan.nx = static_cast<int>(std::min<int64_t>(nx, INT_MAX));
+  plan.items = nx * heads * plan.splits;
   plan.bytes = 256;
   if (plan.splits > 1) plan.bytes += static_cast<size_t>(plan.splits) * T * p->num_q_heads * (p->head_dim + 4) * sizeof(float);
   return plan;
@@ -982,6 +994,7 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
 
 zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st) {
   if (plan.items > INT_MAX / 2) return ZP_ERR_UNSUPPORTED;
+  if (plan.splits > 1 && static_cast<int64_t>(a.T) * p->num_q_heads > INT_MAX) return ZP_ERR_UNSUPPORTED;  // rows to join
   a.err = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
   a.splits = plan.splits;

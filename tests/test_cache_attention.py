@@ -34,7 +34,7 @@ def _refusals(zp, call, base, x, p):
                dict(B=-1), dict(mb=0), dict(window=-1), dict(sinks=-1), dict(params=None), dict(ws=None), dict(ws=base + 64),
                dict(nb=255), dict(q=zp.zp_rows(x.data_ptr() + 1, 128, 64)), dict(out=zp.zp_rows(None, 0, 0)),
                dict(params=params(scale=0.0)), dict(params=params(scale=-1.0)), dict(params=params(scale=math.inf)),
-               dict(params=params(scale=math.nan)), dict(params=params(num_q_heads=3)), dict(params=params(num_kv_heads=0))):
+               dict(params=params(scale=math.nan)), dict(params=params(scale=3.4e38)), dict(params=params(num_q_heads=3)), dict(params=params(num_kv_heads=0))):
         assert call(**kw) == bad, kw
     for kw in (dict(params=params(head_dim=96)), dict(params=params(block_size=8)), dict(params=params(num_q_heads=34)),
                dict(mb=1 << 28), dict(B=65536, nb=1 << 40)):
@@ -93,6 +93,15 @@ def test_workspace_sizes(zp):
     for w in (1, 100, 5000, 10 ** 6):
         assert zp.zp_paged_window_workspace_size(p, 2, 1, 2, 4096, w, 9) <= zp.zp_paged_window_workspace_size(p, 2, 1, 2, 4096, 0, 0)
     assert zp.zp_kv8_decode_workspace_size(p, -1, 4) == 0 and zp.zp_paged_window_workspace_size(p, 4, 1, 0, 4, 1, 1) == 0
+    # heads that no kernel takes
+    assert zp.zp_kv8_decode_workspace_size(_params(400, 2, 128, 16), 1, 4) == 0
+    assert zp.zp_paged_window_workspace_size(_params(400, 2, 128, 16), 4, 1, 4, 4, 1, 1) == 0
+    # any bound on the new tokens; a workspace for many rows is enough for fewer
+    most = 2 ** 31 - 1
+    assert zp.zp_paged_window_workspace_size(p, most, 65535, most, 1 << 26, 0, 0) == 256
+    for mq in (17, 64, 2048, most):
+        sizes = [zp.zp_paged_window_workspace_size(p, T, 1, mq, 4096, 0, 0) for T in (0, 1, 17, 64, 500, 2048, 60000)]
+        assert sizes == sorted(sizes)
 
 
 # ------------------------------------------------------------------ inputs and checks ---------
@@ -420,6 +429,35 @@ def test_window_padded_rows_are_left_alone(zp):
                                 9, 0, n)
         assert zp.zp_read_error(ws) == 0
         assert bool((out[n:] == 7).all()) and not bool((out[:n] == 7).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_q", [200, 2 ** 31 - 1])
+def test_window_takes_a_loose_bound_on_the_new_tokens(zp, max_q):
+    _window_case(zp, 4, 2, 64, 16, [300, 5, 0], [3, 1, 20], 100, 4, seed=14, max_q=max_q, rel=TILED)
+    _window_case(zp, 4, 2, 128, 16, [3000], [70], 0, 0, seed=15, max_q=max_q, rel=TILED)
+
+
+@pytest.mark.gpu
+def test_window_values_in_split_items(zp):
+    # a few rows over a long cache share their tiles between CTAs; one of the last values is not
+    # finite and only the last rows see it
+    def poison(x, tables):
+        x[tables[0, 3059 // 16], 1, 0, 3059 % 16, 11] = math.nan
+    _window_case(zp, 4, 2, 64, 16, [3000], [70], 0, 0, seed=16, poison=poison, rel=TILED)
+
+
+@pytest.mark.gpu
+def test_window_long_items_before_short_ones(zp):
+    # Every CTA takes one item of two query tiles, whose rows are computed plainly (slowly, and the
+    # second tile's longer than the first's) because a value that only the last of them sees is not
+    # finite, and then nine items of one tile, which the second group of warps has no part in.
+    heavy, light = 76, 76 * 9
+
+    def poison(x, tables):
+        for r in range(heavy):
+            x[tables[r, 63 // 16], 1, :, 63 % 16, 5] = math.inf
+    _window_case(zp, 8, 2, 64, 16, [0] * (heavy + light), [64] * heavy + [6] * light, 0, 0, seed=17, poison=poison, rel=TILED)
 
 
 @pytest.mark.gpu
