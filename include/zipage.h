@@ -372,8 +372,9 @@ typedef struct zp_kv8_pool {
 /* Quantises new keys and values of one layer as they enter the cache.
  *   k, v            rows [T][num_kv_heads][head_dim] of the new tokens of all requests, request
  *                   after request.
- *   token_start     device int32 [B + 1], 0 = token_start[0] <= ... <= token_start[B] = T: request r
- *                   owns rows token_start[r] .. token_start[r + 1] - 1 (none is fine).
+ *   token_start     device int32 [B + 1], 0 = token_start[0] <= ... <= token_start[B] <= T: request r
+ *                   owns rows token_start[r] .. token_start[r + 1] - 1 (none is fine).  Rows behind
+ *                   the last request's are not read.
  *   cached          device int32 [B], tokens in request r's cache before the call: its new tokens
  *                   take positions cached[r], cached[r] + 1, ...
  *   block_tables    device int32 [B][max_blocks]; only the entries of blocks that receive tokens
@@ -418,8 +419,8 @@ zp_status zp_kv8_unpack_blocks(const zp_kv8_pool* kv8, const int32_t* src_ids, c
  *   seq_lens      device int32 [B], 0 <= L <= max_blocks * b.  0 (a padded row): zeros are written.
  *   workspace     >= zp_kv8_decode_workspace_size() bytes, 256-byte aligned.
  * A bad seq_len or block id: that row (request and kv head) is not written, ZP_ERR_BAD_TABLE.
- * Only table entries of visible blocks are read.  head_dim 64 or 128, block_size 16 or 32, up to
- * 16 query heads per kv head. */
+ * Table entries of blocks that are not visible may hold anything.  head_dim 64 or 128, block_size
+ * 16 or 32, up to 16 query heads per kv head. */
 zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables,
                              const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window, int32_t sinks,
                              const zp_rows* out, const zp_params* params, void* workspace, size_t workspace_bytes,

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreadsQ, BS * D == 4096 ? 5 : 10) append_ker
     c = a.cached[r];
     // token_start as a whole: each request looks at its own step, the first at both ends
     if (blockIdx.y == 0 && threadIdx.x == 0 &&
-        (s1 < s0 || (r == 0 && (s0 != 0 || a.token_start[a.B] != a.T))))
+        (s1 < s0 || (r == 0 && (s0 != 0 || a.token_start[a.B] > a.T))))
       record(a.err, ZP_ERR_BAD_TABLE);
   } else {
     // the last request whose first further slot is <= u

@@ -216,6 +216,7 @@ extern "C" zp_status zp_rope_init(const zp_rope_config* c, zp_rope* out) {
     // f <= 1, so at most 1 / (2 pi) of a turn per position: the product stays below 2^62
     r.turns[i] = static_cast<uint64_t>(std::llrint(f / two_pi * 18446744073709551616.0));
   }
+  if (!std::isfinite(r.mscale)) return ZP_ERR_INVALID_ARG;
   *out = r;
   return ZP_OK;
 }

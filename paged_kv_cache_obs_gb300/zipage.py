@@ -356,41 +356,54 @@ _addr = ctypes.addressof
 
 def _rows(t):
     """bf16 rows [tokens, heads, head_dim] with any token and head strides, as a zp_rows."""
-    return zp_rows.from_buffer_copy(_row_bytes(t))
+    return zp_rows.from_buffer_copy(_row_bytes(t, t.get_device(), t.shape))
 
 
-def _row_bytes(t):
+def _row_bytes(t, dev, shape):
+    """The same as bytes, of rows of this shape on device `dev`."""
     ts, hs, es = t.stride()
-    if es != 1 or t.dtype is not torch.bfloat16:
-        raise ValueError("rows are bf16 and their last dimension is contiguous")
+    if es != 1 or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"expected bf16 rows {tuple(shape)} with a contiguous last dimension, on the cache's device")
     return _pack_rows(t.data_ptr(), ts, hs)
 
 
-def _i32(t):
-    """Address of a device int32 array."""
-    if t.dtype is not torch.int32 or not t.is_contiguous():
-        raise ValueError("tables, lengths, positions and block ids are contiguous int32 tensors")
+def _i32(t, dev, n):
+    """Address of an int32 array of n entries (rows of a table) or more on device `dev`."""
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.size(0) < n or t.get_device() != dev:
+        raise ValueError(f"expected a contiguous int32 tensor of {n} entries, on the cache's device")
     return t.data_ptr()
 
 
-def _pool(pool):
+def _pool(pool, dev, p):
     """(address, number of blocks) of a bf16 pool."""
-    if pool.dtype is not torch.bfloat16 or not pool.is_contiguous():
-        raise ValueError("the pool is a contiguous bf16 tensor")
-    return pool.data_ptr(), pool.size(1)
+    n = pool.size(1)
+    if (pool.dtype is not torch.bfloat16 or not pool.is_contiguous() or pool.get_device() != dev or
+            pool.numel() != p.num_layers * n * 2 * p.num_kv_heads * p.block_size * p.head_dim):
+        raise ValueError("expected a contiguous bf16 pool [num_layers, blocks, 2, num_kv_heads, block_size, head_dim]")
+    return pool.data_ptr(), n
 
 
-def _kv8(codes, scales):
+def _kv8(codes, scales, dev, p):
     """(address of the codes, address of the scales, number of blocks) of an 8-bit pool."""
-    if codes.element_size() != 1 or scales.dtype is not torch.float32 or not (codes.is_contiguous() and scales.is_contiguous()):
-        raise ValueError("codes are one byte a value and scales fp32, both contiguous")
-    return codes.data_ptr(), scales.data_ptr(), codes.size(1)
+    n = codes.size(1)
+    tiles = p.num_layers * n * 2 * p.num_kv_heads
+    if (codes.element_size() != 1 or scales.dtype is not torch.float32 or not (codes.is_contiguous() and scales.is_contiguous()) or
+            scales.get_device() != dev or scales.numel() != tiles or codes.numel() != tiles * p.block_size * p.head_dim):
+        raise ValueError("expected contiguous codes [num_layers, blocks, 2, num_kv_heads, block_size, head_dim] of one byte a "
+                         "value and fp32 scales [num_layers, blocks, 2, num_kv_heads] on one device")
+    return codes.data_ptr(), scales.data_ptr(), n
 
 
-def _stream_of(t, stream):
-    """The stream to launch on: the given one, or the current one of the tensor's device, which has to
+def _ws(workspace, dev):
+    """(address, bytes) of a workspace."""
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("expected a contiguous workspace on the cache's device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def _stream_of(dev, stream):
+    """The stream to launch on: the given one, or the current one of the tensors' device, which has to
     be the current device (the library launches there)."""
-    dev = t.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("the tensors have to be on the current CUDA device")
     return _current_raw_stream(dev) if stream is None else stream.cuda_stream
@@ -420,14 +433,18 @@ def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream
     """Rotates q [T, H_q, d] and k [T, H_kv, d] (either may be None), in place or into q_out, k_out."""
     rq = oq = rk = ok = None
     hq = hk = 0
+    T, dev = positions.size(0), positions.get_device()
     if q is not None:
-        rq, hq = _row_bytes(q), q.size(1)
-        oq = rq if q_out is None else _row_bytes(q_out)
+        hq = q.size(1)
+        shape = (T, hq, rope.head_dim)
+        rq = _row_bytes(q, dev, shape)
+        oq = rq if q_out is None else _row_bytes(q_out, dev, shape)
     if k is not None:
-        rk, hk = _row_bytes(k), k.size(1)
-        ok = rk if k_out is None else _row_bytes(k_out)
-    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, _i32(positions), positions.size(0),
-                     _stream_of(positions, stream))
+        hk = k.size(1)
+        shape = (T, hk, rope.head_dim)
+        rk = _row_bytes(k, dev, shape)
+        ok = rk if k_out is None else _row_bytes(k_out, dev, shape)
+    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, _i32(positions, dev, T), T, _stream_of(dev, stream))
     if st:
         _check("zp_rope_apply", st)
 
@@ -436,10 +453,11 @@ def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_ta
     """Quantises the new keys and values k, v [T, H_kv, d] of one layer into the 8-bit pool: codes
     (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
     token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
-    p = _params(params)
-    st = _kv8_append(_pack_kv8(*_kv8(codes, scales)), layer, _row_bytes(k), _row_bytes(v), k.size(0), _i32(token_start),
-                     _i32(cached), cached.size(0), _i32(block_tables), block_tables.size(1), _addr(p),
-                     workspace.data_ptr(), workspace.nbytes, _stream_of(codes, stream))
+    p, dev, T, B = _params(params), codes.get_device(), k.size(0), cached.size(0)
+    shape = (T, p.num_kv_heads, p.head_dim)
+    st = _kv8_append(_pack_kv8(*_kv8(codes, scales, dev, p)), layer, _row_bytes(k, dev, shape), _row_bytes(v, dev, shape), T,
+                     _i32(token_start, dev, B + 1), _i32(cached, dev, B), B, _i32(block_tables, dev, B),
+                     block_tables.size(1), _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
     if st:
         _check("zp_kv8_append", st)
 
@@ -449,9 +467,10 @@ def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace,
     """Blocks src_ids of the bf16 pool into blocks dst_ids of the 8-bit pool.  fill: optional device
     int32 [n] of tokens per block; layers: optional (layer_begin, layer_count)."""
     lb, lc = layers if layers is not None else (0, 0)
-    st = lib.zp_kv8_pack_blocks(zp_kv_pool(*_pool(pool)), _i32(src_ids), None if fill is None else _i32(fill),
-                                zp_kv8_pool(*_kv8(codes, scales)), _i32(dst_ids), src_ids.size(0), lb, lc, _params(params),
-                                workspace.data_ptr(), workspace.nbytes, _stream_of(codes, stream))
+    p, dev, n = _params(params), codes.get_device(), src_ids.size(0)
+    st = lib.zp_kv8_pack_blocks(zp_kv_pool(*_pool(pool, dev, p)), _i32(src_ids, dev, n), None if fill is None else _i32(fill, dev, n),
+                                zp_kv8_pool(*_kv8(codes, scales, dev, p)), _i32(dst_ids, dev, n), n, lb, lc, p,
+                                *_ws(workspace, dev), _stream_of(dev, stream))
     _check("zp_kv8_pack_blocks", st)
 
 
@@ -459,9 +478,9 @@ def zp_kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, params, workspac
                          stream=None):
     """Blocks src_ids of the 8-bit pool into blocks dst_ids of the bf16 pool."""
     lb, lc = layers if layers is not None else (0, 0)
-    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(*_kv8(codes, scales)), _i32(src_ids), zp_kv_pool(*_pool(pool)),
-                                  _i32(dst_ids), src_ids.size(0), lb, lc, _params(params), workspace.data_ptr(),
-                                  workspace.nbytes, _stream_of(codes, stream))
+    p, dev, n = _params(params), codes.get_device(), src_ids.size(0)
+    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(*_kv8(codes, scales, dev, p)), _i32(src_ids, dev, n), zp_kv_pool(*_pool(pool, dev, p)),
+                                  _i32(dst_ids, dev, n), n, lb, lc, p, *_ws(workspace, dev), _stream_of(dev, stream))
     _check("zp_kv8_unpack_blocks", st)
 
 
@@ -473,10 +492,11 @@ def zp_kv8_decode_attn(codes, scales, layer: int, q, block_tables, seq_lens, out
                        sinks: int = 0, stream=None):
     """Decode attention over the 8-bit pool: q, out bf16 [B, H_q, d]; a request sees its last
     `window` tokens and the first `sinks` (window 0: all)."""
-    p = _params(params)
-    st = _kv8_decode_attn(_pack_kv8(*_kv8(codes, scales)), layer, _row_bytes(q), _i32(block_tables), _i32(seq_lens),
-                          q.size(0), block_tables.size(1), window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(),
-                          workspace.nbytes, _stream_of(codes, stream))
+    p, dev, B = _params(params), codes.get_device(), q.size(0)
+    shape = (B, p.num_q_heads, p.head_dim)
+    st = _kv8_decode_attn(_pack_kv8(*_kv8(codes, scales, dev, p)), layer, _row_bytes(q, dev, shape), _i32(block_tables, dev, B),
+                          _i32(seq_lens, dev, B), B, block_tables.size(1), window, sinks, _row_bytes(out, dev, shape),
+                          _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
     if st:
         _check("zp_kv8_decode_attn", st)
 
@@ -490,11 +510,11 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
     """Attention of the new tokens q [T, H_q, d] (request r: rows q_start[r] .. q_start[r + 1] - 1, its
     last tokens in the cache) over the bf16 pool, with a window and `sinks` first tokens that stay
     visible.  max_q: the most new tokens of a request."""
-    p = _params(params)
-    st = _paged_window_attn(_pack_pool(*_pool(pool)), layer, _row_bytes(q), _i32(q_start), q.size(0), max_q,
-                            _i32(block_tables), _i32(seq_lens), seq_lens.size(0), block_tables.size(1),
-                            window, sinks, _row_bytes(out), _addr(p), workspace.data_ptr(), workspace.nbytes,
-                            _stream_of(pool, stream))
+    p, dev, T, B = _params(params), pool.get_device(), q.size(0), seq_lens.size(0)
+    shape = (T, p.num_q_heads, p.head_dim)
+    st = _paged_window_attn(_pack_pool(*_pool(pool, dev, p)), layer, _row_bytes(q, dev, shape), _i32(q_start, dev, B + 1), T, max_q,
+                            _i32(block_tables, dev, B), _i32(seq_lens, dev, B), B, block_tables.size(1), window, sinks,
+                            _row_bytes(out, dev, shape), _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
     if st:
         _check("zp_paged_window_attn", st)
 

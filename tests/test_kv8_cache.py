@@ -115,6 +115,30 @@ def test_binding_refuses_what_it_would_misread(zp):
                  lambda: zp.zp_kv8_unpack_blocks(codes, scales, i32, pool.float(), i32, p, ws)):
         with pytest.raises(ValueError):
             call()
+    # sizes that do not go together
+    short, five = torch.zeros(3, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    p8 = _params(2, 64, 16, layers=2)
+    for call in (lambda: zp.zp_rope_apply(rope, bf, None, five), lambda: zp.zp_rope_apply(rope, None, bf[..., :32], i32),
+                 lambda: zp.zp_rope_apply(rope, bf, None, i32, q_out=bf[:, :1]),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32, i32, tables, p, ws),       # B + 1 starts
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf[:3], five, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf[:, :1], bf, five, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, five, i32, tables[:3], p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, five, i32, tables, p8, ws),
+                 lambda: zp.zp_kv8_append(codes, scales[:, :3].contiguous(), 0, bf, bf, five, i32, tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, five, i32, tables, p, ws[::2]),
+                 lambda: zp.zp_kv8_decode_attn(codes, scales, 0, bf, tables, short, bf, p, ws),
+                 lambda: zp.zp_kv8_decode_attn(codes, scales, 0, bf, tables, i32, bf[:3], p, ws),
+                 lambda: zp.zp_paged_window_attn(pool, 0, bf, i32, tables, i32, bf, p, ws, 4, 1, 1),
+                 lambda: zp.zp_paged_window_attn(pool, 0, bf, five, tables, i32, bf, p8, ws, 4, 1, 1),
+                 lambda: zp.zp_kv8_pack_blocks(pool, i32, codes, scales, short, p, ws),
+                 lambda: zp.zp_kv8_pack_blocks(pool, i32, codes, scales, i32, p, ws, fill=short),
+                 lambda: zp.zp_kv8_unpack_blocks(codes, scales, i32, pool[:, :, :1].contiguous(), i32, p, ws)):
+        with pytest.raises(ValueError, match="expected"):
+            call()
+    # and what is right but for its place
+    with pytest.raises(ValueError, match="current CUDA device"):
+        zp.zp_kv8_append(codes, scales, 0, bf, bf, five, i32, tables, p, ws)
 
 
 # ------------------------------------------------------------------ append (GPU) --------------
@@ -261,7 +285,7 @@ def test_append_skips_bad_requests_and_reports(zp):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("start", [[0, 5, 3, 6], [1, 2, 4, 6], [0, 2, 4, 5], [0, 2, 4, 7], [-1, 2, 4, 6]])
+@pytest.mark.parametrize("start", [[0, 5, 3, 6], [1, 2, 4, 6], [0, 2, 4, 7], [-1, 2, 4, 6]])
 def test_append_reports_bad_token_start(zp, start):
     # what is written is not defined then; nothing outside the requests' blocks is touched
     d, b, mb, B = 64, 16, 2, 3
@@ -273,6 +297,22 @@ def test_append_reports_bad_token_start(zp, start):
     assert zp.zp_read_error(c.ws) == zp.ZP_ERR_BAD_TABLE
     got = c.d_codes.cpu().numpy()
     assert np.array_equal(got[1], c.codes[1]) and np.array_equal(got[0, others], c.codes[0, others])
+
+
+@pytest.mark.gpu
+def test_append_leaves_padded_rows_out(zp):
+    # rows behind the last request's, as a step of fixed size has them; they hold NaN
+    for new in ([1, 1, 0, 0], [20, 0, 3, 0]):
+        c = _Cache(zp, 4, 2, 64, 16, 3, layers=1, seed=14)
+        n = sum(new)
+        x = torch.full((n + 40, 2, 64), math.nan, dtype=torch.bfloat16, device="cuda")
+        x[:n] = torch.randn((n, 2, 64), device="cuda").to(torch.bfloat16)
+        start, cached = _starts(new), [5, 16, 0, 7]
+        zp.zp_kv8_append(c.d_codes, c.d_scales, 0, x, x, torch.tensor(start, dtype=torch.int32).cuda(),
+                         torch.tensor(cached, dtype=torch.int32).cuda(), c.d_tables, c.p, c.ws)
+        xs = x[:n].double().cpu().numpy()
+        S.append(c.codes, c.scales, 0, xs, xs, start, cached, c.tables, 16)
+        c.check()
 
 
 # ------------------------------------------------------------------ whole blocks (GPU) --------

@@ -48,7 +48,7 @@ def test_table_takes_a_given_factor(zp):
                                 dict(scaling=5), dict(scaling=-1), dict(scaling=1, factor=0.5), dict(scaling=1, factor=math.nan),
                                 dict(scaling=3, factor=2.0, original_len=0), dict(scaling=4, factor=2.0, original_len=10, low=0.0),
                                 dict(scaling=4, factor=2.0, original_len=10, low=4.0, high=4.0), dict(scaling=2, factor=2.0, rotary_dim=2),
-                                dict(mscale=math.inf), dict(head_dim=512, rotary_dim=258)])
+                                dict(mscale=math.inf), dict(mscale=1e39), dict(head_dim=512, rotary_dim=258)])
 def test_table_refuses(zp, kw):
     full = dict(head_dim=128, rotary_dim=128, theta=THETA)
     full.update(kw)
