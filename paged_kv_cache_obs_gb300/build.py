@@ -1,4 +1,5 @@
-"""Builds libzipage.so in-tree with nvcc for sm_103a (no cmake, translation units in parallel).
+"""Builds libzipage.so in-tree with nvcc for sm_103a, and the compiled part of the Python binding
+(zp_tensors.so) with the host compiler (no cmake, translation units in parallel).
 
 Usage: python -m paged_kv_cache_obs_gb300.build   (or build() from Python)
 """
@@ -14,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libzipage.so")
+BINDING = os.path.join(LIBDIR, "zp_tensors.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -31,8 +33,27 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
+def build_binding() -> None:
+    """Compiles csrc/binding into lib/zp_tensors.so against the headers of this Python and PyTorch."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    dirs = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", *(x for d in dirs for x in ("-isystem", d)),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", os.path.join(CSRC, "binding", "zp_tensors.cpp"),
+           "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compiles every source under csrc/ and links lib/libzipage.so. Returns the library path."""
+    """Compiles every source under csrc/ and links lib/libzipage.so, and the binding. Returns the library path."""
     nvcc = _nvcc()
     os.makedirs(LIBDIR, exist_ok=True)
     objdir = os.path.join(LIBDIR, "obj")
@@ -53,8 +74,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if res.returncode != 0:

@@ -8,8 +8,8 @@ kernels; there is no fallback: if the library is missing, importing this module 
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -37,6 +37,18 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"libzipage.so is not built ({_LIB_PATH}); run __graft_entry__.build() "
                       "or python -m paged_kv_cache_obs_gb300.build")
 lib = ctypes.CDLL(_LIB_PATH)
+
+
+def _load_tensors():
+    """The compiled part of this binding (csrc/binding/zp_tensors.cpp)."""
+    path = os.path.join(os.path.dirname(_LIB_PATH), "zp_tensors.so")
+    if not os.path.exists(path):
+        raise ImportError(f"zp_tensors.so is not built ({path}); run __graft_entry__.build() "
+                          "or python -m paged_kv_cache_obs_gb300.build")
+    spec = importlib.util.spec_from_file_location("zp_tensors", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 class zp_params(ctypes.Structure):
@@ -333,85 +345,18 @@ def zp_paged_decode_attn_static(pool, layer: int, q, block_tables, seq_lens, out
 
 # ------------------------------------------------------------------ per-step operators -------
 #
-# These run once per layer and step, so their marshalling is kept short: structs are packed into
-# bytes (which a void pointer argument takes), and the current stream is read as a number.
+# These run once per layer and step, so zp_tensors (csrc/binding) turns their tensors into the C
+# structs: it refuses (ValueError) tensors whose types, sizes, strides or devices do not go together.
 
-def _fast(name, args):
-    f = lib[name]  # a function object of its own: the one in `lib` keeps its typed pointers
-    f.restype = _I32
-    f.argtypes = args
-    return f
-
-
-_rope_apply = _fast("zp_rope_apply", [_P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P])
-_kv8_append = _fast("zp_kv8_append", [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P])
-_kv8_decode_attn = _fast("zp_kv8_decode_attn", [_P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _SZ, _P])
-_paged_window_attn = _fast("zp_paged_window_attn", [_P, _I32, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
-                                                    _P, _SZ, _P])
-_pack_rows = struct.Struct("Nqq").pack     # zp_rows
-_pack_kv8 = struct.Struct("NNq").pack      # zp_kv8_pool
-_pack_pool = struct.Struct("Nq").pack      # zp_kv_pool
+_t = _load_tensors()
+_t.bind(*(ctypes.cast(lib[name], _P).value for name in
+          ("zp_rope_apply", "zp_kv8_append", "zp_kv8_pack_blocks", "zp_kv8_unpack_blocks", "zp_kv8_decode_attn",
+           "zp_paged_window_attn")))
 _addr = ctypes.addressof
 
 
-def _rows(t):
-    """bf16 rows [tokens, heads, head_dim] with any token and head strides, as a zp_rows."""
-    return zp_rows.from_buffer_copy(_row_bytes(t, t.get_device(), t.shape))
-
-
-def _row_bytes(t, dev, shape):
-    """The same as bytes, of rows of this shape on device `dev`."""
-    ts, hs, es = t.stride()
-    if es != 1 or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"expected bf16 rows {tuple(shape)} with a contiguous last dimension, on the cache's device")
-    return _pack_rows(t.data_ptr(), ts, hs)
-
-
-def _i32(t, dev, n):
-    """Address of an int32 array of n entries (rows of a table) or more on device `dev`."""
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.size(0) < n or t.get_device() != dev:
-        raise ValueError(f"expected a contiguous int32 tensor of {n} entries, on the cache's device")
-    return t.data_ptr()
-
-
-def _pool(pool, dev, p):
-    """(address, number of blocks) of a bf16 pool."""
-    n = pool.size(1)
-    if (pool.dtype is not torch.bfloat16 or not pool.is_contiguous() or pool.get_device() != dev or
-            pool.numel() != p.num_layers * n * 2 * p.num_kv_heads * p.block_size * p.head_dim):
-        raise ValueError("expected a contiguous bf16 pool [num_layers, blocks, 2, num_kv_heads, block_size, head_dim]")
-    return pool.data_ptr(), n
-
-
-def _kv8(codes, scales, dev, p):
-    """(address of the codes, address of the scales, number of blocks) of an 8-bit pool."""
-    n = codes.size(1)
-    tiles = p.num_layers * n * 2 * p.num_kv_heads
-    if (codes.element_size() != 1 or scales.dtype is not torch.float32 or not (codes.is_contiguous() and scales.is_contiguous()) or
-            scales.get_device() != dev or scales.numel() != tiles or codes.numel() != tiles * p.block_size * p.head_dim):
-        raise ValueError("expected contiguous codes [num_layers, blocks, 2, num_kv_heads, block_size, head_dim] of one byte a "
-                         "value and fp32 scales [num_layers, blocks, 2, num_kv_heads] on one device")
-    return codes.data_ptr(), scales.data_ptr(), n
-
-
-def _ws(workspace, dev):
-    """(address, bytes) of a workspace."""
-    if not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("expected a contiguous workspace on the cache's device")
-    return workspace.data_ptr(), workspace.nbytes
-
-
-def _stream_of(dev, stream):
-    """The stream to launch on: the given one, or the current one of the tensors' device, which has to
-    be the current device (the library launches there)."""
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("the tensors have to be on the current CUDA device")
-    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-# the current stream's handle without building a Stream object
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _params(params):
@@ -431,20 +376,7 @@ def zp_rope_init(head_dim: int, rotary_dim: int, theta: float, interleaved: bool
 
 def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream=None):
     """Rotates q [T, H_q, d] and k [T, H_kv, d] (either may be None), in place or into q_out, k_out."""
-    rq = oq = rk = ok = None
-    hq = hk = 0
-    T, dev = positions.size(0), positions.get_device()
-    if q is not None:
-        hq = q.size(1)
-        shape = (T, hq, rope.head_dim)
-        rq = _row_bytes(q, dev, shape)
-        oq = rq if q_out is None else _row_bytes(q_out, dev, shape)
-    if k is not None:
-        hk = k.size(1)
-        shape = (T, hk, rope.head_dim)
-        rk = _row_bytes(k, dev, shape)
-        ok = rk if k_out is None else _row_bytes(k_out, dev, shape)
-    st = _rope_apply(_addr(rope), rq, oq, hq, rk, ok, hk, _i32(positions, dev, T), T, _stream_of(dev, stream))
+    st = _t.rope_apply(_addr(rope), q, k, positions, q_out, k_out, _raw(stream))
     if st:
         _check("zp_rope_apply", st)
 
@@ -453,11 +385,8 @@ def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_ta
     """Quantises the new keys and values k, v [T, H_kv, d] of one layer into the 8-bit pool: codes
     (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
     token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
-    p, dev, T, B = _params(params), codes.get_device(), k.size(0), cached.size(0)
-    shape = (T, p.num_kv_heads, p.head_dim)
-    st = _kv8_append(_pack_kv8(*_kv8(codes, scales, dev, p)), layer, _row_bytes(k, dev, shape), _row_bytes(v, dev, shape), T,
-                     _i32(token_start, dev, B + 1), _i32(cached, dev, B), B, _i32(block_tables, dev, B),
-                     block_tables.size(1), _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
+    p = _params(params)
+    st = _t.kv8_append(codes, scales, layer, k, v, token_start, cached, block_tables, _addr(p), workspace, _raw(stream))
     if st:
         _check("zp_kv8_append", st)
 
@@ -467,21 +396,18 @@ def zp_kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, params, workspace,
     """Blocks src_ids of the bf16 pool into blocks dst_ids of the 8-bit pool.  fill: optional device
     int32 [n] of tokens per block; layers: optional (layer_begin, layer_count)."""
     lb, lc = layers if layers is not None else (0, 0)
-    p, dev, n = _params(params), codes.get_device(), src_ids.size(0)
-    st = lib.zp_kv8_pack_blocks(zp_kv_pool(*_pool(pool, dev, p)), _i32(src_ids, dev, n), None if fill is None else _i32(fill, dev, n),
-                                zp_kv8_pool(*_kv8(codes, scales, dev, p)), _i32(dst_ids, dev, n), n, lb, lc, p,
-                                *_ws(workspace, dev), _stream_of(dev, stream))
-    _check("zp_kv8_pack_blocks", st)
+    p = _params(params)
+    _check("zp_kv8_pack_blocks", _t.kv8_pack_blocks(pool, src_ids, codes, scales, dst_ids, fill, lb, lc, _addr(p), workspace,
+                                                    _raw(stream)))
 
 
 def zp_kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, params, workspace, layers: tuple | None = None,
                          stream=None):
     """Blocks src_ids of the 8-bit pool into blocks dst_ids of the bf16 pool."""
     lb, lc = layers if layers is not None else (0, 0)
-    p, dev, n = _params(params), codes.get_device(), src_ids.size(0)
-    st = lib.zp_kv8_unpack_blocks(zp_kv8_pool(*_kv8(codes, scales, dev, p)), _i32(src_ids, dev, n), zp_kv_pool(*_pool(pool, dev, p)),
-                                  _i32(dst_ids, dev, n), n, lb, lc, p, *_ws(workspace, dev), _stream_of(dev, stream))
-    _check("zp_kv8_unpack_blocks", st)
+    p = _params(params)
+    _check("zp_kv8_unpack_blocks", _t.kv8_unpack_blocks(codes, scales, src_ids, pool, dst_ids, lb, lc, _addr(p), workspace,
+                                                        _raw(stream)))
 
 
 def zp_kv8_decode_workspace_size(params, B: int, max_blocks: int) -> int:
@@ -492,11 +418,8 @@ def zp_kv8_decode_attn(codes, scales, layer: int, q, block_tables, seq_lens, out
                        sinks: int = 0, stream=None):
     """Decode attention over the 8-bit pool: q, out bf16 [B, H_q, d]; a request sees its last
     `window` tokens and the first `sinks` (window 0: all)."""
-    p, dev, B = _params(params), codes.get_device(), q.size(0)
-    shape = (B, p.num_q_heads, p.head_dim)
-    st = _kv8_decode_attn(_pack_kv8(*_kv8(codes, scales, dev, p)), layer, _row_bytes(q, dev, shape), _i32(block_tables, dev, B),
-                          _i32(seq_lens, dev, B), B, block_tables.size(1), window, sinks, _row_bytes(out, dev, shape),
-                          _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
+    p = _params(params)
+    st = _t.kv8_decode_attn(codes, scales, layer, q, block_tables, seq_lens, out, _addr(p), workspace, window, sinks, _raw(stream))
     if st:
         _check("zp_kv8_decode_attn", st)
 
@@ -510,11 +433,9 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
     """Attention of the new tokens q [T, H_q, d] (request r: rows q_start[r] .. q_start[r + 1] - 1, its
     last tokens in the cache) over the bf16 pool, with a window and `sinks` first tokens that stay
     visible.  max_q: the most new tokens of a request."""
-    p, dev, T, B = _params(params), pool.get_device(), q.size(0), seq_lens.size(0)
-    shape = (T, p.num_q_heads, p.head_dim)
-    st = _paged_window_attn(_pack_pool(*_pool(pool, dev, p)), layer, _row_bytes(q, dev, shape), _i32(q_start, dev, B + 1), T, max_q,
-                            _i32(block_tables, dev, B), _i32(seq_lens, dev, B), B, block_tables.size(1), window, sinks,
-                            _row_bytes(out, dev, shape), _addr(p), *_ws(workspace, dev), _stream_of(dev, stream))
+    p = _params(params)
+    st = _t.paged_window_attn(pool, layer, q, q_start, block_tables, seq_lens, out, _addr(p), workspace, window, sinks, max_q,
+                              _raw(stream))
     if st:
         _check("zp_paged_window_attn", st)
 

@@ -20,6 +20,10 @@ def zp():
     return zipage
 
 
+def _rows(zp, t):
+    return zp.zp_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
 def _params(Hq, Hkv, d, b, layers=1, scale=None):
     return dict(num_layers=layers, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, block_size=b, n_max=4, window=1, alpha=0.5,
                 beta=0.5, decay=0.9, scale=scale or 1.0 / math.sqrt(d), protect_window=1, causal=1)
@@ -50,7 +54,7 @@ def _host(zp):
 
 def test_kv8_decode_refuses(zp):
     ws, base, x, p = _host(zp)
-    rows = zp._rows(x)
+    rows = _rows(zp, x)
 
     def call(pool=zp.zp_kv8_pool(base, base, 4), layer=0, q=rows, tables=base, seq=base, B=2, mb=2, window=0, sinks=0, out=rows,
              params=zp.make_params(p), ws=base, nb=1 << 40):
@@ -67,7 +71,7 @@ def test_kv8_decode_refuses(zp):
 
 def test_window_refuses(zp):
     ws, base, x, p = _host(zp)
-    rows = zp._rows(x)
+    rows = _rows(zp, x)
 
     def call(pool=zp.zp_kv_pool(base, 4), layer=0, q=rows, start=base, T=2, max_q=1, tables=base, seq=base, B=2, mb=2, window=4,
              sinks=1, out=rows, params=zp.make_params(p), ws=base, nb=1 << 40):

@@ -21,6 +21,10 @@ def zp():
     return zipage
 
 
+def _rows(zp, t):
+    return zp.zp_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
 def _params(Hkv, d, b, layers=1, n_max=8):
     return dict(num_layers=layers, num_q_heads=Hkv, num_kv_heads=Hkv, head_dim=d, block_size=b, n_max=n_max, window=1,
                 alpha=0.5, beta=0.5, decay=0.9, scale=1.0 / math.sqrt(d), protect_window=1, causal=1)
@@ -49,7 +53,7 @@ def test_append_refuses(zp):
     ws = torch.zeros(512, dtype=torch.uint8)
     base = (ws.data_ptr() + 255) // 256 * 256
     p = zp.make_params(_params(2, 64, 16))
-    rows = zp._rows(x)
+    rows = _rows(zp, x)
     at = ctypes.c_void_p(x.data_ptr())
     pool = zp.zp_kv8_pool(base, base, 4)
 
@@ -135,6 +139,15 @@ def test_binding_refuses_what_it_would_misread(zp):
                  lambda: zp.zp_kv8_pack_blocks(pool, i32, codes, scales, i32, p, ws, fill=short),
                  lambda: zp.zp_kv8_unpack_blocks(codes, scales, i32, pool[:, :, :1].contiguous(), i32, p, ws)):
         with pytest.raises(ValueError, match="expected"):
+            call()
+    # no tensor, or numbers that the library would cut
+    for call, error in ((lambda: zp.zp_kv8_append(codes, scales, 0, bf, None, five, i32, tables, p, ws), ValueError),
+                        (lambda: zp.zp_kv8_append(codes, scales, 1 << 32, bf, bf, five, i32, tables, p, ws), ValueError),
+                        (lambda: zp.zp_kv8_append(codes, scales, None, bf, bf, five, i32, tables, p, ws), TypeError),
+                        (lambda: zp.zp_kv8_append(codes.to_sparse(), scales, 0, bf, bf, five, i32, tables, p, ws), ValueError),
+                        (lambda: zp.zp_kv8_append(codes.to("meta"), scales, 0, bf, bf, five, i32, tables, p, ws), ValueError),
+                        (lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, five, i32, tables[0], p, ws), ValueError)):
+        with pytest.raises(error):
             call()
     # and what is right but for its place
     with pytest.raises(ValueError, match="current CUDA device"):

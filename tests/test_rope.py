@@ -23,6 +23,10 @@ def zp():
     return zipage
 
 
+def _rows(zp, t):
+    return zp.zp_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
 def _init(zp, d, rd, inter, name, kw, theta=THETA):
     return zp.zp_rope_init(d, rd, theta, inter, getattr(zp, "ZP_ROPE_" + name.upper()), **kw)
 
@@ -62,7 +66,7 @@ def test_apply_refuses(zp):
     import ctypes
     rope = zp.zp_rope_init(64, 64, THETA)
     x = torch.zeros((2, 3, 64), dtype=torch.bfloat16)
-    rows, null = zp._rows(x), zp.zp_rows(None, 0, 0)
+    rows, null = _rows(zp, x), zp.zp_rows(None, 0, 0)
     other = zp.zp_rows(rows.data, rows.token_stride * 2, rows.head_stride)
     odd = zp.zp_rows(rows.data + 1, rows.token_stride, rows.head_stride)
     call = lambda r, q, qo, hq, k, ko, hk, pos, T: zp.lib.zp_rope_apply(r, q, qo, hq, k, ko, hk, pos, T, None)
@@ -80,8 +84,9 @@ def test_apply_refuses(zp):
     assert call(rope, rows, rows, 5000, None, None, 0, pos, 2) == zp.ZP_ERR_UNSUPPORTED
     assert call(rope, rows, rows, 3, None, None, 0, pos, 0) == zp.ZP_OK
     assert call(rope, None, None, 0, None, None, 0, pos, 2) == zp.ZP_OK
-    with pytest.raises(ValueError):
-        zp._rows(torch.zeros((2, 3, 128))[:, :, ::2])
+    strided = torch.zeros((2, 3, 128), dtype=torch.bfloat16)[:, :, ::2]
+    with pytest.raises(ValueError, match="contiguous last dimension"):
+        zp.zp_rope_apply(rope, strided, None, torch.zeros(2, dtype=torch.int32))
 
 
 def _check(got, x, pos, freqs, size, inter):
