@@ -19,6 +19,7 @@ struct AttnArgs {
   float* part;             // [B][Hkv][parts][rows][d + 4]: sums, maximum, sum of weights
   int T, B, layer, layers, max_blocks, Hkv, G, b, max_q, window, sinks;
   int splits;              // CTAs that share a row's tokens
+  bool ordered;            // split kernel: long requests first
   float sl2;               // scale * log2(e)
 };
 
@@ -30,6 +31,7 @@ constexpr int kMaxSplitRows = 16;
 struct SplitPlan {
   int rows;             // query rows that a CTA holds: 8 or 16
   int splits, cluster;
+  bool ordered;  // long requests first
   size_t bytes;
 };
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks);

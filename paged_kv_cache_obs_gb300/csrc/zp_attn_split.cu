@@ -154,6 +154,52 @@ __device__ __forceinline__ bool span_of(const AttnArgs& a, int r, Span& s, bool&
   return true;
 }
 
+// The request that comes z-th when the long ones come first: in four classes by the quarters of the
+// longest, in their own order within a class.  Every CTA finds its own (as many ballots as 32 requests
+// a class, and one scan), so nothing is shared between CTAs.
+constexpr int kMaxOrdered = 1024;
+__device__ __forceinline__ int request_at(const AttnArgs& a, int z, uint32_t* words, int* tops) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kMost = 1 << 30;  // above any length that is taken
+  int mx = 0;
+  for (int i = tid; i < a.B; i += kThreads) mx = max(mx, min(a.seq_lens[i], kMost));
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) tops[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = max(mx, tops[w]);
+  const int step = mx / 4 + 1, nw = (a.B + kThreads - 1) / kThreads * kWarps;  // words of a class
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int v = base + tid < a.B ? min(a.seq_lens[base + tid], kMost) : 0;
+    const int k = (v >= step) + (v >= 2 * step) + (v >= 3 * step);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t vote = __ballot_sync(0xffffffffu, base + tid < a.B && k == 3 - c);
+      if (lane == 0) words[c * nw + base / 32 + warp] = vote;
+    }
+  }
+  __syncthreads();
+  for (int w0 = 0;; w0 += 32) {
+    uint32_t word = w0 + lane < 4 * nw ? words[w0 + lane] : 0;
+    const int n = __popc(word);
+    int sum = n;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, x);
+      if (lane >= x) sum += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, sum > z);
+    if (past == 0 && w0 + 32 < 4 * nw) {
+      z -= __shfl_sync(0xffffffffu, sum, 31);
+      continue;
+    }
+    const int at = __ffs(past) - 1;
+    word = __shfl_sync(0xffffffffu, word, at);
+    for (int skip = z - __shfl_sync(0xffffffffu, sum - n, at); skip > 0; --skip) word &= word - 1;
+    return (w0 + at) % nw * 32 + __ffs(word) - 1;
+  }
+}
+
 // v and l += another part's sums, brought from its maximum to M.  A part without a maximum has sums of
 // 0, or NaN if every logit was.
 __device__ __forceinline__ void join(float (&v)[4], float& l, float4 y, float yl, float ym, float M) {
@@ -221,12 +267,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS], cta_m[ROWS], cta_l[ROWS];
   __shared__ __align__(8) uint64_t full[kWarps][SLOTS];
   __shared__ int sm_bad;
+  __shared__ uint32_t words[4 * kMaxOrdered / 32];
+  __shared__ int tops[kWarps];
   extern __shared__ uint8_t dyn[];
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
+  const int split = blockIdx.x, h = blockIdx.y;
+  const int r = a.ordered ? request_at(a, blockIdx.z, words, tops) : blockIdx.z;
   const int bshift = a.b == 2 * kTile ? 1 : 0;  // tiles per block, as a shift
   const int32_t* const table = a.tables + static_cast<int64_t>(r) * a.max_blocks;
   const int first = split * kWarps + warp;  // the warp's first group of SUB tiles
@@ -805,6 +854,12 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // costs about 5 us of an SM's slot in latencies (224 requests of 1 to 2048 tokens, 8 kv heads: 90 us
 // unsplit, 106 us with 2, 139 us with 4), while 4 requests of 100 to 500 tokens take 6.9 us with 4
 // splits and 10.3 us unsplit.
+//
+// An unsplit batch of more than a wave takes its long requests first, so that no CTA starts on one when
+// the others are done: those 224 requests in random order take 84 us so and 90 us as they come.
+// Finding the order costs a CTA about 0.5 us, too much where nothing is gained: with a window, whose
+// rows have nearly equal work (64 requests with a window of 1024: 44.0 us as they come, 43.4 us if
+// the caller has them in order), within a wave, and past 1024 requests, where the last ones are little.
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks) {
   constexpr int64_t kSms = 152;
   SplitPlan s{};
@@ -820,6 +875,7 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   const int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
   s.splits = n >= 8 ? static_cast<int>(n / 8 * 8) : s.cluster;
+  s.ordered = window == 0 && n < 2 && units > kSms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
   const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
   s.bytes = 256;
   if (parts > 1) s.bytes += static_cast<size_t>(units) * parts * s.rows * (p->head_dim + 4) * sizeof(float);
@@ -829,6 +885,7 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   a.splits = plan.splits;
+  a.ordered = plan.ordered;
   a.err = reinterpret_cast<int32_t*>(ws);
   a.part = reinterpret_cast<float*>(ws + 256);
   const int d = p->head_dim;

@@ -214,6 +214,23 @@ def test_kv8_decode_unaligned_rows_and_large_batch(zp):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,top", [(305, 40), (1024, 9), (1025, 9), (512, 1)])
+def test_batches_of_several_waves(zp, B, top):
+    # long requests are taken first, up to 1024 of them: every request once, whatever their lengths
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, top, B)]
+    lens[B // 2] = 200
+
+    def seq(x):
+        x[0], x[B - 1], x[B // 3] = 2 ** 31 - 1, -2 ** 31, 10 ** 6
+        return x
+    _kv8_case(zp, 2, 2, 64, 16, lens, seed=B, seq_edit=seq, expect=zp.ZP_ERR_BAD_TABLE, hidden_nan=False)
+    _window_case(zp, 2, 2, 64, 16, lens, [1 + r % 3 for r in range(B)], 0, 0, seed=B, rel=SPLIT)
+    if B < 400:
+        _window_case(zp, 8, 2, 128, 16, lens, [1 + r % 3 for r in range(B)], 0, 0, seed=B, rel=SPLIT)
+
+
+@pytest.mark.gpu
 def test_kv8_decode_skips_bad_rows_and_reports(zp):
     def edit(t):
         t[1, 2] = 10 ** 6
