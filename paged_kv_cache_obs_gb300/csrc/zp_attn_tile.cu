@@ -69,6 +69,7 @@ struct __align__(1024) TileSmem {
   uint8_t q[2][D / 64][kRows * 128];         // [tile][64-column half][row][128 B], 128-byte swizzle
   uint8_t k[kStages][D / 64][kKeys * 128];
   uint8_t v[kStages][D / 64][kKeys * 128];
+  uint8_t rows[8][32 * 128];                 // a softmax warp's output, 64 columns at a time
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems], item_empty[kItems];
@@ -114,13 +115,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
-}
-
-// 32 bytes to a 32-byte boundary.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // True in one lane of the (whole) warp.
@@ -468,9 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const uint32_t tbase = s.tmem;
   volatile int* const abort = &s.abort;
 
-  // registers follow the roles: 2 x 128 x 200 + 128 x 104 of the 384 x 168 that the launch gave
+  // Registers follow the roles: 2 x 128 x 208 + 128 x 88 of the 384 x 168 that the launch gave.  With 200 the
+  // softmax groups spill inside their loop (2048-token chunks 210 us, 200 us with 208).
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   Item w;
   bool bad;
   Raw raw = load_raw(a, blockIdx.x, items);
@@ -732,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     int count = 0;  // items so far
     const int t = warp >> 2, row = tid & 127;
     const int qi = row / a.G, gi = row - qi * a.G;
@@ -754,10 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (lane == 0) mbar_arrive(let_go);
         continue;
       }
-      const bool have = qi < qpt && i < w.queries;
-      const int p = w.p_first + min(i, w.queries - 1);
       float m = -INFINITY, l = 0.0f;
       for (int j = w.j0; j < w.j1; ++j) {
+        const bool mixed = mixed_tile(w, j);  // before the wait: shared memory's latency is out of the way
         ok = __all_sync(0xffffffffu, wait(&s.s_full[t], s_seen++ & 1, abort));
         if (!ok) break;
         tc_fence_after();
@@ -768,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tmem_ld_dep(x[1]);
         tmem_ld_dep(x[2]);
         tmem_ld_dep(x[3]);
-        if (mixed_tile(w, j)) {
+        if (mixed) {
+          const int p = w.p_first + min(i, w.queries - 1);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t bits = tile_bits(a, w, j, p, c * 32);
@@ -788,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float mn = fmaxf(m, top), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
           if (j > w.j0) {  // O of the tiles so far, complete since s_full follows their products
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32_issue(to + c * 32, o);
@@ -802,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           m = mn;
         }
         const uint64_t ref = pair2(m == -INFINITY ? 0.0f : -m);
-        uint64_t sum[2] = {0, 0};  // pairs of +0
+        uint64_t sum = 0;  // a pair of +0
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
@@ -813,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             unpair(fma2(pair(src[(2 * e) & 31], src[(2 * e + 1) & 31]), sl2x2, ref), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
-            sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(y0), __float_as_uint(y1)));
+            sum = add2(sum, pair(__float_as_uint(y0), __float_as_uint(y1)));
             pk[e] = pack_bf16(y0, y1);
           }
           tmem_st32(ts + c * 32, pk);
@@ -823,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[t]);
         float a0, a1;
-        unpair(add2(sum[0], sum[1]), a0, a1);
+        unpair(sum, a0, a1);
         l += a0 + a1;
       }
       if (!ok) break;
@@ -833,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (!ok) break;
         tc_fence_after();
       }
+      const bool have = qi < qpt && i < w.queries;
       const Sink to_row = sink_of<D>(a, w, i, gi, have);
       const bool marked = *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) == count;
       const bool again = *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) == count;
@@ -842,46 +838,54 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         to_row.part[D + 1] = l;
       }
       if (!empty) {
-        const float inv = to_row.part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-        const uint32_t align = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to_row.out));
-        uint32_t o[D / 32][32];
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        // Rolled: code that runs once an item comes from far away, and its size is time.
+        uint16_t* const mine = write ? to_row.out : nullptr;
+        const bool wide = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(mine) & 15) == 0);
+        uint8_t* const stage = s.rows[warp];
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32_issue(to + c * 32, o);
+          tmem_wait_ld(o);
+          if (a.splits > 1) {
+            if (write) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_ld32_issue(to + c * 32, o[c]);
-        tmem_wait_ld(o[0]);
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            continue;
+          }
+          // Through shared memory, so that 8 lanes write 128 bytes of a row.
 #pragma unroll
-        for (int c = 1; c < D / 32; ++c) tmem_ld_dep(o[c]);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] = pack_bf16(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          if ((c & 1) == 0) continue;
+          __syncwarp();
+#pragma unroll 4
+          for (int q = 0; q < 8; ++q) {
+            const int rr = q * 4 + (lane >> 3);
+            uint16_t* const row_out = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), rr));
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            uint16_t* const dst = row_out + (c >> 1) * 64 + (lane & 7) * 8;
+            if (!row_out) continue;
+            if (wide) {
+              *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+              const uint32_t z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) dst[e] = static_cast<uint16_t>((e < 4 ? (e < 2 ? z[0] : z[1]) : (e < 6 ? z[2] : z[3])) >> (e & 1 ? 16 : 0));
+            }
+          }
+          __syncwarp();
+        }
         tc_fence_before();  // the next item may use O
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.o_empty[t]);
-        if (write && to_row.part) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]);
-        } else if (write) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t y[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              y[e] = pack_bf16(__uint_as_float(o[c][2 * e]) * inv, __uint_as_float(o[c][2 * e + 1]) * inv);
-            if ((align & 31) == 0) {
-              st_global_32(to_row.out + c * 32, y);
-              st_global_32(to_row.out + c * 32 + 16, y + 8);
-            } else if ((align & 15) == 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4*>(to_row.out + c * 32 + e * 8) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                to_row.out[c * 32 + 2 * e] = static_cast<uint16_t>(y[e]);
-                to_row.out[c * 32 + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
-              }
-            }
-          }
-        }
         if (again && !marked) rows_plainly<D>(a, s.items[(count - 1) % kItems], t, warp & 3, lane);
       }
       __syncwarp();
