@@ -117,6 +117,15 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // True in one lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -839,10 +848,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (!empty) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        // Rolled: code that runs once an item comes from far away, and its size is time.
+        // Rolled: code that runs once an item comes from far away, and its size is time.  The rows go through
+        // shared memory, 64 columns at a time, so that 8 lanes write 128 bytes of one.
         uint16_t* const mine = write ? to_row.out : nullptr;
         const bool wide = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(mine) & 15) == 0);
-        uint8_t* const stage = s.rows[warp];
+        const uint32_t stage = smem_u32(s.rows[warp]), put = stage + lane * 128, get = stage + (lane >> 3) * 128;
+        unsigned long long rows[8];  // where the lane's 16 bytes of rows 4 q + lane / 8 go
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          rows[q] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), q * 4 + (lane >> 3));
+          if (rows[q]) rows[q] += (lane & 7) * 16;
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -856,29 +872,31 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
             continue;
           }
-          // Through shared memory, so that 8 lanes write 128 bytes of a row.
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t y[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) y[x] = pack_bf16(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            sts16(put + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
           }
           if ((c & 1) == 0) continue;
           __syncwarp();
-#pragma unroll 4
-          for (int q = 0; q < 8; ++q) {
-            const int rr = q * 4 + (lane >> 3);
-            uint16_t* const row_out = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), rr));
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-            uint16_t* const dst = row_out + (c >> 1) * 64 + (lane & 7) * 8;
-            if (!row_out) continue;
-            if (wide) {
-              *reinterpret_cast<uint4*>(dst) = v;
-            } else {
-              const uint32_t z[4] = {v.x, v.y, v.z, v.w};
+          uint4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = lds16(get + q * 512 + (((lane & 7) ^ ((q * 4 + (lane >> 3)) & 7)) << 4));
+          if (wide) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (rows[q]) *reinterpret_cast<uint4*>(rows[q] + (c >> 1) * 128) = v[q];
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint16_t* const dst = reinterpret_cast<uint16_t*>(rows[q] + (c >> 1) * 128);
+              const uint64_t z[2] = {v[q].x | static_cast<uint64_t>(v[q].y) << 32, v[q].z | static_cast<uint64_t>(v[q].w) << 32};
+              if (rows[q]) {
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) dst[e] = static_cast<uint16_t>((e < 4 ? (e < 2 ? z[0] : z[1]) : (e < 6 ? z[2] : z[3])) >> (e & 1 ? 16 : 0));
+                for (int e = 0; e < 8; ++e) dst[e] = static_cast<uint16_t>((e < 4 ? z[0] : z[1]) >> (e & 3) * 16);
+              }
             }
           }
           __syncwarp();
