@@ -18,14 +18,23 @@
 // while the last sums are still being written out.
 //
 // The running maximum is kept lazily (raised only when a logit passes it by more than 24 in
-// log2), so O is rescaled in TMEM rarely.  Sums and maxima are fp32; P is rounded to bf16 (off by
-// at most 2^-8 of itself), as the second product's operand type asks.
+// log2: P stays below 2^24 and its sums far below fp32's largest), so O is rescaled in TMEM rarely
+// (with 8 in place of 24 2048-token chunks took 5 % longer).  Sums and maxima are fp32; P is rounded
+// to bf16 (off by at most 2^-8 of itself), as the second product's operand type asks.
 //
 // A tile in which some row does not see some token ("mixed": the diagonal, the window's edge, the
 // first tokens, the list's end) takes the masked path.  There the softmax groups also look V over in
 // shared memory: tokens that no row sees are zeroed, and if a value that only some rows see is not
 // finite, the item's rows are computed again by a plain loop, so that 0 * inf never reaches a row
 // that does not see it.
+//
+// Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 189 us, 1280 TFLOP/s
+// over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 247 us, 1460
+// TFLOP/s.  What bounds it is the chain of one query tile: softmax of 128 x 128 logits (1100 to 1250
+// cycles), hand-over to the tensor core (300), its PV and its next S (1024), and back (370), since
+// with d = 128 S, S, O and O fill TMEM and the next S can only take P's place.  Two tiles in turn keep
+// the tensor core at 2048 of about 2900 cycles; an item's end and start cost another two tiles' time.
+// Halving the loads (K and V of every second tile) gained 5 % at most: they do not bound it.
 #include "zp_attn.h"
 
 #include <algorithm>

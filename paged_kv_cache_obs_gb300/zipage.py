@@ -1,4 +1,4 @@
-"""ctypes binding of libzipage.so — argument marshalling only.
+"""Binding of libzipage.so (ctypes, and zp_tensors for the per-step calls) — argument marshalling only.
 
 Every function here has the name of the C entry point it calls (include/zipage.h) and does
 nothing but turn tensors into pointers, fill the C structs and raise on a non-OK status.  All
