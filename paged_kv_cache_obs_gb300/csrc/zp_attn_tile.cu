@@ -39,6 +39,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "zp_ptx.cuh"
 
@@ -425,7 +426,8 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
 
 // Q_TMA: the queries' rows are aligned and come by TMA (one box per tile and 64-column half: the
 // group's heads of 128 / G tokens, which is the order of the tile's rows); else by plain loads.
-template <int D, bool Q_TMA>
+// PARTS: items are split, and leave sums for the joining kernel.
+template <int D, bool Q_TMA, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tq,
                                                            const __grid_constant__ AttnArgs a, int nx, int items) {
   constexpr int NH = D / 64;
@@ -858,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       if (!empty) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         // Rolled: code that runs once an item comes from far away, and its size is time.  The rows go through
-        // shared memory, 64 columns at a time, so that 8 lanes write 128 bytes of one.
-        uint16_t* const mine = write ? to_row.out : nullptr;
+        // shared memory, 128 bytes of each at a time, so that 8 lanes write one row's.
+        void* const mine = !write ? nullptr : PARTS ? static_cast<void*>(to_row.part) : to_row.out;
         const bool wide = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(mine) & 15) == 0);
         const uint32_t stage = smem_u32(s.rows[warp]), put = stage + lane * 128, get = stage + (lane >> 3) * 128;
         unsigned long long rows[8];  // where the lane's 16 bytes of rows 4 q + lane / 8 go
@@ -868,39 +870,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           rows[q] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), q * 4 + (lane >> 3));
           if (rows[q]) rows[q] += (lane & 7) * 16;
         }
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32_issue(to + c * 32, o);
-          tmem_wait_ld(o);
-          if (a.splits > 1) {
-            if (write) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<uint4*>(to_row.part + c * 32)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-            continue;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = pack_bf16(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-            sts16(put + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
-          }
-          if ((c & 1) == 0) continue;
+        const auto rows_out = [&](int at, bool wide16) {  // the staged 128 bytes of each row, `at` bytes into it
           __syncwarp();
           uint4 v[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[q] = lds16(get + q * 512 + (((lane & 7) ^ ((q * 4 + (lane >> 3)) & 7)) << 4));
-          if (wide) {
+          if (wide16) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              if (rows[q]) *reinterpret_cast<uint4*>(rows[q] + (c >> 1) * 128) = v[q];
+              if (rows[q]) *reinterpret_cast<uint4*>(rows[q] + at) = v[q];
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              uint16_t* const dst = reinterpret_cast<uint16_t*>(rows[q] + (c >> 1) * 128);
+              uint16_t* const dst = reinterpret_cast<uint16_t*>(rows[q] + at);
               const uint64_t z[2] = {v[q].x | static_cast<uint64_t>(v[q].y) << 32, v[q].z | static_cast<uint64_t>(v[q].w) << 32};
               if (rows[q]) {
 #pragma unroll 1
@@ -909,6 +891,33 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
           }
           __syncwarp();
+        };
+        if constexpr (PARTS) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_issue(to + c * 32, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sts16(put + ((e ^ (lane & 7)) << 4), make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+            rows_out(c * 128, true);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_issue(to + c * 32, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) y[x] = pack_bf16(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+              sts16(put + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+            }
+            if (c & 1) rows_out((c >> 1) * 128, wide);
+          }
         }
         tc_fence_before();  // the next item may use O
         __syncwarp();
@@ -947,20 +956,23 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
   const int64_t step = static_cast<int64_t>(a.T) * heads * (D + 4);
   float M = -INFINITY;
   bool skip = false;
-  for (int k = 0; k < a.splits; ++k) {
+  for (int k = lane; k < a.splits; k += 32) {
     const float mk = p[k * step + D];
     skip |= isnan(mk);
     M = fmaxf(M, mk);
   }
-  if (skip || lane * 4 >= D) return;
+  if (__any_sync(0xffffffffu, skip)) return;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  if (lane * 4 >= D) return;
   float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
   for (int k = 0; k < a.splits; ++k) {
-    const float mk = p[k * step + D], lk = p[k * step + D + 1];
-    if (mk == -INFINITY && lk == 0.0f) continue;  // a part that saw nothing; its sums may be unset
-    const float c = mk == -INFINITY ? 1.0f : ex2(mk - M);
-    const float4 y = *reinterpret_cast<const float4*>(p + k * step + lane * 4);
-    l = fmaf(lk, c, l);
+    const float2 ml = *reinterpret_cast<const float2*>(p + k * step + D);
+    float4 y = *reinterpret_cast<const float4*>(p + k * step + lane * 4);
+    if (ml.x == -INFINITY && ml.y == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // a part that saw nothing: its sums may be unset
+    const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
+    l = fmaf(ml.y, c, l);
     v[0] = fmaf(y.x, c, v[0]);
     v[1] = fmaf(y.y, c, v[1]);
     v[2] = fmaf(y.z, c, v[2]);
@@ -977,16 +989,16 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
 
 static_assert(sizeof(TileSmem<128>) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
-template <int D, bool Q_TMA>
+template <int D, bool Q_TMA, bool PARTS>
 cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs& a, int nx, int items, cudaStream_t st) {
   constexpr int bytes = sizeof(TileSmem<D>) + 1024;
   static PerDeviceInit attrs;
   cudaError_t e = attrs.run(
-      [] { return cudaFuncSetAttribute(tile_kernel<D, Q_TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+      [] { return cudaFuncSetAttribute(tile_kernel<D, Q_TMA, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
   if (e != cudaSuccess) return e;
-  tile_kernel<D, Q_TMA><<<std::min(items, kSms), kThreads, bytes, st>>>(tm, tq, a, nx, items);
+  tile_kernel<D, Q_TMA, PARTS><<<std::min(items, kSms), kThreads, bytes, st>>>(tm, tq, a, nx, items);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || !PARTS) return e;
   // launched while the tiles still run; it waits for them on the device
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
@@ -1043,8 +1055,15 @@ zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, co
                                          static_cast<uint64_t>(a.q_ts) * 2, 64, a.G, kRows / a.G);
   const int items = static_cast<int>(plan.items);
   cudaError_t e;
-  if (d == 128) e = q_tma ? launch<128, true>(tm, tq, a, plan.nx, items, st) : launch<128, false>(tm, tq, a, plan.nx, items, st);
-  else e = q_tma ? launch<64, true>(tm, tq, a, plan.nx, items, st) : launch<64, false>(tm, tq, a, plan.nx, items, st);
+  const auto pick = [&](auto dim, auto tma) {
+    constexpr int kD = decltype(dim)::value;
+    constexpr bool kTma = decltype(tma)::value;
+    return plan.splits > 1 ? launch<kD, kTma, true>(tm, tq, a, plan.nx, items, st) : launch<kD, kTma, false>(tm, tq, a, plan.nx, items, st);
+  };
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
+  if (d == 128) e = q_tma ? pick(D128{}, std::true_type{}) : pick(D128{}, std::false_type{});
+  else e = q_tma ? pick(D64{}, std::true_type{}) : pick(D64{}, std::false_type{});
   return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
