@@ -79,7 +79,6 @@ struct __align__(1024) TileSmem {
   uint8_t q[2][D / 64][kRows * 128];         // [tile][64-column half][row][128 B], 128-byte swizzle
   uint8_t k[kStages][D / 64][kKeys * 128];
   uint8_t v[kStages][D / 64][kKeys * 128];
-  uint8_t rows[8][32 * 128];                 // a softmax warp's output, 64 columns at a time
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems], item_empty[kItems];
@@ -134,6 +133,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // True in one lane of the (whole) warp.
@@ -859,40 +865,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (!empty) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        // Rolled: code that runs once an item comes from far away, and its size is time.  The rows go through
-        // shared memory, 128 bytes of each at a time, so that 8 lanes write one row's.
-        void* const mine = !write ? nullptr : PARTS ? static_cast<void*>(to_row.part) : to_row.out;
-        const bool wide = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(mine) & 15) == 0);
-        const uint32_t stage = smem_u32(s.rows[warp]), put = stage + lane * 128, get = stage + (lane >> 3) * 128;
-        unsigned long long rows[8];  // where the lane's 16 bytes of rows 4 q + lane / 8 go
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          rows[q] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), q * 4 + (lane >> 3));
-          if (rows[q]) rows[q] += (lane & 7) * 16;
-        }
-        const auto rows_out = [&](int at, bool wide16) {  // the staged 128 bytes of each row, `at` bytes into it
-          __syncwarp();
-          uint4 v[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = lds16(get + q * 512 + (((lane & 7) ^ ((q * 4 + (lane >> 3)) & 7)) << 4));
-          if (wide16) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (rows[q]) *reinterpret_cast<uint4*>(rows[q] + at) = v[q];
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              uint16_t* const dst = reinterpret_cast<uint16_t*>(rows[q] + at);
-              const uint64_t z[2] = {v[q].x | static_cast<uint64_t>(v[q].y) << 32, v[q].z | static_cast<uint64_t>(v[q].w) << 32};
-              if (rows[q]) {
-#pragma unroll 1
-                for (int e = 0; e < 8; ++e) dst[e] = static_cast<uint16_t>((e < 4 ? z[0] : z[1]) >> (e & 3) * 16);
-              }
-            }
-          }
-          __syncwarp();
-        };
+        // Rolled: code that runs once an item comes from far away, and its size is time.
         if constexpr (PARTS) {
+          // Through shared memory, 128 bytes of each row at a time, so that 8 lanes write one row's.  The CTA's only
+          // item is done with its queries.
+          static_assert(sizeof(s.q) >= 8 * 32 * 128, "a warp's rows");
+          const uint32_t stage = smem_u32(s.q) + warp * (32 * 128), put = stage + lane * 128, get = stage + (lane >> 3) * 128;
+          float* const mine = write ? to_row.part : nullptr;
+          unsigned long long rows[8];  // where the lane's 16 bytes of rows 4 q + lane / 8 go
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            rows[q] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), q * 4 + (lane >> 3));
+            if (rows[q]) rows[q] += (lane & 7) * 16;
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -901,22 +886,39 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               sts16(put + ((e ^ (lane & 7)) << 4), make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-            rows_out(c * 128, true);
+            __syncwarp();
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = lds16(get + q * 512 + (((lane & 7) ^ ((q * 4 + (lane >> 3)) & 7)) << 4));
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (rows[q]) *reinterpret_cast<uint4*>(rows[q] + c * 128) = v[q];
+            __syncwarp();
           }
         } else {
+          const uint32_t align = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to_row.out));
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
+            uint32_t o[32], y[16];
             tmem_ld32_issue(to + c * 32, o);
             tmem_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t y[4];
+            for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            uint16_t* const dst = to_row.out + c * 32;
+            if (!write) continue;
+            if ((align & 31) == 0) {
+              st_global_32(dst, y);
+              st_global_32(dst + 16, y + 8);
+            } else if ((align & 15) == 0) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) y[x] = pack_bf16(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-              sts16(put + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+              for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                dst[2 * e] = static_cast<uint16_t>(y[e]);
+                dst[2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
+              }
             }
-            if (c & 1) rows_out((c >> 1) * 128, wide);
           }
         }
         tc_fence_before();  // the next item may use O
