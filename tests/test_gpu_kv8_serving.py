@@ -217,3 +217,49 @@ def test_chunked_prefill_then_8_bit_decode(zp):
             _check_rows(got[0, 4 * h:4 * h + 4], qd[0, 4 * h:4 * h + 4], flat[0, h], flat[1, h], p["scale"],
                         S.window_visible(L, L + 1, window, sinks), 2.0 ** -11)
     assert zp.zp_read_error(ws) == 0
+
+
+def test_pools_past_32_bit_offsets(zp):
+    # the same requests in the first blocks of small pools and in the last blocks of pools of 4.6 GB (8-bit) and
+    # 9.2 GB (bf16), whose offsets pass 2^32; every result is the same bits
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Hq, Hkv, d, b, lens, small, big = 32, 8, 128, 16, [300, 17, 40], 40, 70000
+    used = [-(-n // b) for n in lens]
+    max_blocks, R, T = max(used), len(lens), sum(lens)
+    table = np.zeros((R, max_blocks), dtype=np.int32)
+    ids = np.random.default_rng(3).permutation(small)[:sum(used)]
+    at = 0
+    for r, n in enumerate(used):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    p = zp.make_params(dict(num_layers=2, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, block_size=b, n_max=4, window=1, alpha=0.5,
+                            beta=0.5, decay=0.9, scale=d ** -0.5, protect_window=1, causal=1))
+    kv = torch.randn((T, 2 * Hkv, d), generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn((T, Hq, d), generator=g, device="cuda").to(torch.bfloat16)
+    start = _i32(np.concatenate([[0], np.cumsum(lens)]))
+    results = []
+    for NB, shift in ((small, 0), (big, big - small)):
+        ws = zp.new_workspace(max(zp.zp_kv8_decode_workspace_size(p, R, max_blocks),
+                                  zp.zp_paged_window_workspace_size(p, T, R, max(lens), max_blocks, 100, 4),
+                                  zp.zp_paged_window_workspace_size(p, R, R, 1, max_blocks, 100, 4)))
+        tables, blocks = _i32(table + shift), _i32(ids + shift)
+        codes = torch.zeros((2, NB, 2, Hkv, b, d), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((2, NB, 2, Hkv), device="cuda")
+        zp.zp_kv8_append(codes, scales, 1, kv[:, :Hkv], kv[:, Hkv:], start, _i32([0] * R), tables, p, ws)
+        out8 = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device="cuda")
+        zp.zp_kv8_decode_attn(codes, scales, 1, q[:R], tables, _i32(lens), out8, p, ws)
+        pool = torch.zeros((2, NB, 2, Hkv, b, d), dtype=torch.bfloat16, device="cuda")
+        zp.zp_kv8_unpack_blocks(codes, scales, blocks, pool, blocks, p, ws)
+        many, few = torch.zeros_like(q), torch.zeros((R, Hq, d), dtype=torch.bfloat16, device="cuda")
+        zp.zp_paged_window_attn(pool, 1, q, start, tables, _i32(lens), many, p, ws, 100, 4, max(lens))
+        zp.zp_paged_window_attn(pool, 1, q[:R], _i32([0, 1, 2, 3]), tables, _i32(lens), few, p, ws, 100, 4, 1)
+        codes.zero_()
+        scales.zero_()
+        zp.zp_kv8_pack_blocks(pool, blocks, codes, scales, blocks, p, ws)
+        assert zp.zp_read_error(ws) == 0
+        keep = (ids + shift).tolist()
+        results.append((out8, many, few, codes[:, keep].clone(), scales[:, keep].clone(), pool[:, keep].clone()))
+        del codes, pool
+        torch.cuda.empty_cache()
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(*results))
+    assert float(results[0][1].abs().max()) > 0 and float(results[0][3].float().abs().max()) > 0
