@@ -21,7 +21,9 @@ namespace {
 // Small CTAs with few loads a thread, so that an SM holds many of them at different stages: 8192 tokens
 // of 32 heads of 128 take 21.9 us (6.1 TB/s) so, 24.3 with 256 threads, 25.1 with 4 rows a thread too.
 constexpr int kThreadsR = 128;
-constexpr int kRowsR = 2;        // rows of a thread whose loads are in flight together
+// Rows of a thread whose loads are in flight together: 3 in CTAs of one token, which have few (256 tokens of 40 heads
+// of 128 take 3.45 us so and 3.6 with 2, one token 2.8 and 3.2), 2 in those of two (see above).
+constexpr int kRowsOne = 3, kRowsR = 2;
 constexpr int kMaxTokensR = 2;   // tokens per CTA
 
 struct RopeArgs {
@@ -73,10 +75,9 @@ __device__ __forceinline__ Row row_of(const RopeArgs& a, int t, int head) {
 // item is two 16-byte vectors of a row: the two halves of 8 pairs (half layout), 8 adjacent pairs
 // (interleaved), or 16 values that pass through.  A thread keeps its place in the row and walks the
 // CTA's rows (token, head), so that no item costs a division.
-template <bool INTER>
+template <bool INTER, int U>
 __global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_constant__ zp_rope rope, const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kMaxTokensR * 128];
-  constexpr int U = kRowsR;  // rows whose loads are in flight together
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
   const int per_row = a.d >> 4, rot = a.rd >> 4, half = a.rd >> 1, heads = a.Hq + a.Hkv;
   const int walk = kThreadsR / per_row, v = threadIdx.x % per_row;  // rows of a pass; place in the row
@@ -265,8 +266,13 @@ extern "C" zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const 
   const unsigned grid = static_cast<unsigned>((T + a.tokens - 1) / a.tokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (vec) {
-    if (rope->interleaved) rope_wide_kernel<true><<<grid, kThreadsR, 0, st>>>(*rope, a);
-    else rope_wide_kernel<false><<<grid, kThreadsR, 0, st>>>(*rope, a);
+    if (a.tokens == 1) {
+      if (rope->interleaved) rope_wide_kernel<true, kRowsOne><<<grid, kThreadsR, 0, st>>>(*rope, a);
+      else rope_wide_kernel<false, kRowsOne><<<grid, kThreadsR, 0, st>>>(*rope, a);
+    } else {
+      if (rope->interleaved) rope_wide_kernel<true, kRowsR><<<grid, kThreadsR, 0, st>>>(*rope, a);
+      else rope_wide_kernel<false, kRowsR><<<grid, kThreadsR, 0, st>>>(*rope, a);
+    }
   } else {
     if (rope->interleaved) rope_any_kernel<true><<<grid, kThreadsR, 0, st>>>(*rope, a);
     else rope_any_kernel<false><<<grid, kThreadsR, 0, st>>>(*rope, a);
