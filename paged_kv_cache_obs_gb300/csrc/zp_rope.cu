@@ -24,7 +24,9 @@ constexpr int kThreadsR = 128;
 // Rows of a thread whose loads are in flight together: 3 in CTAs of one token, which have few (256 tokens of 40 heads
 // of 128 take 3.45 us so and 3.6 with 2, one token 2.8 and 3.2), 2 in those of two (see above).
 constexpr int kRowsOne = 3, kRowsR = 2;
-constexpr int kMaxTokensR = 2;   // tokens per CTA
+// Tokens per CTA: two where there are CTAs enough (2047 tokens of 40 heads take 10.6 us so and 11.3 with one),
+// one below 1024 tokens (1000 take 5.8 us with one, 6.6 with two).
+constexpr int kMaxTokensR = 2;
 
 struct RopeArgs {
   const uint16_t *q, *k;
@@ -262,7 +264,7 @@ extern "C" zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const 
   a.d = d;
   a.rd = rd;
   a.mscale = rope->mscale;
-  a.tokens = T >= kMaxTokensR * 1024 ? kMaxTokensR : 1;
+  a.tokens = T >= kMaxTokensR * 512 ? kMaxTokensR : 1;
   const unsigned grid = static_cast<unsigned>((T + a.tokens - 1) / a.tokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (vec) {
