@@ -296,6 +296,8 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
  *     until zp_read_error() reads and clears it, so one read can cover all layers of a step.
  *     Nothing else in a workspace has to hold any value.
  *   - params.scale is finite and above 0 where a call uses it.
+ *   - Kernels are launched with programmatic stream serialization: they come in while the one ahead of
+ *     them on the stream still runs, and wait for it on the device.  The stream's order is kept.
  *   - A zp_rows describes bf16 rows [tokens][heads][head_dim] whose last dimension is
  *     contiguous; strides are in elements.  Any strides are accepted; rows whose base address
  *     and strides are multiples of 16 bytes are moved with wide loads and stores.

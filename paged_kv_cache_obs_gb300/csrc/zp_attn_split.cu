@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "zp_launch.h"
 #include "zp_ptx.cuh"
 
 namespace zp {
@@ -280,6 +281,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
+  if (tid == 0) prefetch_tensormap(&tm);
+  after_previous();
+  next_may_start();
   const int split = blockIdx.x, h = blockIdx.y;
   const int r = a.ordered ? request_at(a, blockIdx.z, words, tops) : blockIdx.z;
   const int bshift = a.b == 2 * kTile ? 1 : 0;  // tiles per block, as a shift
@@ -309,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
-  if (tid == 0) prefetch_tensormap(&tm);
   __syncthreads();
 
   // Lane i holds the block id (and scales) of tile i of the warp's list, 32 tiles at a time, and the
@@ -788,7 +791,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 // Joins the parts of a row: one warp a row, in the order of the parts.
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttnArgs a, int parts, int ROWS) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's writes are visible
+  after_previous();  // the split kernel's writes are visible
+  next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int row = static_cast<int>(w % ROWS), h = static_cast<int>(w / ROWS % a.Hkv);
@@ -824,25 +828,11 @@ cudaError_t launch(const CUtensorMap& tm, const AttnArgs& a, const SplitPlan& pl
   cudaError_t e = attrs.run(
       [] { return cudaFuncSetAttribute(split_kernel<FP8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  cfg.gridDim = dim3(plan.splits, a.Hkv, a.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = plan.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  e = cudaLaunchKernelEx(&cfg, split_kernel<FP8, D, NT>, tm, a);
+  e = launch_in_order(split_kernel<FP8, D, NT>, dim3(plan.splits, a.Hkv, a.B), kThreads, smem, st, plan.cluster, tm, a);
   if (e != cudaSuccess || plan.splits == plan.cluster) return e;
-  // launched while the split kernel still runs; it waits for it on the device
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.B) * a.Hkv * plan.rows + kWarps - 1) / kWarps));
-  cfg.dynamicSmemBytes = 0;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, plan.splits / plan.cluster, plan.rows);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * plan.rows;
+  return launch_in_order(join_kernel<D>, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), kThreads, 0, st, 1, a,
+                         plan.splits / plan.cluster, plan.rows);
 }
 
 template <bool FP8>

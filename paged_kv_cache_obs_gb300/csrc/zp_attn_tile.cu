@@ -41,6 +41,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "zp_launch.h"
 #include "zp_ptx.cuh"
 
 namespace zp {
@@ -485,6 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  after_previous();
+  next_may_start();
   const uint32_t tbase = s.tmem;
   volatile int* const abort = &s.abort;
 
@@ -939,7 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 // Joins the parts of split items: one warp a row (token, head), in the order of the parts.
 template <int D>
 __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ AttnArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete and visible
+  after_previous();  // the parts are complete and visible
+  next_may_start();
   const int lane = threadIdx.x & 31, heads = a.Hkv * a.G;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int64_t t = w / heads;
@@ -998,20 +1002,10 @@ cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs&
   cudaError_t e = attrs.run(
       [] { return cudaFuncSetAttribute(tile_kernel<D, Q_TMA, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
   if (e != cudaSuccess) return e;
-  tile_kernel<D, Q_TMA, PARTS><<<std::min(items, kSms), kThreads, bytes, st>>>(tm, tq, a, nx, items);
-  e = cudaGetLastError();
+  e = launch_in_order(tile_kernel<D, Q_TMA, PARTS>, dim3(std::min(items, kSms)), kThreads, bytes, st, 1, tm, tq, a, nx, items);
   if (e != cudaSuccess || !PARTS) return e;
-  // launched while the tiles still run; it waits for them on the device
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) * a.Hkv * a.G + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, tile_join_kernel<D>, a);
+  const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv * a.G;
+  return launch_in_order(tile_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, 1, a);
 }
 
 }  // namespace

@@ -15,6 +15,7 @@
 // heads appended in 11 us (4.5 TB/s: three dependent loads, then one wave of tiles), 256 single ones in
 // 4.7 us (the same chain, with nothing behind it).
 #include "zp_internal.h"
+#include "zp_launch.h"
 
 namespace zp {
 namespace {
@@ -151,6 +152,8 @@ __global__ void __launch_bounds__(kThreadsQ, BS * D == 4096 ? 5 : 10) append_ker
   constexpr int LPR = D / 8;                 // lanes per row (8 values each)
   constexpr int RPL = 32 / LPR;              // rows per load of the warp
   constexpr int NL = BS / RPL;               // loads per tile
+  after_previous();
+  next_may_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.y * kWarpsQ + warp;
 
@@ -283,6 +286,8 @@ __device__ __forceinline__ bool take_tile(const BlockArgs& a, int64_t w, int bs,
 template <int D, int BS>
 __global__ void __launch_bounds__(kThreadsQ) pack_kernel(const BlockArgs a) {
   constexpr int NL = BS * D / 256;  // loads of 8 values a lane
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   int64_t src, dst;
   int fill;
@@ -305,6 +310,8 @@ __global__ void __launch_bounds__(kThreadsQ) pack_kernel(const BlockArgs a) {
 template <int D, int BS, bool WIDE>
 __global__ void __launch_bounds__(kThreadsQ) unpack_kernel(const BlockArgs a) {
   constexpr int NL = BS * D / 512;  // loads of 16 codes a lane
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   int64_t src, dst;
   int fill;
@@ -353,16 +360,14 @@ zp_status check_pool(const zp_kv8_pool* pool, const zp_params* p, const void* wo
 }
 
 template <int D, int BS>
-void launch_append(const AppendArgs& a, bool vec, dim3 grid, cudaStream_t st) {
-  if (vec) append_kernel<D, BS, true><<<grid, kThreadsQ, 0, st>>>(a);
-  else append_kernel<D, BS, false><<<grid, kThreadsQ, 0, st>>>(a);
+cudaError_t launch_append(const AppendArgs& a, bool vec, dim3 grid, cudaStream_t st) {
+  return launch_in_order(vec ? append_kernel<D, BS, true> : append_kernel<D, BS, false>, grid, kThreadsQ, 0, st, 1, a);
 }
 
 template <int D, int BS>
-void launch_blocks(const BlockArgs& a, bool pack, unsigned grid, cudaStream_t st) {
-  if (pack) pack_kernel<D, BS><<<grid, kThreadsQ, 0, st>>>(a);
-  else if (aligned(a.dst, 32)) unpack_kernel<D, BS, true><<<grid, kThreadsQ, 0, st>>>(a);
-  else unpack_kernel<D, BS, false><<<grid, kThreadsQ, 0, st>>>(a);
+cudaError_t launch_blocks(const BlockArgs& a, bool pack, unsigned grid, cudaStream_t st) {
+  return launch_in_order(pack ? pack_kernel<D, BS> : aligned(a.dst, 32) ? unpack_kernel<D, BS, true> : unpack_kernel<D, BS, false>,
+                         dim3(grid), kThreadsQ, 0, st, 1, a);
 }
 
 zp_status convert(const zp_kv_pool* pool, const zp_kv8_pool* kv8, bool pack, const int32_t* src_ids, const int32_t* fill,
@@ -396,14 +401,10 @@ zp_status convert(const zp_kv_pool* pool, const zp_kv8_pool* kv8, bool pack, con
   if (ctas >= (int64_t(1) << 31)) return ZP_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>(ctas);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (p->head_dim == 128) {
-    if (p->block_size == 16) launch_blocks<128, 16>(a, pack, grid, st);
-    else launch_blocks<128, 32>(a, pack, grid, st);
-  } else {
-    if (p->block_size == 16) launch_blocks<64, 16>(a, pack, grid, st);
-    else launch_blocks<64, 32>(a, pack, grid, st);
-  }
-  return cudaGetLastError() == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
+  const bool wide_heads = p->head_dim == 128, long_blocks = p->block_size == 32;
+  const cudaError_t e = wide_heads ? (long_blocks ? launch_blocks<128, 32>(a, pack, grid, st) : launch_blocks<128, 16>(a, pack, grid, st))
+                                   : (long_blocks ? launch_blocks<64, 32>(a, pack, grid, st) : launch_blocks<64, 16>(a, pack, grid, st));
+  return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
 }  // namespace
@@ -446,14 +447,10 @@ extern "C" zp_status zp_kv8_append(const zp_kv8_pool* pool, int32_t layer, const
   const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(groups));
   const bool vec = wide(k) && wide(v);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (p->head_dim == 128) {
-    if (p->block_size == 16) launch_append<128, 16>(a, vec, grid, st);
-    else launch_append<128, 32>(a, vec, grid, st);
-  } else {
-    if (p->block_size == 16) launch_append<64, 16>(a, vec, grid, st);
-    else launch_append<64, 32>(a, vec, grid, st);
-  }
-  return cudaGetLastError() == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
+  const bool wide_heads = p->head_dim == 128, long_blocks = p->block_size == 32;
+  const cudaError_t e = wide_heads ? (long_blocks ? launch_append<128, 32>(a, vec, grid, st) : launch_append<128, 16>(a, vec, grid, st))
+                                   : (long_blocks ? launch_append<64, 32>(a, vec, grid, st) : launch_append<64, 16>(a, vec, grid, st));
+  return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
 extern "C" zp_status zp_kv8_pack_blocks(const zp_kv_pool* pool, const int32_t* src_ids, const int32_t* fill,

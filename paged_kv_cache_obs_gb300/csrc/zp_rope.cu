@@ -14,6 +14,7 @@
 #include <cmath>
 
 #include "zp_internal.h"
+#include "zp_launch.h"
 
 namespace zp {
 namespace {
@@ -80,6 +81,8 @@ __device__ __forceinline__ Row row_of(const RopeArgs& a, int t, int head) {
 template <bool INTER, int U>
 __global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_constant__ zp_rope rope, const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kMaxTokensR * 128];
+  after_previous();
+  next_may_start();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
   const int per_row = a.d >> 4, rot = a.rd >> 4, half = a.rd >> 1, heads = a.Hq + a.Hkv;
   const int walk = kThreadsR / per_row, v = threadIdx.x % per_row;  // rows of a pass; place in the row
@@ -146,6 +149,8 @@ __global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_const
 template <bool INTER>
 __global__ void __launch_bounds__(kThreadsR) rope_any_kernel(const __grid_constant__ zp_rope rope, const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kMaxTokensR * 128];
+  after_previous();
+  next_may_start();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
   const int half = a.rd >> 1, per_row = half + a.d - a.rd, heads = a.Hq + a.Hkv;
   fill_table(rope, a, t0, nt, cs);
@@ -267,17 +272,9 @@ extern "C" zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const 
   a.tokens = T >= kMaxTokensR * 512 ? kMaxTokensR : 1;
   const unsigned grid = static_cast<unsigned>((T + a.tokens - 1) / a.tokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (vec) {
-    if (a.tokens == 1) {
-      if (rope->interleaved) rope_wide_kernel<true, kRowsOne><<<grid, kThreadsR, 0, st>>>(*rope, a);
-      else rope_wide_kernel<false, kRowsOne><<<grid, kThreadsR, 0, st>>>(*rope, a);
-    } else {
-      if (rope->interleaved) rope_wide_kernel<true, kRowsR><<<grid, kThreadsR, 0, st>>>(*rope, a);
-      else rope_wide_kernel<false, kRowsR><<<grid, kThreadsR, 0, st>>>(*rope, a);
-    }
-  } else {
-    if (rope->interleaved) rope_any_kernel<true><<<grid, kThreadsR, 0, st>>>(*rope, a);
-    else rope_any_kernel<false><<<grid, kThreadsR, 0, st>>>(*rope, a);
-  }
-  return cudaGetLastError() == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
+  const bool inter = rope->interleaved != 0;
+  auto* const kernel = vec && a.tokens == 1 ? (inter ? rope_wide_kernel<true, kRowsOne> : rope_wide_kernel<false, kRowsOne>)
+                       : vec                ? (inter ? rope_wide_kernel<true, kRowsR> : rope_wide_kernel<false, kRowsR>)
+                                            : (inter ? rope_any_kernel<true> : rope_any_kernel<false>);
+  return launch_in_order(kernel, dim3(grid), kThreadsR, 0, st, 1, *rope, a) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }

@@ -263,3 +263,71 @@ def test_pools_past_32_bit_offsets(zp):
         torch.cuda.empty_cache()
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(*results))
     assert float(results[0][1].abs().max()) > 0 and float(results[0][3].float().abs().max()) > 0
+
+
+def _chain(zp, steps, sync, graph=False):
+    """Operators whose inputs are the outputs of the ones before, torch's own kernels between some of them."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    p, R = zp.make_params(_params()), 3
+    q = torch.randn((R, HQ, D), generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn((R, 2 * HKV, D), generator=g, device="cuda").to(torch.bfloat16)
+    codes = torch.zeros((LAYERS, 24, 2, HKV, B, D), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((LAYERS, 24, 2, HKV), device="cuda")
+    pool = torch.zeros((LAYERS, 24, 2, HKV, B, D), dtype=torch.bfloat16, device="cuda")
+    tables, start, lens = _i32(np.arange(18).reshape(R, N_MAX)), _i32([0, 1, 2, 3]), _i32([0, 5, 30])
+    many, more = (torch.zeros((3 * R, HQ, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids, rope = _i32(np.arange(18)), zp.zp_rope_init(D, D, THETA)
+    ws = zp.new_workspace(max(zp.zp_kv8_decode_workspace_size(p, R, N_MAX), zp.zp_paged_window_workspace_size(p, 3 * R, R, 5, N_MAX, 40, 2)))
+    out8, out16 = torch.zeros_like(q), torch.zeros_like(q)
+    done = torch.cuda.synchronize if sync else (lambda: None)
+
+    def step():
+        zp.zp_rope_apply(rope, q, kv[:, :HKV], lens)
+        done()
+        zp.zp_kv8_append(codes, scales, 1, kv[:, :HKV], kv[:, HKV:], start, lens, tables, p, ws)
+        done()
+        lens.add_(1)
+        done()
+        zp.zp_kv8_decode_attn(codes, scales, 1, q, tables, lens, out8, p, ws)
+        done()
+        zp.zp_rope_apply(rope, out8, kv[:, HKV:], lens)
+        done()
+        zp.zp_kv8_unpack_blocks(codes, scales, ids, pool, ids, p, ws)
+        done()
+        zp.zp_paged_window_attn(pool, 1, out8, start, tables, lens, out16, p, ws, 40, 2, 1)
+        done()
+        many[:R] = out16
+        zp.zp_paged_window_attn(pool, 1, many, start, tables, lens, more, p, ws, 40, 2, 5)
+        done()
+        zp.zp_kv8_pack_blocks(pool, ids, codes, scales, ids, p, ws)
+        done()
+        kv.copy_(more[:R, :2 * HKV])
+        q.copy_(out16)
+        done()
+    if graph:
+        step()
+        c = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(c):
+            for _ in range(5):
+                step()
+        for _ in range(steps // 5):
+            c.replay()
+    else:
+        for _ in range(steps):
+            step()
+    assert zp.zp_read_error(ws) == 0
+    return [x.clone() for x in (q, kv, codes, scales, pool, more, out8, out16, lens)]
+
+
+def test_calls_follow_one_another_in_order(zp):
+    # kernels come in before the ones ahead of them are complete; what they compute is what calls with a
+    # synchronisation after each compute, on a stream and in a captured graph
+    want = _chain(zp, 51, True)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(want, _chain(zp, 51, False)))
+    assert all(torch.equal(x, y) for x, y in zip(want, _chain(zp, 51, False, graph=True)))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = _chain(zp, 51, False)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
