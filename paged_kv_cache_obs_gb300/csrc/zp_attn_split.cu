@@ -281,7 +281,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  if (tid == 0) prefetch_tensormap(&tm);
+  if (tid == 0) {
+    prefetch_tensormap(&tm);
+    sm_bad = 0;
+  }
+  if (lane == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+  }
   after_previous();
   next_may_start();
   const int split = blockIdx.x, h = blockIdx.y;
@@ -308,11 +315,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   const int groups = (s.tiles + SUB - 1) / SUB;
   const int todo = max(0, (groups - first + stride - 1) / stride);  // groups of SUB tiles of this warp
 
-  if (tid == 0) sm_bad = 0;
-  if (lane == 0) {
-    for (int i = 0; i < SLOTS; ++i) mbar_init(&full[warp][i], 1);
-    fence_mbar_init();
-  }
   __syncthreads();
 
   // Lane i holds the block id (and scales) of tile i of the warp's list, 32 tiles at a time, and the
