@@ -29,7 +29,7 @@
 // that does not see it.
 //
 // Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 189 us, 1280 TFLOP/s
-// over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 247 us, 1460
+// over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 244 us, 1480
 // TFLOP/s.  What bounds it is the chain of one query tile: softmax of 128 x 128 logits (1100 to 1250
 // cycles), hand-over to the tensor core (300), its PV and its next S (1024), and back (370), since
 // with d = 128 S, S, O and O fill TMEM and the next S can only take P's place.  Two tiles in turn keep

@@ -11,9 +11,9 @@
 // All kernels give a tile to one warp, which holds it in registers: values are read once, the
 // maximum is a warp reduction, and nothing is staged.  They are bound by HBM (2 bytes read and
 // 1 written a value, or the reverse).  Measured: 1016 blocks of 32 layers and 8 heads packed in 447 us
-// (7.1 TB/s), 64 blocks of 28 layers and 4 heads read back in 28 us (6.2 TB/s), 8200 new tokens of 8
-// heads appended in 11 us (4.5 TB/s: three dependent loads, then one wave of tiles), 256 single ones in
-// 4.7 us (the same chain, with nothing behind it).
+// (7.1 TB/s), 64 blocks of 28 layers and 4 heads read back in 27.6 us (6.4 TB/s), 8200 new tokens of 8
+// heads appended in 11 us (4.7 TB/s: three dependent loads, then one wave of tiles), 256 single ones in
+// 4.8 us (the same chain, with nothing behind it).
 #include "zp_internal.h"
 #include "zp_launch.h"
 

@@ -331,3 +331,43 @@ def test_calls_follow_one_another_in_order(zp):
         got = _chain(zp, 51, False)
     side.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_wait_for_other_streams_and_for_copies(zp, captured):
+    # a call behind an event of another stream, whose work takes long, and behind a copy, right after a call of
+    # the same operator
+    g = torch.Generator(device="cuda").manual_seed(5)
+    T = 64
+    fresh, other = (torch.randn((T, HQ, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    x, copied = torch.zeros_like(fresh), torch.zeros_like(fresh)
+    out, out2, scrap = torch.zeros_like(fresh), torch.zeros_like(fresh), torch.zeros_like(fresh)
+    pos = _i32(np.arange(T))
+    rope = zp.zp_rope_init(D, D, THETA)
+    want = torch.zeros_like(fresh)
+    zp.zp_rope_apply(rope, fresh, None, pos, q_out=want)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def work():
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)           # about a millisecond
+            x.copy_(fresh)
+        zp.zp_rope_apply(rope, other, None, pos, q_out=scrap)
+        main.wait_stream(side)
+        zp.zp_rope_apply(rope, x, None, pos, q_out=out)
+        copied.copy_(fresh)
+        zp.zp_rope_apply(rope, copied, None, pos, q_out=out2)
+
+    with torch.cuda.stream(main):
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                work()
+        for _ in range(5):
+            for t in (x, copied, out, out2):
+                t.zero_()
+            graph.replay() if captured else work()
+            main.synchronize()
+            assert torch.equal(out, want) and torch.equal(out2, want)
