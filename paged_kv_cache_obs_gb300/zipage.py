@@ -39,16 +39,25 @@ if not os.path.exists(_LIB_PATH):
 lib = ctypes.CDLL(_LIB_PATH)
 
 
-def _load_tensors():
-    """The compiled part of this binding (csrc/binding/zp_tensors.cpp)."""
-    path = os.path.join(os.path.dirname(_LIB_PATH), "zp_tensors.so")
-    if not os.path.exists(path):
-        raise ImportError(f"zp_tensors.so is not built ({path}); run __graft_entry__.build() "
-                          "or python -m paged_kv_cache_obs_gb300.build")
-    spec = importlib.util.spec_from_file_location("zp_tensors", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    return module
+_TENSORS_PATH = os.path.join(os.path.dirname(_LIB_PATH), "zp_tensors.so")
+
+
+class _Tensors:
+    """The compiled part of this binding (csrc/binding/zp_tensors.cpp).  It is built against one Python and
+    PyTorch and only the per-step operators need it, so the first of their calls loads it; its functions
+    become attributes here."""
+
+    def __getattr__(self, name):
+        if not os.path.exists(_TENSORS_PATH):
+            raise ImportError(f"zp_tensors.so is not built ({_TENSORS_PATH}); run __graft_entry__.build() "
+                              "or python -m paged_kv_cache_obs_gb300.build")
+        spec = importlib.util.spec_from_file_location("zp_tensors", _TENSORS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        entries = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn")
+        module.bind(*(ctypes.cast(lib["zp_" + e], _P).value for e in entries))
+        self.__dict__.update({e: getattr(module, e) for e in entries})
+        return self.__dict__[name]
 
 
 class zp_params(ctypes.Structure):
@@ -348,10 +357,7 @@ def zp_paged_decode_attn_static(pool, layer: int, q, block_tables, seq_lens, out
 # These run once per layer and step, so zp_tensors (csrc/binding) turns their tensors into the C
 # structs: it refuses (ValueError) tensors whose types, sizes, strides or devices do not go together.
 
-_t = _load_tensors()
-_t.bind(*(ctypes.cast(lib[name], _P).value for name in
-          ("zp_rope_apply", "zp_kv8_append", "zp_kv8_pack_blocks", "zp_kv8_unpack_blocks", "zp_kv8_decode_attn",
-           "zp_paged_window_attn")))
+_t = _Tensors()
 _addr = ctypes.addressof
 
 
