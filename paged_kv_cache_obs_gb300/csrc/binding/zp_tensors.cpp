@@ -59,17 +59,19 @@ zp_rows rows(PyObject* o, int dev, int64_t tokens, int64_t heads, int64_t d) {
            "] with a contiguous last dimension, all tensors on one device");
   return {t.data_ptr(), t.stride(0), t.stride(1)};
 }
-// int32 of n entries (rows of a table) or more.
-const int32_t* entries(PyObject* o, int dev, int64_t n) {
+// int32 of n entries or more, one number each (or one row of a table each).
+const int32_t* entries(PyObject* o, int dev, int64_t n, bool rows = false) {
   const at::Tensor& t = tensor(o);
-  if (t.dim() < 1 || t.size(0) < n || t.scalar_type() != at::kInt || !t.is_contiguous() || device_of(t) != dev)
-    refuse("expected a contiguous int32 tensor of " + std::to_string(n) + " entries, all tensors on one device");
+  if (t.dim() < 1 || t.size(0) < n || !(rows ? t.dim() == 2 : t.numel() == t.size(0)) || t.scalar_type() != at::kInt ||
+      !t.is_contiguous() || device_of(t) != dev)
+    refuse("expected a contiguous int32 " + (rows ? "table [" + std::to_string(n) + ", max_blocks]" : "tensor of " + std::to_string(n) + " entries") +
+           ", all tensors on one device");
   return static_cast<const int32_t*>(t.data_ptr());
 }
 const int32_t* table(PyObject* o, int dev, int64_t n, int32_t& max_blocks) {
-  const int32_t* const p = entries(o, dev, n);
+  const int32_t* const p = entries(o, dev, n, true);
   const at::Tensor& t = tensor(o);
-  if (t.dim() != 2 || t.size(1) > INT_MAX) refuse("expected a block table [requests, max_blocks]");
+  if (t.size(1) > INT_MAX) refuse("expected a block table [requests, max_blocks]");
   max_blocks = static_cast<int32_t>(t.size(1));
   return p;
 }

@@ -42,3 +42,36 @@ else:
     res = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
                          env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert res.returncode == 0, res.stderr
+
+
+def _host_args():
+    bf = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((1, 4, 2, 2, 16, 64), dtype=torch.uint8), torch.zeros((1, 4, 2, 2))
+    p = dict(num_layers=1, num_q_heads=2, num_kv_heads=2, head_dim=64, block_size=16, n_max=8, window=1, alpha=0.5, beta=0.5,
+             decay=0.9, scale=0.125, protect_window=1, causal=1)
+    return bf, codes, scales, torch.zeros((4, 6), dtype=torch.int32), p, torch.zeros(1024, dtype=torch.uint8)
+
+
+def test_index_tensors_hold_one_number_an_entry(zp):
+    """Positions, lengths and block ids with further dimensions (above 1) hold more numbers than the library would read."""
+    bf, codes, scales, tables, p, ws = _host_args()
+    pool = torch.zeros(codes.shape, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    rope = zp.zp_rope_init(64, 64, 1e4)
+    for call in (lambda: zp.zp_rope_apply(rope, bf, None, i32(4, 2)),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32(5, 2), i32(4), tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32(5), i32(4, 3), tables, p, ws),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32(5), i32(4), i32(4, 6, 2), p, ws),
+                 lambda: zp.zp_kv8_decode_attn(codes, scales, 0, bf, tables, i32(4, 2), bf, p, ws),
+                 lambda: zp.zp_paged_window_attn(pool, 0, bf, i32(5), tables, i32(4, 2), bf, p, ws, 4, 1, 1),
+                 lambda: zp.zp_paged_window_attn(pool, 0, bf, i32(5, 2), tables, i32(4), bf, p, ws, 4, 1, 1),
+                 lambda: zp.zp_kv8_pack_blocks(pool, i32(4, 2), codes, scales, i32(4), p, ws),
+                 lambda: zp.zp_kv8_pack_blocks(pool, i32(4), codes, scales, i32(4), p, ws, fill=i32(4, 2)),
+                 lambda: zp.zp_kv8_unpack_blocks(codes, scales, i32(4), pool, i32(4, 2), p, ws)):
+        with pytest.raises(ValueError, match="expected"):
+            call()
+    # a column is as good as a row of numbers
+    for call in (lambda: zp.zp_rope_apply(rope, bf, None, i32(4, 1)),
+                 lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32(5, 1), i32(4), tables, p, ws)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
