@@ -90,11 +90,13 @@ zp_kv_pool pool(PyObject* o, int dev, const zp_params& p) {
 }
 zp_kv8_pool kv8(PyObject* c, PyObject* s, int dev, const zp_params& p) {
   const at::Tensor &codes = tensor(c), &scales = tensor(s);
-  if (codes.dim() < 2 || codes.element_size() != 1 || scales.scalar_type() != at::kFloat || !codes.is_contiguous() ||
+  // E4M3, or bytes that hold its codes; other types of one byte stand for other values
+  const bool type = codes.scalar_type() == at::kFloat8_e4m3fn || codes.scalar_type() == at::kByte || codes.scalar_type() == at::kChar;
+  if (codes.dim() < 2 || !type || scales.scalar_type() != at::kFloat || !codes.is_contiguous() ||
       !scales.is_contiguous() || device_of(scales) != dev ||
       scales.numel() != p.num_layers * codes.size(1) * 2 * p.num_kv_heads ||
       codes.numel() != scales.numel() * p.block_size * p.head_dim)
-    refuse("expected contiguous codes [num_layers, blocks, 2, num_kv_heads, block_size, head_dim] of one byte a value and fp32 "
+    refuse("expected contiguous codes [num_layers, blocks, 2, num_kv_heads, block_size, head_dim] in E4M3 (float8_e4m3fn, uint8 or int8) and fp32 "
            "scales [num_layers, blocks, 2, num_kv_heads], all tensors on one device");
   return {codes.data_ptr(), static_cast<float*>(scales.data_ptr()), codes.size(1)};
 }

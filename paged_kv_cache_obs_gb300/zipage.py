@@ -389,7 +389,7 @@ def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream
 
 def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_tables, params, workspace, stream=None):
     """Quantises the new keys and values k, v [T, H_kv, d] of one layer into the 8-bit pool: codes
-    (one byte a value, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
+    (E4M3 as float8_e4m3fn, uint8 or int8, [layers, blocks, 2, H_kv, b, d]) and scales (fp32 [layers, blocks, 2, H_kv]).
     token_start [B + 1] and cached [B] are device int32 (see include/zipage.h)."""
     p = _params(params)
     st = _t.kv8_append(codes, scales, layer, k, v, token_start, cached, block_tables, _addr(p), workspace, _raw(stream))

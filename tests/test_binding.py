@@ -75,3 +75,16 @@ def test_index_tensors_hold_one_number_an_entry(zp):
                  lambda: zp.zp_kv8_append(codes, scales, 0, bf, bf, i32(5, 1), i32(4), tables, p, ws)):
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+def test_codes_are_e4m3(zp):
+    """Other types of one byte would be read as E4M3 and written with its codes."""
+    bf, codes, scales, tables, p, ws = _host_args()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    call = lambda c: zp.zp_kv8_append(c, scales, 0, bf, bf, i32(5), i32(4), tables, p, ws)
+    for t in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.bool):
+        with pytest.raises(ValueError, match="E4M3"):
+            call(codes.view(t))
+    for t in (torch.uint8, torch.int8, torch.float8_e4m3fn):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call(codes.view(t))
