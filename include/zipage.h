@@ -299,8 +299,10 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
  *   - Kernels are launched with programmatic stream serialization: they come in while the one ahead of
  *     them on the stream still runs, and wait for it on the device.  The stream's order is kept.
  *   - A zp_rows describes bf16 rows [tokens][heads][head_dim] whose last dimension is
- *     contiguous; strides are in elements.  Any strides are accepted; rows whose base address
- *     and strides are multiples of 16 bytes are moved with wide loads and stores.
+ *     contiguous; strides are in elements.  Any strides are accepted (0 for broadcast rows that are only
+ *     read), but rows that a call writes must not overlap: a stride below head_dim between several of them
+ *     is refused.  Rows whose base address and strides are multiples of 16 bytes are moved with wide
+ *     loads and stores.
  * --------------------------------------------------------------------------------------- */
 typedef struct zp_rows {
   void* data;             /* device, bf16; NULL only where the call says so */

@@ -12,7 +12,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_rows* q, const zp_rows* out,
-                const int32_t* tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
+                const int32_t* tables, const int32_t* seq_lens, int32_t T, int32_t B, int32_t max_blocks, int32_t window,
                 int32_t sinks) {
   if (!p || B < 0 || max_blocks < 1 || window < 0 || sinks < 0 || num_blocks <= 0) return ZP_ERR_INVALID_ARG;
   if (layer < 0 || layer >= p->num_layers) return ZP_ERR_INVALID_ARG;
@@ -27,6 +27,7 @@ zp_status check(const zp_params* p, int32_t layer, int64_t num_blocks, const zp_
   if (static_cast<int64_t>(max_blocks) * p->block_size > (1 << 30)) return ZP_ERR_UNSUPPORTED;
   if (B == 0) return ZP_OK;
   if (!q || !out || !q->data || !out->data || !aligned(q->data, 2) || !aligned(out->data, 2)) return ZP_ERR_INVALID_ARG;
+  if (rows_overlap(*out, T, p->num_q_heads, p->head_dim)) return ZP_ERR_INVALID_ARG;
   if (!tables || !seq_lens) return ZP_ERR_INVALID_ARG;
   return ZP_OK;
 }
@@ -78,7 +79,7 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
                                         const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
   zp::NvtxRange nvtx_range("zp_kv8_decode_attn");
   if (!pool || !pool->codes || !pool->scales) return ZP_ERR_INVALID_ARG;
-  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
   if (!aligned(pool->codes, 16) || !aligned(pool->scales, 4)) return ZP_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < zp_kv8_decode_workspace_size(p, B, max_blocks))
@@ -108,7 +109,7 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   zp::NvtxRange nvtx_range("zp_paged_window_attn");
   if (!pool || !pool->base || T < 0 || max_q < 1) return ZP_ERR_INVALID_ARG;
   if (T == 0) B = 0;  // nothing to do, and q and out may be empty
-  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, T, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
   if (!aligned(pool->base, 16) || (B > 0 && !q_start)) return ZP_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||

@@ -27,6 +27,12 @@ int num_sms();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Rows [tokens][heads][d] that a call writes and that share elements whatever the values are (broadcast ones
+// above all): each would be written several times, with different results.
+inline bool rows_overlap(const zp_rows& r, int64_t tokens, int64_t heads, int64_t d) {
+  return (tokens > 1 && r.token_stride > -d && r.token_stride < d) || (heads > 1 && r.head_stride > -d && r.head_stride < d);
+}
+
 // Runs a set-up step once per device.  Kernel attributes such as the dynamic shared-memory
 // limit belong to the device that is current when they are set, so a process that launches on
 // several devices must set them on each.  run() calls fn() with the current device's index the

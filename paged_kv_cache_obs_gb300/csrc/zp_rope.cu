@@ -243,21 +243,22 @@ extern "C" zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const 
   RopeArgs a{};
   bool vec = d % 16 == 0 && rd % 16 == 0;
   // rows are bf16 at 2-byte addresses; in place means the same rows, strides included
-  const auto take = [&](const zp_rows* in, const zp_rows* out, int& same) {
+  const auto take = [&](const zp_rows* in, const zp_rows* out, int heads, int& same) {
     if (!out || !in->data || !out->data || !aligned(in->data, 2) || !aligned(out->data, 2)) return false;
+    if (rows_overlap(*out, T, heads, d)) return false;
     same = in->data == out->data;
     if (same && (in->token_stride != out->token_stride || in->head_stride != out->head_stride)) return false;
     vec = vec && wide(in) && wide(out);
     return true;
   };
   if (Hq > 0) {
-    if (!take(q, q_out, a.inplace_q)) return ZP_ERR_INVALID_ARG;
+    if (!take(q, q_out, Hq, a.inplace_q)) return ZP_ERR_INVALID_ARG;
     a.q = static_cast<const uint16_t*>(q->data);
     a.qo = static_cast<uint16_t*>(q_out->data);
     a.q_ts = q->token_stride, a.q_hs = q->head_stride, a.qo_ts = q_out->token_stride, a.qo_hs = q_out->head_stride;
   }
   if (Hkv > 0) {
-    if (!take(k, k_out, a.inplace_k)) return ZP_ERR_INVALID_ARG;
+    if (!take(k, k_out, Hkv, a.inplace_k)) return ZP_ERR_INVALID_ARG;
     a.k = static_cast<const uint16_t*>(k->data);
     a.ko = static_cast<uint16_t*>(k_out->data);
     a.k_ts = k->token_stride, a.k_hs = k->head_stride, a.ko_ts = k_out->token_stride, a.ko_hs = k_out->head_stride;

@@ -88,3 +88,35 @@ def test_codes_are_e4m3(zp):
     for t in (torch.uint8, torch.int8, torch.float8_e4m3fn):
         with pytest.raises(ValueError, match="current CUDA device"):
             call(codes.view(t))
+
+
+def test_rows_that_are_written_do_not_overlap(zp):
+    """Broadcast or overlapping rows are refused where a call writes them: on the host, before any launch."""
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    base = (ws.data_ptr() + 255) // 256 * 256
+    _, _, _, _, p, _ = _host_args()
+    params, bad = zp.make_params(p), zp.ZP_ERR_INVALID_ARG
+    rope = zp.zp_rope_init(64, 64, 1e4)
+    good, rows = zp.zp_rows(base, 128, 64), lambda t, h: zp.zp_rows(base, t, h)
+    apply = lambda q, qo, T=2, H=2: zp.lib.zp_rope_apply(rope, q, qo, H, None, None, 0, base, T, None)
+    for T, H, t, h in ((2, 1, 0, 64), (2, 1, 32, 64), (2, 2, 128, 0), (2, 2, 128, 63), (2, 2, 0, 64), (2, 2, -8, 64)):
+        r = rows(t, h)
+        assert apply(r, r, T, H) == bad and apply(good, r, T, H) == bad            # in place, and as a result
+        params.num_q_heads, params.num_kv_heads = H, 1
+        pool8, pool = zp.zp_kv8_pool(base, base, 4), zp.zp_kv_pool(base, 4)
+        assert zp.lib.zp_kv8_decode_attn(pool8, 0, good, base, base, T, 2, 0, 0, r, params, base, 1 << 40, None) == bad
+        for mq in (1, 40):
+            assert zp.lib.zp_paged_window_attn(pool, 0, good, base, T, mq, base, base, 1, 2, 0, 0, r, params, base, 1 << 40, None) == bad
+
+
+@pytest.mark.gpu
+def test_rows_that_are_read_may_be_broadcast(zp):
+    x = torch.randn((1, 1, 64), device="cuda").to(torch.bfloat16)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    rope = zp.zp_rope_init(64, 64, 1e4)
+    a, b = (torch.zeros((5, 3, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    zp.zp_rope_apply(rope, x.expand(5, 3, 64), None, pos, q_out=a)
+    zp.zp_rope_apply(rope, x.expand(5, 3, 64).contiguous(), None, pos, q_out=b)
+    assert torch.equal(a, b) and bool((a != 0).any())
+    # one row of one head has no second one to overlap
+    zp.zp_rope_apply(rope, x, None, pos[:1], q_out=torch.empty(64, dtype=torch.bfloat16, device="cuda").as_strided((1, 1, 64), (0, 0, 1)))
