@@ -295,6 +295,11 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
  *     new_workspace does).  A call writes it only when it finds an error, and it keeps the first one
  *     until zp_read_error() reads and clears it, so one read can cover all layers of a step.
  *     Nothing else in a workspace has to hold any value.
+ *   - Attention splits few requests, or few new tokens, among more CTAs, and then asks for a larger
+ *     workspace than for a larger batch.  A call also takes a smaller one whose size is a multiple of 256
+ *     bytes, as the sizes of all these operators are, and then splits its work less: one workspace can serve
+ *     a batch that grows and shrinks, at full speed if it is the largest that any of its sizes asks for.
+ *     The splits decide how sums are grouped, so a row's last bit may depend on the workspace's size.
  *   - params.scale is finite and above 0 where a call uses it.
  *   - Kernels are launched with programmatic stream serialization: they come in while the one ahead of
  *     them on the stream still runs, and wait for it on the device.  The stream's order is kept.

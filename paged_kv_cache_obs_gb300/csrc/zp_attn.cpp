@@ -58,6 +58,13 @@ AttnArgs args_of(const zp_params* p, int32_t layer, int64_t num_blocks, const zp
   return a;
 }
 
+// A workspace of a call that asks for `need` bytes.  Fewer are taken if they are a multiple of 256 bytes,
+// as the sizes of other batches and of other operators are: a batch that has shrunk asks for more than it
+// did when it was large, since it is split further.  Any other number is not a workspace's size.
+bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
+  return workspace && aligned(workspace, 256) && bytes >= kHeader && (bytes >= need || bytes % 256 == 0);
+}
+
 bool sizes_ok(const zp_params* p, int32_t B, int32_t max_blocks) {
   return p && B >= 0 && max_blocks >= 1 && p->num_kv_heads > 0 && p->num_q_heads > 0 &&
          p->num_q_heads % p->num_kv_heads == 0 && p->num_q_heads / p->num_kv_heads <= 16 && p->head_dim > 0 && p->block_size > 0;
@@ -82,15 +89,14 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
   const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
   if (!aligned(pool->codes, 16) || !aligned(pool->scales, 4)) return ZP_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < zp_kv8_decode_workspace_size(p, B, max_blocks))
-    return ZP_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, zp_kv8_decode_workspace_size(p, B, max_blocks))) return ZP_ERR_INVALID_ARG;
   if (B == 0) return ZP_OK;
   AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
   a.pool = static_cast<const uint8_t*>(pool->codes);
   a.scales = pool->scales;
   a.T = B;
   a.max_q = 1;
-  return split_launch(a, p, true, split_plan(p, B, 1, max_blocks, window, sinks), workspace,
+  return split_launch(a, p, true, split_plan(p, B, 1, max_blocks, window, sinks, workspace_bytes), workspace,
                       reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -112,8 +118,7 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, T, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
   if (!aligned(pool->base, 16) || (B > 0 && !q_start)) return ZP_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks))
+  if (!workspace_ok(workspace, workspace_bytes, zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks)))
     return ZP_ERR_INVALID_ARG;
   if (B == 0) return ZP_OK;
   AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
@@ -124,7 +129,7 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   a.max_q = std::min(max_q, max_blocks * p->block_size);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
-    return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks), workspace, st);
+    return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
   }
-  return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks), workspace, st);
+  return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
 }

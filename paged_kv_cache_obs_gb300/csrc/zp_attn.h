@@ -34,7 +34,9 @@ struct SplitPlan {
   bool ordered;  // long requests first
   size_t bytes;
 };
-SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks);
+// `room`: bytes of the workspace; what does not fit it is split among fewer CTAs.
+constexpr size_t kHeader = 256;  // of a workspace: the error word
+SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX);
 
 // Launches the split kernel (and the one that joins its parts).
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st);
@@ -46,7 +48,7 @@ struct TilePlan {
   int64_t items;
   size_t bytes;
 };
-TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks);
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX);
 
 // Launches the tiled kernel (rows above kMaxSplitRows), and the one that joins the parts.
 zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);

@@ -1017,7 +1017,7 @@ cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs&
 
 }  // namespace
 
-TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks) {
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room) {
   TilePlan plan{};
   int64_t tokens = static_cast<int64_t>(max_blocks) * p->block_size;
   const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
@@ -1030,11 +1030,13 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
   if (window > 0) tokens = std::min(tokens, static_cast<int64_t>(window) + per_item + sinks + 2 * p->block_size);
   const int64_t tiles = (tokens + kKeys - 1) / kKeys;
   // a part has four tiles at least: below that its sums cost more than the tiles
-  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(items, 1), tiles / 4)));
+  const size_t part = static_cast<size_t>(std::max(T, 1)) * p->num_q_heads * (p->head_dim + 4) * sizeof(float);  // of every row
+  const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
+  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(kSms / std::max<int64_t>(items, 1), tiles / 4), fit)));
   plan.nx = static_cast<int>(std::min<int64_t>(nx, INT_MAX));
   plan.items = nx * heads * plan.splits;
-  plan.bytes = 256;
-  if (plan.splits > 1) plan.bytes += static_cast<size_t>(plan.splits) * T * p->num_q_heads * (p->head_dim + 4) * sizeof(float);
+  plan.bytes = kHeader;
+  if (plan.splits > 1 && T > 0) plan.bytes += (plan.splits * part + 255) / 256 * 256;
   return plan;
 }
 
@@ -1042,7 +1044,7 @@ zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, co
   if (plan.items > INT_MAX / 2) return ZP_ERR_UNSUPPORTED;
   if (plan.splits > 1 && static_cast<int64_t>(a.T) * p->num_q_heads > INT_MAX) return ZP_ERR_UNSUPPORTED;  // rows to join
   a.err = static_cast<int32_t*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeader);
   a.splits = plan.splits;
   const int d = p->head_dim;
   CUtensorMap tm, tq{};

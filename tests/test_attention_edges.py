@@ -1,0 +1,125 @@
+"""Calls at the edges of the attention operators around the cache: workspaces of other sizes, values
+that are not finite or very large, strides, and waits that run out."""
+import math
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import test_cache_attention as A
+from oracle import serving_oracle as S
+
+
+@pytest.fixture(scope="module")
+def zp():
+    from paged_kv_cache_obs_gb300 import build
+    if not os.path.exists(build.LIB):
+        build.build()
+    from paged_kv_cache_obs_gb300 import zipage
+    return zipage
+
+
+def _i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32).cuda()
+
+
+# ------------------------------------------------------------------ workspaces ----------------
+
+def test_workspace_sizes_are_multiples_of_256(zp):
+    # the sizes that a call takes although it asks for more
+    for Hq, Hkv, d, b in A.SHAPES:
+        p = A._params(Hq, Hkv, d, b)
+        for B in (1, 2, 3, 5, 17, 300):
+            for mb in (1, 40, 777, 8192):
+                sizes = [zp.zp_kv8_decode_workspace_size(p, B, mb)]
+                sizes += [zp.zp_paged_window_workspace_size(p, B * n, B, n, mb, w, 4) for n in (1, 3, 40, 700) for w in (0, 1000)]
+                assert all(x >= 256 and x % 256 == 0 for x in sizes)
+
+
+def _exact(q, k, v, visible, scale):
+    """Rows q [.., d] over k, v [L, d] in 64 bits: the outputs and the weighted magnitudes.  visible [.., L]."""
+    x = (scale * (q.double() @ k.double().T)).masked_fill(~visible, -math.inf)
+    w = torch.softmax(x, -1)
+    return w @ v.double(), w @ v.double().abs()
+
+
+def _visible(pos, L, window, sinks):
+    t = torch.arange(L, device="cuda")
+    p = torch.as_tensor(pos, device="cuda")[..., None]
+    return (t <= p) & ((t > p - window) | (t < sinks) | (window == 0))
+
+
+def _tokens(pool, layer, table, kv, h, L):
+    return pool[layer][table.long()][:, kv, h].reshape(-1, pool.shape[-1])[:L]
+
+
+def _check_rows(got, want, mass, rel):
+    err = (got.double() - want).abs()
+    tol = 2.0 ** -8 * want.abs() + (rel + 2.0 ** -14) * mass + 1e-30        # as in test_cache_attention
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def _check_kv8(codes, scales, layer, q, tables, seq, out, p, ws=None, window=0, sinks=0, rel=2.0 ** -11):
+    Hkv, G = p["num_kv_heads"], p["num_q_heads"] // p["num_kv_heads"]
+    pool = codes.view(torch.float8_e4m3fn).double() * scales.double()[..., None, None]
+    for r, L in enumerate(seq.tolist()):
+        vis = _visible(L - 1, L, window, sinks)
+        for h in range(Hkv):
+            k, v = (_tokens(pool, layer, tables[r][:-(-L // p["block_size"])], i, h, L) for i in (0, 1))
+            _check_rows(out[r, h * G:(h + 1) * G], *_exact(q[r, h * G:(h + 1) * G], k, v, vis, p["scale"]), rel)
+
+
+def _check_window(pool, layer, q, start, tables, seq, out, p, ws, window, sinks, max_q, rel):
+    Hkv, G = p["num_kv_heads"], p["num_q_heads"] // p["num_kv_heads"]
+    start = start.tolist()
+    for r, L in enumerate(seq.tolist()):
+        n = start[r + 1] - start[r]
+        vis = _visible(range(L - n, L), L, window, sinks)[:, None].expand(n, G, L)
+        rows = slice(start[r], start[r + 1])
+        for h in range(Hkv):
+            k, v = (_tokens(pool, layer, tables[r][:-(-L // p["block_size"])], i, h, L) for i in (0, 1))
+            heads = slice(h * G, (h + 1) * G)
+            _check_rows(out[rows, heads], *_exact(q[rows, heads], k, v, vis, p["scale"]), rel)
+
+
+def _with_workspaces(args, sizes, call, check):
+    """The call of `args` (output at 6, workspace at 8) with workspaces of other sizes and a band behind each."""
+    for n in sizes:
+        buf = torch.zeros(n + 512, dtype=torch.uint8, device="cuda")
+        buf[n:] = 0xA5
+        a = list(args)
+        a[8], a[6] = buf[:n], torch.full_like(args[6], 7.0)
+        for _ in range(2):
+            call(*a)
+        torch.cuda.synchronize()
+        assert bool((buf[n:] == 0xA5).all()) and int(buf[:4].view(torch.int32)) == 0
+        check(*a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[40000], [9000, 5], [3000, 2000, 70, 1]])
+def test_decode_with_the_workspace_of_a_larger_batch(zp, lens):
+    # 256 bytes: what a batch that is not split asks for, whose last requests these may be
+    args = A._kv8_case(zp, 8, 2, 128, 16, lens, seed=len(lens), hidden_nan=False)
+    p, mb = args[7], args[4].shape[1]
+    own = zp.zp_kv8_decode_workspace_size(p, len(lens), mb)
+    assert zp.zp_kv8_decode_workspace_size(p, 500, mb) == 256 and own > 256
+    _with_workspaces(args, (256, own // 512 * 256, own, own + 256), zp.zp_kv8_decode_attn, _check_kv8)
+    for n in (255, 300, own - 1):                               # no workspace's size
+        with pytest.raises(zp.ZipageError):
+            zp.zp_kv8_decode_attn(*args[:8], torch.zeros(n, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,window", [(2, 0), (2, 3000), (70, 0), (300, 0)])
+def test_window_with_the_workspace_of_a_larger_batch(zp, new, window):
+    rel = A.SPLIT if new <= 4 else A.TILED
+    args = A._window_case(zp, 4, 1, 64, 16, [9000], [new], window, 4, seed=new, rel=rel)
+    p, mb = args[7], args[4].shape[1]
+    own = zp.zp_paged_window_workspace_size(p, new, 1, new, mb, window, 4)
+    assert own > 256 and args[8].numel() == own
+    _with_workspaces(args, (256, own // 512 * 256, own, own + 256), zp.zp_paged_window_attn,
+                     lambda *a: _check_window(*a, rel=rel))
+    with pytest.raises(zp.ZipageError):
+        zp.zp_paged_window_attn(*args[:8], torch.zeros(own - 1, dtype=torch.uint8, device="cuda"), *args[9:])
