@@ -18,7 +18,10 @@
 // E4M3 codes are converted to f16, which holds them exactly; queries are brought to f16 by a power
 // of two per row, the block's K scale joins the logit scale, and its V scale multiplies the tile's
 // own product, so scales of any size cost no precision.  P is f16 (11 bits; the accumulators and
-// the sum are fp32).  With a bf16 pool P is a bf16 part plus a bf16 remainder (16 bits).
+// the sum are fp32).  With a bf16 pool P is a bf16 part plus a bf16 remainder (off by at most 2^-16).  The part
+// is P cut off and P's lowest bit is set, so that the remainder of a weight is above 0 as well: both times
+// an infinite value are that infinity (a remainder of 0 or below made it NaN).  Weights below 2^-103 have
+// no room for it.
 //
 // The running maximum is kept lazily: a row's reference is raised only when a logit passes it by
 // more than 8 (in log2), so that P stays below 2^8 and most tiles need one vote in place of
@@ -682,9 +685,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t hi = pack_bf16(x[sub][nt][2 * e], x[sub][nt][2 * e + 1]);
-            ph[nt][e] = transpose8(hi);
-            pl[nt][e] = transpose8(pack_bf16(x[sub][nt][2 * e] - lo_f(hi), x[sub][nt][2 * e + 1] - hi_f(hi)));
+            // 0 stays 0: the bit alone is rounded away
+            const uint32_t y0 = __float_as_uint(x[sub][nt][2 * e]) | 1u, y1 = __float_as_uint(x[sub][nt][2 * e + 1]) | 1u;
+            ph[nt][e] = transpose8(__byte_perm(y0, y1, 0x7632));
+            pl[nt][e] = transpose8(pack_bf16(__uint_as_float(y0) - hi_f(y0), __uint_as_float(y1) - hi_f(y1)));
           }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {

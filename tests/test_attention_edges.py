@@ -123,3 +123,71 @@ def test_window_with_the_workspace_of_a_larger_batch(zp, new, window):
                      lambda *a: _check_window(*a, rel=rel))
     with pytest.raises(zp.ZipageError):
         zp.zp_paged_window_attn(*args[:8], torch.zeros(own - 1, dtype=torch.uint8, device="cuda"), *args[9:])
+
+
+# ------------------------------------------------------------------ special values ------------
+
+def _same(got, want, mass, rel, where):
+    """Finite where the exact value is, within the tolerance of test_cache_attention; else the same infinity
+    or NaN."""
+    nan, fin = np.isnan(want), np.isfinite(want)
+    assert np.array_equal(nan, np.isnan(got)), (where, got[nan != np.isnan(got)][:4], want[nan != np.isnan(got)][:4])
+    assert np.array_equal(want[~nan & ~fin], got[~nan & ~fin]), where
+    err = np.abs(got[fin] - want[fin])
+    assert (err <= A._tolerance(want[fin], mass[fin], rel)).all(), (where, float(err.max()))
+
+
+def _window_rows(zp, x, cached, new, q, window, sinks, rel, b=16, max_q=None, ordered=False):
+    """Requests over a bf16 pool whose keys and values are x [B][2][Hkv][L][d] (float64): every row
+    against 64 bits over the tokens that it sees."""
+    B, Hkv, d = len(x), x[0].shape[1], x[0].shape[-1]
+    T, Hq, _ = q.shape
+    G = Hq // Hkv
+    lens = [y.shape[2] for y in x]
+    rng = np.random.default_rng(0)
+    tables, NB = A._tables(rng, lens, b)
+    pool = torch.zeros((1, NB, 2, Hkv, b, d), dtype=torch.bfloat16)
+    for r in range(B):
+        for t in range(lens[r]):
+            pool[0, tables[r, t // b], :, :, t % b] = torch.from_numpy(x[r][:, :, t]).to(torch.bfloat16)
+    kv = [torch.from_numpy(y).to(torch.bfloat16).double().numpy() for y in x]
+    qb = torch.from_numpy(q).to(torch.bfloat16)
+    out = torch.full(qb.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    p = A._params(Hq, Hkv, d, b)
+    start = np.concatenate([[0], np.cumsum(new)])
+    mq = max_q or max(new)
+    ws = zp.new_workspace(zp.zp_paged_window_workspace_size(p, T, B, mq, tables.shape[1], window, sinks))
+    zp.zp_paged_window_attn(pool.cuda(), 0, qb.cuda(), _i32(start), _i32(tables), _i32(lens), out, p, ws, window, sinks, mq)
+    assert zp.zp_read_error(ws) == 0
+    got, qd = out.double().cpu().numpy(), qb.double().numpy()
+    for r in range(B):
+        for i in range(new[r]):
+            vis = S.window_visible(cached[r] + i, lens[r], window, sinks)
+            for h in range(Hq):
+                with np.errstate(all="ignore"):
+                    want, mass = S.attention_row(qd[start[r] + i, h], kv[r][0, h // G], kv[r][1, h // G], p["scale"], vis)
+                want = np.where(np.isfinite(want) & (np.abs(want) >= 3.3961775292304958e38), np.sign(want) * np.inf, want)  # past bf16
+                _same(got[start[r] + i, h], want, mass, rel, (r, i, h))
+    return got
+
+
+FORMS = [(1, A.SPLIT), (3, A.SPLIT), (70, A.TILED)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,rel", FORMS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 20)])
+def test_infinite_values_of_tokens_that_are_seen(zp, new, rel, window, sinks):
+    # an infinity that a row sees makes its output infinite, two of different signs NaN; beside the
+    # row's largest weight, early, late, and in tiles that only some rows see
+    rng = np.random.default_rng(new)
+    L, d = 300 + new, 64
+    x = rng.standard_normal((2, 2, L, d))
+    q = rng.standard_normal((new, 4, d)) * 2
+    for t, dim, value in ((3, 0, math.inf), (17, 1, -math.inf), (299, 2, math.inf), (L - 1, 3, math.inf), (L - 1, 4, -math.inf),
+                          (L - 1, 5, math.nan), (10, 6, math.inf), (12, 6, -math.inf), (280, 7, math.inf), (L - 1, 7, -math.inf)):
+        x[1, 0, t, dim] = value
+    x[0, 1, L - 1] = 3 * q[-1, 2]        # the second kv head's last token takes nearly all of the weight
+    x[1, 1, L - 1, :8] = math.inf
+    _window_rows(zp, [x], [300], [new], q, window, sinks, rel)
+
