@@ -221,11 +221,12 @@ __device__ __forceinline__ void join(float (&v)[4], float& l, float4 y, float yl
   v[3] = fmaf(y.w, w, v[3]);
 }
 
-// Four dims of an output row: sums over the sum of weights (0 where nothing is seen).
+// Four dims of an output row: sums over the sum of weights.  Zeros where there are no tokens; a row whose
+// logits are all -inf has weights of 0 alone, and is 0 / 0 like the softmax of them.
 __device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int h, int row, int dim, const float (&v)[4], float l) {
   const int i = row / a.G, g = row - i * a.G;
   uint16_t* const o = a.out + (s.q0 + i) * a.o_ts + (h * a.G + g) * a.o_hs + dim;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = s.L == 0 ? 0.0f : 1.0f / l;
   const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
   if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);

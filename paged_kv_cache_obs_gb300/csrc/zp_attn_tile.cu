@@ -380,7 +380,7 @@ __device__ __noinline__ void rows_plainly(const AttnArgs& a, const Item& w, int 
         s.part[D + 1] = l;
       }
     } else {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = 1.0f / l;
 #pragma unroll
       for (int e = 0; e < DL; e += 2) {
         const uint32_t y = pack_bf16(o[e] * inv, o[e + 1] * inv);
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         to_row.part[D + 1] = l;
       }
       if (!empty) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = 1.0f / l;  // a row sees itself; logits of -inf alone give 0 / 0, as their softmax
         // Rolled: code that runs once an item comes from far away, and its size is time.
         if constexpr (PARTS) {
           // Through shared memory, 128 bytes of each row at a time, so that 8 lanes write one row's.  The CTA's only
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
     v[2] = fmaf(y.z, c, v[2]);
     v[3] = fmaf(y.w, c, v[3]);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = 1.0f / l;
   uint16_t* const out = a.out + t * a.o_ts + head * a.o_hs + lane * 4;
   const uint32_t y0 = pack_bf16(v[0] * inv, v[1] * inv), y1 = pack_bf16(v[2] * inv, v[3] * inv);
   out[0] = static_cast<uint16_t>(y0);

@@ -191,3 +191,31 @@ def test_infinite_values_of_tokens_that_are_seen(zp, new, rel, window, sinks):
     x[1, 1, L - 1, :8] = math.inf
     _window_rows(zp, [x], [300], [new], q, window, sinks, rel)
 
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,rel", FORMS)
+def test_rows_whose_logits_are_all_minus_infinity_are_nan(zp, new, rel):
+    # as the softmax of them is; the second request is an ordinary one
+    rng = np.random.default_rng(1)
+    L, d = 40 + new, 64
+    x = [rng.standard_normal((2, 1, L, d)) for _ in range(2)]
+    q = rng.standard_normal((2 * new, 4, d))
+    q[:new, :2, 5], q[:new, 2:, 5] = 1.0, -1.0
+    x[0][0, 0, :, 5] = -math.inf           # rows of heads 0 and 1: all -inf; of heads 2 and 3: all inf
+    got = _window_rows(zp, x, [40, 40], [new, new], q, 0, 0, rel)
+    assert np.isnan(got[:new]).all() and np.isfinite(got[new:]).all()
+
+
+@pytest.mark.gpu
+def test_8_bit_rows_whose_logits_are_all_minus_infinity_are_nan(zp):
+    p = A._params(2, 1, 64, 16)
+    codes = torch.full((1, 4, 2, 1, 16, 64), 0x38, dtype=torch.uint8, device="cuda")   # 1.0
+    q = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q[0] = -math.inf
+    q[1, 0, :] = 1.0
+    out = torch.full_like(q, 7.0)
+    ws = zp.new_workspace(zp.zp_kv8_decode_workspace_size(p, 3, 4))
+    zp.zp_kv8_decode_attn(codes, torch.ones((1, 4, 2, 1), device="cuda"), 0, q, _i32([[0, 1, 2, 3]] * 3), _i32([40, 50, 0]), out, p, ws)
+    assert zp.zp_read_error(ws) == 0
+    assert bool(torch.isnan(out[0]).all()) and bool((out[1] == 1).all()) and bool((out[2] == 0).all())
+
