@@ -23,9 +23,9 @@
 // an infinite value are that infinity (a remainder of 0 or below made it NaN).  Weights below 2^-103 have
 // no room for it.
 //
-// The running maximum is kept lazily: a row's reference is raised only when a logit passes it by
-// more than 8 (in log2), so that P stays below 2^8 and most tiles need one vote in place of
-// reductions and rescaling.
+// The running maximum is kept lazily: a row's reference is set 8 (in log2) above the largest logit so far,
+// and again only when a logit passes it, so that most tiles need one vote in place of reductions and
+// rescaling.  P is at most 1, so sums over V overflow no earlier than the weighted sum itself.
 //
 // Grid (split, kv head, request), 4 warps a CTA; a row's visible 16-token tiles are dealt evenly
 // over its splits.  Up to 8 splits are one thread-block cluster, which joins its sums through
@@ -53,6 +53,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                    // tokens
 constexpr float kLazy = 8.0f;
+constexpr float kGain = 256.0f;              // 2^kLazy
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) raise |= fmaxf(x[sub][nt][e], x[sub][nt][e + 2]) > m[nt][e] + kLazy;
+        for (int e = 0; e < 2; ++e) raise |= fmaxf(x[sub][nt][e], x[sub][nt][e + 2]) > m[nt][e];
     }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > m[nt][e]) {
+          mx += kLazy;
+          if (mx > m[nt][e]) {  // every row whose maximum has grown, once some row's has to
             const float corr = ex2(m[nt][e] - mx);  // 0 from -inf
             m[nt][e] = mx;
             l[nt][e] *= corr;
@@ -612,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         // o is in units of vref, which follows the tiles' V scales: P times their ratio is what
         // meets the codes.  A ratio above 64 raises vref; one below 1/64 would cost P its small
         // values (f16 has 2^-24), so such a tile's product is made by itself and scaled in fp32.
+        // P times 2^8 (kGain), which the sums are brought back by, is what f16 holds of it: its values are
+        // normal down to 2^-14 of a reference that is up to 2^8 above the largest.
         if (fabsf(vs[sub]) > 64.0f * vref) {
           const float next = fmaxf(fabsf(vs[sub]), 1.17549435e-38f), corr = vref / next;
 #pragma unroll
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         }
         const float ratio = vs[sub] * vinv;
         const bool small = fabsf(ratio) < 0.015625f;
-        const float pm = small ? 1.0f : ratio;
+        const float pm = small ? kGain : ratio * kGain;
         uint32_t ph[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -734,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         sm_m[warp][row] = m[nt][e];
         sm_l[warp][row] = sum;
       }
-      const float unit = FP8 ? vref : 1.0f;
+      const float unit = FP8 ? vref : 1.0f, gain = FP8 ? 1.0f / kGain : 1.0f;
       float4* const dst = reinterpret_cast<float4*>(sm_acc) + (warp * ROWS + row) * (D / 4);
 #pragma unroll
       for (int mt = 0; mt < MT; mt += 2) {
         // FP8: dims (D/8) g + 2 mt .. + 3;  bf16: dims 8 (g + 8 (mt / 4)) + 2 (mt % 4) .. + 3
         const int dim = FP8 ? (D / 8) * g + 2 * mt : 8 * (g + 8 * (mt >> 2)) + 2 * (mt & 3);
-        dst[acc_at<FP8>(row, dim / 4)] = make_float4(o[nt][mt][e] * unit, o[nt][mt][e + 2] * unit, o[nt][mt + 1][e] * unit,
-                                                     o[nt][mt + 1][e + 2] * unit);
+        dst[acc_at<FP8>(row, dim / 4)] = make_float4(o[nt][mt][e] * gain * unit, o[nt][mt][e + 2] * gain * unit,
+                                                     o[nt][mt + 1][e] * gain * unit, o[nt][mt + 1][e + 2] * gain * unit);
       }
     }
   __syncthreads();

@@ -17,9 +17,10 @@
 // softmax, the tensor core multiplies for the other tile; the next item's first products start
 // while the last sums are still being written out.
 //
-// The running maximum is kept lazily (raised only when a logit passes it by more than 24 in
-// log2: P stays below 2^24 and its sums far below fp32's largest), so O is rescaled in TMEM rarely
-// (with 8 in place of 24 2048-token chunks took 5 % longer).  Sums and maxima are fp32; P is rounded
+// The running maximum is kept lazily: a row's reference is set 24 (in log2) above the largest logit so
+// far, and again only when a logit passes it, so O is rescaled in TMEM rarely (with 8 in place of 24
+// 2048-token chunks took 5 % longer).  P is at most 1, so sums over V overflow no earlier than the
+// weighted sum itself; weights below 2^-102 of the largest are 0.  Sums and maxima are fp32; P is rounded
 // to bf16 (off by at most 2^-8 of itself), as the second product's operand type asks.
 //
 // A tile in which some row does not see some token ("mixed": the diagonal, the window's edge, the
@@ -809,8 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float mn = fmaxf(m, top), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
+        if (__any_sync(0xffffffffu, top > m)) {
+          const float mn = fmaxf(m, top + kLazy), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
           if (j > w.j0) {  // O of the tiles so far, complete since s_full follows their products
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {

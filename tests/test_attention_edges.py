@@ -219,3 +219,48 @@ def test_8_bit_rows_whose_logits_are_all_minus_infinity_are_nan(zp):
     assert zp.zp_read_error(ws) == 0
     assert bool(torch.isnan(out[0]).all()) and bool((out[1] == 1).all()) and bool((out[2] == 0).all())
 
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,rel", FORMS)
+def test_values_near_the_types_largest(zp, new, rel):
+    # Finite values of up to 2^122 with logits that rise from tile to tile by what the running maximum lets
+    # pass before it is raised: weights are at most 1, and 300 tokens of them stay far below fp32's largest.
+    rng = np.random.default_rng(2)
+    L, d = 300 + new, 64
+    x = rng.standard_normal((2, 1, L, d)) * 0.01
+    x[1] = np.sign(x[1]) * 2.0 ** 122 * rng.uniform(0.5, 1.0, x[1].shape)
+    q = np.zeros((new, 4, d))
+    q[:, :, 0] = 8.0                                   # logit = x[0][.., 0] (scale 1/8)
+    x[0, 0, :, 0] = 0.0
+    x[0, 0, 150, 0], x[0, 0, 260, 0] = 5.25, 14.0      # 7.6 and 20.2 in log2
+    _window_rows(zp, [x], [300], [new], q, 0, 0, rel)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_8_bit_values_near_the_types_largest(zp, d):
+    rng = np.random.default_rng(3)
+    p = A._params(1, 1, d, 16, scale=0.125)
+    NB, L = 16, 256
+    codes = S.e4m3_encode(rng.uniform(128, 256, (1, NB, 2, 1, 16, d)))           # values of 2^121 to 2^122
+    codes[0, :, 0] = 0
+    codes[0, 10, 0, 0, 3, 0] = S.e4m3_encode(np.array(5.0))                       # 7.2 in log2, in a warp's second tile or later
+    scales = np.ones((1, NB, 2, 1), dtype=np.float32)
+    scales[:, :, 1] = 2.0 ** 114
+    q = torch.zeros((1, 1, d), dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0] = 8.0
+    # one long request among many: a warp takes a quarter of its tiles, one after another
+    B = 700
+    seq = np.zeros(B, dtype=np.int32)
+    seq[0] = L
+    qs = q.expand(B, 1, d).contiguous()
+    out = torch.zeros_like(qs)
+    ws = zp.new_workspace(zp.zp_kv8_decode_workspace_size(p, B, NB))
+    tables = np.zeros((B, NB), dtype=np.int32)
+    tables[0] = np.arange(NB)
+    zp.zp_kv8_decode_attn(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 0, qs, _i32(tables), _i32(seq), out, p, ws)
+    assert zp.zp_read_error(ws) == 0
+    k, v = (S.e4m3_decode(codes[0, :, i, 0]).reshape(-1, d) * float(scales[0, 0, i, 0]) for i in (0, 1))
+    want, mass = S.attention_row(qs[0, 0].double().cpu().numpy(), k, v, p["scale"], np.ones(L, dtype=bool))
+    _same(out[0, 0].double().cpu().numpy(), want, mass, 2.0 ** -11, "row")
+
