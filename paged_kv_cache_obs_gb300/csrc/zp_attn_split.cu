@@ -16,8 +16,8 @@
 //   - P goes from the accumulator layout (a lane holds tokens) to the operand layout (a lane holds
 //     a row) with movmatrix.
 // E4M3 codes are converted to f16, which holds them exactly; queries are brought to f16 by a power
-// of two per row, the block's K scale joins the logit scale, and its V scale multiplies the tile's
-// own product, so scales of any size cost no precision.  P is f16 (11 bits; the accumulators and
+// of two per row, the block's K scale joins the logit scale, and its V scale multiplies P or the tile's
+// own product, so that scales of any size cost no precision.  P is f16 (11 bits; the accumulators and
 // the sum are fp32).  With a bf16 pool P is a bf16 part plus a bf16 remainder (off by at most 2^-16).  The part
 // is P cut off and P's lowest bit is set, so that the remainder of a weight is above 0 as well: both times
 // an infinite value are that infinity (a remainder of 0 or below made it NaN).  Weights below 2^-103 have
@@ -53,7 +53,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                    // tokens
 constexpr float kLazy = 8.0f;
-constexpr float kGain = 256.0f;              // 2^kLazy
+constexpr float kGain = 32768.0f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -612,11 +612,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
       }
       if constexpr (FP8) {
         // o is in units of vref, which follows the tiles' V scales: P times their ratio is what
-        // meets the codes.  A ratio above 64 raises vref; one below 1/64 would cost P its small
-        // values (f16 has 2^-24), so such a tile's product is made by itself and scaled in fp32.
-        // P times 2^8 (kGain), which the sums are brought back by, is what f16 holds of it: its values are
-        // normal down to 2^-14 of a reference that is up to 2^8 above the largest.
-        if (fabsf(vs[sub]) > 64.0f * vref) {
+        // meets the codes.  vref is the largest scale so far, so the ratio is at most 1, and P times it
+        // and kGain = 2^15 fits f16: all 11 bits down to 2^-29 of the row's reference.  A ratio below 1/8
+        // would cost small weights more than three powers of two of that, so such a tile's product is made
+        // by itself and scaled in fp32: in sum, weights keep 11 bits down to 2^-18 of the row's largest
+        // (where the reference stands at most 2^8 above it), and 2^-28 of it is the last that counts.
+        if (fabsf(vs[sub]) > vref) {
           const float next = fmaxf(fabsf(vs[sub]), 1.17549435e-38f), corr = vref / next;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           vinv = 1.0f / next;
         }
         const float ratio = vs[sub] * vinv;
-        const bool small = fabsf(ratio) < 0.015625f;
+        const bool small = fabsf(ratio) < 0.125f;
         const float pm = small ? kGain : ratio * kGain;
         uint32_t ph[NT][2];
 #pragma unroll

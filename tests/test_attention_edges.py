@@ -264,3 +264,41 @@ def test_8_bit_values_near_the_types_largest(zp, d):
     want, mass = S.attention_row(qs[0, 0].double().cpu().numpy(), k, v, p["scale"], np.ones(L, dtype=bool))
     _same(out[0, 0].double().cpu().numpy(), want, mass, 2.0 ** -11, "row")
 
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ratio", [1.5, 3.0, 30.0, 60.0, 500.0, 2.0 ** 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_8_bit_values_behind_a_block_of_a_larger_scale(zp, d, ratio):
+    # Blocks of weight 0 with a V scale `ratio` times the others' come first; then one token of each warp's
+    # tiles takes most of the weight with a value of 0, and the result is the sum of 4000 equal weights of
+    # e^-9 of it: an error of one weight is the result's.
+    p = A._params(1, 1, d, 16, scale=0.125)
+    first = 8 if d == 64 else 4                        # a tile, or two of them, for each of the four warps
+    NB = 2 * first + 256
+    L = NB * 16
+    codes = np.zeros((1, NB, 2, 1, 16, d), dtype=np.uint8)
+    enc = lambda v: S.e4m3_encode(np.array(float(v)))
+    codes[0, :, 0, 0, :, 0] = enc(-9)
+    codes[0, :, 1, 0] = enc(1.5)
+    codes[0, :first, 0, 0, :, 0] = enc(-88)
+    codes[0, first:2 * first, 0, 0, 0, 0] = 0
+    codes[0, first:2 * first, 1, 0, 0] = 0
+    scales = np.ones((1, NB, 2, 1), dtype=np.float32)
+    scales[0, :, 1] = 2.0 ** -6
+    scales[0, :first, 1] = 2.0 ** -6 * ratio
+    B = 700                                            # not split: 4 warps take every fourth tile
+    seq = np.zeros(B, dtype=np.int32)
+    seq[0] = L
+    qs = torch.zeros((B, 1, d), dtype=torch.bfloat16, device="cuda")
+    qs[:, 0, 0] = 8.0
+    out = torch.zeros_like(qs)
+    tables = np.zeros((B, NB), dtype=np.int32)
+    tables[0] = np.arange(NB)
+    ws = zp.new_workspace(zp.zp_kv8_decode_workspace_size(p, B, NB))
+    zp.zp_kv8_decode_attn(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 0, qs, _i32(tables), _i32(seq), out, p, ws)
+    assert zp.zp_read_error(ws) == 0
+    kv = S.e4m3_decode(codes[0]) * scales[0].astype(np.float64)[..., None, None]
+    k, v = (kv[:, i, 0].reshape(-1, d) for i in (0, 1))
+    want, mass = S.attention_row(qs[0, 0].double().cpu().numpy(), k, v, p["scale"], np.ones(L, dtype=bool))
+    _same(out[0, 0].double().cpu().numpy(), want, mass, 2.0 ** -11, "row")
+
