@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
     }
     float mult = 1.0f;
     if (FP8) {
-      // to f16 by a power of two that brings the row's largest magnitude to [1, 2): values below
-      // 2^-14 of it lose bits, far below what the fp32 sums hold
+      // to f16 by a power of two that brings the row's largest magnitude to [2^14, 2^15): exact for values
+      // down to 2^-31 of it (8 bits fit f16's subnormals from 2^-17 on), less than the fp32 sums hold
       uint32_t m = 0;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
@@ -425,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         for (int e = 0; e < 2; ++e) m = max(m, max(qb[nt][ks][e] & 0x7FFFu, (qb[nt][ks][e] >> 16) & 0x7FFFu));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int ex = min(max(static_cast<int>(m >> 7), 1), 253);  // biased exponent, both 2^+-(ex - 127) are normal
-      const float inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-      mult = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+      const int ex = min(max(static_cast<int>(m >> 7), 15), 253);  // biased exponent, both 2^+-(ex - 141) are normal
+      const float inv = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+      mult = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

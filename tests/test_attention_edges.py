@@ -302,3 +302,22 @@ def test_8_bit_values_behind_a_block_of_a_larger_scale(zp, d, ratio):
     want, mass = S.attention_row(qs[0, 0].double().cpu().numpy(), k, v, p["scale"], np.ones(L, dtype=bool))
     _same(out[0, 0].double().cpu().numpy(), want, mass, 2.0 ** -11, "row")
 
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gain", [2.0 ** 10, 2.0 ** 16, 2.0 ** 24])
+def test_8_bit_queries_with_one_large_value(zp, gain):
+    # a value of the query `gain` times the others, where the keys are 0: the logits are the others'
+    rng = np.random.default_rng(5)
+    p = A._params(4, 1, 128, 16)
+    NB = 13
+    codes = S.e4m3_encode(np.clip(rng.standard_normal((1, NB, 2, 1, 16, 128)) * 64, -448, 448))
+    codes[0, :, 0, 0, :, 77] = 0
+    scales = np.full((1, NB, 2, 1), 2.0 ** -6, dtype=np.float32)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 128)) * 2).to(torch.bfloat16)
+    q[:, :, 77] = gain
+    args = (torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 0, q.cuda(), _i32([np.arange(NB)] * 2), _i32([200, 33]),
+            torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda"), p, zp.new_workspace(zp.zp_kv8_decode_workspace_size(p, 2, NB)))
+    zp.zp_kv8_decode_attn(*args)
+    assert zp.zp_read_error(args[8]) == 0
+    _check_kv8(*args)
