@@ -24,10 +24,11 @@
 // to bf16 (off by at most 2^-8 of itself), as the second product's operand type asks.
 //
 // A tile in which some row does not see some token ("mixed": the diagonal, the window's edge, the
-// first tokens, the list's end) takes the masked path.  There the softmax groups also look V over in
-// shared memory: tokens that no row sees are zeroed, and if a value that only some rows see is not
-// finite, the item's rows are computed again by a plain loop, so that 0 * inf never reaches a row
-// that does not see it.
+// first tokens, the list's end) takes the masked path.  There a warp also looks V over in shared memory:
+// tokens that no row sees are zeroed, and so are values that are not finite and that only some rows see
+// (0 * inf must not reach the others).  The rows that do see them get them added to their sums at the
+// item's end: an infinity or NaN times a weight above 0 is itself, so no weight has to be known.  That
+// takes a look at the tiles concerned alone, about 10 us each, however long the cache is.
 //
 // Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 189 us, 1280 TFLOP/s
 // over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 244 us, 1480
@@ -87,7 +88,8 @@ struct __align__(1024) TileSmem {
   uint32_t tmem;
   int abort;
   Item items[kItems];
-  int bad[kFlags], redo[kFlags];             // the last item (counted from 1) that a block id or a value marked
+  int bad[kFlags], odd[kFlags];              // the last item (counted from 1) that a block id or a value marked
+  int odd_lo[kFlags], odd_hi[kFlags];        // the first and last tile with such values
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -321,80 +323,96 @@ __device__ __forceinline__ Sink sink_of(const AttnArgs& a, const Item& w, int i,
   return s;
 }
 
-// Rows of one query tile by plain loops: one warp per row, a lane per token for the logits and a lane
-// per dims for the sums.  For the rare inputs that the tiles cannot take.
+// Whether the 8 tokens from t0 on, which stand in one block, are seen by every row of the item.
+__device__ __forceinline__ bool whole8(const AttnArgs& a, const Item& w, int t0) {
+  return t0 + 7 <= w.p_first && (a.window == 0 || t0 > w.p_last - a.window || t0 + 7 < a.sinks);
+}
+// Whether some row of the item sees token t.
+__device__ __forceinline__ bool seen_by_some(const AttnArgs& a, const Item& w, int t) {
+  return t <= w.p_last && (a.window == 0 || t > w.p_first - a.window || t < a.sinks);
+}
+// Whether the low or the high bf16 of a word is not finite.
+__device__ __forceinline__ bool odd_lo(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ bool odd_hi(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }
+
+// Adds what look_over took out of V in tiles lo to hi to the rows of one query tile that see it, whose
+// results stand in memory: 32 rows a warp, D / 32 dims a lane.  Rolled and a call of its own: with its loop over
+// tokens unrolled, calls that never come here took 1 % longer.
 template <int D>
-__device__ __noinline__ void rows_plainly(const AttnArgs& a, const Item& w, int t, int warp, int lane) {
-  constexpr int DL = D / 32;
+__device__ __noinline__ void add_odd_values(const AttnArgs& a, const Item& w, int lo, int hi, int t, int warp, int lane) {
+  constexpr int DW = D / 64;  // words of a lane
   const int qpt = kRows / a.G;
   const int64_t tile_values = static_cast<int64_t>(a.b) * D;  // of a (block, K|V, head)
-  const uint16_t* const pool = reinterpret_cast<const uint16_t*>(a.pool);
-  for (int rr = warp; rr < qpt * a.G; rr += 4) {
-    const int i = t * qpt + rr / a.G, g = rr % a.G, p = w.p_first + i;
-    if (i >= w.queries) break;
-    const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs;
-    float m = -INFINITY, l = 0.0f, o[DL];
+  const uint16_t* const pool = reinterpret_cast<const uint16_t*>(a.pool) + lane * (2 * DW);
+  for (int e = lo * (kKeys / 8); e < (hi + 1) * (kKeys / 8); ++e) {
+    const int j = e / (kKeys / 8), t0 = token_of(a, w, j, e % (kKeys / 8) * 8);
+    if (!mixed_tile(w, j) || e * 8 >= w.blocks * a.b || whole8(a, w, t0)) continue;
+    const int64_t phys = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + t0 / a.b];
+    const uint16_t* const k = pool + ((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 * a.Hkv + w.h) * tile_values + t0 % a.b * D;
+    const uint16_t* const v = k + a.Hkv * tile_values;
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < DL; ++e) o[e] = 0.0f;
-    for (int j = w.j0; j < w.j1; ++j)
-      for (int c0 = 0; c0 < kKeys; c0 += 32) {
-        const int e = j * kKeys + c0 + lane, tok = token_of(a, w, j, c0 + lane);
-        const bool on = e < w.blocks * a.b && sees(a, p, tok);
-        float x = -INFINITY;
-        const uint16_t* kv = nullptr;
-        if (on) {
-          const int64_t phys = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + tok / a.b];
-          kv = pool + (((static_cast<int64_t>(a.layer) * a.num_blocks + phys) * 2 * a.Hkv + w.h) * tile_values) + (tok % a.b) * D;
-          x = 0.0f;
-          for (int dd = 0; dd < D; ++dd) x = fmaf(lo_f(q[dd]), lo_f(kv[dd]), x);
-          x *= a.sl2;
-        }
-        float mx = x;
+    for (int c = 0; c < 8; ++c)
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        const float mn = fmaxf(m, mx);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float corr = m == -INFINITY ? 1.0f : ex2(m - ref);
-        const float pt = on ? ex2(x - ref) : 0.0f;
-        m = mn;
-        l *= corr;
+      for (int i = 0; i < DW; ++i) top = max_u16x2(top, reinterpret_cast<const uint32_t*>(v + c * D)[i] & 0x7FFF7FFFu);
+    if (!__any_sync(0xffffffffu, odd_lo(top) || odd_hi(top))) continue;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      uint32_t x[DW];
+      bool odd = false;
 #pragma unroll
-        for (int e2 = 0; e2 < DL; ++e2) o[e2] *= corr;
-        uint32_t vote = __ballot_sync(0xffffffffu, on);
-        while (vote) {
-          const int src = __ffs(vote) - 1;
-          vote &= vote - 1;
-          const float ps = __shfl_sync(0xffffffffu, pt, src);
-          const uint16_t* const vt = reinterpret_cast<const uint16_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kv), src)) + a.Hkv * tile_values;
-          l += ps;
-#pragma unroll
-          for (int e2 = 0; e2 < DL; ++e2) o[e2] = fmaf(ps, lo_f(vt[lane * DL + e2]), o[e2]);
-        }
+      for (int i = 0; i < DW; ++i) {
+        x[i] = reinterpret_cast<const uint32_t*>(v + c * D)[i];
+        odd |= odd_lo(x[i]) || odd_hi(x[i]);
       }
-    const Sink s = sink_of<D>(a, w, i, g, true);
-    if (s.part) {
+      if (!seen_by_some(a, w, t0 + c) || !__any_sync(0xffffffffu, odd)) continue;
+      // A weight of 0 (a logit of -inf) makes NaN of it, and only an infinite key can give one; a key of
+      // NaN has made the whole row NaN.
+      uint32_t kw[DW];
+      bool inf = false, nan = false;
 #pragma unroll
-      for (int e = 0; e < DL; ++e) s.part[lane * DL + e] = o[e];
-      if (lane == 0) {
-        s.part[D] = m;
-        s.part[D + 1] = l;
+      for (int i = 0; i < DW; ++i) {
+        kw[i] = reinterpret_cast<const uint32_t*>(k + c * D)[i];
+        inf |= odd_lo(kw[i]) || odd_hi(kw[i]);
+        nan |= (kw[i] & 0x7FFFu) > 0x7F80u || (kw[i] & 0x7FFF0000u) > 0x7F800000u;
       }
-    } else {
-      const float inv = 1.0f / l;
+      if (__any_sync(0xffffffffu, nan)) continue;
+      inf = __any_sync(0xffffffffu, inf);
+      for (int rr = warp * 32; rr < warp * 32 + 32; ++rr) {
+        const int qi = rr / a.G, i = t * qpt + qi;
+        if (qi >= qpt || i >= w.queries) break;
+        if (!sees(a, w.p_first + i, t0 + c)) continue;
+        bool nothing = false;
+        if (inf) {
+          const uint16_t* const q = a.q + (w.q0 + w.i0 + i) * a.q_ts + (w.h * a.G + rr - qi * a.G) * a.q_hs + lane * (2 * DW);
+          float dot = 0.0f;
 #pragma unroll
-      for (int e = 0; e < DL; e += 2) {
-        const uint32_t y = pack_bf16(o[e] * inv, o[e + 1] * inv);
-        s.out[lane * DL + e] = static_cast<uint16_t>(y);
-        s.out[lane * DL + e + 1] = static_cast<uint16_t>(y >> 16);
+          for (int d = 0; d < DW; ++d) {
+            dot = fmaf(lo_f(q[2 * d]), lo_f(kw[d]), dot);
+            dot = fmaf(lo_f(q[2 * d + 1]), __uint_as_float(kw[d] & 0xFFFF0000u), dot);
+          }
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+          nothing = dot == -INFINITY;
+        }
+        const Sink to = sink_of<D>(a, w, i, rr - qi * a.G, true);
+#pragma unroll
+        for (int d = 0; d < 2 * DW; ++d) {
+          const uint32_t word = x[d >> 1];
+          if (!(d & 1 ? odd_hi(word) : odd_lo(word))) continue;
+          const float value = nothing ? NAN : d & 1 ? __uint_as_float(word & 0xFFFF0000u) : lo_f(word);
+          const int dim = lane * (2 * DW) + d;
+          if (to.part) to.part[dim] += value;
+          else to.out[dim] = static_cast<uint16_t>(pack_bf16(lo_f(to.out[dim]) + value, 0.0f));
+        }
       }
     }
   }
 }
 
-// Looks V of mixed tile j over in shared memory (one warp): tokens that no row sees are zeroed; true (in
-// some lane) if a value that only some rows see is not finite.  8 tokens at a time, which are tokens
-// of one block; a lane holds 16-byte chunk lane % (D / 8) of every (256 / D)th of them.
+// Looks V of mixed tile j over in shared memory (one warp): tokens that no row sees are zeroed, and values
+// that are not finite where only some rows see them; true if there were any of those.  8 tokens at a
+// time, which are tokens of one block; a lane holds 16-byte chunk lane % (D / 8) of every (256 / D)th of them.
 template <int D>
 __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int j, uint8_t* v, int lane) {
   constexpr int kPer = 256 / D, kLoads = 8 / kPer;
@@ -407,9 +425,9 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
   }
   // lane g < 16: whether the g-th 8 tokens need a look (blocks past the list's end are zeros)
   const int t0 = token_of(a, w, j, (lane & 15) * 8);
-  const bool whole = t0 + 7 <= w.p_first && (a.window == 0 || t0 > w.p_last - a.window || t0 + 7 < a.sinks);
   const bool listed = j * kKeys + (lane & 15) * 8 < w.blocks * a.b;
-  uint32_t todo = __ballot_sync(0xffffffffu, listed && !whole) & 0xFFFFu;
+  const uint32_t look = __ballot_sync(0xffffffffu, listed && !whole8(a, w, t0)) & 0xFFFFu;
+  uint32_t todo = look;
   uint32_t top = 0;
   while (todo) {
     const int g = __ffs(todo) - 1;
@@ -420,8 +438,7 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
     for (int y = 0; y < kLoads; ++y) x[y] = *reinterpret_cast<const uint4*>(at[y] + g * 1024);
 #pragma unroll
     for (int y = 0; y < kLoads; ++y) {
-      const int t = tk + y * kPer;
-      if (t <= w.p_last && (a.window == 0 || t > w.p_first - a.window || t < a.sinks)) {
+      if (seen_by_some(a, w, tk + y * kPer)) {
         top = max_u16x2(max_u16x2(top, x[y].x & 0x7FFF7FFFu), x[y].y & 0x7FFF7FFFu);
         top = max_u16x2(max_u16x2(top, x[y].z & 0x7FFF7FFFu), x[y].w & 0x7FFF7FFFu);
       } else {
@@ -429,7 +446,22 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
       }
     }
   }
-  return (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+  if (!__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u)) return false;
+  for (todo = look; todo; todo &= todo - 1) {
+    const int g = __ffs(todo) - 1;
+#pragma unroll 1
+    for (int y = 0; y < kLoads; ++y) {
+      uint32_t* const x = reinterpret_cast<uint32_t*>(v + (ch >> 3) * (kKeys * 128) + (y * kPer + sub) * 128 + (((ch & 7) ^ (y * kPer + sub)) << 4) + g * 1024);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        uint32_t z = x[i];
+        if (odd_lo(z)) z &= 0xFFFF0000u;
+        if (odd_hi(z)) z &= 0x0000FFFFu;
+        x[i] = z;
+      }
+    }
+  }
+  return true;
 }
 
 // Q_TMA: the queries' rows are aligned and come by TMA (one box per tile and 64-column half: the
@@ -474,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(&s.item_empty[i], 8);
     }
     s.abort = 0;
-    for (int i = 0; i < kFlags; ++i) s.bad[i] = s.redo[i] = 0;
+    for (int i = 0; i < kFlags; ++i) s.bad[i] = s.odd[i] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm);
     if (Q_TMA) prefetch_tensormap(&tq);
@@ -616,7 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         go = __all_sync(0xffffffffu, wait(&s.v_mixed[st], (seen_mixed >> st) & 1, abort));
         if (!go) break;
         seen_mixed ^= 1u << st;
-        if (look_over<D>(a, w, j, s.v[st][0], lane)) *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) = count;
+        if (look_over<D>(a, w, j, s.v[st][0], lane) && lane == 0) {
+          const int f = count % kFlags;
+          if (s.odd[f] != count) s.odd[f] = count, s.odd_lo[f] = j;
+          s.odd_hi[f] = j;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.v_clean[st]);
@@ -861,8 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const bool have = qi < qpt && i < w.queries;
       const Sink to_row = sink_of<D>(a, w, i, gi, have);
       const bool marked = *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) == count;
-      const bool again = *reinterpret_cast<volatile int*>(&s.redo[count % kFlags]) == count;
-      const bool write = have && !marked && !again;
+      const bool odd = *reinterpret_cast<volatile int*>(&s.odd[count % kFlags]) == count;
+      const bool write = have && !marked;
       if (to_row.part && (write || marked || empty)) {
         to_row.part[D] = marked ? NAN : m;  // a maximum is never NaN: marks a part with a bad block id
         to_row.part[D + 1] = l;
@@ -928,7 +964,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tc_fence_before();  // the next item may use O
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.o_empty[t]);
-        if (again && !marked) rows_plainly<D>(a, s.items[(count - 1) % kItems], t, warp & 3, lane);
+        if (odd && !marked) {
+          __syncwarp();  // the rows as written
+          const volatile int* const lo = &s.odd_lo[count % kFlags], *const hi = &s.odd_hi[count % kFlags];
+          add_odd_values<D>(a, s.items[(count - 1) % kItems], *lo, *hi, t, warp & 3, lane);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(let_go);

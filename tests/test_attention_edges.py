@@ -321,3 +321,64 @@ def test_8_bit_queries_with_one_large_value(zp, gain):
     zp.zp_kv8_decode_attn(*args)
     assert zp.zp_read_error(args[8]) == 0
     _check_kv8(*args)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,heads,cached,new", [(64, 8, 100000, 5120), (128, 2, 20000, 300), (64, 1, 40000, 70)])
+def test_odd_values_in_a_long_cache_cost_little_and_stay_where_they_are_seen(zp, d, heads, cached, new):
+    # A value that only the last rows see is not finite: they get it in its dimension, every other result
+    # keeps its bits, and the call stays far inside the time that its waits allow (whole items, and items
+    # whose tiles are split).
+    g = torch.Generator(device="cuda").manual_seed(d)
+    L = cached + new
+    nb = -(-L // 16)
+    pool = torch.randn((1, nb, 2, heads, 16, d), generator=g, device="cuda").to(torch.bfloat16)
+    tables = torch.randperm(nb, generator=g, device="cuda").to(torch.int32)[None]
+    q = torch.randn((new, heads, d), generator=g, device="cuda").to(torch.bfloat16)
+    p = A._params(heads, heads, d, 16)
+    ws = zp.new_workspace(zp.zp_paged_window_workspace_size(p, new, 1, new, nb, 0, 0))
+
+    def run():
+        out = torch.full_like(q, 7.0)
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        ev[0].record()
+        zp.zp_paged_window_attn(pool, 0, q, _i32([0, new]), tables, _i32([L]), out, p, ws, 0, 0, new)
+        ev[1].record()
+        assert zp.zp_read_error(ws) == 0
+        return out, ev[0].elapsed_time(ev[1])
+
+    places = [(L - 1, 5, math.nan, 0), (L - 40, 9, math.inf, 0), (L - 3, 9, -math.inf, 0), (L - new + 1, 20, -math.inf, heads - 1),
+              (L - new // 2, 33, math.inf, heads - 1)]
+    for t, dim, _, h in places:
+        pool[0, tables[0, t // 16], 1, h, t % 16, dim] = 0
+    want, _ = run()
+    for t, dim, value, h in places:
+        pool[0, tables[0, t // 16], 1, h, t % 16, dim] = value
+    got, ms = run()
+    row = torch.arange(cached, L, device="cuda")
+    for t, dim, value, h in places:
+        seen = row >= t
+        want[seen, h, dim] = want[seen, h, dim] + value
+    assert torch.equal(torch.nan_to_num(got.float(), nan=1e38, posinf=2e38, neginf=-2e38),
+                       torch.nan_to_num(want.float(), nan=1e38, posinf=2e38, neginf=-2e38))
+    assert ms < 200
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (100, 20), (130, 300)])
+@pytest.mark.parametrize("d,Hq,Hkv,b", [(64, 4, 2, 16), (128, 7, 1, 32)])
+def test_odd_keys_and_values_anywhere(zp, window, sinks, d, Hq, Hkv, b):
+    # infinities and NaN in keys, in values and in both of a token: 0 times an infinity is NaN where an infinite
+    # key gives a weight of 0
+    rng = np.random.default_rng(d + window)
+    cached, new = [150, 0], [70, 200]
+    x = [rng.standard_normal((2, Hkv, c + n, d)) for c, n in zip(cached, new)]
+    q = np.abs(rng.standard_normal((sum(new), Hq, d)))
+    for r in range(2):
+        L = x[r].shape[2]
+        for t in rng.choice(L, 6, replace=False):
+            x[r][1, rng.integers(Hkv), t, rng.integers(d, size=2)] = rng.choice([math.inf, -math.inf, math.nan])
+        t, h = L - 30, Hkv - 1
+        x[r][0, h, t, 3], x[r][1, h, t, 8] = -math.inf, math.inf          # weight 0: NaN in dim 8
+        x[r][0, 0, L - 9, 4], x[r][1, 0, L - 9, 1] = math.nan, math.inf   # rows that see it: NaN
+    _window_rows(zp, x, cached, new, q, window, sinks, A.TILED, b=b)
