@@ -428,6 +428,7 @@ zp_status zp_kv8_unpack_blocks(const zp_kv8_pool* kv8, const int32_t* src_ids, c
  *   seq_lens      device int32 [B], 0 <= L <= max_blocks * b.  0 (a padded row): zeros are written.
  *   workspace     >= zp_kv8_decode_workspace_size() bytes, 256-byte aligned.
  * A bad seq_len or block id: that row (request and kv head) is not written, ZP_ERR_BAD_TABLE.
+ * ZP_ERR_TIMEOUT (a wait inside the kernel gave up) as for zp_compress: the output is undefined.
  * Table entries of blocks that are not visible may hold anything.  head_dim 64 or 128, block_size
  * 16 or 32, up to 16 query heads per kv head. */
 zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables,
@@ -461,6 +462,21 @@ zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_r
 
 size_t zp_paged_window_workspace_size(const zp_params* params, int32_t T, int32_t B, int32_t max_q,
                                       int32_t max_blocks, int32_t window, int32_t sinks);
+
+/* Test hooks of the bounded waits inside the two attention operators: same operation, arguments and
+ * workspace, plus stall_limit_ns (1 .. 1e9).  With the first copies (and products) in flight a warp of
+ * each CTA waits, for at most stall_limit_ns, on a barrier that nothing completes.  That wait
+ * runs out, the kernel drains what is in flight, records ZP_ERR_TIMEOUT and returns; the output rows are
+ * undefined, nothing else is written, and the next call is an ordinary one. */
+zp_status zp_test_kv8_decode_stalled(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables,
+                                     const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window, int32_t sinks,
+                                     const zp_rows* out, const zp_params* params, void* workspace, size_t workspace_bytes,
+                                     int64_t stall_limit_ns, zp_stream stream);
+zp_status zp_test_paged_window_stalled(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                       int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                       int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                       const zp_params* params, void* workspace, size_t workspace_bytes,
+                                       int64_t stall_limit_ns, zp_stream stream);
 
 /* Synchronises `stream`, copies the error word at the start of `workspace` to *out_status and
  * clears it.  Returns ZP_ERR_CUDA if the copy fails. */

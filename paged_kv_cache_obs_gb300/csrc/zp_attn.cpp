@@ -70,21 +70,10 @@ bool sizes_ok(const zp_params* p, int32_t B, int32_t max_blocks) {
          p->num_q_heads % p->num_kv_heads == 0 && p->num_q_heads / p->num_kv_heads <= 16 && p->head_dim > 0 && p->block_size > 0;
 }
 
-}  // namespace
-}  // namespace zp
-
-using namespace zp;
-
-extern "C" size_t zp_kv8_decode_workspace_size(const zp_params* p, int32_t B, int32_t max_blocks) {
-  if (!sizes_ok(p, B, max_blocks)) return 0;
-  return split_plan(p, B, 1, max_blocks, 0, 0).bytes;
-}
-
-extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
-                                        const int32_t* block_tables, const int32_t* seq_lens, int32_t B,
-                                        int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
-                                        const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
-  zp::NvtxRange nvtx_range("zp_kv8_decode_attn");
+// The two calls; stall_ns != 0 only from the test hooks.
+zp_status kv8_decode(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables, const int32_t* seq_lens,
+                     int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out, const zp_params* p,
+                     void* workspace, size_t workspace_bytes, zp_stream stream, uint64_t stall_ns) {
   if (!pool || !pool->codes || !pool->scales) return ZP_ERR_INVALID_ARG;
   const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, B, max_blocks, window, sinks);
   if (s != ZP_OK) return s;
@@ -96,23 +85,15 @@ extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, 
   a.scales = pool->scales;
   a.T = B;
   a.max_q = 1;
+  a.stall_ns = stall_ns;
   return split_launch(a, p, true, split_plan(p, B, 1, max_blocks, window, sinks, workspace_bytes), workspace,
                       reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q,
-                                                 int32_t max_blocks, int32_t window, int32_t sinks) {
-  if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
-  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
-    return tile_plan(p, T, B, max_q, max_blocks, window, sinks).bytes;
-  return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
-}
-
-extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
-                                          int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
-                                          int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
-                                          const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
-  zp::NvtxRange nvtx_range("zp_paged_window_attn");
+zp_status paged_window(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start, int32_t T, int32_t max_q,
+                       const int32_t* block_tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
+                       int32_t sinks, const zp_rows* out, const zp_params* p, void* workspace, size_t workspace_bytes,
+                       zp_stream stream, uint64_t stall_ns) {
   if (!pool || !pool->base || T < 0 || max_q < 1) return ZP_ERR_INVALID_ARG;
   if (T == 0) B = 0;  // nothing to do, and q and out may be empty
   const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, T, B, max_blocks, window, sinks);
@@ -127,9 +108,67 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   a.T = T;
   // a request of more tokens than its blocks hold is refused by its length in any case
   a.max_q = std::min(max_q, max_blocks * p->block_size);
+  a.stall_ns = stall_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
     return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
   }
   return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+}
+
+bool stall_ok(int64_t ns) { return ns >= 1 && ns <= 1000000000; }
+
+}  // namespace
+}  // namespace zp
+
+using namespace zp;
+
+extern "C" size_t zp_kv8_decode_workspace_size(const zp_params* p, int32_t B, int32_t max_blocks) {
+  if (!sizes_ok(p, B, max_blocks)) return 0;
+  return split_plan(p, B, 1, max_blocks, 0, 0).bytes;
+}
+
+extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q,
+                                                 int32_t max_blocks, int32_t window, int32_t sinks) {
+  if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
+  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
+    return tile_plan(p, T, B, max_q, max_blocks, window, sinks).bytes;
+  return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
+}
+
+extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
+                                        const int32_t* block_tables, const int32_t* seq_lens, int32_t B,
+                                        int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                        const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_kv8_decode_attn");
+  return kv8_decode(pool, layer, q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace, workspace_bytes, stream, 0);
+}
+
+extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                          int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                          int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                          const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_paged_window_attn");
+  return paged_window(pool, layer, q, q_start, T, max_q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace,
+                      workspace_bytes, stream, 0);
+}
+
+extern "C" zp_status zp_test_kv8_decode_stalled(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
+                                                const int32_t* block_tables, const int32_t* seq_lens, int32_t B,
+                                                int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                                const zp_params* p, void* workspace, size_t workspace_bytes,
+                                                int64_t stall_limit_ns, zp_stream stream) {
+  if (!stall_ok(stall_limit_ns)) return ZP_ERR_INVALID_ARG;
+  return kv8_decode(pool, layer, q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace, workspace_bytes, stream,
+                    static_cast<uint64_t>(stall_limit_ns));
+}
+
+extern "C" zp_status zp_test_paged_window_stalled(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                                  int32_t T, int32_t max_q, const int32_t* block_tables,
+                                                  const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window,
+                                                  int32_t sinks, const zp_rows* out, const zp_params* p, void* workspace,
+                                                  size_t workspace_bytes, int64_t stall_limit_ns, zp_stream stream) {
+  if (!stall_ok(stall_limit_ns)) return ZP_ERR_INVALID_ARG;
+  return paged_window(pool, layer, q, q_start, T, max_q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace,
+                      workspace_bytes, stream, static_cast<uint64_t>(stall_limit_ns));
 }

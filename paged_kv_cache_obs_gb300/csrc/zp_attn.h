@@ -21,6 +21,7 @@ struct AttnArgs {
   int splits;              // CTAs that share a row's tokens
   bool ordered;            // split kernel: long requests first
   float sl2;               // scale * log2(e)
+  uint64_t stall_ns;       // test hooks: 0, or the limit of a wait on a barrier that nothing completes
 };
 
 // The most rows (queries times heads of a group) that the split kernel takes.

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   constexpr int MT = D / 16;                   // 16-dim row tiles of O^T
   constexpr int VW = RB / 32;                  // words of a value row that a lane holds: 2, 4 or 8
   __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS], cta_m[ROWS], cta_l[ROWS];
-  __shared__ __align__(8) uint64_t full[kWarps][SLOTS];
+  __shared__ __align__(8) uint64_t full[kWarps][SLOTS + 1];  // and one that nothing completes, for the test hook
   __shared__ int sm_bad;
   __shared__ uint32_t words[4 * kMaxOrdered / 32];
   __shared__ int tops[kWarps];
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
     sm_bad = 0;
   }
   if (lane == 0) {
-    for (int i = 0; i < SLOTS; ++i) mbar_init(&full[warp][i], 1);
+    for (int i = 0; i <= SLOTS; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
   after_previous();
@@ -452,7 +452,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   int fill = 0, slot = 0;  // the fill that comes next, and its slot
   uint32_t phase = 0;      // of the ring's current round
   // waits for it, and what follows its last use
-  const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][slot], phase, kWaitNs)) != 0; };
+  // (the test hook waits in its place for one that nothing completes, with the ring's first fills in flight)
+  const uint64_t limit = a.stall_ns != 0 ? a.stall_ns : kWaitNs;
+  const auto arrived = [&] {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][a.stall_ns != 0 ? SLOTS : slot], phase, limit)) != 0;
+  };
   const auto used = [&] {
     __syncwarp();  // every lane has read it
     if (fill + SLOTS < FILLS * todo) issue(fill + SLOTS, slot);

@@ -85,6 +85,7 @@ struct __align__(1024) TileSmem {
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems], item_empty[kItems];
+  uint64_t never;                            // the test hook's, completed by nothing
   uint32_t tmem;
   int abort;
   Item items[kItems];
@@ -110,14 +111,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // Waits for phase `parity` of `bar`; gives up (false) after the time limit, or when another role
 // has given up.  A thread that gives up raises the flag.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns = kWaitNs) {
   const uint32_t addr = smem_u32(bar);
   if (mbar_try_wait(addr, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait(addr, parity)) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (globaltimer_ns() - t0 > limit_ns) {
       *abort = 1;
       return false;
     }
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     mbar_init(&s.q_full, Q_TMA ? 1 : 32);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.drain, 1);
+    mbar_init(&s.never, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], 1);
@@ -627,11 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         __syncwarp();
       }
     }
-    // copies still in flight after a give-up land before the shared memory is released
-    if (lane == 0 && *abort)
+    // Copies still in flight land before the shared memory is released.  A role may give up after this
+    // warp is through, so it waits for its last ones in any case (they have landed, but for that).
+    if (lane == 0)
       for (int st = 0; st < kStages; ++st)
         if (last[st]) mbar_wait_bounded(last[st], (last_parity >> st) & 1, kWaitNs);
-    if (Q_TMA && lane == 0 && *abort && q_loads > 0) mbar_wait_bounded(&s.q_full, (q_loads - 1) & 1, kWaitNs);
+    if (Q_TMA && lane == 0 && q_loads > 0) mbar_wait_bounded(&s.q_full, (q_loads - 1) & 1, kWaitNs);
     __syncwarp();
   } else if (warp == kCleanWarp) {
     // V of the mixed tiles: see the head of this file
@@ -753,6 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (n <= 1) commit(&s.q_empty);
       publish(count);  // while the softmax groups have their first tile
+      // the test hook gives up here, with copies and products in flight
+      if (a.stall_ns != 0) ok = __all_sync(0xffffffffu, wait(&s.never, 0, abort, a.stall_ns));
       for (int j = 0; ok && j < n; ++j, ++tiles, st ^= 1) {
         const bool more = j + 1 < n;
         if (j >= c0 && (j < c1 || j >= c2)) {

@@ -159,6 +159,10 @@ _sig("zp_kv8_decode_attn", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, 
 _sig("zp_paged_window_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32, _I32, _I32, _I32, _I32])
 _sig("zp_paged_window_attn", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
                                     _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_test_kv8_decode_stalled", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, _P, _I32, _I32, _I32, _I32, _ROWS,
+                                          ctypes.POINTER(zp_params), _P, _SZ, _I64, _P])
+_sig("zp_test_paged_window_stalled", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
+                                            _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _I64, _P])
 _sig("zp_read_error", _I32, [_P, _P, _I32P])
 _sig("zp_alloc_create", _I32, [_I64, ctypes.POINTER(_P)])
 _sig("zp_alloc_destroy", None, [_P])
@@ -444,6 +448,32 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
                               _raw(stream))
     if st:
         _check("zp_paged_window_attn", st)
+
+
+def _rows_of(t):
+    return ctypes.byref(zp_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+def zp_test_kv8_decode_stalled(codes, scales, layer: int, q, block_tables, seq_lens, out, params, workspace,
+                               stall_limit_ns: int, window: int = 0, sinks: int = 0, stream=None):
+    """Test hook of the bounded waits: zp_kv8_decode_attn whose warps first wait, at most stall_limit_ns, on a
+    barrier that nothing completes, and so report ZP_ERR_TIMEOUT."""
+    pool = zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1])
+    _check("zp_test_kv8_decode_stalled", lib.zp_test_kv8_decode_stalled(
+        ctypes.byref(pool), layer, _rows_of(q), _ptr(block_tables), _ptr(seq_lens), q.shape[0], block_tables.shape[1], window,
+        sinks, _rows_of(out), ctypes.byref(_params(params)), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        int(stall_limit_ns), _stream(stream)))
+
+
+def zp_test_paged_window_stalled(pool, layer: int, q, q_start, block_tables, seq_lens, out, params, workspace, window: int,
+                                 sinks: int, max_q: int, stall_limit_ns: int, stream=None):
+    """Test hook of the bounded waits: zp_paged_window_attn whose warps (the issuing warp of each CTA in the form
+    for many queries) first wait, at most stall_limit_ns, on a barrier that nothing completes, and so report ZP_ERR_TIMEOUT."""
+    kv = zp_kv_pool(pool.data_ptr(), pool.shape[1])
+    _check("zp_test_paged_window_stalled", lib.zp_test_paged_window_stalled(
+        ctypes.byref(kv), layer, _rows_of(q), _ptr(q_start), q.shape[0], max_q, _ptr(block_tables), _ptr(seq_lens),
+        seq_lens.shape[0], block_tables.shape[1], window, sinks, _rows_of(out), ctypes.byref(_params(params)), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), int(stall_limit_ns), _stream(stream)))
 
 
 def zp_read_error(workspace, stream=None) -> int:

@@ -382,3 +382,68 @@ def test_odd_keys_and_values_anywhere(zp, window, sinks, d, Hq, Hkv, b):
         x[r][0, h, t, 3], x[r][1, h, t, 8] = -math.inf, math.inf          # weight 0: NaN in dim 8
         x[r][0, 0, L - 9, 4], x[r][1, 0, L - 9, 1] = math.nan, math.inf   # rows that see it: NaN
     _window_rows(zp, x, cached, new, q, window, sinks, A.TILED, b=b)
+
+
+# ------------------------------------------------------------------ waits that run out --------
+
+BAND = 4096
+
+
+def _banded(t):
+    """A copy of `t` with a band of 0xA5 behind it."""
+    n = t.numel() * t.element_size()
+    buf = torch.full((n + BAND,), 0xA5, dtype=torch.uint8, device="cuda")
+    buf[:n] = t.contiguous().view(torch.uint8).flatten()
+    return buf[:n].view(t.dtype).view(t.shape), buf[n:]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,form", [
+    ("a cluster of splits", dict(kv8=(8, 2, 128, 16, [5, 300, 1100]))),
+    ("parts of several clusters", dict(kv8=(8, 2, 128, 16, [9000, 1, 0, 4097]))),
+    ("not split, two tiles at a time", dict(kv8=(4, 2, 64, 16, [40, 700, 3] * 110))),
+    ("bf16, a ring of keys or values", dict(window=(32, 8, 128, 16, [0, 700, 1999], [1, 1, 1]))),
+    ("bf16, 16 rows", dict(window=(8, 2, 128, 16, [0, 300, 3000], [4, 3, 4]))),
+    ("one short item a CTA", dict(window=(4, 2, 64, 16, [0, 50], [40, 20]))),
+    ("items of several tiles", dict(window=(4, 2, 128, 16, [900, 100], [300, 70]))),
+    ("several items a CTA", dict(window=(4, 4, 64, 16, [0, 300] * 40, [40, 150] * 40))),
+    ("items split over their tiles", dict(window=(4, 1, 128, 16, [9000], [70]))),
+    ("queries without a tensor map", dict(window=(4, 2, 128, 16, [700] * 50, [60] * 50), off=1)),
+])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(zp, name, form):
+    if "kv8" in form:
+        args = A._kv8_case(zp, *form["kv8"], seed=1, hidden_nan=False)
+        call, stalled, tail = zp.zp_kv8_decode_attn, zp.zp_test_kv8_decode_stalled, ()
+    else:
+        Hq, Hkv, d, b, cached, new = form["window"]
+        args = A._window_case(zp, Hq, Hkv, d, b, cached, new, 0, 0, seed=1, rel=A.TILED, off=form.get("off", 0))
+        call, stalled, tail = zp.zp_paged_window_attn, zp.zp_test_paged_window_stalled, args[9:]
+    want = args[6].clone()
+    a = list(args[:9])
+    bands = [None] * 9
+    for i in (0, 6, 8):
+        if i != 6 or not form.get("off"):
+            a[i], bands[i] = _banded(a[i])
+    if "kv8" in form:
+        a[1], bands[1] = _banded(a[1])
+    before = [x.clone() if isinstance(x, torch.Tensor) else None for x in a]
+    for limit in (2_000_000, 1):
+        stalled(*a, *tail, stall_limit_ns=limit)
+        assert zp.zp_read_error(a[8]) == zp.ZP_ERR_TIMEOUT
+        torch.cuda.synchronize()
+        assert all(bool((x == 0xA5).all()) for x in bands if x is not None)
+        for i in (0, 1, 2, 3, 4, 5):
+            if isinstance(a[i], torch.Tensor):
+                assert torch.equal(a[i].view(torch.uint8), before[i].view(torch.uint8)), i
+        a[6].fill_(7.0)
+        call(*a, *tail)
+        assert zp.zp_read_error(a[8]) == 0
+        assert torch.equal(a[6], want)
+        assert all(bool((x == 0xA5).all()) for x in bands if x is not None)
+
+
+def test_stall_limits_are_checked(zp):
+    p = zp.make_params(A._params(2, 2, 64, 16))
+    for ns in (0, -5, 2_000_000_000):
+        assert zp.lib.zp_test_kv8_decode_stalled(None, 0, None, None, None, 1, 1, 0, 0, None, p, None, 0, ns, None) == zp.ZP_ERR_INVALID_ARG
+        assert zp.lib.zp_test_paged_window_stalled(None, 0, None, None, 1, 1, None, None, 1, 1, 0, 0, None, p, None, 0, ns, None) == zp.ZP_ERR_INVALID_ARG
