@@ -424,7 +424,7 @@ zp_status zp_kv8_unpack_blocks(const zp_kv8_pool* kv8, const int32_t* src_ids, c
  * optionally with a window.  Request r's one query is at position L - 1, L = seq_lens[r]:
  *   out[r][qh] = softmax_t(params.scale * <q[r][qh], k_t>) . v_t over t < L with
  *   t >= L - window or t < sinks   (window 0: every t < L).
- *   q, out        rows [B][H_q][head_dim].
+ *   q, out        rows [B][H_q][head_dim]; out does not overlap q.
  *   seq_lens      device int32 [B], 0 <= L <= max_blocks * b.  0 (a padded row): zeros are written.
  *   workspace     >= zp_kv8_decode_workspace_size() bytes, 256-byte aligned.
  * A bad seq_len or block id: that row (request and kv head) is not written, ZP_ERR_BAD_TABLE.
@@ -443,9 +443,11 @@ size_t zp_kv8_decode_workspace_size(const zp_params* params, int32_t B, int32_t 
  * new tokens' keys and values are already in the pool.  Query i of request r's n is at position
  * p = seq_lens[r] - n + i and sees
  *   t <= p with t > p - window or t < sinks   (window 0: every t <= p).
- *   q, out        rows [T][H_q][head_dim], request after request.
- *   q_start       device int32 [B + 1], as token_start of zp_kv8_append.  Rows of q and out
- *                 outside q_start's range are neither read nor written.
+ *   q, out        rows [T][H_q][head_dim], request after request; out does not overlap q.
+ *   q_start       device int32 [B + 1], as token_start of zp_kv8_append.  Rows of out
+ *                 outside q_start's range are not written; those of q have to be memory that can be
+ *                 read (tiles of queries are loaded whole), but have no effect, whatever they hold
+ *                 and even if they are written meanwhile.
  *   max_q         the most new tokens of a request of this call (an upper bound is fine; a request
  *                 above it is skipped: ZP_ERR_BAD_TABLE).
  *   seq_lens      device int32 [B], tokens in the cache, the new ones included: n <= L <=

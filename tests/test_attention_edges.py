@@ -447,3 +447,21 @@ def test_stall_limits_are_checked(zp):
     for ns in (0, -5, 2_000_000_000):
         assert zp.lib.zp_test_kv8_decode_stalled(None, 0, None, None, None, 1, 1, 0, 0, None, p, None, 0, ns, None) == zp.ZP_ERR_INVALID_ARG
         assert zp.lib.zp_test_paged_window_stalled(None, 0, None, None, 1, 1, None, None, 1, 1, 0, 0, None, p, None, 0, ns, None) == zp.ZP_ERR_INVALID_ARG
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_behind_a_request_do_not_reach_it(zp, d):
+    # q holds NaN and infinities in the rows of no request, and in those of the request behind
+    for n in (1, 2, 50, 130):
+        args = A._window_case(zp, 4, 2, d, 16, [100, 5], [n, n], 40, 3, seed=n, rel=A.TILED)
+        T = args[2].shape[0]
+        q = torch.empty((T + 150, 4, d), dtype=torch.bfloat16, device="cuda")
+        q[0::3], q[1::3], q[2::3] = math.nan, math.inf, -math.inf
+        q[:n] = args[2][:n]
+        out = torch.full_like(q, 7.0)
+        a = list(args)
+        a[2], a[6] = q, out
+        zp.zp_paged_window_attn(*a)
+        assert zp.zp_read_error(args[8]) == 0
+        assert torch.equal(out[:n], args[6][:n]) and bool((out[T:] == 7).all())
+        assert not bool(torch.isfinite(out[n:T]).any())
