@@ -465,3 +465,56 @@ def test_rows_behind_a_request_do_not_reach_it(zp, d):
         assert zp.zp_read_error(args[8]) == 0
         assert torch.equal(out[:n], args[6][:n]) and bool((out[T:] == 7).all())
         assert not bool(torch.isfinite(out[n:T]).any())
+
+# ------------------------------------------------------------------ strides -------------------
+
+def _layouts(T, heads, d, g):
+    """Rows [T, heads, d] in orders that a program has them in."""
+    yield "fused", torch.zeros((T, heads + 5, d), dtype=torch.bfloat16, device="cuda")[:, 2:2 + heads]
+    yield "head-major", torch.zeros((heads, T, d), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    yield "padded rows", torch.zeros((T, heads, d + 8), dtype=torch.bfloat16, device="cuda")[..., :d]
+    yield "odd rows", torch.zeros((T, heads, d + 1), dtype=torch.bfloat16, device="cuda")[..., :d]
+    yield "every other token", torch.zeros((2 * T, heads, d), dtype=torch.bfloat16, device="cuda")[::2]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", ["kv8", "few", "many", "split"])
+def test_strides_of_queries_and_outputs(zp, form, d):
+    if form == "kv8":
+        args = A._kv8_case(zp, 28, 4, d, 16, [40, 1, 500, 0, 17], seed=d, hidden_nan=False)
+        call = zp.zp_kv8_decode_attn
+    else:
+        cached, new = dict(few=([30, 500, 0], [1, 2, 2]), many=([30, 500, 0], [90, 20, 41]), split=([3000], [70]))[form]
+        args = A._window_case(zp, 28, 4, d, 16, cached, new, 100 if form != "split" else 0, 4, seed=d, rel=A.TILED)
+        call = zp.zp_paged_window_attn
+    qat = 3 if form == "kv8" else 2
+    T, H, _ = args[qat].shape
+    ins, outs = list(_layouts(T, H, d, None)), list(_layouts(T, H, d, None))
+    for i, (name, q) in enumerate(ins):
+        for oname, o in (outs[i], outs[(i + 1) % len(outs)], outs[(i + 3) % len(outs)]):
+            whole = o._base
+            whole.fill_(7.0)
+            q.copy_(args[qat])
+            a = list(args)
+            a[qat], a[6] = q, o
+            call(*a)
+            assert zp.zp_read_error(args[8]) == 0
+            assert torch.equal(o, args[6]), (name, oname)
+            o.fill_(7.0)
+            assert bool((whole == 7).all()), (name, oname)          # nothing between the rows
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [2, 70])
+def test_queries_may_be_broadcast(zp, new, d):
+    args = A._window_case(zp, 4, 2, d, 16, [100], [new], 60, 3, seed=new, rel=A.TILED)
+    one = torch.randn((1, 1, d), device="cuda").to(torch.bfloat16)
+    outs = []
+    for q in (one.expand(new, 4, d), one.expand(new, 4, d).contiguous()):
+        a = list(args)
+        a[2], a[6] = q, torch.zeros_like(args[6])
+        zp.zp_paged_window_attn(*a)
+        outs.append(a[6])
+    assert zp.zp_read_error(args[8]) == 0 and torch.equal(*outs)
