@@ -27,6 +27,12 @@ struct AttnArgs {
 // The most rows (queries times heads of a group) that the split kernel takes.
 constexpr int kMaxSplitRows = 16;
 
+// The SMs that plans are made for: the current device's, or a GB300's where there is none (workspace sizes).
+inline int plan_sms() {
+  const int n = num_sms();
+  return n > 0 ? n : 152;
+}
+
 // How a call is cut: CTAs of a (request, kv head), how many of them form a cluster, and what the
 // partial sums of the clusters take.
 struct SplitPlan {
@@ -43,9 +49,9 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st);
 
 // How a call of the tiled kernel is cut: items (2 x 128 rows) of a request and kv head, CTAs that
-// share an item's tiles, items in all.
+// share an item's tiles, CTAs that are launched, items in all.
 struct TilePlan {
-  int nx, splits;
+  int nx, splits, ctas;
   int64_t items;
   size_t bytes;
 };

@@ -873,7 +873,7 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // rows have nearly equal work (64 requests with a window of 1024: 44.0 us as they come, 43.4 us if
 // the caller has them in order), within a wave, and past 1024 requests, where the last ones are little.
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room) {
-  constexpr int64_t kSms = 152;
+  const int64_t sms = plan_sms();
   SplitPlan s{};
   s.rows = p->num_q_heads / p->num_kv_heads * max_q <= 8 ? 8 : 16;
   int64_t tiles = (static_cast<int64_t>(max_blocks) * p->block_size + kTile - 1) / kTile;
@@ -883,13 +883,13 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
     tiles = std::min(tiles, seen);
   }
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
-  const int64_t wave = kSms * (s.rows == 16 ? 2 : 4) * 7 / 8;
+  const int64_t wave = sms * (s.rows == 16 ? 2 : 4) * 7 / 8;
   const int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
   const size_t part = static_cast<size_t>(units) * s.rows * (p->head_dim + 4) * sizeof(float);  // of one cluster a row
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
   s.splits = n >= 8 ? static_cast<int>(std::max<int64_t>(1, std::min(n / 8, fit))) * 8 : s.cluster;
-  s.ordered = window == 0 && n < 2 && units > kSms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
+  s.ordered = window == 0 && n < 2 && units > sms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
   const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
   s.bytes = kHeader;
   if (parts > 1) s.bytes += (parts * part + 255) / 256 * 256;

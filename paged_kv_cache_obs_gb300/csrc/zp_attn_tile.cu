@@ -5,7 +5,7 @@
 // heads of the group, so K and V are read once for the whole group — and walks the 128-token
 // tiles of the cache that any of its rows sees: first the blocks with always-visible first
 // tokens, then the window's.  Blocks between the two are never loaded.  A resident CTA per SM takes
-// every 152nd item.  Where a call has fewer items than SMs, the tiles of an item are shared by
+// its share of the items one after another.  Where a call has fewer items than SMs, the tiles of an item are shared by
 // several CTAs, whose sums a second kernel joins.
 //
 // Roles: a producer warp brings K and V through the block table (one TMA box per block and
@@ -54,7 +54,6 @@ constexpr int kKeys = 128;            // tokens of a KV tile
 constexpr int kStages = 2;
 constexpr int kKWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;         // two softmax groups, and a group of the other roles
-constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLazy = 24.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
@@ -263,7 +262,7 @@ __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, c
   w.win_block = first >> bs;
   w.sink_blocks = min((min(a.sinks, w.L) + a.b - 1) >> bs, w.win_block);
   w.blocks = w.sink_blocks + (w.p_last >> bs) + 1 - w.win_block;
-  const int tiles = ((w.blocks << bs) + kKeys - 1) / kKeys;  // at most 2^23, and 152 splits
+  const int tiles = ((w.blocks << bs) + kKeys - 1) / kKeys;  // at most 2^23, and as many splits as SMs
   w.j0 = 0;
   w.j1 = tiles;
   if (a.splits > 1) {
@@ -1042,7 +1041,8 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
 static_assert(sizeof(TileSmem<128>) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 template <int D, bool Q_TMA, bool PARTS>
-cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs& a, int nx, int items, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs& a, const TilePlan& plan, cudaStream_t st) {
+  const int nx = plan.nx, items = static_cast<int>(plan.items);
   constexpr int bytes = sizeof(TileSmem<D>) + 1024;
   static PerDeviceInit attrs;
   cudaError_t e = attrs.run(
@@ -1050,10 +1050,10 @@ cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs&
   if (e != cudaSuccess) return e;
   // Calls of one item a CTA come in early (64 queries over 16000 tokens 34.2 -> 33.4 us).  Longer ones do not: 2048-token
   // chunks take 192 us so and 196.6 when they come in early, for a reason that was not found.
-  if (items <= kSms) {
+  if (items <= plan.ctas) {
     e = launch_in_order(tile_kernel<D, Q_TMA, PARTS>, dim3(items), kThreads, bytes, st, 1, tm, tq, a, nx, items);
   } else {
-    tile_kernel<D, Q_TMA, PARTS><<<kSms, kThreads, bytes, st>>>(tm, tq, a, nx, items);
+    tile_kernel<D, Q_TMA, PARTS><<<plan.ctas, kThreads, bytes, st>>>(tm, tq, a, nx, items);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !PARTS) return e;
@@ -1065,6 +1065,7 @@ cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tq, const AttnArgs&
 
 TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room) {
   TilePlan plan{};
+  plan.ctas = plan_sms();
   int64_t tokens = static_cast<int64_t>(max_blocks) * p->block_size;
   const int per_item = 2 * (kRows / (p->num_q_heads / p->num_kv_heads));
   const auto items_of = [&](int64_t n) { return (n + per_item - 1) / per_item; };  // of a request and head with n queries
@@ -1078,7 +1079,7 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
   // a part has four tiles at least: below that its sums cost more than the tiles
   const size_t part = static_cast<size_t>(std::max(T, 1)) * p->num_q_heads * (p->head_dim + 4) * sizeof(float);  // of every row
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
-  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(kSms / std::max<int64_t>(items, 1), tiles / 4), fit)));
+  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(plan.ctas / std::max<int64_t>(items, 1), tiles / 4), fit)));
   plan.nx = static_cast<int>(std::min<int64_t>(nx, INT_MAX));
   plan.items = nx * heads * plan.splits;
   plan.bytes = kHeader;
@@ -1104,12 +1105,11 @@ zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, co
   const bool q_tma = aligned(a.q, 16) && a.q_ts > 0 && a.q_hs > 0 && a.q_ts % 8 == 0 && a.q_hs % 8 == 0 &&
                      encode_tmap_3d_bf16(&tq, a.q, d, static_cast<uint64_t>(a.Hkv) * a.G, a.T, static_cast<uint64_t>(a.q_hs) * 2,
                                          static_cast<uint64_t>(a.q_ts) * 2, 64, a.G, kRows / a.G);
-  const int items = static_cast<int>(plan.items);
   cudaError_t e;
   const auto pick = [&](auto dim, auto tma) {
     constexpr int kD = decltype(dim)::value;
     constexpr bool kTma = decltype(tma)::value;
-    return plan.splits > 1 ? launch<kD, kTma, true>(tm, tq, a, plan.nx, items, st) : launch<kD, kTma, false>(tm, tq, a, plan.nx, items, st);
+    return plan.splits > 1 ? launch<kD, kTma, true>(tm, tq, a, plan, st) : launch<kD, kTma, false>(tm, tq, a, plan, st);
   };
   using D128 = std::integral_constant<int, 128>;
   using D64 = std::integral_constant<int, 64>;

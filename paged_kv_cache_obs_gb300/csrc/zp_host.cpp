@@ -9,6 +9,7 @@
 // of a compressed request is released (zh §2.1) once the compression kernel that still reads
 // it has finished, which is what the event-deferred decref provides.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -67,9 +68,13 @@ bool encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t
 }
 
 int num_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (keep) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

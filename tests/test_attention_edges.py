@@ -37,6 +37,18 @@ def test_workspace_sizes_are_multiples_of_256(zp):
                 assert all(x >= 256 and x % 256 == 0 for x in sizes)
 
 
+@pytest.mark.gpu
+def test_splits_follow_the_devices_sms(zp):
+    # one kv head and one item of queries: as many parts of 4 tiles as there are SMs; one row of 8, 7/8 of
+    # four CTAs an SM, in clusters of 8
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    p = A._params(2, 1, 64, 16)
+    size = zp.zp_paged_window_workspace_size(p, 64, 1, 64, 1 << 16, 0, 0)
+    assert (size - 256) // (64 * 2 * 68 * 4) == sms
+    size = zp.zp_kv8_decode_workspace_size(p, 1, 1 << 16)
+    assert (size - 256) // (8 * 68 * 4) == sms * 4 * 7 // 8 // 8
+
+
 def _exact(q, k, v, visible, scale):
     """Rows q [.., d] over k, v [L, d] in 64 bits: the outputs and the weighted magnitudes.  visible [.., L]."""
     x = (scale * (q.double() @ k.double().T)).masked_fill(~visible, -math.inf)
