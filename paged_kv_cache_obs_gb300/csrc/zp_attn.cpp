@@ -85,7 +85,8 @@ zp_status kv8_decode(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, c
   a.scales = pool->scales;
   a.T = B;
   a.max_q = 1;
-  a.stall_ns = stall_ns;
+  a.stall = stall_ns != 0;
+  a.limit_ns = a.stall ? stall_ns : kWaitNs;
   return split_launch(a, p, true, split_plan(p, B, 1, max_blocks, window, sinks, workspace_bytes), workspace,
                       reinterpret_cast<cudaStream_t>(stream));
 }
@@ -108,7 +109,8 @@ zp_status paged_window(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, 
   a.T = T;
   // a request of more tokens than its blocks hold is refused by its length in any case
   a.max_q = std::min(max_q, max_blocks * p->block_size);
-  a.stall_ns = stall_ns;
+  a.stall = stall_ns != 0;
+  a.limit_ns = a.stall ? stall_ns : kWaitNs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
     return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);

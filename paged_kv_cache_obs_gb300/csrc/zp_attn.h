@@ -5,6 +5,8 @@
 
 namespace zp {
 
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside a kernel gives up after this
+
 // What the split and the tiled attention kernels take.
 struct AttnArgs {
   const uint8_t* pool;     // bf16 or E4M3 tiles
@@ -21,7 +23,8 @@ struct AttnArgs {
   int splits;              // CTAs that share a row's tokens
   bool ordered;            // split kernel: long requests first
   float sl2;               // scale * log2(e)
-  uint64_t stall_ns;       // test hooks: 0, or the limit of a wait on a barrier that nothing completes
+  uint64_t limit_ns;       // of a wait: kWaitNs, or the test hooks' limit
+  bool stall;              // test hooks: a wait goes to a barrier that nothing completes
 };
 
 // The most rows (queries times heads of a group) that the split kernel takes.

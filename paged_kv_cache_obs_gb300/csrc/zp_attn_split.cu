@@ -53,13 +53,19 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                    // tokens
 constexpr float kLazy = 8.0f;
-constexpr float kGain = 32768.0f;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kGain = 32768.0f;            // E4M3: what P is multiplied by for f16
+constexpr float kLeastRef = 3.85185989e-34f;  // 2^-111: kGain over a V scale and a scale over kGain are normal numbers
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// x + y, where subnormal numbers count as 0
+__device__ __forceinline__ float add_ftz(float x, float y) {
+  float z;
+  asm("add.rn.ftz.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -222,12 +228,12 @@ __device__ __forceinline__ void join(float (&v)[4], float& l, float4 y, float yl
   v[3] = fmaf(y.w, w, v[3]);
 }
 
-// Four dims of an output row: sums over the sum of weights.  Zeros where there are no tokens; a row whose
-// logits are all -inf has weights of 0 alone, and is 0 / 0 like the softmax of them.
+// Four dims of an output row: sums over the sum of weights.  A row whose logits are all -inf has weights
+// of 0 alone, and is 0 / 0 like the softmax of them.
 __device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int h, int row, int dim, const float (&v)[4], float l) {
   const int i = row / a.G, g = row - i * a.G;
   uint16_t* const o = a.out + (s.q0 + i) * a.o_ts + (h * a.G + g) * a.o_hs + dim;
-  const float inv = s.L == 0 ? 0.0f : 1.0f / l;
+  const float inv = 1.0f / l;
   const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
   if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
@@ -313,6 +319,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   bool bad;
   if (!span_of(a, r, s, bad)) {  // the same for every CTA of the cluster
     if (bad && split == 0 && h == 0 && tid == 0) atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
+    return;
+  }
+  if (s.L == 0) {  // a padded row: zeros
+    if (split == 0)
+      for (int i = tid; i < a.G * D; i += kThreads) a.out[s.q0 * a.o_ts + (h * a.G + i / D) * a.o_hs + i % D] = 0;
     return;
   }
   // the row's tiles are dealt out one by one to the warps of its splits
@@ -447,16 +458,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   }
 
   const int p_last = s.p0 + s.n - 1;
-  float vref = 0.0f, vinv = 0.0f;  // FP8: V scale that o is in units of, and its inverse
+  float vref = 0.0f, vinv = 0.0f;  // FP8: V scale that o is in units of (over kGain), and its inverse
   bool ok = true;
-  int fill = 0, slot = 0;  // the fill that comes next, and its slot
+  int fill = 0;                    // the fill that comes next
+  int slot = a.stall ? SLOTS : 0;  // its slot; the test hook starts at the barrier that nothing completes
   uint32_t phase = 0;      // of the ring's current round
   // waits for it, and what follows its last use
-  // (the test hook waits in its place for one that nothing completes, with the ring's first fills in flight)
-  const uint64_t limit = a.stall_ns != 0 ? a.stall_ns : kWaitNs;
-  const auto arrived = [&] {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][a.stall_ns != 0 ? SLOTS : slot], phase, limit)) != 0;
-  };
+  const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][slot], phase, a.limit_ns)) != 0; };
   const auto used = [&] {
     __syncwarp();  // every lane has read it
     if (fill + SLOTS < FILLS * todo) issue(fill + SLOTS, slot);
@@ -566,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
           x[sub][nt][e] = ex2(x[sub][nt][e] - ref);
-          l[nt][e & 1] += x[sub][nt][e];
+          // bf16: the lowest bit (see above), which is neither summed nor, alone, left over by rounding to bf16
+          if (!FP8) x[sub][nt][e] = __uint_as_float(__float_as_uint(x[sub][nt][e]) | 1u);
+          l[nt][e & 1] = FP8 ? l[nt][e & 1] + x[sub][nt][e] : add_ftz(l[nt][e & 1], x[sub][nt][e]);
         }
       }
     if constexpr (!Sh::JOINT) {
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         // by itself and scaled in fp32: in sum, weights keep 11 bits down to 2^-18 of the row's largest
         // (where the reference stands at most 2^8 above it), and 2^-28 of it is the last that counts.
         if (fabsf(vs[sub]) > vref) {
-          const float next = fmaxf(fabsf(vs[sub]), 1.17549435e-38f), corr = vref / next;
+          const float next = fmaxf(fabsf(vs[sub]), kLeastRef), inv = 1.0f / next, corr = vref * inv;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -630,11 +640,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[nt][mt][e] *= corr;
           vref = next;
-          vinv = 1.0f / next;
+          vinv = kGain * inv;
         }
-        const float ratio = vs[sub] * vinv;
+        const float gained = vs[sub] * vinv, ratio = gained * (1.0f / kGain);
         const bool small = fabsf(ratio) < 0.125f;
-        const float pm = small ? kGain : ratio * kGain;
+        const float pm = small ? kGain : gained;
         uint32_t ph[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -695,10 +705,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // 0 stays 0: the bit alone is rounded away
-            const uint32_t y0 = __float_as_uint(x[sub][nt][2 * e]) | 1u, y1 = __float_as_uint(x[sub][nt][2 * e + 1]) | 1u;
-            ph[nt][e] = transpose8(__byte_perm(y0, y1, 0x7632));
-            pl[nt][e] = transpose8(pack_bf16(__uint_as_float(y0) - hi_f(y0), __uint_as_float(y1) - hi_f(y1)));
+            const float y0 = x[sub][nt][2 * e], y1 = x[sub][nt][2 * e + 1];
+            ph[nt][e] = transpose8(__byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632));
+            pl[nt][e] = transpose8(pack_bf16(y0 - hi_f(__float_as_uint(y0)), y1 - hi_f(__float_as_uint(y1))));
           }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
@@ -716,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
   }
   if (!ok) {
     // copies still in flight after a failed wait land (bounded) before the ring is used again
+    if (slot == SLOTS) slot = 0;
     for (int n = fill; n < min(FILLS * todo, fill + SLOTS); ++n) {
       mbar_wait_bounded(&full[warp][slot], phase, kWaitNs);
       if (++slot == SLOTS) slot = 0, phase ^= 1;
@@ -743,14 +753,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
         sm_m[warp][row] = m[nt][e];
         sm_l[warp][row] = sum;
       }
-      const float unit = FP8 ? vref : 1.0f, gain = FP8 ? 1.0f / kGain : 1.0f;
+      const float unit = FP8 ? vref * (1.0f / kGain) : 1.0f;
       float4* const dst = reinterpret_cast<float4*>(sm_acc) + (warp * ROWS + row) * (D / 4);
 #pragma unroll
       for (int mt = 0; mt < MT; mt += 2) {
         // FP8: dims (D/8) g + 2 mt .. + 3;  bf16: dims 8 (g + 8 (mt / 4)) + 2 (mt % 4) .. + 3
         const int dim = FP8 ? (D / 8) * g + 2 * mt : 8 * (g + 8 * (mt >> 2)) + 2 * (mt & 3);
-        dst[acc_at<FP8>(row, dim / 4)] = make_float4(o[nt][mt][e] * gain * unit, o[nt][mt][e + 2] * gain * unit,
-                                                     o[nt][mt + 1][e] * gain * unit, o[nt][mt + 1][e + 2] * gain * unit);
+        dst[acc_at<FP8>(row, dim / 4)] = make_float4(o[nt][mt][e] * unit, o[nt][mt][e + 2] * unit, o[nt][mt + 1][e] * unit,
+                                                     o[nt][mt + 1][e + 2] * unit);
       }
     }
   __syncthreads();
@@ -816,7 +826,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   if (r >= a.B) return;
   Span s;
   bool bad;
-  if (!span_of(a, static_cast<int>(r), s, bad) || row >= a.G * s.n) return;
+  if (!span_of(a, static_cast<int>(r), s, bad) || s.L == 0 || row >= a.G * s.n) return;
   const float* const p = a.part + ((r * a.Hkv + h) * parts * ROWS + row) * (D + 4);
   const int64_t step = static_cast<int64_t>(ROWS) * (D + 4);
   float M = -INFINITY;

@@ -54,7 +54,6 @@ constexpr int kKeys = 128;            // tokens of a KV tile
 constexpr int kStages = 2;
 constexpr int kKWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;         // two softmax groups, and a group of the other roles
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLazy = 24.0f;
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
 constexpr int kFlags = 8;             // items: K's warp is at most 6 ahead of a softmax group (the ring's 3, 2 stages, one)
@@ -756,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       if (n <= 1) commit(&s.q_empty);
       publish(count);  // while the softmax groups have their first tile
       // the test hook gives up here, with copies and products in flight
-      if (a.stall_ns != 0) ok = __all_sync(0xffffffffu, wait(&s.never, 0, abort, a.stall_ns));
+      if (a.stall) ok = __all_sync(0xffffffffu, wait(&s.never, 0, abort, a.limit_ns));
       for (int j = 0; ok && j < n; ++j, ++tiles, st ^= 1) {
         const bool more = j + 1 < n;
         if (j >= c0 && (j < c1 || j >= c2)) {
