@@ -56,29 +56,17 @@ constexpr float kLazy = 8.0f;
 constexpr float kGain = 32768.0f;            // E4M3: what P is multiplied by for f16
 constexpr float kLeastRef = 3.85185989e-34f;  // 2^-111: kGain over a V scale and a scale over kGain are normal numbers
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // x + y, where subnormal numbers count as 0
 __device__ __forceinline__ float add_ftz(float x, float y) {
   float z;
   asm("add.rn.ftz.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 // the low and the high two E4M3 codes of a word, as f16 pairs
 __device__ __forceinline__ void dec4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
@@ -105,11 +93,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -234,7 +217,7 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, const Span& s, int
   const int i = row / a.G, g = row - i * a.G;
   uint16_t* const o = a.out + (s.q0 + i) * a.o_ts + (h * a.G + g) * a.o_hs + dim;
   const float inv = 1.0f / l;
-  const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
+  const uint32_t lo = pack_bf16x2(v[0] * inv, v[1] * inv), hi = pack_bf16x2(v[2] * inv, v[3] * inv);
   if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
   } else {
@@ -442,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qb[nt][ks][e] = pack_f16(lo_f(qb[nt][ks][e]) * inv, hi_f(qb[nt][ks][e]) * inv);
+        for (int e = 0; e < 2; ++e) qb[nt][ks][e] = pack_f16(bf16x2_lo(qb[nt][ks][e]) * inv, bf16x2_hi(qb[nt][ks][e]) * inv);
     }
     qs[nt][0] = a.sl2 * __shfl_sync(0xffffffffu, mult, 8 * c);
     qs[nt][1] = a.sl2 * __shfl_sync(0xffffffffu, mult, 8 * c + 4);
@@ -692,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
                   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                   for (int mt = 0; mt < 4; ++mt) {
-                    o[nt][4 * j + mt][e] += pt * lo_f(w[mt]);
-                    o[nt][4 * j + mt][e + 2] += pt * hi_f(w[mt]);
+                    o[nt][4 * j + mt][e] += pt * bf16x2_lo(w[mt]);
+                    o[nt][4 * j + mt][e + 2] += pt * bf16x2_hi(w[mt]);
                   }
                 }
               }
@@ -707,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           for (int e = 0; e < 2; ++e) {
             const float y0 = x[sub][nt][2 * e], y1 = x[sub][nt][2 * e + 1];
             ph[nt][e] = transpose8(__byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632));
-            pl[nt][e] = transpose8(pack_bf16(y0 - hi_f(__float_as_uint(y0)), y1 - hi_f(__float_as_uint(y1))));
+            pl[nt][e] = transpose8(pack_bf16x2(y0 - bf16x2_hi(__float_as_uint(y0)), y1 - bf16x2_hi(__float_as_uint(y1))));
           }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {

@@ -91,17 +91,6 @@ struct __align__(1024) TileSmem {
   int odd_lo[kFlags], odd_hi[kFlags];        // the first and last tile with such values
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -123,17 +112,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -387,8 +365,8 @@ __device__ __noinline__ void add_odd_values(const AttnArgs& a, const Item& w, in
           float dot = 0.0f;
 #pragma unroll
           for (int d = 0; d < DW; ++d) {
-            dot = fmaf(lo_f(q[2 * d]), lo_f(kw[d]), dot);
-            dot = fmaf(lo_f(q[2 * d + 1]), __uint_as_float(kw[d] & 0xFFFF0000u), dot);
+            dot = fmaf(bf16x2_lo(q[2 * d]), bf16x2_lo(kw[d]), dot);
+            dot = fmaf(bf16x2_lo(q[2 * d + 1]), __uint_as_float(kw[d] & 0xFFFF0000u), dot);
           }
 #pragma unroll
           for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
@@ -399,10 +377,10 @@ __device__ __noinline__ void add_odd_values(const AttnArgs& a, const Item& w, in
         for (int d = 0; d < 2 * DW; ++d) {
           const uint32_t word = x[d >> 1];
           if (!(d & 1 ? odd_hi(word) : odd_lo(word))) continue;
-          const float value = nothing ? NAN : d & 1 ? __uint_as_float(word & 0xFFFF0000u) : lo_f(word);
+          const float value = nothing ? NAN : d & 1 ? __uint_as_float(word & 0xFFFF0000u) : bf16x2_lo(word);
           const int dim = lane * (2 * DW) + d;
           if (to.part) to.part[dim] += value;
-          else to.out[dim] = static_cast<uint16_t>(pack_bf16(lo_f(to.out[dim]) + value, 0.0f));
+          else to.out[dim] = static_cast<uint16_t>(pack_bf16x2(bf16x2_lo(to.out[dim]) + value, 0.0f));
         }
       }
     }
@@ -878,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             y0 = ex2(y0);
             y1 = ex2(y1);
             sum = add2(sum, pair(__float_as_uint(y0), __float_as_uint(y1)));
-            pk[e] = pack_bf16(y0, y1);
+            pk[e] = pack_bf16x2(y0, y1);
           }
           tmem_st32(ts + c * 32, pk);
         }
@@ -946,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             tmem_ld32_issue(to + c * 32, o);
             tmem_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            for (int e = 0; e < 16; ++e) y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             uint16_t* const dst = to_row.out + c * 32;
             if (!write) continue;
             if ((align & 31) == 0) {
@@ -1030,7 +1008,7 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
   }
   const float inv = 1.0f / l;
   uint16_t* const out = a.out + t * a.o_ts + head * a.o_hs + lane * 4;
-  const uint32_t y0 = pack_bf16(v[0] * inv, v[1] * inv), y1 = pack_bf16(v[2] * inv, v[3] * inv);
+  const uint32_t y0 = pack_bf16x2(v[0] * inv, v[1] * inv), y1 = pack_bf16x2(v[2] * inv, v[3] * inv);
   out[0] = static_cast<uint16_t>(y0);
   out[1] = static_cast<uint16_t>(y0 >> 16);
   out[2] = static_cast<uint16_t>(y1);

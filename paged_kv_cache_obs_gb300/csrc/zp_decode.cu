@@ -51,13 +51,6 @@ struct DecodeArgs {
   uint64_t stall_ns;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-
 __device__ __forceinline__ uint16_t f2bf16(float f) {
   // round to nearest even; NaN stays NaN
   uint32_t u = __float_as_uint(f);
@@ -65,15 +58,6 @@ __device__ __forceinline__ uint16_t f2bf16(float f) {
   u += 0x7FFFu + ((u >> 16) & 1u);
   return static_cast<uint16_t>(u >> 16);
 }
-
-// Packs two floats into a bf16x2 register (lo in the low half), rounding to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float bf16x2_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf16x2_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
 // Byte offset, inside a (16-row, D-column) chunk stored as [d/64 half][16 rows][128 B] with the
 // 128-byte swizzle that TMA applies, of 16-byte column group `cg` (0 .. D/8-1) of row `row`.

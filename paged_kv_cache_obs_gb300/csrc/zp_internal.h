@@ -27,6 +27,9 @@ int num_sms();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Rows that 16-byte loads and stores can take.
+inline bool wide(const zp_rows* r) { return aligned(r->data, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0; }
+
 // Rows [tokens][heads][d] that a call writes and that share elements whatever the values are (broadcast ones
 // above all): each would be written several times, with different results.
 inline bool rows_overlap(const zp_rows& r, int64_t tokens, int64_t heads, int64_t d) {

@@ -16,6 +16,7 @@
 // 4.8 us (the same chain, with nothing behind it).
 #include "zp_internal.h"
 #include "zp_launch.h"
+#include "zp_ptx.cuh"
 
 namespace zp {
 namespace {
@@ -42,20 +43,10 @@ __device__ __forceinline__ float2 dec2(uint32_t two) {
   asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(h));
   return make_float2(lo, hi);
 }
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Largest magnitude of bf16 pairs, as two 15-bit patterns (which order like the values); inf and
 // NaN come out as 0x7F80 and above.
 __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7FFF7FFFu));
-  return r;
+  return max_u16x2(m, x & 0x7FFF7FFFu);
 }
 // The same over the finite values only.
 __device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t x) {
@@ -78,7 +69,7 @@ __device__ __forceinline__ float inverse(float s) { return s > 0.0f ? 1.0f / s :
 // (E4M3 has none).
 template <bool ODD>
 __device__ __forceinline__ uint32_t enc_pair(uint32_t x, float inv) {
-  uint32_t c = enc2(lo_f(x) * inv, hi_f(x) * inv);
+  uint32_t c = enc2(bf16x2_lo(x) * inv, bf16x2_hi(x) * inv);
   if (ODD && (x & 0x7F80u) == 0x7F80u) c |= 0x7Fu;
   if (ODD && (x & 0x7F800000u) == 0x7F800000u) c |= 0x7F00u;
   return c;
@@ -329,8 +320,8 @@ __global__ void __launch_bounds__(kThreadsQ) unpack_kernel(const BlockArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 lo = dec2(c[e] & 0xFFFFu), hi = dec2(c[e] >> 16);
-      v[2 * e] = pack2(lo.x * s, lo.y * s);
-      v[2 * e + 1] = pack2(hi.x * s, hi.y * s);
+      v[2 * e] = pack_bf16x2(lo.x * s, lo.y * s);
+      v[2 * e + 1] = pack_bf16x2(hi.x * s, hi.y * s);
     }
     if constexpr (WIDE) {
       asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + l * 1024), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -341,10 +332,6 @@ __global__ void __launch_bounds__(kThreadsQ) unpack_kernel(const BlockArgs a) {
       *reinterpret_cast<uint4*>(y + l * 1024 + 16) = make_uint4(v[4], v[5], v[6], v[7]);
     }
   }
-}
-
-bool wide(const zp_rows* r) {
-  return aligned(r->data, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
 
 // Sizes that the 8-bit pool's operators share.

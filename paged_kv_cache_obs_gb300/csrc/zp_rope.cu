@@ -15,6 +15,7 @@
 
 #include "zp_internal.h"
 #include "zp_launch.h"
+#include "zp_ptx.cuh"
 
 namespace zp {
 namespace {
@@ -37,14 +38,6 @@ struct RopeArgs {
   int T, Hq, Hkv, d, rd, inplace_q, inplace_k, tokens;  // tokens: per CTA
   float mscale;
 };
-
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // One pair; the roundings are written out so that every form of the kernel gives the same bits.
 __device__ __forceinline__ float turn_a(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
@@ -130,12 +123,12 @@ __global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_const
           if (INTER) {
             uint32_t& x0 = e < 2 ? xa[2 * e] : xb[2 * e - 4];
             uint32_t& x1 = e < 2 ? xa[2 * e + 1] : xb[2 * e - 3];
-            x0 = pack2(turn_a(lo_f(x0), hi_f(x0), w.x, w.y), turn_b(lo_f(x0), hi_f(x0), w.x, w.y));
-            x1 = pack2(turn_a(lo_f(x1), hi_f(x1), w.z, w.w), turn_b(lo_f(x1), hi_f(x1), w.z, w.w));
+            x0 = pack_bf16x2(turn_a(bf16x2_lo(x0), bf16x2_hi(x0), w.x, w.y), turn_b(bf16x2_lo(x0), bf16x2_hi(x0), w.x, w.y));
+            x1 = pack_bf16x2(turn_a(bf16x2_lo(x1), bf16x2_hi(x1), w.z, w.w), turn_b(bf16x2_lo(x1), bf16x2_hi(x1), w.z, w.w));
           } else {
-            const float a0 = lo_f(xa[e]), a1 = hi_f(xa[e]), b0 = lo_f(xb[e]), b1 = hi_f(xb[e]);
-            xa[e] = pack2(turn_a(a0, b0, w.x, w.y), turn_a(a1, b1, w.z, w.w));
-            xb[e] = pack2(turn_b(a0, b0, w.x, w.y), turn_b(a1, b1, w.z, w.w));
+            const float a0 = bf16x2_lo(xa[e]), a1 = bf16x2_hi(xa[e]), b0 = bf16x2_lo(xb[e]), b1 = bf16x2_hi(xb[e]);
+            xa[e] = pack_bf16x2(turn_a(a0, b0, w.x, w.y), turn_a(a1, b1, w.z, w.w));
+            xb[e] = pack_bf16x2(turn_b(a0, b0, w.x, w.y), turn_b(a1, b1, w.z, w.w));
           }
         }
       }
@@ -165,15 +158,11 @@ __global__ void __launch_bounds__(kThreadsR) rope_any_kernel(const __grid_consta
     }
     const int ia = INTER ? 2 * v : v, ib = INTER ? 2 * v + 1 : v + half;
     const float2 w = cs[tk * half + v];
-    const float xa = lo_f(r.in[ia]), xb = lo_f(r.in[ib]);
-    const uint32_t y = pack2(turn_a(xa, xb, w.x, w.y), turn_b(xa, xb, w.x, w.y));
+    const float xa = bf16x2_lo(r.in[ia]), xb = bf16x2_lo(r.in[ib]);
+    const uint32_t y = pack_bf16x2(turn_a(xa, xb, w.x, w.y), turn_b(xa, xb, w.x, w.y));
     r.out[ia] = static_cast<uint16_t>(y);
     r.out[ib] = static_cast<uint16_t>(y >> 16);
   }
-}
-
-bool wide(const zp_rows* r) {
-  return aligned(r->data, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
 
 }  // namespace
