@@ -387,8 +387,8 @@ typedef struct zp_kv8_pool {
  *   cached          device int32 [B], tokens in request r's cache before the call: its new tokens
  *                   take positions cached[r], cached[r] + 1, ...
  *   block_tables    device int32 [B][max_blocks]; only the entries of blocks that receive tokens
- *                   are read.  A block that receives tokens belongs to one request (shared
- *                   prefix blocks are full, and never appended to).
+ *                   are read.  A block that receives tokens belongs to one request and stands once
+ *                   in its table (shared prefix blocks are full, and never appended to).
  * A block whose first token is new starts with a scale of its own.  In a part-full block the
  * scale is the larger of the old one and the one the new tokens need; if that is larger, the
  * codes already there are brought to it (rounded once more).  Rows behind the last token are not
@@ -397,7 +397,7 @@ typedef struct zp_kv8_pool {
  * A request whose entries of token_start or cached are out of range, or that would pass
  * max_blocks, is skipped; so is a block with an id outside the pool: ZP_ERR_BAD_TABLE.  If
  * token_start decreases anywhere, which requests are written is undefined (nothing outside their
- * blocks is).  head_dim 64 or 128, block_size 16 or 32. */
+ * blocks is).  Tokens without a request (B = 0 with T > 0) are refused.  head_dim 64 or 128, block_size 16 or 32. */
 zp_status zp_kv8_append(const zp_kv8_pool* pool, int32_t layer, const zp_rows* k, const zp_rows* v, int32_t T,
                         const int32_t* token_start, const int32_t* cached, int32_t B, const int32_t* block_tables,
                         int32_t max_blocks, const zp_params* params, void* workspace, size_t workspace_bytes,
@@ -455,6 +455,8 @@ size_t zp_kv8_decode_workspace_size(const zp_params* params, int32_t B, int32_t 
  *   workspace     >= zp_paged_window_workspace_size() bytes, 256-byte aligned.
  * A bad length, q_start or block id: the rows concerned are not written, ZP_ERR_BAD_TABLE.
  * ZP_ERR_TIMEOUT (a wait inside the kernel gave up) as for zp_compress: the output is undefined.
+ * Weights are held to 16 bits where head groups times max_q is 16 or less, and rounded to bf16 above
+ * (off by at most 2^-8 of themselves, as the tensor cores take them); sums and maxima are fp32.
  * Keys and values that a row does not see do not reach it, whatever they hold.  head_dim 64 or
  * 128, block_size 16 or 32, up to 16 query heads per kv head. */
 zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,

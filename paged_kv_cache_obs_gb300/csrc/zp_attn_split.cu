@@ -35,7 +35,7 @@
 //
 // Measured (one layer): 8 requests of 100000 to 131072 E4M3 tokens, 28 heads on 4, d 128: 160 us, 5.9
 // TB/s; 224 requests of 1 to 2048, 32 heads on 8: 84 us, 5.6 TB/s; 64 requests that see 1028 bf16 tokens
-// of 8 heads: 44 us, 5.7 TB/s.  The long case fills 54 % of its
+// of 8 heads: 45 us, 5.6 TB/s.  The long case fills 54 % of its
 // issue slots, many of them with turning codes into f16; the warp-level MMA that takes E4M3 operands
 // ran 20 % more instructions in all and was slower.
 #include "zp_attn.h"

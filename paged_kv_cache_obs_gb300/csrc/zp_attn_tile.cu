@@ -28,11 +28,13 @@
 // tokens that no row sees are zeroed, and so are values that are not finite and that only some rows see
 // (0 * inf must not reach the others).  The rows that do see them get them added to their sums at the
 // item's end: an infinity or NaN times a weight above 0 is itself, so no weight has to be known.  That
-// takes a look at the tiles concerned alone, about 10 us each, however long the cache is.
+// takes a look at the tiles concerned alone, however long the cache is: 30 us for a tile with one such
+// value, 1 ms where all of its tokens have some.
 //
-// Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 189 us, 1280 TFLOP/s
+// Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 191 us, 1270 TFLOP/s
 // over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 244 us, 1480
-// TFLOP/s.  What bounds it is the chain of one query tile: softmax of 128 x 128 logits (1100 to 1250
+// TFLOP/s (a dozen calls after a pause; 200 and 262 us in calls that follow one another for seconds, where
+// the power limit takes the clock from 2.07 to 1.97 and 1.94 GHz).  What bounds it is the chain of one query tile: softmax of 128 x 128 logits (1100 to 1250
 // cycles), hand-over to the tensor core (300), its PV and its next S (1024), and back (370), since
 // with d = 128 S, S, O and O fill TMEM and the next S can only take P's place.  Two tiles in turn keep
 // the tensor core at 2048 of about 2900 cycles; an item's end and start cost another two tiles' time.

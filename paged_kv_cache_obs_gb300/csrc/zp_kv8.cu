@@ -12,8 +12,8 @@
 // maximum is a warp reduction, and nothing is staged.  They are bound by HBM (2 bytes read and
 // 1 written a value, or the reverse).  Measured: 1016 blocks of 32 layers and 8 heads packed in 447 us
 // (7.1 TB/s), 64 blocks of 28 layers and 4 heads read back in 27.6 us (6.4 TB/s), 8200 new tokens of 8
-// heads appended in 11 us (4.7 TB/s: three dependent loads, then one wave of tiles), 256 single ones in
-// 4.8 us (the same chain, with nothing behind it).
+// heads appended in 10.7 us (4.7 TB/s: a chain of dependent loads before the values are needed, in 2176 CTAs,
+// 1.43 times what the SMs hold at once), 256 single ones in 4.8 us (the same chain, with nothing behind it).
 #include "zp_internal.h"
 #include "zp_launch.h"
 #include "zp_ptx.cuh"
@@ -137,7 +137,8 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
 // a time, and the host needs no per-request sizes: T / b + 2 B slots in all.  Grid (slot, group
 // of kWarpsQ tiles); a warp takes one (K|V, head) tile of the slot's block.
 // Registers are held to 10 CTAs an SM (5 with 32 x 128 tiles): the chains of dependent loads need the
-// warps (8200 prompt tokens: 10.7 us so, 11.6 with the compiler's choice of 64 registers).
+// warps (8200 prompt tokens: 10.7 us so, 11.6 with the compiler's choice of 64 registers, although 6 to 12
+// registers are spilled for it in the 32 x 64 and 16 x 128 forms).
 template <int D, int BS, bool VEC>
 __global__ void __launch_bounds__(kThreadsQ, BS * D == 4096 ? 5 : 10) append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;                 // lanes per row (8 values each)

@@ -3,8 +3,8 @@
 // Pair i of a token at position p is turned by the angle p * f_i:
 //   (y_a, y_b) = m * (x_a cos - x_b sin, x_b cos + x_a sin).
 // f_i is held as turns per position in units of 2^-64, so p * f_i modulo one turn is one 64-bit
-// integer product, exact for every int32 position (its only error is the table's own rounding,
-// |p| 2^-65 turns); in fp32 the angle of position 10^6 would be off by 0.06 rad.  The top 32 bits
+// integer product, exact for every int32 position (its only error is the table's own, which is fp64's
+// rounding of f_i / 2 pi: |p| 2^-56 turns for the fastest pair); in fp32 the angle of position 10^6 would be off by 0.06 rad.  The top 32 bits
 // are the signed fraction of a turn that sincospif takes.
 //
 // The kernel is bound by HBM: every value is read once and written once (out of place).  A CTA
