@@ -47,16 +47,19 @@ class _Tensors:
     PyTorch and only the per-step operators need it, so the first of their calls loads it; its functions
     become attributes here."""
 
+    _ENTRIES = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn")
+
     def __getattr__(self, name):
+        if name not in self._ENTRIES:
+            raise AttributeError(name)
         if not os.path.exists(_TENSORS_PATH):
             raise ImportError(f"zp_tensors.so is not built ({_TENSORS_PATH}); run __graft_entry__.build() "
                               "or python -m paged_kv_cache_obs_gb300.build")
         spec = importlib.util.spec_from_file_location("zp_tensors", _TENSORS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        entries = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn")
-        module.bind(*(ctypes.cast(lib["zp_" + e], _P).value for e in entries))
-        self.__dict__.update({e: getattr(module, e) for e in entries})
+        module.bind(*(ctypes.cast(lib["zp_" + e], _P).value for e in self._ENTRIES))
+        self.__dict__.update({e: getattr(module, e) for e in self._ENTRIES})
         return self.__dict__[name]
 
 
