@@ -250,8 +250,8 @@ __device__ __forceinline__ bool take_item(const AttnArgs& a, int item, int nx, c
   }
   w.two = w.queries > qpt;
   // runs of the list: first tokens' blocks, where column e is token e, and the window's, where it is
-  // token e + shift; one run where the two meet
-  const int sink = w.sink_blocks == w.win_block ? 0 : w.sink_blocks << bs, shift = sink ? (w.win_block << bs) - sink : 0;
+  // token e + shift (the window's alone where there are no first tokens); one run where the two meet
+  const int shift = (w.win_block - w.sink_blocks) << bs, sink = shift ? w.sink_blocks << bs : 0;
   w.c0 = min(min(sink, a.sinks), w.p_first + 1) / kKeys;
   w.c1 = (max(sink, a.window == 0 ? 0 : w.p_last - a.window + 1 - shift) + kKeys - 1) / kKeys;
   w.c2 = min(w.p_first + 1 - shift, w.blocks << bs) / kKeys;

@@ -530,3 +530,13 @@ def test_queries_may_be_broadcast(zp, new, d):
         zp.zp_paged_window_attn(*a)
         outs.append(a[6])
     assert zp.zp_read_error(args[8]) == 0 and torch.equal(*outs)
+
+
+# ------------------------------------------------------------------ masks ---------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cached,new,window", [(1000, 300, 700), (1500, 700, 1300), (3000, 200, 2100), (700, 64, 600), (4000, 130, 1000)])
+@pytest.mark.parametrize("d,b", [(64, 16), (128, 32)])
+def test_a_window_without_first_tokens(zp, cached, new, window, d, b):
+    # positions of less than two windows, where the window's start lies before its middle, and further ones
+    A._window_case(zp, 4, 2, d, b, [cached, 5], [new, 20], window, 0, seed=new, hidden_nan=True, rel=A.TILED)
