@@ -284,8 +284,8 @@ zp_status zp_test_compress_stalled(const zp_kv_pool* pool, const int32_t* block_
                                    int64_t stall_limit_ns, zp_stream stream);
 
 /* ---------------------------------------------------------------------------------------
- * Operators around the cache: rotary positions, an 8-bit form of the pool, and attention with
- * a sliding window.
+ * Operators around the cache: rotary positions, a step's slots and cache writes, an 8-bit form of
+ * the pool, and attention with a sliding window.
  *
  * They share these conventions, on top of the ones at the top of this file:
  *   - A workspace belongs to one call in flight at a time; calls of any of these operators may
@@ -363,6 +363,84 @@ zp_status zp_rope_init(const zp_rope_config* config, zp_rope* out);
 zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const zp_rows* q_out, int32_t num_q_heads,
                         const zp_rows* k, const zp_rows* k_out, int32_t num_kv_heads, const int32_t* positions,
                         int32_t T, zp_stream stream);
+
+/* Rotary positions with several axes: a token of an image or video frame has a time, a height and a
+ * width (text has the same number on each), and every pair of a head is turned by one of them. */
+#define ZP_ROPE_MAX_AXES 4
+enum {
+  ZP_AXES_SECTIONS = 0,   /* the first sections[0] pairs belong to axis 0, the next sections[1] to axis 1, ... */
+  ZP_AXES_CYCLE = 1,      /* pair i belongs to axis i % num_axes while that axis has had fewer than its
+                             section's pairs, and to axis 0 otherwise */
+  ZP_AXES_RESTART = 2     /* as ZP_AXES_SECTIONS, and each section has the angles of a head whose rotary_dim
+                             is twice the section: the f_i start again */
+};
+
+typedef struct zp_rope_axes_config {
+  int32_t num_axes;       /* 1 .. ZP_ROPE_MAX_AXES */
+  int32_t layout;         /* ZP_AXES_* */
+  int32_t sections[ZP_ROPE_MAX_AXES]; /* pairs of each axis, >= 1, together rotary_dim / 2; a layout that
+                             cannot give an axis its pairs is refused */
+} zp_rope_axes_config;
+
+/* What zp_rope_apply_axes needs, filled by zp_rope_axes_init. */
+typedef struct zp_rope_axes {
+  zp_rope rope;           /* its turns hold each pair's own */
+  int32_t num_axes;
+  uint8_t axis[128];      /* of each pair */
+} zp_rope_axes;
+
+/* Host only. */
+zp_status zp_rope_axes_init(const zp_rope_config* config, const zp_rope_axes_config* axes, zp_rope_axes* out);
+
+/* zp_rope_apply where pair i of token t is turned by positions[axis[i] * axis_stride + t] * f_i.
+ *   positions       device int32 [num_axes][axis_stride], any values; axis_stride 0: all axes share one row.
+ * Tokens with the same position on every axis get the bits that zp_rope_apply gives them (but for
+ * ZP_AXES_RESTART, whose angles are others). */
+zp_status zp_rope_apply_axes(const zp_rope_axes* axes, const zp_rows* q, const zp_rows* q_out, int32_t num_q_heads,
+                             const zp_rows* k, const zp_rows* k_out, int32_t num_kv_heads, const int32_t* positions,
+                             int64_t axis_stride, int32_t T, zp_stream stream);
+
+/* The blocks, slots and positions of a step, made on the device in one launch from lengths that the
+ * device alone may know (what the step before accepted of its drafts, say), so that steps follow one another
+ * without the host, and can be captured and replayed.
+ *   cached          device int32 [B], tokens in request r's cache before the step
+ *   new_tokens      device int32 [B], tokens that the step adds (0: none, as for a padded request)
+ *   first_pos       device int32 [B] or NULL: the position of request r's first new token, where it is not
+ *                   cached[r] (a compression pass drops tokens, and positions go on).  NULL: cached[r].
+ *   free_ids        device int32 [num_free], ids of free blocks (zp_alloc_blocks gives the host some to hand out)
+ *   free_at         device int32 [1] or NULL: how many of free_ids are taken.  The call takes the next ones,
+ *                   in the order of requests and tokens, and advances it.  NULL: none are taken before the call.
+ *   num_blocks      blocks of the pool (num_blocks * block_size <= 2^31 - 1)
+ *   block_tables    device int32 [B][max_blocks].  The call writes the entries of blocks whose first token is
+ *                   new, and reads those of part-full blocks that get tokens; no others.
+ *   token_start     device int32 [B + 1], written: request r owns rows token_start[r] .. token_start[r + 1] - 1.
+ *   seq_lens        device int32 [B], written: cached + new.  May be `cached` itself; no other arrays overlap.
+ *   positions       device int32 [T] or NULL, written.  Rows behind the last request's: 0.
+ *   slots           device int32 [T], written: block * block_size + place in the block, as zp_kv_append takes
+ *                   it.  Rows behind the last request's: -1.
+ *   T               rows of the step's buffers, at least the tokens of all requests.
+ *   params          block_size (16 or 32) is used.
+ *   workspace       device, >= 256 bytes, 256-byte aligned.
+ * A request whose cached or new_tokens is out of range (or that would pass max_blocks) takes part without
+ * tokens (seq_lens: its cached tokens, 0 if those are out of range), ZP_ERR_BAD_TABLE; so do tokens of a block
+ * with an id outside the pool (slot -1).  If the requests' tokens do not fit T (ZP_ERR_BAD_TABLE) or their blocks do not fit
+ * free_ids (ZP_ERR_NO_BLOCKS; a free_at outside 0 .. num_free: ZP_ERR_BAD_TABLE), the step is one without tokens:
+ * token_start is all 0, seq_lens what was cached, slots all -1, and tables and free_at stay.  B up to 65535. */
+zp_status zp_step_slots(const int32_t* cached, const int32_t* new_tokens, const int32_t* first_pos, int32_t B,
+                        const int32_t* free_ids, int32_t num_free, int32_t* free_at, int64_t num_blocks,
+                        int32_t* block_tables, int32_t max_blocks, int32_t* token_start, int32_t* seq_lens,
+                        int32_t* positions, int32_t* slots, int32_t T, const zp_params* params, void* workspace,
+                        size_t workspace_bytes, zp_stream stream);
+
+/* New keys and values of one layer into the bf16 pool, bit for bit.
+ *   k, v            rows [T][num_kv_heads][head_dim]
+ *   slots           device int32 [T]: row t becomes token slots[t] % block_size of block slots[t] / block_size.
+ *                   Below 0: the row goes nowhere.  Other slots are distinct.
+ *   workspace       device, >= 256 bytes, 256-byte aligned.
+ * A slot outside the pool: that row is not written, ZP_ERR_BAD_TABLE.  head_dim 64 or 128, block_size 16 or 32,
+ * num_blocks * block_size <= 2^31 - 1. */
+zp_status zp_kv_append(const zp_kv_pool* pool, int32_t layer, const zp_rows* k, const zp_rows* v, const int32_t* slots,
+                       int32_t T, const zp_params* params, void* workspace, size_t workspace_bytes, zp_stream stream);
 
 /* The 8-bit pool: E4M3 codes in the bf16 pool's layout, [num_layers][num_blocks][2]
  * [num_kv_heads][block_size][head_dim], and one fp32 scale per (layer, block, K|V, head); a value

@@ -1,5 +1,5 @@
-"""Plain 64-bit definitions of the operators around the paged cache: rotary positions, the 8-bit
-cache and attention with a sliding window.
+"""Plain 64-bit definitions of the operators around the paged cache: rotary positions (of one axis and of several), the
+slots of a step, the 8-bit cache and attention with a sliding window.
 
 TEST INFRASTRUCTURE ONLY, like the compression oracle beside it: numpy in fp64, one row, block or
 token at a time, sharing no code with the library.
@@ -46,6 +46,67 @@ def rope(x, positions, freqs, size, interleaved):
     y[..., ia] = x[..., ia] * c - x[..., ib] * s
     y[..., ib] = x[..., ib] * c + x[..., ia] * s
     return y
+
+
+def rope_axes(x, positions, rotary_dim, theta, sections, layout, interleaved, scaling="none", **kw):
+    """x [T, H, d] and positions [axes, T] -> rotated [T, H, d], one pair at a time."""
+    half, n = rotary_dim // 2, len(sections)
+    freqs, size = rope_frequencies(rotary_dim, theta, scaling, **kw)
+    y = x.copy()
+    had = [0] * n
+    for i in range(half):
+        if layout == "cycle":
+            axis = i % n if had[i % n] < sections[i % n] else 0
+        else:
+            axis = next(a for a in range(n) if i < sum(sections[:a + 1]))
+        f = freqs[i]
+        if layout == "restart":
+            f = rope_frequencies(2 * sections[axis], theta, scaling, **kw)[0][had[axis]]
+        had[axis] += 1
+        ang = positions[axis].astype(np.float64) * f
+        c, s = (size * np.cos(ang))[:, None], (size * np.sin(ang))[:, None]
+        ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        y[..., ia] = x[..., ia] * c - x[..., ib] * s
+        y[..., ib] = x[..., ib] * c + x[..., ia] * s
+    return y
+
+
+# ------------------------------------------------------------------ a step's slots -----------
+
+
+def step_slots(cached, new, free, tables, b, T, num_blocks, first=None, free_at=0):
+    """(tables, token_start, seq_lens, positions, slots, free_at, error) of a step, a token at a time; error is None,
+    "table" or "blocks"."""
+    B, capacity = len(cached), tables.shape[1] * b
+    had, add, error = [], [], None
+    for r in range(B):
+        c, n = int(cached[r]), int(new[r])
+        good = 0 <= c <= capacity
+        if not good or n < 0 or c + n > capacity:
+            error, n = "table", 0
+        had.append(c if good else 0)
+        add.append(n)
+    need = sum(-(-(c + n) // b) - -(-c // b) for c, n in zip(had, add))
+    if not 0 <= free_at <= len(free) or sum(add) > T or need > len(free) - free_at:
+        if error is None:
+            error = "table" if not 0 <= free_at <= len(free) or sum(add) > T else "blocks"
+        return tables, [0] * (B + 1), had, [0] * T, [-1] * T, free_at, error
+    tables, start, positions, slots = tables.copy(), [0], [], []
+    for r in range(B):
+        for i in range(add[r]):
+            p = had[r] + i
+            if p % b == 0:
+                tables[r, p // b] = free[free_at]
+                free_at += 1
+            block = int(tables[r, p // b])
+            inside = 0 <= block < num_blocks
+            if not inside:
+                error = "table"
+            slots.append(block * b + p % b if inside else -1)
+            positions.append((had[r] if first is None else int(first[r])) + i)
+        start.append(len(slots))
+    rest = T - len(slots)
+    return tables, start, [c + n for c, n in zip(had, add)], positions + [0] * rest, slots + [-1] * rest, free_at, error
 
 
 # ------------------------------------------------------------------ 8-bit cache --------------

@@ -27,6 +27,9 @@ struct Library {
   decltype(&zp_kv8_unpack_blocks) kv8_unpack_blocks;
   decltype(&zp_kv8_decode_attn) kv8_decode_attn;
   decltype(&zp_paged_window_attn) paged_window_attn;
+  decltype(&zp_rope_apply_axes) rope_apply_axes;
+  decltype(&zp_step_slots) step_slots;
+  decltype(&zp_kv_append) kv_append;
 } lib;
 
 [[noreturn]] void refuse(const std::string& what) { throw std::invalid_argument(what); }
@@ -42,6 +45,11 @@ int32_t i32(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw PythonError{};
   if (v < INT_MIN || v > INT_MAX) refuse("expected 32-bit numbers");
   return static_cast<int32_t>(v);
+}
+int64_t i64(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError{};
+  return v;
 }
 template <class T>
 T* address(PyObject* o) {
@@ -124,28 +132,90 @@ PyObject* call(F f) {
   return PyLong_FromLong(st);
 }
 
+// The rows of q and k (either may be None) and where their results go.
+struct Turned {
+  zp_rows r[4];
+  int32_t heads[2] = {0, 0};
+  bool have[2];
+  Turned(PyObject* const* in, PyObject* const* out, int dev, int32_t T, int32_t d) {
+    for (int i = 0; i < 2; ++i) {
+      have[i] = in[i] != Py_None;
+      if (!have[i]) continue;
+      const at::Tensor& x = tensor(in[i]);
+      if (x.dim() != 3 || x.size(1) > INT_MAX) refuse("expected rows [tokens, heads, head_dim]");
+      heads[i] = static_cast<int32_t>(x.size(1));
+      r[2 * i] = rows(in[i], dev, T, heads[i], d);
+      r[2 * i + 1] = out[i] == Py_None ? r[2 * i] : rows(out[i], dev, T, heads[i], d);
+    }
+  }
+  const zp_rows* at(int i) const { return have[i / 2] ? &r[i] : nullptr; }
+};
+
 // rope, q, k, positions, q_out, k_out, stream
 PyObject* rope_apply(PyObject* const* a) {
   const zp_rope* const rope = address<const zp_rope>(a[0]);
   const int dev = device_of(tensor(a[3]));
   const int32_t T = count(a[3], "positions [tokens]");
-  zp_rows r[4];
-  int32_t heads[2] = {0, 0};
-  for (int i = 0; i < 2; ++i) {
-    if (a[1 + i] == Py_None) continue;
-    const at::Tensor& x = tensor(a[1 + i]);
-    if (x.dim() != 3 || x.size(1) > INT_MAX) refuse("expected rows [tokens, heads, head_dim]");
-    heads[i] = static_cast<int32_t>(x.size(1));
-    r[2 * i] = rows(a[1 + i], dev, T, heads[i], rope->head_dim);
-    r[2 * i + 1] = a[4 + i] == Py_None ? r[2 * i] : rows(a[4 + i], dev, T, heads[i], rope->head_dim);
-  }
+  const Turned x(a + 1, a + 4, dev, T, rope->head_dim);
   const int32_t* const pos = entries(a[3], dev, T);
   const zp_stream st = stream(a[6], dev);
-  const bool q = a[1] != Py_None, k = a[2] != Py_None;
+  return call([&] { return lib.rope_apply(rope, x.at(0), x.at(1), x.heads[0], x.at(2), x.at(3), x.heads[1], pos, T, st); });
+}
+
+// axes, q, k, positions, q_out, k_out, stream
+PyObject* rope_apply_axes(PyObject* const* a) {
+  const zp_rope_axes* const axes = address<const zp_rope_axes>(a[0]);
+  const at::Tensor& p = tensor(a[3]);
+  const int dev = device_of(p);
+  // a row of each axis; the same row may stand for all
+  if (p.dim() != 2 || p.size(0) != axes->num_axes || p.size(1) > INT_MAX || p.scalar_type() != at::kInt || (p.size(1) > 1 && p.stride(1) != 1))
+    refuse("expected int32 positions [" + std::to_string(axes->num_axes) + ", tokens] with contiguous rows");
+  const int32_t T = static_cast<int32_t>(p.size(1));
+  const Turned x(a + 1, a + 4, dev, T, axes->rope.head_dim);
+  const zp_stream st = stream(a[6], dev);
+  const int32_t* const pos = static_cast<const int32_t*>(p.data_ptr());
+  const int64_t step = p.size(0) > 1 ? p.stride(0) : 0;
   return call([&] {
-    return lib.rope_apply(rope, q ? &r[0] : nullptr, q ? &r[1] : nullptr, heads[0], k ? &r[2] : nullptr, k ? &r[3] : nullptr,
-                          heads[1], pos, T, st);
+    return lib.rope_apply_axes(axes, x.at(0), x.at(1), x.heads[0], x.at(2), x.at(3), x.heads[1], pos, step, T, st);
   });
+}
+
+// cached, new_tokens, first_pos, free_ids, free_at, num_blocks, block_tables, token_start, seq_lens, positions, slots, params,
+// workspace, stream
+PyObject* step_slots(PyObject* const* a) {
+  const zp_params& p = *address<const zp_params>(a[11]);
+  const int dev = device_of(tensor(a[10]));
+  const int32_t B = count(a[0], "cached [requests]"), T = count(a[10], "slots [tokens]"), free = count(a[3], "free block ids");
+  const auto optional = [&](PyObject* o, int64_t n) { return o == Py_None ? nullptr : entries(o, dev, n); };
+  const int32_t *const cached = entries(a[0], dev, B), *const more = entries(a[1], dev, B), *const first = optional(a[2], B);
+  const int32_t *const ids = entries(a[3], dev, free), *const at = optional(a[4], 1);
+  int32_t max_blocks;
+  const int32_t* const tables = table(a[6], dev, B, max_blocks);
+  const int32_t *const start = entries(a[7], dev, static_cast<int64_t>(B) + 1), *const lens = entries(a[8], dev, B);
+  const int32_t *const pos = optional(a[9], T), *const slots = entries(a[10], dev, T);
+  const int64_t blocks = i64(a[5]);
+  size_t bytes;
+  void* const ws = workspace(a[12], dev, bytes);
+  const zp_stream st = stream(a[13], dev);
+  const auto out = [](const int32_t* x) { return const_cast<int32_t*>(x); };
+  return call([&] {
+    return lib.step_slots(cached, more, first, B, ids, free, out(at), blocks, out(tables), max_blocks, out(start), out(lens), out(pos),
+                          out(slots), T, &p, ws, bytes, st);
+  });
+}
+
+// pool, layer, k, v, slots, params, workspace, stream
+PyObject* kv_append(PyObject* const* a) {
+  const zp_params& p = *address<const zp_params>(a[5]);
+  const int dev = device_of(tensor(a[0]));
+  const zp_kv_pool to = pool(a[0], dev, p);
+  const int32_t layer = i32(a[1]), T = count(a[2], "keys [tokens, heads, head_dim]");
+  const zp_rows k = rows(a[2], dev, T, p.num_kv_heads, p.head_dim), v = rows(a[3], dev, T, p.num_kv_heads, p.head_dim);
+  const int32_t* const slots = entries(a[4], dev, T);
+  size_t bytes;
+  void* const ws = workspace(a[6], dev, bytes);
+  const zp_stream st = stream(a[7], dev);
+  return call([&] { return lib.kv_append(&to, layer, &k, &v, slots, T, &p, ws, bytes, st); });
 }
 
 // codes, scales, layer, k, v, token_start, cached, block_tables, params, workspace, stream
@@ -244,6 +314,9 @@ PyObject* bind(PyObject* const* a) {
   lib.kv8_unpack_blocks = reinterpret_cast<decltype(lib.kv8_unpack_blocks)>(address<void>(a[3]));
   lib.kv8_decode_attn = reinterpret_cast<decltype(lib.kv8_decode_attn)>(address<void>(a[4]));
   lib.paged_window_attn = reinterpret_cast<decltype(lib.paged_window_attn)>(address<void>(a[5]));
+  lib.rope_apply_axes = reinterpret_cast<decltype(lib.rope_apply_axes)>(address<void>(a[6]));
+  lib.step_slots = reinterpret_cast<decltype(lib.step_slots)>(address<void>(a[7]));
+  lib.kv_append = reinterpret_cast<decltype(lib.kv_append)>(address<void>(a[8]));
   Py_RETURN_NONE;
 }
 
@@ -270,13 +343,16 @@ constexpr PyMethodDef def(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&method<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {def<bind, 6>("bind"),
+PyMethodDef methods[] = {def<bind, 9>("bind"),
                          def<rope_apply, 7>("rope_apply"),
                          def<kv8_append, 11>("kv8_append"),
                          def<kv8_pack_blocks, 11>("kv8_pack_blocks"),
                          def<kv8_unpack_blocks, 10>("kv8_unpack_blocks"),
                          def<kv8_decode_attn, 12>("kv8_decode_attn"),
                          def<paged_window_attn, 13>("paged_window_attn"),
+                         def<rope_apply_axes, 7>("rope_apply_axes"),
+                         def<step_slots, 14>("step_slots"),
+                         def<kv_append, 8>("kv_append"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "zp_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

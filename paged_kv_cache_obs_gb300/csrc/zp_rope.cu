@@ -35,6 +35,7 @@ struct RopeArgs {
   uint16_t *qo, *ko;
   int64_t q_ts, q_hs, k_ts, k_hs, qo_ts, qo_hs, ko_ts, ko_hs;
   const int32_t* positions;
+  int64_t axis_stride;  // from one axis' positions to the next's
   int T, Hq, Hkv, d, rd, inplace_q, inplace_k, tokens;  // tokens: per CTA
   float mscale;
 };
@@ -43,11 +44,20 @@ struct RopeArgs {
 __device__ __forceinline__ float turn_a(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
 __device__ __forceinline__ float turn_b(float a, float b, float c, float s) { return fmaf(b, c, __fmul_rn(a, s)); }
 
-__device__ __forceinline__ void fill_table(const zp_rope& rope, const RopeArgs& a, int t0, int nt, float2* cs) {
+// The angle table of a handle, and the position that turns a pair of token t.
+__device__ __forceinline__ const zp_rope& table_of(const zp_rope& rope) { return rope; }
+__device__ __forceinline__ const zp_rope& table_of(const zp_rope_axes& axes) { return axes.rope; }
+__device__ __forceinline__ int32_t position_of(const zp_rope&, const RopeArgs& a, int t, int) { return a.positions[t]; }
+__device__ __forceinline__ int32_t position_of(const zp_rope_axes& axes, const RopeArgs& a, int t, int pair) {
+  return a.positions[axes.axis[pair] * a.axis_stride + t];
+}
+
+template <class Handle>
+__device__ __forceinline__ void fill_table(const Handle& rope, const RopeArgs& a, int t0, int nt, float2* cs) {
   const int half = a.rd >> 1;
   for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
     const int tk = i / half, pair = i - tk * half;
-    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(a.positions[t0 + tk])) * rope.turns[pair];
+    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(position_of(rope, a, t0 + tk, pair))) * table_of(rope).turns[pair];
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
     cs[i] = make_float2(c * a.mscale, s * a.mscale);
@@ -71,8 +81,8 @@ __device__ __forceinline__ Row row_of(const RopeArgs& a, int t, int head) {
 // item is two 16-byte vectors of a row: the two halves of 8 pairs (half layout), 8 adjacent pairs
 // (interleaved), or 16 values that pass through.  A thread keeps its place in the row and walks the
 // CTA's rows (token, head), so that no item costs a division.
-template <bool INTER, int U>
-__global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_constant__ zp_rope rope, const RopeArgs a) {
+template <class Handle, bool INTER, int U>
+__global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_constant__ Handle rope, const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kMaxTokensR * 128];
   after_previous();
   next_may_start();
@@ -139,8 +149,8 @@ __global__ void __launch_bounds__(kThreadsR) rope_wide_kernel(const __grid_const
 }
 
 // Any sizes and strides: an item is one pair, or one value that passes through.
-template <bool INTER>
-__global__ void __launch_bounds__(kThreadsR) rope_any_kernel(const __grid_constant__ zp_rope rope, const RopeArgs a) {
+template <class Handle, bool INTER>
+__global__ void __launch_bounds__(kThreadsR) rope_any_kernel(const __grid_constant__ Handle rope, const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kMaxTokensR * 128];
   after_previous();
   next_may_start();
@@ -163,6 +173,58 @@ __global__ void __launch_bounds__(kThreadsR) rope_any_kernel(const __grid_consta
     r.out[ia] = static_cast<uint16_t>(y);
     r.out[ib] = static_cast<uint16_t>(y >> 16);
   }
+}
+
+// The two calls' checks and launch.
+template <class Handle>
+zp_status apply(const zp_rope* rope, const Handle* handle, const zp_rows* q, const zp_rows* q_out, int32_t num_q_heads, const zp_rows* k,
+                const zp_rows* k_out, int32_t num_kv_heads, const int32_t* positions, int64_t axis_stride, int32_t T, zp_stream stream) {
+  if (!rope || T < 0 || num_q_heads < 0 || num_kv_heads < 0) return ZP_ERR_INVALID_ARG;
+  const int d = rope->head_dim, rd = rope->rotary_dim;
+  if (d < 2 || d > 512 || d % 2 || rd < 2 || rd > d || rd > 256 || rd % 2) return ZP_ERR_INVALID_ARG;
+  const int Hq = q ? num_q_heads : 0, Hkv = k ? num_kv_heads : 0;
+  if (Hq > 4096 || Hkv > 4096) return ZP_ERR_UNSUPPORTED;
+  if (T == 0 || Hq + Hkv == 0) return ZP_OK;
+  if (!positions) return ZP_ERR_INVALID_ARG;
+  RopeArgs a{};
+  bool vec = d % 16 == 0 && rd % 16 == 0;
+  // rows are bf16 at 2-byte addresses; in place means the same rows, strides included
+  const auto take = [&](const zp_rows* in, const zp_rows* out, int heads, int& same) {
+    if (!out || !in->data || !out->data || !aligned(in->data, 2) || !aligned(out->data, 2)) return false;
+    if (rows_overlap(*out, T, heads, d)) return false;
+    same = in->data == out->data;
+    if (same && (in->token_stride != out->token_stride || in->head_stride != out->head_stride)) return false;
+    vec = vec && wide(in) && wide(out);
+    return true;
+  };
+  if (Hq > 0) {
+    if (!take(q, q_out, Hq, a.inplace_q)) return ZP_ERR_INVALID_ARG;
+    a.q = static_cast<const uint16_t*>(q->data);
+    a.qo = static_cast<uint16_t*>(q_out->data);
+    a.q_ts = q->token_stride, a.q_hs = q->head_stride, a.qo_ts = q_out->token_stride, a.qo_hs = q_out->head_stride;
+  }
+  if (Hkv > 0) {
+    if (!take(k, k_out, Hkv, a.inplace_k)) return ZP_ERR_INVALID_ARG;
+    a.k = static_cast<const uint16_t*>(k->data);
+    a.ko = static_cast<uint16_t*>(k_out->data);
+    a.k_ts = k->token_stride, a.k_hs = k->head_stride, a.ko_ts = k_out->token_stride, a.ko_hs = k_out->head_stride;
+  }
+  a.positions = positions;
+  a.axis_stride = axis_stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.rd = rd;
+  a.mscale = rope->mscale;
+  a.tokens = T >= kMaxTokensR * 512 ? kMaxTokensR : 1;
+  const unsigned grid = static_cast<unsigned>((T + a.tokens - 1) / a.tokens);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool inter = rope->interleaved != 0;
+  auto* const kernel = vec && a.tokens == 1 ? (inter ? rope_wide_kernel<Handle, true, kRowsOne> : rope_wide_kernel<Handle, false, kRowsOne>)
+                       : vec                ? (inter ? rope_wide_kernel<Handle, true, kRowsR> : rope_wide_kernel<Handle, false, kRowsR>)
+                                            : (inter ? rope_any_kernel<Handle, true> : rope_any_kernel<Handle, false>);
+  return launch_in_order(kernel, dim3(grid), kThreadsR, 0, st, 1, *handle, a) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
 }  // namespace
@@ -222,49 +284,49 @@ extern "C" zp_status zp_rope_apply(const zp_rope* rope, const zp_rows* q, const 
                                    const zp_rows* k, const zp_rows* k_out, int32_t num_kv_heads,
                                    const int32_t* positions, int32_t T, zp_stream stream) {
   zp::NvtxRange nvtx_range("zp_rope_apply");
-  if (!rope || T < 0 || num_q_heads < 0 || num_kv_heads < 0) return ZP_ERR_INVALID_ARG;
-  const int d = rope->head_dim, rd = rope->rotary_dim;
-  if (d < 2 || d > 512 || d % 2 || rd < 2 || rd > d || rd > 256 || rd % 2) return ZP_ERR_INVALID_ARG;
-  const int Hq = q ? num_q_heads : 0, Hkv = k ? num_kv_heads : 0;
-  if (Hq > 4096 || Hkv > 4096) return ZP_ERR_UNSUPPORTED;
-  if (T == 0 || Hq + Hkv == 0) return ZP_OK;
-  if (!positions) return ZP_ERR_INVALID_ARG;
-  RopeArgs a{};
-  bool vec = d % 16 == 0 && rd % 16 == 0;
-  // rows are bf16 at 2-byte addresses; in place means the same rows, strides included
-  const auto take = [&](const zp_rows* in, const zp_rows* out, int heads, int& same) {
-    if (!out || !in->data || !out->data || !aligned(in->data, 2) || !aligned(out->data, 2)) return false;
-    if (rows_overlap(*out, T, heads, d)) return false;
-    same = in->data == out->data;
-    if (same && (in->token_stride != out->token_stride || in->head_stride != out->head_stride)) return false;
-    vec = vec && wide(in) && wide(out);
-    return true;
-  };
-  if (Hq > 0) {
-    if (!take(q, q_out, Hq, a.inplace_q)) return ZP_ERR_INVALID_ARG;
-    a.q = static_cast<const uint16_t*>(q->data);
-    a.qo = static_cast<uint16_t*>(q_out->data);
-    a.q_ts = q->token_stride, a.q_hs = q->head_stride, a.qo_ts = q_out->token_stride, a.qo_hs = q_out->head_stride;
+  return apply(rope, rope, q, q_out, num_q_heads, k, k_out, num_kv_heads, positions, 0, T, stream);
+}
+
+extern "C" zp_status zp_rope_axes_init(const zp_rope_config* c, const zp_rope_axes_config* x, zp_rope_axes* out) {
+  if (!c || !x || !out) return ZP_ERR_INVALID_ARG;
+  zp_rope_axes r{};
+  zp_status s = zp_rope_init(c, &r.rope);
+  if (s != ZP_OK) return s;
+  const int pairs = c->rotary_dim / 2, n = x->num_axes;
+  if (n < 1 || n > ZP_ROPE_MAX_AXES || x->layout < ZP_AXES_SECTIONS || x->layout > ZP_AXES_RESTART) return ZP_ERR_INVALID_ARG;
+  int64_t sum = 0;
+  for (int i = 0; i < n; ++i) {
+    if (x->sections[i] < 1) return ZP_ERR_INVALID_ARG;
+    sum += x->sections[i];
   }
-  if (Hkv > 0) {
-    if (!take(k, k_out, Hkv, a.inplace_k)) return ZP_ERR_INVALID_ARG;
-    a.k = static_cast<const uint16_t*>(k->data);
-    a.ko = static_cast<uint16_t*>(k_out->data);
-    a.k_ts = k->token_stride, a.k_hs = k->head_stride, a.ko_ts = k_out->token_stride, a.ko_hs = k_out->head_stride;
+  if (sum != pairs) return ZP_ERR_INVALID_ARG;
+  r.num_axes = n;
+  for (int axis = 0, first = 0; axis < n; first += x->sections[axis++]) {
+    for (int i = 0; i < x->sections[axis]; ++i) r.axis[first + i] = static_cast<uint8_t>(axis);
+    if (x->layout != ZP_AXES_RESTART) continue;
+    zp_rope_config part = *c;  // a table of the section's own
+    part.rotary_dim = 2 * x->sections[axis];
+    zp_rope own;
+    if ((s = zp_rope_init(&part, &own)) != ZP_OK) return s;
+    for (int i = 0; i < x->sections[axis]; ++i) r.rope.turns[first + i] = own.turns[i];
   }
-  a.positions = positions;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.d = d;
-  a.rd = rd;
-  a.mscale = rope->mscale;
-  a.tokens = T >= kMaxTokensR * 512 ? kMaxTokensR : 1;
-  const unsigned grid = static_cast<unsigned>((T + a.tokens - 1) / a.tokens);
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool inter = rope->interleaved != 0;
-  auto* const kernel = vec && a.tokens == 1 ? (inter ? rope_wide_kernel<true, kRowsOne> : rope_wide_kernel<false, kRowsOne>)
-                       : vec                ? (inter ? rope_wide_kernel<true, kRowsR> : rope_wide_kernel<false, kRowsR>)
-                                            : (inter ? rope_any_kernel<true> : rope_any_kernel<false>);
-  return launch_in_order(kernel, dim3(grid), kThreadsR, 0, st, 1, *rope, a) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
+  if (x->layout == ZP_AXES_CYCLE) {
+    for (int i = 0; i < pairs; ++i) r.axis[i] = static_cast<uint8_t>(i / n < x->sections[i % n] ? i % n : 0);
+    int count[ZP_ROPE_MAX_AXES] = {};
+    for (int i = 0; i < pairs; ++i) ++count[r.axis[i]];
+    for (int i = 0; i < n; ++i)
+      if (count[i] != x->sections[i]) return ZP_ERR_INVALID_ARG;  // an axis other than the first has more than its turns
+  }
+  *out = r;
+  return ZP_OK;
+}
+
+extern "C" zp_status zp_rope_apply_axes(const zp_rope_axes* axes, const zp_rows* q, const zp_rows* q_out, int32_t num_q_heads,
+                                        const zp_rows* k, const zp_rows* k_out, int32_t num_kv_heads, const int32_t* positions,
+                                        int64_t axis_stride, int32_t T, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_rope_apply_axes");
+  if (!axes || axes->num_axes < 1 || axes->num_axes > ZP_ROPE_MAX_AXES) return ZP_ERR_INVALID_ARG;
+  for (int i = 0; i < axes->rope.rotary_dim / 2 && i < 128; ++i)
+    if (axes->axis[i] >= axes->num_axes) return ZP_ERR_INVALID_ARG;  // a handle that no init filled
+  return apply(&axes->rope, axes, q, q_out, num_q_heads, k, k_out, num_kv_heads, positions, axis_stride, T, stream);
 }

@@ -47,7 +47,8 @@ class _Tensors:
     PyTorch and only the per-step operators need it, so the first of their calls loads it; its functions
     become attributes here."""
 
-    _ENTRIES = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn")
+    _ENTRIES = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn",
+                "rope_apply_axes", "step_slots", "kv_append")
 
     def __getattr__(self, name):
         if name not in self._ENTRIES:
@@ -112,6 +113,20 @@ class zp_rope(ctypes.Structure):
                 ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
 
 
+ZP_ROPE_MAX_AXES = 4
+ZP_AXES_SECTIONS = 0
+ZP_AXES_CYCLE = 1
+ZP_AXES_RESTART = 2
+
+
+class zp_rope_axes_config(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("layout", ctypes.c_int32), ("sections", ctypes.c_int32 * ZP_ROPE_MAX_AXES)]
+
+
+class zp_rope_axes(ctypes.Structure):
+    _fields_ = [("rope", zp_rope), ("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
+
+
 class zp_kv8_pool(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int64)]
 
@@ -150,6 +165,11 @@ _sig("zp_redundancy_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32
 _ROWS = ctypes.POINTER(zp_rows)
 _sig("zp_rope_init", _I32, [ctypes.POINTER(zp_rope_config), ctypes.POINTER(zp_rope)])
 _sig("zp_rope_apply", _I32, [ctypes.POINTER(zp_rope), _ROWS, _ROWS, _I32, _ROWS, _ROWS, _I32, _P, _I32, _P])
+_sig("zp_rope_axes_init", _I32, [ctypes.POINTER(zp_rope_config), ctypes.POINTER(zp_rope_axes_config), ctypes.POINTER(zp_rope_axes)])
+_sig("zp_rope_apply_axes", _I32, [ctypes.POINTER(zp_rope_axes), _ROWS, _ROWS, _I32, _ROWS, _ROWS, _I32, _P, _I64, _I32, _P])
+_sig("zp_step_slots", _I32, [_P, _P, _P, _I32, _P, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _I32, ctypes.POINTER(zp_params),
+                             _P, _SZ, _P])
+_sig("zp_kv_append", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _ROWS, _P, _I32, ctypes.POINTER(zp_params), _P, _SZ, _P])
 _sig("zp_kv8_append", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _ROWS, _I32, _P, _P, _I32, _P, _I32,
                              ctypes.POINTER(zp_params), _P, _SZ, _P])
 _sig("zp_kv8_pack_blocks", _I32, [ctypes.POINTER(zp_kv_pool), _P, _P, ctypes.POINTER(zp_kv8_pool), _P, _I32, _I32, _I32,
@@ -392,6 +412,50 @@ def zp_rope_apply(rope: zp_rope, q, k, positions, q_out=None, k_out=None, stream
     st = _t.rope_apply(_addr(rope), q, k, positions, q_out, k_out, _raw(stream))
     if st:
         _check("zp_rope_apply", st)
+
+
+def zp_rope_axes_init(head_dim: int, rotary_dim: int, theta: float, sections, layout: int = ZP_AXES_SECTIONS,
+                      interleaved: bool = False, scaling: int = ZP_ROPE_NONE, factor: float = 1.0, original_len: int = 0,
+                      low: float = 1.0, high: float = 4.0, mscale: float = 0.0) -> zp_rope_axes:
+    """The handle of zp_rope_apply_axes (host only): sections holds the pairs of each axis, 1 to 4 of them
+    (see zp_rope_axes_config in include/zipage.h)."""
+    cfg = zp_rope_config(head_dim, rotary_dim, int(interleaved), scaling, theta, factor, original_len, low, high, mscale)
+    sections = [int(n) for n in sections]
+    if len(sections) > ZP_ROPE_MAX_AXES:
+        raise ValueError(f"at most {ZP_ROPE_MAX_AXES} axes")
+    axes = zp_rope_axes_config(len(sections), layout, (ctypes.c_int32 * ZP_ROPE_MAX_AXES)(*sections))
+    out = zp_rope_axes()
+    _check("zp_rope_axes_init", lib.zp_rope_axes_init(ctypes.byref(cfg), ctypes.byref(axes), ctypes.byref(out)))
+    return out
+
+
+def zp_rope_apply_axes(axes: zp_rope_axes, q, k, positions, q_out=None, k_out=None, stream=None):
+    """zp_rope_apply with positions [axes, T] (int32): each pair of a head is turned by its own axis' position."""
+    st = _t.rope_apply_axes(_addr(axes), q, k, positions, q_out, k_out, _raw(stream))
+    if st:
+        _check("zp_rope_apply_axes", st)
+
+
+def zp_step_slots(cached, new_tokens, free_ids, block_tables, token_start, seq_lens, slots, params, workspace, num_blocks: int,
+                  positions=None, first_pos=None, free_at=None, stream=None):
+    """The blocks, slots and positions of a step from its requests' lengths, all device int32: reads cached [B],
+    new_tokens [B], free_ids [n] (from free_at [1] on, which advances) and first_pos [B]; writes token_start [B + 1],
+    seq_lens [B] (may be cached), slots [T], positions [T] and the new entries of block_tables [B, max_blocks].
+    num_blocks: blocks of the pool (see include/zipage.h)."""
+    p = _params(params)
+    st = _t.step_slots(cached, new_tokens, first_pos, free_ids, free_at, num_blocks, block_tables, token_start, seq_lens, positions, slots,
+                       _addr(p), workspace, _raw(stream))
+    if st:
+        _check("zp_step_slots", st)
+
+
+def zp_kv_append(pool, layer: int, k, v, slots, params, workspace, stream=None):
+    """Writes the new keys and values k, v [T, H_kv, d] of one layer to the bf16 pool: row t to slot slots[t] (device
+    int32, block * block_size + place in the block; below 0: nowhere)."""
+    p = _params(params)
+    st = _t.kv_append(pool, layer, k, v, slots, _addr(p), workspace, _raw(stream))
+    if st:
+        _check("zp_kv_append", st)
 
 
 def zp_kv8_append(codes, scales, layer: int, k, v, token_start, cached, block_tables, params, workspace, stream=None):
