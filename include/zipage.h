@@ -545,7 +545,43 @@ zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer, const zp_r
 size_t zp_paged_window_workspace_size(const zp_params* params, int32_t T, int32_t B, int32_t max_q,
                                       int32_t max_blocks, int32_t window, int32_t sinks);
 
-/* Test hooks of the bounded waits inside the two attention operators: same operation, arguments and
+/* Attention of whole prompts over their own keys and values, which are rows of memory: before they enter a
+ * cache, or where none is kept, and before they are rounded to 8 bits.  Prompts are packed: prompt r owns rows
+ * token_start[r] .. token_start[r + 1] - 1 of q, k, v and out, and its i-th token sees the tokens of its own prompt with
+ *   t <= i and t > i - window or t < sinks   (window 0: every t <= i).
+ *   q, out        rows [T][H_q][head_dim];  k, v  rows [T][H_kv][head_dim].  out overlaps none of the others.
+ *   token_start   device int32 [B + 1], as for zp_kv8_append.  Rows of out outside its range are not written;
+ *                 those of q, k and v have to be memory that can be read (tiles are loaded whole), but have no
+ *                 effect, whatever they hold.
+ *   max_len       the most tokens of a prompt (an upper bound is fine; a prompt above it is skipped:
+ *                 ZP_ERR_BAD_TABLE).  At most 2^30.
+ *   params        num_q_heads, num_kv_heads, head_dim and scale are used.
+ *   workspace     >= zp_prompt_workspace_size() bytes, 256-byte aligned.
+ * A bad token_start: that prompt is not written, ZP_ERR_BAD_TABLE; ZP_ERR_TIMEOUT, weights and what a row does not
+ * see as for zp_paged_window_attn's form for many rows.  Rows of k and v at other than 16-byte boundaries or
+ * strides are loaded value by value, at a tenth of the speed.  head_dim 64 or 128, up to 16 query heads per kv head. */
+zp_status zp_prompt_attn(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T,
+                         int32_t B, int32_t max_len, int32_t window, int32_t sinks, const zp_rows* out,
+                         const zp_params* params, void* workspace, size_t workspace_bytes, zp_stream stream);
+
+size_t zp_prompt_workspace_size(const zp_params* params, int32_t T, int32_t B, int32_t max_len, int32_t window, int32_t sinks);
+
+/* zp_paged_window_attn over the 8-bit pool: attention of a chunk of new tokens (drafts, chunked prefill, a question
+ * about a document in the cache), whose codes are already in the pool.  Arguments, masks and errors are
+ * zp_paged_window_attn's.
+ * Where head groups times max_q is 16 or less, weights are held as by zp_kv8_decode_attn (11 bits).  Above, the
+ * values are bf16(code * scale), as zp_kv8_unpack_blocks gives them (exact with the scales that the
+ * library writes), and the result is, bit for bit, that of zp_paged_window_attn over the unpacked pool.  Any
+ * finite scales are taken. */
+zp_status zp_kv8_window_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                             int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                             int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                             const zp_params* params, void* workspace, size_t workspace_bytes, zp_stream stream);
+
+size_t zp_kv8_window_workspace_size(const zp_params* params, int32_t T, int32_t B, int32_t max_q, int32_t max_blocks,
+                                    int32_t window, int32_t sinks);
+
+/* Test hooks of the bounded waits inside the attention operators: same operation, arguments and
  * workspace, plus stall_limit_ns (1 .. 1e9).  With the first copies (and products) in flight a warp of
  * each CTA waits, for at most stall_limit_ns, on a barrier that nothing completes.  That wait
  * runs out, the kernel drains what is in flight, records ZP_ERR_TIMEOUT and returns; the output rows are
@@ -559,6 +595,15 @@ zp_status zp_test_paged_window_stalled(const zp_kv_pool* pool, int32_t layer, co
                                        int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
                                        const zp_params* params, void* workspace, size_t workspace_bytes,
                                        int64_t stall_limit_ns, zp_stream stream);
+zp_status zp_test_prompt_stalled(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T,
+                                 int32_t B, int32_t max_len, int32_t window, int32_t sinks, const zp_rows* out,
+                                 const zp_params* params, void* workspace, size_t workspace_bytes, int64_t stall_limit_ns,
+                                 zp_stream stream);
+zp_status zp_test_kv8_window_stalled(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                     int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                     int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                     const zp_params* params, void* workspace, size_t workspace_bytes,
+                                     int64_t stall_limit_ns, zp_stream stream);
 
 /* Synchronises `stream`, copies the error word at the start of `workspace` to *out_status and
  * clears it.  Returns ZP_ERR_CUDA if the copy fails. */

@@ -30,6 +30,8 @@ struct Library {
   decltype(&zp_rope_apply_axes) rope_apply_axes;
   decltype(&zp_step_slots) step_slots;
   decltype(&zp_kv_append) kv_append;
+  decltype(&zp_prompt_attn) prompt_attn;
+  decltype(&zp_kv8_window_attn) kv8_window_attn;
 } lib;
 
 [[noreturn]] void refuse(const std::string& what) { throw std::invalid_argument(what); }
@@ -306,6 +308,42 @@ PyObject* paged_window_attn(PyObject* const* a) {
   });
 }
 
+// codes, scales, layer, q, q_start, block_tables, seq_lens, out, params, workspace, window, sinks, max_q, stream
+PyObject* kv8_window_attn(PyObject* const* a) {
+  const zp_params& p = *address<const zp_params>(a[8]);
+  const int dev = device_of(tensor(a[0]));
+  const zp_kv8_pool from = kv8(a[0], a[1], dev, p);
+  const int32_t layer = i32(a[2]), T = count(a[3], "queries [tokens, heads, head_dim]"), B = count(a[6], "lengths [requests]");
+  const zp_rows q = rows(a[3], dev, T, p.num_q_heads, p.head_dim), out = rows(a[7], dev, T, p.num_q_heads, p.head_dim);
+  const int32_t* const start = entries(a[4], dev, static_cast<int64_t>(B) + 1);
+  int32_t max_blocks;
+  const int32_t* const tables = table(a[5], dev, B, max_blocks);
+  const int32_t* const lens = entries(a[6], dev, B);
+  size_t bytes;
+  void* const ws = workspace(a[9], dev, bytes);
+  const int32_t window = i32(a[10]), sinks = i32(a[11]), max_q = i32(a[12]);
+  const zp_stream st = stream(a[13], dev);
+  return call([&] {
+    return lib.kv8_window_attn(&from, layer, &q, start, T, max_q, tables, lens, B, max_blocks, window, sinks, &out, &p, ws, bytes, st);
+  });
+}
+
+// q, k, v, token_start, out, params, workspace, max_len, window, sinks, stream
+PyObject* prompt_attn(PyObject* const* a) {
+  const zp_params& p = *address<const zp_params>(a[5]);
+  const int dev = device_of(tensor(a[0]));
+  const int32_t T = count(a[0], "queries [tokens, heads, head_dim]"), n = count(a[3], "token_start [prompts + 1]");
+  if (n < 1) refuse("expected token_start [prompts + 1]");
+  const zp_rows q = rows(a[0], dev, T, p.num_q_heads, p.head_dim), out = rows(a[4], dev, T, p.num_q_heads, p.head_dim);
+  const zp_rows k = rows(a[1], dev, T, p.num_kv_heads, p.head_dim), v = rows(a[2], dev, T, p.num_kv_heads, p.head_dim);
+  const int32_t* const start = entries(a[3], dev, n);
+  size_t bytes;
+  void* const ws = workspace(a[6], dev, bytes);
+  const int32_t max_len = i32(a[7]), window = i32(a[8]), sinks = i32(a[9]);
+  const zp_stream st = stream(a[10], dev);
+  return call([&] { return lib.prompt_attn(&q, &k, &v, start, T, n - 1, max_len, window, sinks, &out, &p, ws, bytes, st); });
+}
+
 // The addresses of the library's entry points, in the order of Library.
 PyObject* bind(PyObject* const* a) {
   lib.rope_apply = reinterpret_cast<decltype(lib.rope_apply)>(address<void>(a[0]));
@@ -317,6 +355,8 @@ PyObject* bind(PyObject* const* a) {
   lib.rope_apply_axes = reinterpret_cast<decltype(lib.rope_apply_axes)>(address<void>(a[6]));
   lib.step_slots = reinterpret_cast<decltype(lib.step_slots)>(address<void>(a[7]));
   lib.kv_append = reinterpret_cast<decltype(lib.kv_append)>(address<void>(a[8]));
+  lib.prompt_attn = reinterpret_cast<decltype(lib.prompt_attn)>(address<void>(a[9]));
+  lib.kv8_window_attn = reinterpret_cast<decltype(lib.kv8_window_attn)>(address<void>(a[10]));
   Py_RETURN_NONE;
 }
 
@@ -343,7 +383,7 @@ constexpr PyMethodDef def(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&method<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {def<bind, 9>("bind"),
+PyMethodDef methods[] = {def<bind, 11>("bind"),
                          def<rope_apply, 7>("rope_apply"),
                          def<kv8_append, 11>("kv8_append"),
                          def<kv8_pack_blocks, 11>("kv8_pack_blocks"),
@@ -353,6 +393,8 @@ PyMethodDef methods[] = {def<bind, 9>("bind"),
                          def<rope_apply_axes, 7>("rope_apply_axes"),
                          def<step_slots, 14>("step_slots"),
                          def<kv_append, 8>("kv_append"),
+                         def<prompt_attn, 11>("prompt_attn"),
+                         def<kv8_window_attn, 14>("kv8_window_attn"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "zp_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,5 +1,5 @@
-// zp_attn.cpp — the entry points of decode attention over the 8-bit pool and of attention with a
-// sliding window: argument checks, workspace, and the choice of the kernel.
+// zp_attn.cpp — the entry points of decode attention over the 8-bit pool, of attention with a sliding
+// window over either pool and of attention of packed prompts: argument checks, workspace, and the choice of the kernel.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -115,7 +115,73 @@ zp_status paged_window(const zp_kv_pool* pool, int32_t layer, const zp_rows* q, 
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows) {
     return split_launch(a, p, false, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
   }
-  return tile_launch(a, pool, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+  return tile_launch(a, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+}
+
+zp_status kv8_window(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start, int32_t T, int32_t max_q,
+                     const int32_t* block_tables, const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window, int32_t sinks,
+                     const zp_rows* out, const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream, uint64_t stall_ns) {
+  if (!pool || !pool->codes || !pool->scales || T < 0 || max_q < 1) return ZP_ERR_INVALID_ARG;
+  if (T == 0) B = 0;  // nothing to do, and q and out may be empty
+  const zp_status s = check(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, T, B, max_blocks, window, sinks);
+  if (s != ZP_OK) return s;
+  if (!aligned(pool->codes, 16) || !aligned(pool->scales, 4) || (B > 0 && !q_start)) return ZP_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, zp_kv8_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks)))
+    return ZP_ERR_INVALID_ARG;
+  if (B == 0) return ZP_OK;
+  AttnArgs a = args_of(p, layer, pool->num_blocks, q, out, block_tables, seq_lens, B, max_blocks, window, sinks);
+  a.pool = static_cast<const uint8_t*>(pool->codes);
+  a.scales = pool->scales;
+  a.q_start = q_start;
+  a.T = T;
+  a.max_q = std::min(max_q, max_blocks * p->block_size);
+  a.stall = stall_ns != 0;
+  a.limit_ns = a.stall ? stall_ns : kWaitNs;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows)
+    return split_launch(a, p, true, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+  return tile8_launch(a, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+}
+
+// Prompts walk their rows in runs of tokens as requests walk blocks.  A run is what one copy brings: a whole tile of
+// 128 tokens, or 32 where a window starts and first tokens end inside of tiles.
+struct PromptRuns {
+  zp_params p;
+  int32_t runs;  // of the longest prompt
+};
+PromptRuns prompt_runs(const zp_params* p, int32_t max_len, int32_t window) {
+  PromptRuns r{*p, 0};
+  r.p.block_size = window == 0 || window >= max_len ? 128 : 32;
+  r.runs = (max_len + r.p.block_size - 1) / r.p.block_size;
+  return r;
+}
+
+zp_status prompt(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T, int32_t B, int32_t max_len,
+                 int32_t window, int32_t sinks, const zp_rows* out, const zp_params* p, void* workspace, size_t workspace_bytes,
+                 zp_stream stream, uint64_t stall_ns) {
+  if (!p || T < 0 || max_len < 1 || window < 0 || sinks < 0) return ZP_ERR_INVALID_ARG;
+  if (max_len > (1 << 30)) return ZP_ERR_UNSUPPORTED;
+  if (T == 0) B = 0;  // nothing to do, and the rows may be empty
+  const PromptRuns r = prompt_runs(p, std::min(max_len, std::max(T, 1)), window);
+  zp_params one = *p;  // the checks that a pool of one layer gets
+  one.num_layers = 1;
+  one.block_size = 16;
+  const zp_status s = check(&one, 0, 1, q, out, token_start, token_start, T, B, 1, window, sinks);
+  if (s != ZP_OK) return s;
+  if (B > 0 && (!k || !v || !k->data || !v->data || !aligned(k->data, 2) || !aligned(v->data, 2))) return ZP_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, zp_prompt_workspace_size(p, T, B, max_len, window, sinks))) return ZP_ERR_INVALID_ARG;
+  if (B == 0) return ZP_OK;
+  AttnArgs a = args_of(&r.p, 0, 1, q, out, nullptr, nullptr, B, r.runs, window, sinks);
+  a.k = static_cast<const uint16_t*>(k->data);
+  a.v = static_cast<const uint16_t*>(v->data);
+  a.k_ts = k->token_stride, a.k_hs = k->head_stride, a.v_ts = v->token_stride, a.v_hs = v->head_stride;
+  a.q_start = token_start;
+  a.T = T;
+  a.max_q = max_len;
+  a.stall = stall_ns != 0;
+  a.limit_ns = a.stall ? stall_ns : kWaitNs;
+  return tile_rows_launch(a, p, tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, workspace_bytes), workspace,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 bool stall_ok(int64_t ns) { return ns >= 1 && ns <= 1000000000; }
@@ -138,6 +204,19 @@ extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, 
   return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
 }
 
+// Its kernels are those of the bf16 pool, and so are its plans.
+extern "C" size_t zp_kv8_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q, int32_t max_blocks,
+                                               int32_t window, int32_t sinks) {
+  return zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks);
+}
+
+extern "C" size_t zp_prompt_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_len, int32_t window, int32_t sinks) {
+  if (!p || T < 0 || max_len < 1 || max_len > (1 << 30) || window < 0 || sinks < 0) return 0;
+  const PromptRuns r = prompt_runs(p, std::min(max_len, std::max(T, 1)), window);
+  if (!sizes_ok(&r.p, B, r.runs)) return 0;
+  return tile_plan(&r.p, T, B, max_len, r.runs, window, sinks).bytes;
+}
+
 extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,
                                         const int32_t* block_tables, const int32_t* seq_lens, int32_t B,
                                         int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
@@ -153,6 +232,41 @@ extern "C" zp_status zp_paged_window_attn(const zp_kv_pool* pool, int32_t layer,
   zp::NvtxRange nvtx_range("zp_paged_window_attn");
   return paged_window(pool, layer, q, q_start, T, max_q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace,
                       workspace_bytes, stream, 0);
+}
+
+extern "C" zp_status zp_kv8_window_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                        int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                        int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                        const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_kv8_window_attn");
+  return kv8_window(pool, layer, q, q_start, T, max_q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace,
+                    workspace_bytes, stream, 0);
+}
+
+extern "C" zp_status zp_prompt_attn(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T,
+                                    int32_t B, int32_t max_len, int32_t window, int32_t sinks, const zp_rows* out,
+                                    const zp_params* p, void* workspace, size_t workspace_bytes, zp_stream stream) {
+  zp::NvtxRange nvtx_range("zp_prompt_attn");
+  return prompt(q, k, v, token_start, T, B, max_len, window, sinks, out, p, workspace, workspace_bytes, stream, 0);
+}
+
+extern "C" zp_status zp_test_kv8_window_stalled(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
+                                                int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
+                                                int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,
+                                                const zp_params* p, void* workspace, size_t workspace_bytes,
+                                                int64_t stall_limit_ns, zp_stream stream) {
+  if (!stall_ok(stall_limit_ns)) return ZP_ERR_INVALID_ARG;
+  return kv8_window(pool, layer, q, q_start, T, max_q, block_tables, seq_lens, B, max_blocks, window, sinks, out, p, workspace,
+                    workspace_bytes, stream, static_cast<uint64_t>(stall_limit_ns));
+}
+
+extern "C" zp_status zp_test_prompt_stalled(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T,
+                                            int32_t B, int32_t max_len, int32_t window, int32_t sinks, const zp_rows* out,
+                                            const zp_params* p, void* workspace, size_t workspace_bytes, int64_t stall_limit_ns,
+                                            zp_stream stream) {
+  if (!stall_ok(stall_limit_ns)) return ZP_ERR_INVALID_ARG;
+  return prompt(q, k, v, token_start, T, B, max_len, window, sinks, out, p, workspace, workspace_bytes, stream,
+                static_cast<uint64_t>(stall_limit_ns));
 }
 
 extern "C" zp_status zp_test_kv8_decode_stalled(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,

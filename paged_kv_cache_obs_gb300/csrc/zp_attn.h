@@ -11,6 +11,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside a kernel gives up 
 struct AttnArgs {
   const uint8_t* pool;     // bf16 or E4M3 tiles
   const float* scales;     // E4M3 only
+  const uint16_t *k, *v;   // rows of packed prompts, in place of a pool
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  bool kv_tma;             // they are aligned, and come by TMA
   int64_t num_blocks;
   const uint16_t* q;
   uint16_t* out;
@@ -60,7 +63,10 @@ struct TilePlan {
 };
 TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX);
 
-// Launches the tiled kernel (rows above kMaxSplitRows), and the one that joins the parts.
-zp_status tile_launch(AttnArgs a, const zp_kv_pool* pool, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
+// Launch the tiled kernel (rows above kMaxSplitRows, and prompts), and the one that joins the parts: over the bf16 pool, the
+// 8-bit pool, or rows of packed prompts (whose a.b is the run of tokens that a copy brings: 32 or 128).
+zp_status tile_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
+zp_status tile8_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
+zp_status tile_rows_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
 
 }  // namespace zp

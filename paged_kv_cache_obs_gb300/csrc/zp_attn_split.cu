@@ -1,6 +1,6 @@
 // zp_attn_split.cu — attention of a few query rows over a long paged cache, bf16 or E4M3, sm_103a:
-// decode over the 8-bit pool, and decode (or a handful of new tokens) with a sliding window and
-// first tokens that stay visible over the bf16 pool.
+// decode (or a handful of new tokens) with a sliding window and first tokens that stay visible, over the 8-bit or
+// the bf16 pool.
 //
 //   out[row] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale <q_row, k_t>) over the t that the row sees
 //
@@ -66,6 +66,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ void unpack_f16(uint32_t x, float& lo, float& hi) {
+  asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(x));
 }
 // the low and the high two E4M3 codes of a word, as f16 pairs
 __device__ __forceinline__ void dec4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -257,7 +260,8 @@ __device__ __forceinline__ int acc_at(int row, int ch) {
   return ch ^ (FP8 ? c : (c & 1) | (c & 2) << 1);
 }
 
-template <bool FP8, int D, int NT>
+// MANY: requests may have more than one query (which the bf16 form always allows).
+template <bool FP8, int D, int NT, bool MANY>
 __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<FP8, D, NT>;
   constexpr int ROWS = Sh::ROWS, RB = Sh::RB, SLOTS = Sh::SLOTS, TILE = Sh::TILE, SUB = Sh::SUB;
@@ -602,10 +606,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           for (int w = 0; w < VW; ++w) {
             if (!any) vr[t][w] = 0;
             if (!FP8) odd |= (vr[t][w] & 0x7F80u) == 0x7F80u || (vr[t][w] & 0x7F800000u) == 0x7F800000u;
+            if (FP8 && MANY) odd |= (((vr[t][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;  // a code that is NaN
           }
         }
         // a value that some rows see and others do not must not reach the others as 0 * inf
-        if (!FP8 && s.n > 1) redo = __any_sync(0xffffffffu, odd);
+        if ((!FP8 || MANY) && s.n > 1) redo = __any_sync(0xffffffffu, odd);
       }
       if constexpr (FP8) {
         // o is in units of vref, which follows the tiles' V scales: P times their ratio is what
@@ -626,6 +631,38 @@ __global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_ker
           vinv = kGain * inv;
         }
         const float gained = vs[sub] * vinv, ratio = gained * (1.0f / kGain);
+        if (MANY && redo) {
+          // plain products, token by token, for the rows that see it
+#pragma unroll 1
+          for (int k = 0; k < kTile; ++k) {
+            const int tt = token_at(k), t = t0[sub] + tt;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float pa = __shfl_sync(0xffffffffu, x[sub][nt][e], (k & 7) * 4 + c);
+                const float pb = __shfl_sync(0xffffffffu, x[sub][nt][e + 2], (k & 7) * 4 + c);
+                const float pt = (k < 8 ? pa : pb) * gained;
+                const int p = s.p0 + min((nt * 8 + 2 * c + e) / a.G, s.n - 1);
+                if (t > p || !(a.window == 0 || t > p - a.window || t < a.sinks)) continue;
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                  uint32_t word, lo, hi;
+                  const uint32_t at = vbuf + (VW == 2 ? chunk_at<RB>(tt, g >> 1) + (g & 1) * 8 : chunk_at<RB>(tt, g)) + w * 4;
+                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(at));
+                  dec4(word, lo, hi);
+                  float y0, y1;
+                  unpack_f16(lo, y0, y1);
+                  o[nt][2 * w][e] += pt * y0;
+                  o[nt][2 * w][e + 2] += pt * y1;
+                  unpack_f16(hi, y0, y1);
+                  o[nt][2 * w + 1][e] += pt * y0;
+                  o[nt][2 * w + 1][e + 2] += pt * y1;
+                }
+              }
+          }
+          continue;
+        }
         const bool small = fabsf(ratio) < 0.125f;
         const float pm = small ? kGain : gained;
         uint32_t ph[NT][2];
@@ -830,24 +867,24 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   store_row4(a, s, h, row, lane * 4, v, Ls);
 }
 
-template <bool FP8, int D, int NT>
+template <bool FP8, int D, int NT, bool MANY>
 cudaError_t launch(const CUtensorMap& tm, const AttnArgs& a, const SplitPlan& plan, cudaStream_t st) {
   constexpr int smem = Shape<FP8, D, NT>::SMEM;
   static PerDeviceInit attrs;
   cudaError_t e = attrs.run(
-      [] { return cudaFuncSetAttribute(split_kernel<FP8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+      [] { return cudaFuncSetAttribute(split_kernel<FP8, D, NT, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  e = launch_in_order(split_kernel<FP8, D, NT>, dim3(plan.splits, a.Hkv, a.B), kThreads, smem, st, plan.cluster, tm, a);
+  e = launch_in_order(split_kernel<FP8, D, NT, MANY>, dim3(plan.splits, a.Hkv, a.B), kThreads, smem, st, plan.cluster, tm, a);
   if (e != cudaSuccess || plan.splits == plan.cluster) return e;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * plan.rows;
   return launch_in_order(join_kernel<D>, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), kThreads, 0, st, 1, a,
                          plan.splits / plan.cluster, plan.rows);
 }
 
-template <bool FP8>
+template <bool FP8, bool MANY>
 cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const SplitPlan& plan, cudaStream_t st) {
-  if (d == 128) return plan.rows == 8 ? launch<FP8, 128, 1>(tm, a, plan, st) : launch<FP8, 128, 2>(tm, a, plan, st);
-  return plan.rows == 8 ? launch<FP8, 64, 1>(tm, a, plan, st) : launch<FP8, 64, 2>(tm, a, plan, st);
+  if (d == 128) return plan.rows == 8 ? launch<FP8, 128, 1, MANY>(tm, a, plan, st) : launch<FP8, 128, 2, MANY>(tm, a, plan, st);
+  return plan.rows == 8 ? launch<FP8, 64, 1, MANY>(tm, a, plan, st) : launch<FP8, 64, 2, MANY>(tm, a, plan, st);
 }
 
 }  // namespace
@@ -902,7 +939,7 @@ zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan
   const bool ok = fp8 ? encode_tmap_3d_u8(&tm, a.pool, d, rows, blocks, d, rows * d, d, kTile, 1, d)
                       : encode_tmap_3d_bf16(&tm, a.pool, d, rows, blocks, static_cast<uint64_t>(d) * 2, rows * d * 2, 64, kTile, 1);
   if (!ok) return ZP_ERR_CUDA;
-  const cudaError_t e = fp8 ? dispatch<true>(tm, a, d, plan, st) : dispatch<false>(tm, a, d, plan, st);
+  const cudaError_t e = !fp8 ? dispatch<false, true>(tm, a, d, plan, st) : a.q_start ? dispatch<true, true>(tm, a, d, plan, st) : dispatch<true, false>(tm, a, d, plan, st);
   return e == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 

@@ -48,7 +48,7 @@ class _Tensors:
     become attributes here."""
 
     _ENTRIES = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn",
-                "rope_apply_axes", "step_slots", "kv_append")
+                "rope_apply_axes", "step_slots", "kv_append", "prompt_attn", "kv8_window_attn")
 
     def __getattr__(self, name):
         if name not in self._ENTRIES:
@@ -182,6 +182,15 @@ _sig("zp_kv8_decode_attn", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, 
 _sig("zp_paged_window_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32, _I32, _I32, _I32, _I32])
 _sig("zp_paged_window_attn", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
                                     _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_kv8_window_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32, _I32, _I32, _I32, _I32])
+_sig("zp_kv8_window_attn", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
+                                  _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_prompt_workspace_size", _SZ, [ctypes.POINTER(zp_params), _I32, _I32, _I32, _I32, _I32])
+_sig("zp_prompt_attn", _I32, [_ROWS, _ROWS, _ROWS, _P, _I32, _I32, _I32, _I32, _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _P])
+_sig("zp_test_kv8_window_stalled", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
+                                          _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ, _I64, _P])
+_sig("zp_test_prompt_stalled", _I32, [_ROWS, _ROWS, _ROWS, _P, _I32, _I32, _I32, _I32, _I32, _ROWS, ctypes.POINTER(zp_params), _P, _SZ,
+                                      _I64, _P])
 _sig("zp_test_kv8_decode_stalled", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _P, _P, _I32, _I32, _I32, _I32, _ROWS,
                                           ctypes.POINTER(zp_params), _P, _SZ, _I64, _P])
 _sig("zp_test_paged_window_stalled", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _P, _I32, _I32, _P, _P, _I32, _I32, _I32,
@@ -517,6 +526,34 @@ def zp_paged_window_attn(pool, layer: int, q, q_start, block_tables, seq_lens, o
         _check("zp_paged_window_attn", st)
 
 
+def zp_kv8_window_workspace_size(params, T: int, B: int, max_q: int, max_blocks: int, window: int, sinks: int) -> int:
+    return lib.zp_kv8_window_workspace_size(_params(params), T, B, max_q, max_blocks, window, sinks)
+
+
+def zp_kv8_window_attn(codes, scales, layer: int, q, q_start, block_tables, seq_lens, out, params, workspace, window: int,
+                       sinks: int, max_q: int, stream=None):
+    """zp_paged_window_attn over the 8-bit pool: the new tokens' codes are already in it."""
+    p = _params(params)
+    st = _t.kv8_window_attn(codes, scales, layer, q, q_start, block_tables, seq_lens, out, _addr(p), workspace, window, sinks, max_q,
+                            _raw(stream))
+    if st:
+        _check("zp_kv8_window_attn", st)
+
+
+def zp_prompt_workspace_size(params, T: int, B: int, max_len: int, window: int = 0, sinks: int = 0) -> int:
+    return lib.zp_prompt_workspace_size(_params(params), T, B, max_len, window, sinks)
+
+
+def zp_prompt_attn(q, k, v, token_start, out, params, workspace, max_len: int, window: int = 0, sinks: int = 0, stream=None):
+    """Causal attention of packed prompts over their own keys and values: q, out bf16 [T, H_q, d], k, v [T, H_kv, d], prompt r
+    at rows token_start[r] .. token_start[r + 1] - 1, with an optional window and first tokens that stay visible.
+    max_len: the most tokens of a prompt."""
+    p = _params(params)
+    st = _t.prompt_attn(q, k, v, token_start, out, _addr(p), workspace, max_len, window, sinks, _raw(stream))
+    if st:
+        _check("zp_prompt_attn", st)
+
+
 def _rows_of(t):
     return ctypes.byref(zp_rows(t.data_ptr(), t.stride(0), t.stride(1)))
 
@@ -541,6 +578,25 @@ def zp_test_paged_window_stalled(pool, layer: int, q, q_start, block_tables, seq
         ctypes.byref(kv), layer, _rows_of(q), _ptr(q_start), q.shape[0], max_q, _ptr(block_tables), _ptr(seq_lens),
         seq_lens.shape[0], block_tables.shape[1], window, sinks, _rows_of(out), ctypes.byref(_params(params)), _ptr(workspace),
         workspace.numel() * workspace.element_size(), int(stall_limit_ns), _stream(stream)))
+
+
+def zp_test_kv8_window_stalled(codes, scales, layer: int, q, q_start, block_tables, seq_lens, out, params, workspace, window: int,
+                               sinks: int, max_q: int, stall_limit_ns: int, stream=None):
+    """Test hook of the bounded waits, as zp_test_paged_window_stalled over the 8-bit pool."""
+    pool = zp_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[1])
+    _check("zp_test_kv8_window_stalled", lib.zp_test_kv8_window_stalled(
+        ctypes.byref(pool), layer, _rows_of(q), _ptr(q_start), q.shape[0], max_q, _ptr(block_tables), _ptr(seq_lens),
+        seq_lens.shape[0], block_tables.shape[1], window, sinks, _rows_of(out), ctypes.byref(_params(params)), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), int(stall_limit_ns), _stream(stream)))
+
+
+def zp_test_prompt_stalled(q, k, v, token_start, out, params, workspace, max_len: int, stall_limit_ns: int, window: int = 0,
+                           sinks: int = 0, stream=None):
+    """Test hook of the bounded waits, as zp_test_paged_window_stalled over rows of packed prompts."""
+    _check("zp_test_prompt_stalled", lib.zp_test_prompt_stalled(
+        _rows_of(q), _rows_of(k), _rows_of(v), _ptr(token_start), q.shape[0], token_start.shape[0] - 1, max_len, window, sinks,
+        _rows_of(out), ctypes.byref(_params(params)), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        int(stall_limit_ns), _stream(stream)))
 
 
 def zp_read_error(workspace, stream=None) -> int:
