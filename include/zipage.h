@@ -569,10 +569,13 @@ size_t zp_prompt_workspace_size(const zp_params* params, int32_t T, int32_t B, i
 /* zp_paged_window_attn over the 8-bit pool: attention of a chunk of new tokens (drafts, chunked prefill, a question
  * about a document in the cache), whose codes are already in the pool.  Arguments, masks and errors are
  * zp_paged_window_attn's.
- * Where head groups times max_q is 16 or less, weights are held as by zp_kv8_decode_attn (11 bits).  Above, the
- * values are bf16(code * scale), as zp_kv8_unpack_blocks gives them (exact with the scales that the
- * library writes), and the result is, bit for bit, that of zp_paged_window_attn over the unpacked pool.  Any
- * finite scales are taken. */
+ * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn.  Above:
+ *   - keys are taken as they are; values are exact where their scale is a power of two, not below 2^-15 of the
+ *     largest of the 128 tokens that are walked together, and within 2^-11 of themselves (2^-25 of that scale) otherwise;
+ *   - weights times V scales keep 11 bits down to 2^-18 of the row's largest, and 2^-29 of it is the last that counts; sums of
+ *     weights are fp32;
+ *   - V scales that a row sees are within 2^100 of one another; below 2^-104 they count as that, and above 2^104 values
+ *     may overflow. */
 zp_status zp_kv8_window_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
                              int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
                              int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,

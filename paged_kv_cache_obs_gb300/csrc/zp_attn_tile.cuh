@@ -32,6 +32,15 @@
 // takes a look at the tiles concerned alone, however long the cache is: 30 us for a tile with one such
 // value, 1 ms where all of its tokens have some.
 //
+// Over the 8-bit pool four more warps bring the codes and turn them into f16, which holds them exactly, times what their
+// blocks' scales are of the tile's (a power of two of them, as the library writes scales, is exact): the tile's K scale joins
+// the logits', its V scale the exponent of the weights.  Queries are brought to f16 by a power of two for each row, by the
+// softmax groups as they come.  P is f16, in units of 2^-15 of a reference 11 (in log2) above the largest weight times
+// scale: 11 bits down to 2^-18 of it, 2^-29 of it is the last that counts; sums of weights are fp32 throughout.
+// 4 requests of 2048 new tokens over 0 to 6144, 32 heads on 8: 532 us, 1030 TFLOP/s over the pairs that are seen.  The tensor core
+// works 41 % of the time: the softmax of a tile takes 2.3 times as long beside the warps that turn codes (without them
+// the call takes 396 us), for issue slots and instruction fetches that they share.
+//
 // Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 191 us, 1270 TFLOP/s
 // over the pairs that are seen; a prompt of 8191 tokens, 28 heads on 4, a window of 4096: 244 us, 1480
 // TFLOP/s (a dozen calls after a pause; 200 and 262 us in calls that follow one another for seconds, where
@@ -46,6 +55,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstddef>
 #include <type_traits>
 
 #include "zp_launch.h"
@@ -66,9 +76,10 @@ constexpr bool kCodes = SRC == Source::kPaged8;  // which a group of four warps 
 template <Source SRC>
 constexpr int kThreads = kCodes<SRC> ? 512 : 384;
 constexpr int kTurnWarp = 12;         // the first of the four
-constexpr float kLazy = 24.0f;
+constexpr float kLazy = 24.0f, kLazyCodes = 11.0f;
+constexpr float kGain = 15.0f;        // codes: log2 of what weights are multiplied by for f16
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
-constexpr int kFlags = 8;             // items: K's warp is at most 6 ahead of a softmax group (the ring's 3, 2 stages, one)
+constexpr int kFlags = 16;            // items: K's warp is at most 7 ahead of a softmax group (the ring's 3, 2 stages, codes, one)
 
 // An item: which, and what it walks.
 struct Item {
@@ -87,13 +98,29 @@ struct Item {
 // would keep the others from running away from it while it writes a long item out.
 constexpr int kItems = 4;
 
+// A tile of codes: where its blocks are, their scales, and what the warps that turn it are to make of it.
+enum { kPlainTile = 0, kMixedTile = 1, kNoMoreTiles = 2 };
+struct ListedTile {
+  int z[8];               // of each block: the pool's (layer, block), or past its end
+  uint16_t k[8], v[8];    // for each 16 tokens: what codes are multiplied by, in f16
+  float k_rest[8];        // and what K's logits are besides, where k_odd
+  float k_scale, v_log, v_inv;  // of the whole tile: K's scale; V's, a power of two: its log2, and 2^-kGain over it
+  int row;                // of K in a block
+  int what;               // V's: kPlainTile, ...
+  int k_odd;
+};
+// Ring of them.  The warp that fills it is 4 tiles ahead of those that turn them: V of tile n + 4 is turned when the second
+// product of tile n + 2 is done with the stage, so no softmax group still reads the scales of tile n when n + 8 takes its place.
+constexpr int kList = 8, kListLead = 4;
+
 template <int D, Source SRC>
 struct __align__(1024) TileSmem {
   uint8_t q[2][D / 64][kRows * 128];         // [tile][64-column half][row][128 B], 128-byte swizzle
   uint8_t k[kStages][D / 64][kKeys * 128];
   uint8_t v[kStages][D / 64][kKeys * 128];
   uint8_t codes[2][4][kCodes<SRC> ? kKeys / 4 * D : 16];  // of K and V, a quarter of a tile for each warp that turns them
-  uint64_t codes_full[2][4];
+  uint64_t codes_full[2][4], q_turned, listed[kList], unlisted[kList];
+  ListedTile list[kCodes<SRC> ? kList : 1];
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t v_mixed[kStages], v_clean[kStages];  // in place of v_full where a tile is mixed: loaded, and looked over
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, item_full[kItems], item_empty[kItems];
@@ -103,7 +130,13 @@ struct __align__(1024) TileSmem {
   Item items[kItems];
   int bad[kFlags], odd[kFlags];              // the last item (counted from 1) that a block id or a value marked
   int odd_lo[kFlags], odd_hi[kFlags];        // the first and last tile with such values
+  int end;                                   // of what is used
 };
+// Bytes that a CTA asks for: any base is brought to 1024.
+template <class Smem>
+constexpr int used_bytes() { return static_cast<int>(offsetof(Smem, end)); }
+template <int D, Source SRC>
+constexpr int kSmemBytes = used_bytes<TileSmem<D, SRC>>() + 1024;
 
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -324,17 +357,19 @@ __device__ __forceinline__ bool whole8(const AttnArgs& a, const Item& w, int t0)
 __device__ __forceinline__ bool seen_by_some(const AttnArgs& a, const Item& w, int t) {
   return t <= w.p_last && (a.window == 0 || t > w.p_first - a.window || t < a.sinks);
 }
-// Whether the low or the high bf16 of a word is not finite.
-__device__ __forceinline__ bool odd_lo(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
-__device__ __forceinline__ bool odd_hi(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }
+// Whether the low or the high bf16 (or f16) of a word is not finite.
+template <bool F16 = false>
+__device__ __forceinline__ bool odd_lo(uint32_t x) { return (x & (F16 ? 0x7C00u : 0x7F80u)) == (F16 ? 0x7C00u : 0x7F80u); }
+template <bool F16 = false>
+__device__ __forceinline__ bool odd_hi(uint32_t x) { return odd_lo<F16>(x >> 16); }
 
-// bf16(code * scale) of two E4M3 codes (the low bytes), as the blocks' conversion gives them.
-__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t two, float scale) {
+// Two E4M3 codes (the low bytes) as bf16: NaN, or finite.
+__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t two) {
   uint32_t h;
   asm("{.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(two));
   float lo, hi;
   asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(h));
-  return pack_bf16x2(lo * scale, hi * scale);
+  return pack_bf16x2(lo, hi);
 }
 
 // The lane's D / 32 dims of keys (kv 0) or values (1) of 8 tokens from t0 on, which stand in one block.
@@ -343,7 +378,6 @@ struct OddRows {
   static constexpr int DW = D / 64;  // words of a lane
   const uint8_t* at[2];
   int64_t step[2];                   // bytes from one token to the next
-  float scale[2];
   int left;                          // tokens that there are (rows of prompts end anywhere)
   __device__ __forceinline__ OddRows(const AttnArgs& a, const Item& w, int t0, int lane) {
     left = 8;
@@ -362,10 +396,6 @@ struct OddRows {
       at[0] = a.pool + tile * tile_bytes + (t0 % a.b * D + lane * (2 * DW)) * kBytes;
       at[1] = at[0] + a.Hkv * tile_bytes;
       step[0] = step[1] = D * kBytes;
-      if constexpr (kCodes<SRC>) {
-        scale[0] = a.scales[tile];
-        scale[1] = a.scales[tile + a.Hkv];
-      }
     }
   }
   // word i of token c
@@ -376,7 +406,7 @@ struct OddRows {
       const uint16_t* const x = reinterpret_cast<const uint16_t*>(p) + 2 * i;
       return static_cast<uint32_t>(x[0]) | static_cast<uint32_t>(x[1]) << 16;
     }
-    if constexpr (kCodes<SRC>) return bf16_of_codes(reinterpret_cast<const uint16_t*>(p)[i], scale[kv]);
+    if constexpr (kCodes<SRC>) return bf16_of_codes(reinterpret_cast<const uint16_t*>(p)[i]);
     return reinterpret_cast<const uint32_t*>(p)[i];
   }
 };
@@ -455,7 +485,7 @@ __device__ __noinline__ void add_odd_values(const AttnArgs& a, const Item& w, in
 // Looks V of mixed tile j over in shared memory (one warp): tokens that no row sees are zeroed, and values
 // that are not finite where only some rows see them; true if there were any of those.  8 tokens at a
 // time, which are tokens of one block; a lane holds 16-byte chunk lane % (D / 8) of every (256 / D)th of them.
-template <int D>
+template <int D, bool F16>
 __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int j, uint8_t* v, int lane) {
   constexpr int kPer = 256 / D, kLoads = 8 / kPer;
   const int ch = lane % (D / 8), sub = lane / (D / 8);
@@ -488,7 +518,7 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
       }
     }
   }
-  if (!__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u)) return false;
+  if (!__any_sync(0xffffffffu, odd_lo<F16>(top) || odd_hi<F16>(top))) return false;
   for (todo = look; todo; todo &= todo - 1) {
     const int g = __ffs(todo) - 1;
 #pragma unroll 1
@@ -497,8 +527,8 @@ __device__ __forceinline__ bool look_over(const AttnArgs& a, const Item& w, int 
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         uint32_t z = x[i];
-        if (odd_lo(z)) z &= 0xFFFF0000u;
-        if (odd_hi(z)) z &= 0x0000FFFFu;
+        if (odd_lo<F16>(z)) z &= 0xFFFF0000u;
+        if (odd_hi<F16>(z)) z &= 0x0000FFFFu;
         x[i] = z;
       }
     }
@@ -526,135 +556,112 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, const Item& w, int 
   __syncwarp();
 }
 
-// Two bf16 values times two.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+// E4M3 codes of 4 bytes as two pairs of f16, which holds them (NaN too) exactly.
+__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// Turns a quarter of a tile (32 tokens, which the warp's copies have brought) from codes into bf16(code * scale), in the
-// place and order that a bf16 tile has.  A code's bits stand 4 places higher in bf16, times 2^-120, so that one
-// product with scale * 2^120 gives the value, subnormal codes and results included: rounded once, as in fp32, if the scale has
-// bf16's 8 bits and is below 2^8 (powers of two above all, which the library's own scales are).  Other scales, and
-// codes that are NaN, take the products in fp32.
-template <int D>
-__device__ __forceinline__ void turn_quarter(const uint8_t* codes, uint8_t* tile, int quarter, int lane, float s0, float s1) {
-  constexpr int N = kKeys / 4 * D / 16 / 32;  // 16-byte pieces of a lane
+// Turns a quarter of a tile (32 tokens) from codes into f16(code * factor), a factor for each 16 tokens, in the place and
+// order that a bf16 tile has (one warp).  `refill` starts the next copy into the codes' place: every lane has used its loads.
+// What bounds it is how fast one warp gets its instructions beside the softmax groups (8 cycles each), so it is a short loop
+// over 8 tokens at a time, whose code stays at hand: 2048-token chunks of 4 requests over 0 to 6144 tokens take 532 us so, 622
+// unrolled, and took 740 with values turned into bf16 by 6 integer steps a pair in place of a conversion and a product.
+template <int D, class Refill>
+__device__ __forceinline__ void turn_quarter(uint32_t codes, uint32_t tile, const uint16_t* factors, int quarter, int lane, const Refill& refill) {
+  constexpr int N = D / 64;  // 16-byte pieces of a lane, of 8 tokens
   // Which piece (row, 16 codes): 8 lanes at a time read and write every bank once.  With 8 pieces a row, lanes 4 to 7 of
-  // 8 have the row whose bits 0 and 2 differ from the others'.
+  // 8 have the row whose bits 0 and 2 differ from the others'; the second piece's row differs in bit 2.
   const int sub = lane & 7, ch = D == 128 ? (sub & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
-  const auto row_of = [&](int i) { return D == 128 ? (i * 4 + (lane >> 4) * 2) ^ ((sub >> 2) * 5) : i * 8 + (lane >> 2); };
-  const auto read = [&](int row) {
-    return lds16(smem_u32(codes) + row * D + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4));
-  };
-  const auto write = [&](int row, const uint32_t (&y)[8]) {
-    const int r = quarter * (kKeys / 4) + row, c = (ch & 3) * 2;
-    uint8_t* const to = tile + (ch >> 2) * (kKeys * 128) + r * 128;
-    *reinterpret_cast<uint4*>(to + ((c ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<uint4*>(to + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-  };
-  const auto plain = [](float x) { return (__float_as_uint(x) & 0xFFFFu) == 0 && fabsf(x) < 256.0f; };
-  uint32_t top = 0;
-  const bool fast = plain(s0) && plain(s1);
-  if (fast) {
-    const uint32_t b0 = __float_as_uint(s0 * 0x1p120f) >> 16, b1 = __float_as_uint(s1 * 0x1p120f) >> 16;
-    const uint32_t f0 = b0 | b0 << 16, f1 = b1 | b1 << 16;
+  const int row = D == 128 ? ((lane >> 4) * 2) ^ ((sub >> 2) * 5) : lane >> 2;
+  uint32_t from = codes + row * D + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4);
+  uint32_t to = tile + (ch >> 2) * (kKeys * 128) + (quarter * 32 + row) * 128 + ((((ch & 3) * 2) ^ (row & 7)) << 4);
+  constexpr uint32_t kSecond = 4 * 128 + (4 << 4);
+  uint4 x[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint4 x = read(row_of(i));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t t = __byte_perm(w[e >> 1], 0, e & 1 ? 0x3424 : 0x1404);  // two codes, each in the high byte of a half
-        const uint32_t m = (t >> 4) & 0x07F007F0u;
-        top = max_u16x2(top, m);
-        y[e] = mul_bf16x2(m | (t & 0x80008000u), i < N / 2 ? f0 : f1);
-      }
-      write(row_of(i), y);
-    }
-  }
-  if (__any_sync(0xffffffffu, !fast || (top & 0xFFFFu) == 0x07F0u || (top >> 16) == 0x07F0u)) {
+  for (int i = 0; i < N; ++i) x[i] = lds16(i ? from ^ kSecond : from);
 #pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t f = factors[quarter * 2 + (g >> 1)] * 0x10001u;
+    from += 8 * D;
+    uint4 next[N];
+    if (g < 3)
+#pragma unroll
+      for (int i = 0; i < N; ++i) next[i] = lds16(i ? from ^ kSecond : from);
+#pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint4 x = read(row_of(i));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = bf16_of_codes(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu, i < N / 2 ? s0 : s1);
-      write(row_of(i), y);
+      for (int e = 0; e < 4; ++e) {
+        f16_of_codes(w[e], y[2 * e], y[2 * e + 1]);
+        y[2 * e] = mul_f16x2(y[2 * e], f);
+        y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
+      }
+      const uint32_t at = i ? to ^ kSecond : to;
+      sts16(at, make_uint4(y[0], y[1], y[2], y[3]));
+      sts16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
     }
+    to += 8 * 128;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = next[i];
   }
+  refill();
 }
 
-// The part of a warp of the group that brings and turns codes: a quarter of each tile of K and of V, 32 tokens.
-template <int D, class Smem, class Next>
-__device__ __forceinline__ void turn_codes(Smem& s, const CUtensorMap& tm, const AttnArgs& a, int nx, int items, const Next& next_item,
-                                           int quarter, int lane, volatile int* abort) {
-  const int bpq = kKeys / 4 / a.b, bpt = kKeys / a.b;  // blocks of a quarter, of a tile
-  bool go = true;
-  uint32_t done = 0, fetched[2] = {0, 0};  // tiles
-  int count = 0;
-  Item w;
-  bool bad;
-  Raw raw = load_raw<Source::kPaged8>(a, blockIdx.x, items);
-  for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
-    const Raw now = raw;
-    raw = load_raw<Source::kPaged8>(a, next_item(item), items);
-    if (!take_item<Source::kPaged8>(a, item, nx, now, w, bad)) continue;  // K's warp reports it
-    ++count;
-    const int32_t* const table = a.tables + static_cast<int64_t>(w.r) * a.max_blocks;
-    const auto listed = [&](int j) { return lane < bpq && j * bpt + quarter * bpq + lane < w.blocks; };
-    const auto id_of = [&](int j) {  // block id that the lane loads for tile j
-      const int e = j * bpt + quarter * bpq + lane;
-      return j < w.j1 && listed(j) ? table[e < w.sink_blocks ? e : w.win_block + e - w.sink_blocks] : 0;
-    };
-    // An id outside the pool: the item's rows are not written, and block 0 is read in its place.
-    const auto checked = [&](int id) {
-      const bool out = id < 0 || id >= a.num_blocks;
-      if (__any_sync(0xffffffffu, out) && lane == 0) {
-        *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) = count;
-        atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
-      }
-      return out ? 0 : id;
-    };
-    const auto fetch = [&](int j, int kv, int id) {  // blocks past the list's end: zeros
-      const int z = listed(j) ? a.layer * static_cast<int>(a.num_blocks) + id : a.layers * static_cast<int>(a.num_blocks);
-      if (lane == 0) mbar_arrive_expect_tx(&s.codes_full[kv][quarter], kKeys / 4 * D);
-      __syncwarp();
-      if (lane < bpq) tma_load_3d(s.codes[kv][quarter] + lane * a.b * D, &tm, &s.codes_full[kv][quarter], 0, (kv * a.Hkv + w.h) * a.b, z);
-      ++fetched[kv];
-    };
-    const auto scale_of = [&](int j, int kv, int id) {
-      return listed(j) ? a.scales[((static_cast<int64_t>(a.layer) * a.num_blocks + id) * 2 + kv) * a.Hkv + w.h] : 0.0f;
-    };
-    if (w.j0 == w.j1) continue;
-    int id = checked(id_of(w.j0));
-    fetch(w.j0, 0, id);
-    fetch(w.j0, 1, id);
-    float scale[2] = {scale_of(w.j0, 0, id), scale_of(w.j0, 1, id)};
-    int next = id_of(w.j0 + 1);
-    for (int j = w.j0; go && j < w.j1; ++j, ++done) {
-      const uint32_t st = done % kStages, ph = (done / kStages) & 1;
-      const bool more = j + 1 < w.j1;
-      if (more) id = checked(next);
-      next = id_of(j + 2);
-#pragma unroll
+// The part of one of the four warps that bring and turn codes: a quarter of each tile.
+template <int D, class Smem>
+__device__ __forceinline__ void turn_codes(Smem& s, const CUtensorMap& tm, const AttnArgs& a, int quarter, int lane, volatile int* abort) {
+  const uint32_t k = smem_u32(s.k[0][0]), v = smem_u32(s.v[0][0]);
+  const int bpq = kKeys / 4 / a.b;  // blocks of a quarter
+  uint32_t fetched[2] = {0, 0};
+  const auto listed = [&](uint32_t n) { return __all_sync(0xffffffffu, wait(&s.listed[n % kList], (n / kList) & 1, abort)) != 0; };
+  const auto fetch = [&](uint32_t n, int kv) {
+    const ListedTile& e = s.list[n % kList];
+    if (lane == 0) mbar_arrive_expect_tx(&s.codes_full[kv][quarter], kKeys / 4 * D);
+    __syncwarp();
+    if (lane < bpq)
+      tma_load_3d(s.codes[kv][quarter] + lane * a.b * D, &tm, &s.codes_full[kv][quarter], 0, e.row + kv * a.Hkv * a.b, e.z[quarter * bpq + lane]);
+    ++fetched[kv];
+  };
+  bool go = listed(0);
+  if (go && s.list[0].what != kNoMoreTiles) {
+    fetch(0, 0);
+    fetch(0, 1);
+    for (uint32_t n = 0; go; ++n) {
+      const uint32_t st = n % kStages, ph = (n / kStages) & 1;
+      const ListedTile& e = s.list[n % kList];
+      go = listed(n + 1);
+      if (!go) break;
+      const bool more = s.list[(n + 1) % kList].what != kNoMoreTiles;
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         uint64_t* const empty = kv ? &s.v_empty[st] : &s.k_empty[st];
-        go = __all_sync(0xffffffffu, wait(&s.codes_full[kv][quarter], done & 1, abort) && (done < kStages || wait(empty, ph ^ 1, abort)));
+        go = __all_sync(0xffffffffu, wait(&s.codes_full[kv][quarter], n & 1, abort) && (n < kStages || wait(empty, ph ^ 1, abort)));
         if (!go) break;
-        const float s0 = __shfl_sync(0xffffffffu, scale[kv], 0), s1 = __shfl_sync(0xffffffffu, scale[kv], bpq - 1);
-        turn_quarter<D>(s.codes[kv][quarter], kv ? s.v[st][0] : s.k[st][0], quarter, lane, s0, s1);
+        turn_quarter<D>(smem_u32(s.codes[kv][quarter]), (kv ? v : k) + st * (kKeys * D * 2), kv ? e.v : e.k, quarter, lane, [&] {
+          __syncwarp();
+          if (more) fetch(n + 1, kv);
+        });
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(!kv ? &s.k_full[st] : mixed_tile(w, j) ? &s.v_mixed[st] : &s.v_full[st]);
-        if (more) {
-          fetch(j + 1, kv, id);
-          scale[kv] = scale_of(j + 1, kv, id);
+        if (lane == 0) {
+          mbar_arrive(!kv ? &s.k_full[st] : e.what == kMixedTile ? &s.v_mixed[st] : &s.v_full[st]);
+          if (kv) mbar_arrive(&s.unlisted[n % kList]);
         }
       }
+      if (!go) break;
+      go = more;
     }
   }
   // copies still in flight after a give-up land before the shared memory is released
@@ -662,6 +669,32 @@ __device__ __forceinline__ void turn_codes(Smem& s, const CUtensorMap& tm, const
     for (int kv = 0; kv < 2; ++kv)
       if (fetched[kv] > 0) mbar_wait_bounded(&s.codes_full[kv][quarter], (fetched[kv] - 1) & 1, kWaitNs);
   __syncwarp();
+}
+
+// Brings a row of queries to f16 in place, by a power of two that brings its largest magnitude to [2^14, 2^15): exact for
+// values down to 2^-31 of it, less than the fp32 sums hold.  Returns what the logits are then multiplied by.
+template <int D>
+__device__ __forceinline__ float turn_queries(uint8_t* q, int row) {  // q: [64-column half][row][128 B]
+  const uint32_t at = smem_u32(q) + row * 128;
+  uint32_t m = 0;
+  const auto piece = [&](int c) { return at + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4); };
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = lds16(piece(c));
+    m = max_u16x2(max_u16x2(m, x.x & 0x7FFF7FFFu), max_u16x2(x.y & 0x7FFF7FFFu, max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+  }
+  const int ex = min(max(static_cast<int>(max(m & 0xFFFFu, m >> 16) >> 7), 15), 253);  // both powers of two are normal
+  const float inv = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = lds16(piece(c));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(bf16x2_lo(w[e]) * inv, bf16x2_hi(w[e]) * inv);
+    sts16(piece(c), make_uint4(y[0], y[1], y[2], y[3]));
+  }
+  return __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 }
 
 // Q_TMA: the queries' rows are aligned and come by TMA (one box per tile and 64-column half: the
@@ -700,8 +733,14 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       mbar_init(&s.v_mixed[i], kFills);
       mbar_init(&s.v_clean[i], 1);
     }
-    if (kCodes<SRC>)
+    if (kCodes<SRC>) {
+      mbar_init(&s.q_turned, 8);
       for (int i = 0; i < 8; ++i) mbar_init(&s.codes_full[i >> 2][i & 3], 1);
+      for (int i = 0; i < kList; ++i) {
+        mbar_init(&s.listed[i], 1);
+        mbar_init(&s.unlisted[i], 4);
+      }
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
@@ -734,10 +773,11 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
 
   // Registers follow the roles: 2 x 128 x 208 + 128 x 88 of the 384 x 168 that the launch gave.  With 200 the
   // softmax groups spill inside their loop (2048-token chunks 210 us, 200 us with 208).  With codes to turn:
-  // 2 x 128 x 192 + 2 x 128 x 64 of 512 x 128.
+  // 2 x 128 x 192 + 2 x 128 x 64 of 512 x 128 (200 with 48 for those that turn them, or 192 with 80 and 48, took 589 us where
+  // this takes 532: 2048-token chunks of 4 requests over 0 to 6144 tokens).
   if (kCodes<SRC> && warp >= kTurnWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if constexpr (kCodes<SRC>) turn_codes<D>(s, tm, a, nx, items, next_item, warp - kTurnWarp, lane, abort);
+    if constexpr (kCodes<SRC>) turn_codes<D>(s, tm, a, warp - kTurnWarp, lane, abort);
   } else if (warp >= 8) {
   if constexpr (kCodes<SRC>) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -758,8 +798,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     int q_loads = 0;              // items whose queries were
     uint64_t* last[kStages] = {};  // barrier of each stage's last tile, and how often each was used
     uint32_t used_full = 0, used_mixed = 0, last_parity = 0;  // bits by stage
+    int v_exp = 0;                 // codes: log2 of V's scale of the tile
     for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
-      if (kCodes<SRC> && kv) break;  // K's warp brings the queries alone, the others turn K and V
       const Raw now = raw;
       raw = load_raw<SRC>(a, next_item(item), items);
       if (!take_item<SRC>(a, item, nx, now, w, bad)) {
@@ -805,11 +845,11 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         }
         __syncwarp();
       };
-      if (kCodes<SRC>) {
+      if (kCodes<SRC> && kv) {  // V's warp brings the queries alone
         load_q();
         continue;
       }
-      if (!kv && w.j0 == w.j1) load_q();  // a part without tiles
+      if (!kCodes<SRC> && !kv && w.j0 == w.j1) load_q();  // a part without tiles
       int id = id_of(w.j0);
       for (int j = w.j0; go && j < w.j1; ++j, ++done) {
         const uint32_t st = done % kStages, ph = (done / kStages) & 1;
@@ -824,7 +864,46 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         const int z = SRC == Source::kRows ? (lane < nb ? w.q0 + id * a.b : a.T)
                       : lane < nb          ? a.layer * static_cast<int>(a.num_blocks) + (out ? 0 : id)
                                            : a.layers * static_cast<int>(a.num_blocks);
+        const int now_id = id;
         id = id_of(j + 1);
+        if constexpr (kCodes<SRC>) {  // K's warp lists the tiles, the ones that turn them bring them
+          const int64_t at = (static_cast<int64_t>(a.layer) * a.num_blocks + (out ? 0 : now_id)) * 2 * a.Hkv + w.h;
+          const float k_scale = lane < nb ? a.scales[at] : 0.0f, v_scale = lane < nb ? a.scales[at + a.Hkv] : 0.0f;
+          if (done >= kListLead) {
+            const uint32_t before = done - kListLead;
+            go = __all_sync(0xffffffffu, wait(&s.unlisted[before % kList], (before / kList) & 1, abort)) != 0;
+            if (!go) break;
+          }
+          // The tile's own scales, and what its blocks' are of them.  K: the largest; where another is not a power of two
+          // (or 0) of 2^-15 or more times it, which f16 takes exactly, the logits are scaled instead.  V: a power of two, at
+          // least the largest, from 2^-104 to 2^104 (sums of weights are divided by it).
+          const float k_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(k_scale))));
+          const uint32_t v_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v_scale)));
+          if (v_bits != 0) v_exp = min(max(static_cast<int>(v_bits >> 23) - 127 + ((v_bits & 0x7FFFFFu) != 0), -104), 104);  // values of 0: as before
+          const float k_all = k_top > 0.0f ? k_top : 1.0f, k_of = k_scale / k_all;
+          const float v_of = v_scale * __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
+          const bool odd = __any_sync(0xffffffffu, k_of != 0.0f && ((__float_as_uint(k_of) & 0x7FFFFFu) != 0 || fabsf(k_of) < 0x1p-15f));
+          ListedTile& e = s.list[done % kList];
+          const int of = a.b == 16 ? lane & 7 : (lane & 7) >> 1;  // the block of 16 tokens
+          const float k16 = __shfl_sync(0xffffffffu, k_of, of), v16 = __shfl_sync(0xffffffffu, v_of, of);
+          if (lane < 8) {
+            e.z[lane] = z;
+            e.k[lane] = odd ? 0x3C00 : static_cast<uint16_t>(pack_f16x2(k16, 0.0f));
+            e.v[lane] = static_cast<uint16_t>(pack_f16x2(v16, 0.0f));
+            e.k_rest[lane] = k16;
+          }
+          if (lane == 0) {
+            e.k_scale = k_all;
+            e.v_log = static_cast<float>(v_exp);
+            e.v_inv = __uint_as_float(static_cast<uint32_t>(127 - v_exp - static_cast<int>(kGain)) << 23);
+            e.row = w.h * a.b;
+            e.what = mixed_tile(w, j) ? kMixedTile : kPlainTile;
+            e.k_odd = odd;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.listed[done % kList]);
+          continue;
+        }
         uint64_t* full = kv ? &s.v_full[st] : &s.k_full[st];
         uint32_t* used = &used_full;
         if (kv && mixed_tile(w, j)) {
@@ -856,6 +935,14 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         __syncwarp();
       }
     }
+    if (kCodes<SRC> && go && !kv && lane == 0) {  // the list's end
+      const uint32_t before = done - kListLead;
+      if (done < kListLead || wait(&s.unlisted[before % kList], (before / kList) & 1, abort)) {
+        s.list[done % kList].what = kNoMoreTiles;
+        mbar_arrive(&s.listed[done % kList]);
+      }
+    }
+    __syncwarp();
     // Copies still in flight land before the shared memory is released.  A role may give up after this
     // warp is through, so it waits for its last ones in any case (they have landed, but for that).
     if (lane == 0)
@@ -878,7 +965,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         go = __all_sync(0xffffffffu, wait(&s.v_mixed[st], (seen_mixed >> st) & 1, abort));
         if (!go) break;
         seen_mixed ^= 1u << st;
-        if (look_over<D>(a, w, j, s.v[st][0], lane) && lane == 0) {
+        if (look_over<D, kCodes<SRC>>(a, w, j, s.v[st][0], lane) && lane == 0) {
           const int f = count % kFlags;
           if (s.odd[f] != count) s.odd[f] = count, s.odd_lo[f] = j;
           s.odd_hi[f] = j;
@@ -897,8 +984,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     // Descriptors are made once; a step along the contraction adds to their start address (in
     // units of 16 bytes).
     static_assert(kStages == 2, "descriptors below");
-    const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-    const uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kTransposeB;
+    const uint32_t idesc_s = kCodes<SRC> ? idesc_f16_f32(kRows, kKeys) : idesc_bf16_f32(kRows, kKeys);
+    const uint32_t idesc_o = (kCodes<SRC> ? idesc_f16_f32(kRows, D) : idesc_bf16_f32(kRows, D)) | kTransposeB;
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
     const uint64_t qd0 = smem_desc_sw128(smem_u32(s.q[0])), qd1 = smem_desc_sw128(smem_u32(s.q[1]));
     const uint64_t kd0 = smem_desc_sw128(smem_u32(s.k[0])), kd1 = smem_desc_sw128(smem_u32(s.k[1]));
@@ -970,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     while (ok && n_next >= 0) {
       const int n = n_next, c0 = c0_next, c1 = c1_next, c2 = c2_next;
       const bool two = two_next;
-      ok = wait_all(&s.q_full, count & 1);
+      ok = wait_all(kCodes<SRC> ? &s.q_turned : &s.q_full, count & 1);
       ++count;
       uint32_t st = __shfl_sync(0xffffffffu, tiles & 1, 0);
       if (ok && n > 0) ok = wait_all(&s.k_full[st], (tiles >> 1) & 1);
@@ -1035,6 +1122,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     const uint32_t ts = tbase + lanes + t * kKeys, to = tbase + lanes + 256 + t * 128;
     const uint64_t sl2x2 = pair2(a.sl2);
     uint32_t s_seen = 0, o_seen = 0;
+    uint32_t scale_tile = 0;  // tiles of the items before, of both groups
     bool ok = true;
     while (true) {
       ok = __all_sync(0xffffffffu, wait(&s.item_full[count % kItems], (count / kItems) & 1, abort));
@@ -1043,7 +1131,19 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       uint64_t* const let_go = &s.item_empty[count % kItems];
       if (w.r < 0) break;
       ++count;
+      float gain = 1.0f;  // of the row's logits, where its queries were turned
+      if constexpr (kCodes<SRC>) {
+        if (t == 0 || w.two) {
+          ok = __all_sync(0xffffffffu, wait(&s.q_full, (count - 1) & 1, abort));
+          if (!ok) break;
+          gain = turn_queries<D>(s.q[t][0], row);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_turned);
+      }
       if (t == 1 && !w.two) {
+        if (kCodes<SRC>) scale_tile += static_cast<uint32_t>(w.j1 - w.j0);
         __syncwarp();
         if (lane == 0) mbar_arrive(let_go);
         continue;
@@ -1061,6 +1161,23 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         tmem_ld_dep(x[1]);
         tmem_ld_dep(x[2]);
         tmem_ld_dep(x[3]);
+        float sl2 = a.sl2, v_log = 0.0f, v_inv = 0.0f;  // of the tile
+        if constexpr (kCodes<SRC>) {
+          const uint32_t slot = scale_tile % kList;
+          ok = __all_sync(0xffffffffu, wait(&s.listed[slot], (scale_tile / kList) & 1, abort));
+          if (!ok) break;
+          ++scale_tile;
+          const ListedTile& e = s.list[slot];
+          sl2 *= e.k_scale * gain;
+          v_log = e.v_log;
+          v_inv = e.v_inv;
+          if (e.k_odd) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int f = 0; f < 32; ++f) x[c][f] = __float_as_uint(__uint_as_float(x[c][f]) * e.k_rest[2 * c + (f >> 4)]);
+          }
+        }
         if (mixed) {
           const int p = w.p_first + min(i, w.queries - 1);
 #pragma unroll
@@ -1078,9 +1195,10 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         for (int e = 0; e < 32; ++e)
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
+        const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = kCodes<SRC> ? fmaf(all, sl2, v_log) : all * a.sl2;
         if (__any_sync(0xffffffffu, top > m)) {
-          const float mn = fmaxf(m, top + kLazy), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
+          const float mn = fmaxf(m, top + (kCodes<SRC> ? kLazyCodes : kLazy)), corr = m == -INFINITY ? 0.0f : ex2(m - mn);
           if (j > w.j0) {  // O of the tiles so far, complete since s_full follows their products
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -1095,7 +1213,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
           l *= corr;
           m = mn;
         }
-        const uint64_t ref = pair2(m == -INFINITY ? 0.0f : -m);
+        const uint64_t ref = pair2((m == -INFINITY ? 0.0f : -m) + (kCodes<SRC> ? v_log + kGain : 0.0f));
+        const uint64_t by = kCodes<SRC> ? pair2(sl2) : sl2x2;
         uint64_t sum = 0;  // a pair of +0
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -1104,11 +1223,11 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
           for (int e = 0; e < 32; ++e) {
             const uint32_t (&src)[32] = x[2 * c + (e >> 4)];
             float y0, y1;
-            unpair(fma2(pair(src[(2 * e) & 31], src[(2 * e + 1) & 31]), sl2x2, ref), y0, y1);
+            unpair(fma2(pair(src[(2 * e) & 31], src[(2 * e + 1) & 31]), by, ref), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
             sum = add2(sum, pair(__float_as_uint(y0), __float_as_uint(y1)));
-            pk[e] = pack_bf16x2(y0, y1);
+            pk[e] = kCodes<SRC> ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
           }
           tmem_st32(ts + c * 32, pk);
         }
@@ -1118,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&s.p_full[t]);
         float a0, a1;
         unpair(sum, a0, a1);
-        l += a0 + a1;
+        if (kCodes<SRC>) l = fmaf(a0 + a1, v_inv, l);
+        else l += a0 + a1;
       }
       if (!ok) break;
       const bool empty = w.j0 == w.j1;  // a part without tiles
@@ -1137,7 +1257,9 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         to_row.part[D + 1] = l;
       }
       if (!empty) {
-        const float inv = 1.0f / l;  // a row sees itself; logits of -inf alone give 0 / 0, as their softmax
+        // a row sees itself; logits of -inf alone give 0 / 0, as their softmax
+        const float unit = kCodes<SRC> ? 0x1p-15f : 1.0f, inv = unit / l;
+        static_assert(kGain == 15.0f, "unit");
         // Rolled: code that runs once an item comes from far away, and its size is time.
         if constexpr (PARTS) {
           // Through shared memory, 128 bytes of each row at a time, so that 8 lanes write one row's.  The CTA's only
@@ -1158,7 +1280,12 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
             tmem_wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
+            {
+              if (kCodes<SRC>)
+#pragma unroll
+                for (int f = 4 * e; f < 4 * e + 4; ++f) o[f] = __float_as_uint(__uint_as_float(o[f]) * unit);
               sts16(put + ((e ^ (lane & 7)) << 4), make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+            }
             __syncwarp();
             uint4 v[8];
 #pragma unroll
@@ -1267,13 +1394,12 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
   out[3] = static_cast<uint16_t>(y1 >> 16);
 }
 
-static_assert(sizeof(TileSmem<128, Source::kPaged>) + 1024 <= 227 * 1024, "shared memory of one CTA");
-static_assert(sizeof(TileSmem<128, Source::kPaged8>) + 1024 <= 227 * 1024, "shared memory of one CTA");
+static_assert(kSmemBytes<128, Source::kPaged> <= 227 * 1024 && kSmemBytes<128, Source::kPaged8> <= 227 * 1024, "shared memory of one CTA");
 
 template <int D, bool Q_TMA, bool PARTS, Source SRC>
 cudaError_t launch(const CUtensorMap& tm, const CUtensorMap& tv, const CUtensorMap& tq, const AttnArgs& a, const TilePlan& plan, cudaStream_t st) {
   const int nx = plan.nx, items = static_cast<int>(plan.items);
-  constexpr int bytes = sizeof(TileSmem<D, SRC>) + 1024;
+  constexpr int bytes = kSmemBytes<D, SRC>;
   static PerDeviceInit attrs;
   cudaError_t e = attrs.run(
       [] { return cudaFuncSetAttribute(tile_kernel<D, Q_TMA, PARTS, SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });

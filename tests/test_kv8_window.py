@@ -10,7 +10,9 @@ import torch
 import test_cache_attention as A
 from oracle import serving_oracle as S
 
-FEW, MANY = 2.0 ** -11, 2.0 ** -8      # how far weights are held in the two forms
+# How far weights are held (f16: half a step is 2^-12 of the value, counted as 2^-11).  In the form for many rows values of
+# scales that are not powers of two are rounded too, scale and product: 2^-12 each.
+FEW, MANY = 2.0 ** -11, 2.0 ** -11 + 2.0 ** -11
 
 
 @pytest.fixture(scope="module")
@@ -72,6 +74,11 @@ def _pool(rng, NB, layers, Hkv, b, d, scale_exp=(-8, -4), plain=False):
     return codes, scales.astype(np.float32)
 
 
+def _exact_pool(codes, scales):
+    """What is attended to, in 64 bits."""
+    return codes.view(torch.float8_e4m3fn).double() * scales.double()[..., None, None]
+
+
 def _case(zp, Hq, Hkv, d, b, cached, new, window=0, sinks=0, seed=0, max_q=None, off=0, expect=0, hidden_nan=True, skip=(), start_edit=None,
           seq_edit=None, tables_edit=None, pad=0, scale_exp=(-8, -4), gain=2.0, ws_bytes=None, plain=False, check=True):
     """Ragged requests over layer 1 of two; tokens that none of a request's rows sees hold NaN."""
@@ -110,9 +117,7 @@ def _case(zp, Hq, Hkv, d, b, cached, new, window=0, sinks=0, seed=0, max_q=None,
     rest[off:off + sum(new) * Hq * d] = 7.0
     assert bool((rest == 7).all())                          # nothing around the requests' rows
     rel = FEW if G * mq <= 16 else MANY
-    pool = args[0].view(torch.float8_e4m3fn)[1].double() * args[1][1].double()[..., None, None]
-    if rel == MANY:                                         # the values that are attended to: bf16(code * scale)
-        pool = pool.float().to(torch.bfloat16).double()
+    pool = _exact_pool(args[0][1], args[1][1])
     for r in range(B):
         rows = slice(start[r], start[r + 1])
         if r in skip:
@@ -141,7 +146,10 @@ def _exact_rows(pool, table, q, L, window, sinks, p):
 def _check(pool, table, q, got, L, window, sinks, p, rel, where):
     want, mass = _exact_rows(pool, table, q, L, window, sinks, p)
     err = (got.double() - want).abs()
-    tol = 2.0 ** -8 * want.abs() + (rel + 2.0 ** -14) * mass + 1e-30       # as in test_cache_attention
+    # As in test_cache_attention; and weights below 2^-18 of the largest are held to 2^-29 of it (f16's last bit is 2^-24, half
+    # of it 2^-25, and the largest weight stands at 2^4 or above), each times a value of up to the largest.
+    most = pool[table[:-(-L // p["block_size"])].long(), 1].abs().nan_to_num(0.0).max()
+    tol = 2.0 ** -8 * want.abs() + (rel + 2.0 ** -14) * mass + (rel == MANY) * 2.0 ** -29 * L * most + 1e-30
     assert bool((err <= tol).all()), (where, float((err / tol).max()))
 
 
@@ -190,47 +198,151 @@ def test_long_chunks_and_caches(zp):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("new", [4, 80])
-@pytest.mark.parametrize("lo,hi", [(-60, -50), (40, 50), (-30, 20), (-126, -120)])
+@pytest.mark.parametrize("lo,hi", [(-60, -50), (40, 50), (-12, 2), (-100, -90)])
 def test_scales_of_any_size(zp, new, lo, hi):
     _case(zp, 8, 2, 128, 16, [300, 33], [new, new], seed=3, scale_exp=(lo, hi), gain=min(2.0 ** -(hi + 6), 2.0 ** 90))
     _case(zp, 8, 2, 64, 32, [300, 33], [new, new], seed=3, scale_exp=(lo, hi), gain=min(2.0 ** -(hi + 6), 2.0 ** 90), plain=True)
 
 
-SCALES = [0.0, 2.0 ** -126, 2.0 ** -133, 2.0 ** -149, 3 * 2.0 ** -140, 2.0 ** -20, 1.0, -1.0, 1.5, 0.1, 255.0, 256.0, 257.0, 2.0 ** 100, 2.0 ** 118, 3.3e38, -0.0625, 1.0 + 2.0 ** -7,
-          1.0 + 2.0 ** -8, 2.0 ** 127]
-
-
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,b", [(128, 16), (128, 32), (64, 16), (64, 32)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
-def test_chunks_equal_those_over_the_unpacked_pool(zp, d, b, window, sinks):
-    """Bit for bit, for every code and scales of every kind (NaN and values past bf16's range among them)."""
+def test_every_code(zp, d, b, window, sinks):
+    """All codes that are numbers, under scales as the library writes them; and over blocks of a pool that the library
+    packed, the values of the pool."""
     rng = np.random.default_rng(d + b)
     Hq, Hkv, new, cached = 4, 2, [200, 37, 64], [0, 300, 700]
     lens = [c + n for c, n in zip(cached, new)]
     tables, NB = A._tables(rng, lens, b)
     p = A._params(Hq, Hkv, d, b)
     T, mb = sum(new), tables.shape[1]
-    q = torch.from_numpy(rng.standard_normal((T, Hq, d))).to(torch.bfloat16).cuda()
+    q = torch.from_numpy(rng.standard_normal((T, Hq, d)) / 4).to(torch.bfloat16).cuda()
     start, seq, dt = _i32(np.concatenate([[0], np.cumsum(new)])), _i32(lens), torch.from_numpy(np.where(tables < 0, 0, tables).astype(np.int32)).cuda()
-    ids = torch.arange(NB, dtype=torch.int32, device="cuda")
-    finite = rng.integers(0, 0x7F, (1, NB, 2, Hkv, b, d)) + 0x80 * rng.integers(0, 2, (1, NB, 2, Hkv, b, d))
-    every = rng.integers(0, 256, finite.shape)
-    some = np.where(rng.random(finite.shape) < 2e-4, 0x7F, finite)
-    pick = lambda x: rng.choice(np.array(x, dtype=np.float32), (1, NB, 2, Hkv))
-    small = [s for s in SCALES if abs(s) < 2.0 ** 90]
-    for codes, scales in ((finite, pick([2.0 ** -6, 2.0 ** -7, 2.0 ** -5])), (finite, pick(small)), (some, pick([2.0 ** -6, 0.01])), (every, pick([2.0 ** -6])),
-                          (finite, pick(SCALES))):
-        c, s = torch.from_numpy(codes.astype(np.uint8)).cuda(), torch.from_numpy(scales).cuda()
-        pool = torch.zeros(codes.shape, dtype=torch.bfloat16, device="cuda")
-        ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, T, 3, 200, mb, window, sinks))
-        zp.zp_kv8_unpack_blocks(c, s, ids, pool, ids, p, ws)
-        a, w = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
-        zp.zp_kv8_window_attn(c, s, 0, q, start, dt, seq, a, p, ws, window, sinks, 200)
-        zp.zp_paged_window_attn(pool, 0, q, start, dt, seq, w, p, ws, window, sinks, 200)
+    ws = zp.new_workspace(max(zp.zp_kv8_window_workspace_size(p, T, 3, 200, mb, window, sinks), 256))
+
+    def attend(c, s):
+        out = torch.full_like(q, 7.0)
+        zp.zp_kv8_window_attn(c, s, 0, q, start, dt, seq, out, p, ws, window, sinks, 200)
         assert zp.zp_read_error(ws) == 0
-        assert torch.equal(torch.isnan(a), torch.isnan(w))
-        assert torch.equal(torch.nan_to_num(a, nan=5.0), torch.nan_to_num(w, nan=5.0))
+        for r, L in enumerate(lens):
+            rows = slice(start[r].item(), start[r + 1].item())
+            _check(_exact_pool(c[0], s[0]), dt[r], q[rows], out[rows], L, window, sinks, p, MANY, r)
+        return out
+    codes = rng.integers(0, 0x7F, (1, NB, 2, Hkv, b, d)) + 0x80 * rng.integers(0, 2, (1, NB, 2, Hkv, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))
+    attend(torch.from_numpy(codes.astype(np.uint8)).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda())
+    # packed from bf16 blocks of very different sizes, one of zeros: the same as from the bf16 pool read back
+    ids = torch.arange(NB, dtype=torch.int32, device="cuda")
+    pool = (torch.randn((1, NB, 2, Hkv, b, d), device="cuda") * 2.0 ** torch.randint(-6, 3, (1, NB, 2, Hkv, 1, 1), device="cuda")).to(torch.bfloat16)
+    pool[0, int(tables[2][1])] = 0
+    c, s = torch.zeros(pool.shape, dtype=torch.uint8, device="cuda"), torch.zeros((1, NB, 2, Hkv), device="cuda")
+    zp.zp_kv8_pack_blocks(pool, ids, c, s, ids, p, ws)
+    got = attend(c, s)
+    zp.zp_kv8_unpack_blocks(c, s, ids, pool, ids, p, ws)
+    want = torch.full_like(q, 7.0)
+    wws = zp.new_workspace(zp.zp_paged_window_workspace_size(p, T, 3, 200, mb, window, sinks))
+    zp.zp_paged_window_attn(pool, 0, q, start, dt, seq, want, p, wws, window, sinks, 200)
+    for r, L in enumerate(lens):                                # both are near the exact rows
+        rows = slice(start[r].item(), start[r + 1].item())
+        exact, mass = _exact_rows(_exact_pool(c[0], s[0]), dt[r], q[rows], L, window, sinks, p)
+        tol = 2.0 ** -8 * (2 * exact.abs() + mass) + (MANY + 2.0 ** -13) * mass + 2.0 ** -29 * L * pool.float().abs().max() + 1e-30
+        assert bool(((got[rows].double() - want[rows].double()).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,b", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("new", [4, 70])
+def test_keys_with_scales_of_every_kind(zp, d, b, new):
+    """Scales of 0 and below, of many bits, subnormal: logits are code * scale as they are."""
+    rng = np.random.default_rng(new)
+    Hq, Hkv, L = 4, 2, 900 + new
+    tables, NB = A._tables(rng, [L], b)
+    codes, scales = _pool(rng, NB, 1, Hkv, b, d)
+    scales[0, :, 0] = rng.choice(np.array([0.0, -0.0, -2.0 ** -6, 2.0 ** -6, -0.01, 0.013, 2.0 ** -140, 1e-30, 3e-3], dtype=np.float32), (NB, Hkv))
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p, rel = A._params(Hq, Hkv, d, b), FEW if 2 * new <= 16 else MANY
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), torch.from_numpy(tables).cuda()
+    for window, sinks in ((0, 0), (333, 20)):
+        out = torch.full_like(q, 7.0)
+        ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, new, 1, new, tables.shape[1], window, sinks))
+        zp.zp_kv8_window_attn(c, s, 0, q, _i32([0, new]), dt, _i32([L]), out, p, ws, window, sinks, new)
+        assert zp.zp_read_error(ws) == 0
+        _check(_exact_pool(c[0], s[0]), dt[0], q, out, L, window, sinks, p, rel, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,b", [(128, 32), (64, 16)])
+@pytest.mark.parametrize("new", [4, 70])
+def test_values_with_scales_of_every_kind(zp, d, b, new):
+    """Scales of 0 and below, of many bits, 2^90 apart from one 128 tokens to the next, and up to 2^15 apart within."""
+    rng = np.random.default_rng(new)
+    Hq, Hkv, L = 4, 2, 900 + new
+    tables, NB = A._tables(rng, [L], b)
+    codes, scales = _pool(rng, NB, 1, Hkv, b, d)
+    per = 128 // b
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p, rel = A._params(Hq, Hkv, d, b), FEW if 2 * new <= 16 else MANY
+    c, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(tables).cuda()
+    for spread in (0, 12, 45):
+        for i in range(-(-L // b)):
+            far = 2.0 ** (spread * ((i // per) % 3 - 1)) if spread else 1.0
+            scales[0, tables[0, i], 1] = rng.choice(np.array([0.0, -2.0 ** -6, 2.0 ** -6, 2.0 ** -7, -0.01, 0.013, 0.9, 2.0 ** -15, 3e-3], dtype=np.float64)) * far
+        s = torch.from_numpy(scales).cuda()
+        out = torch.full_like(q, 7.0)
+        ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, new, 1, new, tables.shape[1], 0, 0))
+        zp.zp_kv8_window_attn(c, s, 0, q, _i32([0, new]), dt, _i32([L]), out, p, ws, 0, 0, new)
+        assert zp.zp_read_error(ws) == 0
+        _check(_exact_pool(c[0], s[0]), dt[0], q, out, L, 0, 0, p, rel, spread)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ratio", [30.0, 2.0 ** 14, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_behind_a_block_of_a_larger_scale(zp, d, ratio):
+    """Blocks of weight 0 with a V scale `ratio` times the others' come first, then one token takes most of the weight with a
+    value of 0, and the result is the sum of 4000 equal weights of e^-9 of it."""
+    p = A._params(1, 1, d, 16, scale=0.125)
+    NB, new = 8 + 8 + 256, 20
+    L = NB * 16
+    codes = np.zeros((1, NB, 2, 1, 16, d), dtype=np.uint8)
+    enc = lambda v: S.e4m3_encode(np.array(float(v)))
+    codes[0, :, 0, 0, :, 0] = enc(-9)
+    codes[0, :, 1, 0] = enc(1.5)
+    codes[0, :8, 0, 0, :, 0] = enc(-88)
+    codes[0, 8, 0, 0, 0, 0] = 0
+    codes[0, 8, 1, 0, 0] = 0
+    scales = np.ones((1, NB, 2, 1), dtype=np.float32)
+    scales[0, :, 1] = 2.0 ** -6
+    scales[0, :8, 1] = 2.0 ** -6 * ratio
+    q = torch.zeros((new, 1, d), dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 8.0
+    out = torch.zeros_like(q)
+    tables = np.arange(NB, dtype=np.int32)[None]
+    ws = zp.new_workspace(256)
+    c, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    zp.zp_kv8_window_attn(c, s, 0, q, _i32([0, new]), _i32(tables), _i32([L]), out, p, ws, 0, 0, new)
+    assert zp.zp_read_error(ws) == 0
+    _check(_exact_pool(c[0], s[0]), torch.arange(NB, device="cuda"), q, out, L, 0, 0, p, MANY, ratio)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gain", [2.0 ** 10, 2.0 ** 16, 2.0 ** 24])
+def test_queries_with_one_large_value(zp, gain):
+    """A value of the query `gain` times the others, where the keys are 0: the logits are the others'."""
+    rng = np.random.default_rng(5)
+    Hq, d, b, new, L = 4, 128, 16, 60, 300
+    tables, NB = A._tables(rng, [L], b)
+    codes, scales = _pool(rng, NB, 1, 1, b, d)
+    codes[0, :, 0, :, :, 77] = 0
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    q[:, :, 77] = gain
+    p = A._params(Hq, 1, d, b)
+    out = torch.full_like(q, 7.0)
+    ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, new, 1, new, tables.shape[1], 0, 0))
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), torch.from_numpy(tables).cuda()
+    zp.zp_kv8_window_attn(c, s, 0, q, _i32([0, new]), dt, _i32([L]), out, p, ws, 0, 0, new)
+    assert zp.zp_read_error(ws) == 0
+    _check(_exact_pool(c[0], s[0]), dt[0], q, out, L, 0, 0, p, MANY, gain)
 
 
 @pytest.mark.gpu
@@ -264,13 +376,11 @@ def test_nan_reaches_only_the_rows_that_see_it(zp, new, d, b, Hq):
     want[new - 1, G:] = True
     assert torch.equal(nan, want)
     clean = np.where((codes & 0x7F) == 0x7F, 0, codes)
-    pool = torch.from_numpy(clean).cuda().view(torch.float8_e4m3fn)[0].double() * s[0].double()[..., None, None]
     rel = FEW if G * new <= 16 else MANY
-    if rel == MANY:                                          # attends to bf16(code * scale)
-        pool = pool.float().to(torch.bfloat16).double()
+    pool = _exact_pool(torch.from_numpy(clean).cuda()[0], s[0])
     exact, mass = _exact_rows(pool, dt[0], q, L, window, sinks, p)
     fine = ~want.cuda()
-    tol = 2.0 ** -8 * exact.abs() + (rel + 2.0 ** -14) * mass + 1e-30      # as in test_cache_attention
+    tol = 2.0 ** -8 * exact.abs() + (rel + 2.0 ** -14) * mass + 2.0 ** -29 * L * pool[:, 1].abs().max() + 1e-30      # as in _check
     assert bool(((out.double() - exact).abs() <= tol)[fine].all())
 
 
@@ -313,9 +423,7 @@ def test_workspaces_of_other_batches(zp, new, window):
     args = _case(zp, 4, 1, 64, 16, [9000], [new], window, 4, seed=new)
     own = args[9].numel()
     assert own > 256
-    pool = args[0].view(torch.float8_e4m3fn)[1].double() * args[1][1].double()[..., None, None]
-    if 4 * new > 16:
-        pool = pool.float().to(torch.bfloat16).double()
+    pool = _exact_pool(args[0][1], args[1][1])
     for n in (256, own // 512 * 256, own, own + 256):
         buf = torch.zeros(n + 512, dtype=torch.uint8, device="cuda")
         buf[n:] = 0xA5
@@ -380,9 +488,7 @@ def test_captured_and_replayed(zp, new):
     assert torch.equal(args[7], want)
     args[6].copy_(_i32([200 + new, 10 + new]))           # shorter caches: the same captured call
     graph.replay()
-    pool = args[0].view(torch.float8_e4m3fn)[1].double() * args[1][1].double()[..., None, None]
-    if 2 * new > 16:
-        pool = pool.float().to(torch.bfloat16).double()
+    pool = _exact_pool(args[0][1], args[1][1])
     for r, L in enumerate((200 + new, 10 + new)):
         rows = slice(r * new, (r + 1) * new)
         _check(pool, args[5][r], args[3][rows], args[7][rows], L, 0, 0, args[8], FEW if 2 * new <= 16 else MANY, r)
