@@ -140,7 +140,7 @@ zp_status kv8_window(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, c
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows)
     return split_launch(a, p, true, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
-  return tile8_launch(a, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+  return tile8_launch(a, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes, true), workspace, st);
 }
 
 // Prompts walk their rows in runs of tokens as requests walk blocks.  A run is what one copy brings: a whole tile of
@@ -180,7 +180,7 @@ zp_status prompt(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int
   a.max_q = max_len;
   a.stall = stall_ns != 0;
   a.limit_ns = a.stall ? stall_ns : kWaitNs;
-  return tile_rows_launch(a, p, tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, workspace_bytes), workspace,
+  return tile_rows_launch(a, p, tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, workspace_bytes, true), workspace,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -204,17 +204,19 @@ extern "C" size_t zp_paged_window_workspace_size(const zp_params* p, int32_t T, 
   return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
 }
 
-// Its kernels are those of the bf16 pool, and so are its plans.
 extern "C" size_t zp_kv8_window_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_q, int32_t max_blocks,
                                                int32_t window, int32_t sinks) {
-  return zp_paged_window_workspace_size(p, T, B, max_q, max_blocks, window, sinks);
+  if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
+  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
+    return tile_plan(p, T, B, max_q, max_blocks, window, sinks, SIZE_MAX, true).bytes;
+  return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
 }
 
 extern "C" size_t zp_prompt_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_len, int32_t window, int32_t sinks) {
   if (!p || T < 0 || max_len < 1 || max_len > (1 << 30) || window < 0 || sinks < 0) return 0;
   const PromptRuns r = prompt_runs(p, std::min(max_len, std::max(T, 1)), window);
   if (!sizes_ok(&r.p, B, r.runs)) return 0;
-  return tile_plan(&r.p, T, B, max_len, r.runs, window, sinks).bytes;
+  return tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, SIZE_MAX, true).bytes;
 }
 
 extern "C" zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q,

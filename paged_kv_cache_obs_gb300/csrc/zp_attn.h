@@ -61,7 +61,10 @@ struct TilePlan {
   int64_t items;
   size_t bytes;
 };
-TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX);
+// `rounds`: a CTA may take several parts one after another (over the bf16 pool it takes one, so that rows keep the sums that
+// they had).
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX,
+                   bool rounds = false);
 
 // Launch the tiled kernel (rows above kMaxSplitRows, and prompts), and the one that joins the parts: over the bf16 pool, the
 // 8-bit pool, or rows of packed prompts (whose a.b is the run of tokens that a copy brings: 32 or 128).

@@ -4,7 +4,7 @@
 
 namespace zp {
 
-TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room) {
+TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, int window, int sinks, size_t room, bool rounds) {
   TilePlan plan{};
   plan.ctas = plan_sms();
   int64_t tokens = static_cast<int64_t>(max_blocks) * p->block_size;
@@ -20,7 +20,20 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
   // a part has four tiles at least: below that its sums cost more than the tiles
   const size_t part = static_cast<size_t>(std::max(T, 1)) * p->num_q_heads * (p->head_dim + 4) * sizeof(float);  // of every row
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
-  plan.splits = static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(plan.ctas / std::max<int64_t>(items, 1), tiles / 4), fit)));
+  const int64_t most_splits = std::max<int64_t>(1, std::min(tiles / 4, fit));
+  plan.splits = 1;
+  if (!rounds) {
+    plan.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(plan.ctas / std::max<int64_t>(items, 1), most_splits)));
+  } else {
+    // As many as make the longest CTA's share shortest, in tiles: a part costs about 3 beside its own, and where there are
+    // several 2 more for its sums.  64 items of up to 783 tiles take 547 us with 7 splits (3 parts a CTA) and 753 with 2 (one each).
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= std::min<int64_t>(most_splits, 32); ++n) {
+      const int64_t parts = (std::max<int64_t>(items, 1) * n + plan.ctas - 1) / plan.ctas;  // of a CTA
+      const int64_t cost = parts * ((tiles + n - 1) / n + (n > 1 ? 5 : 3));
+      if (cost < best) best = cost, plan.splits = static_cast<int>(n);
+    }
+  }
   plan.nx = static_cast<int>(std::min<int64_t>(nx, INT_MAX));
   plan.items = nx * heads * plan.splits;
   plan.bytes = kHeader;

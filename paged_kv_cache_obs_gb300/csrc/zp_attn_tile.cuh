@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
 
   if (tid == 0) {
     mbar_init(&s.q_full, Q_TMA ? 1 : 32);
-    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.q_empty, PARTS ? 9 : 1);  // parts go out through the queries' place: the softmax groups let go of it too
     mbar_init(&s.drain, 1);
     mbar_init(&s.never, 1);
     constexpr int kFills = kCodes<SRC> ? 4 : 1;  // warps that fill a stage
@@ -1146,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         if (kCodes<SRC>) scale_tile += static_cast<uint32_t>(w.j1 - w.j0);
         __syncwarp();
         if (lane == 0) mbar_arrive(let_go);
+        if (PARTS && lane == 0) mbar_arrive(&s.q_empty);
         continue;
       }
       float m = -INFINITY, l = 0.0f;
@@ -1262,8 +1263,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         static_assert(kGain == 15.0f, "unit");
         // Rolled: code that runs once an item comes from far away, and its size is time.
         if constexpr (PARTS) {
-          // Through shared memory, 128 bytes of each row at a time, so that 8 lanes write one row's.  The CTA's only
-          // item is done with its queries.
+          // Through shared memory, 128 bytes of each row at a time, so that 8 lanes write one row's: in the place of the item's
+          // queries, which it is done with and which the next one's take when every warp has let go (q_empty).
           static_assert(sizeof(s.q) >= 8 * 32 * 128, "a warp's rows");
           const uint32_t stage = smem_u32(s.q) + warp * (32 * 128), put = stage + lane * 128, get = stage + (lane >> 3) * 128;
           float* const mine = write ? to_row.part : nullptr;
@@ -1332,6 +1333,11 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(let_go);
+      if (PARTS) {
+        fence_proxy_async_smem();  // the rows that went through it, ahead of the next copy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_empty);
+      }
     }
   }
   tc_fence_before();
