@@ -139,7 +139,7 @@ zp_status kv8_window(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, c
   a.limit_ns = a.stall ? stall_ns : kWaitNs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_q <= kMaxSplitRows)
-    return split_launch(a, p, true, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes), workspace, st);
+    return split_launch(a, p, true, split_plan(p, B, max_q, max_blocks, window, sinks, workspace_bytes, true), workspace, st);
   return tile8_launch(a, p, tile_plan(p, T, B, max_q, max_blocks, window, sinks, workspace_bytes, true), workspace, st);
 }
 
@@ -209,7 +209,7 @@ extern "C" size_t zp_kv8_window_workspace_size(const zp_params* p, int32_t T, in
   if (!sizes_ok(p, B, max_blocks) || T < 0 || max_q < 1 || window < 0 || sinks < 0) return 0;
   if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * max_q > kMaxSplitRows)
     return tile_plan(p, T, B, max_q, max_blocks, window, sinks, SIZE_MAX, true).bytes;
-  return split_plan(p, B, max_q, max_blocks, window, sinks).bytes;
+  return split_plan(p, B, max_q, max_blocks, window, sinks, SIZE_MAX, true).bytes;
 }
 
 extern "C" size_t zp_prompt_workspace_size(const zp_params* p, int32_t T, int32_t B, int32_t max_len, int32_t window, int32_t sinks) {

@@ -49,7 +49,8 @@ struct SplitPlan {
 };
 // `room`: bytes of the workspace; what does not fit it is split among fewer CTAs.
 constexpr size_t kHeader = 256;  // of a workspace: the error word
-SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX);
+// `many8`: codes, and requests of several queries.
+SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room = SIZE_MAX, bool many8 = false);
 
 // Launches the split kernel (and the one that joins its parts).
 zp_status split_launch(AttnArgs a, const zp_params* p, bool fp8, const SplitPlan& plan, void* workspace, cudaStream_t st);

@@ -260,9 +260,11 @@ __device__ __forceinline__ int acc_at(int row, int ch) {
   return ch ^ (FP8 ? c : (c & 1) | (c & 2) << 1);
 }
 
-// MANY: requests may have more than one query (which the bf16 form always allows).
+// MANY: requests may have more than one query (which the bf16 form always allows).  Codes with 16 rows: three CTAs on the SM,
+// as a warp issues every fifth cycle at most (64 requests of 4 tokens over up to 8192, in clusters of 2: 136 us, 164 with two).
+constexpr int kManyCtas = 3;
 template <bool FP8, int D, int NT, bool MANY>
-__global__ void __launch_bounds__(kThreads, (Shape<FP8, D, NT>::CTAS)) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, FP8 && MANY && NT == 2 ? kManyCtas : Shape<FP8, D, NT>::CTAS) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<FP8, D, NT>;
   constexpr int ROWS = Sh::ROWS, RB = Sh::RB, SLOTS = Sh::SLOTS, TILE = Sh::TILE, SUB = Sh::SUB;
   constexpr int KC = RB / 64;                  // 16-byte chunks of a key that a lane holds
@@ -902,7 +904,12 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // Finding the order costs a CTA about 0.5 us, too much where nothing is gained: with a window, whose
 // rows have nearly equal work (64 requests with a window of 1024: 44.0 us as they come, 43.4 us if
 // the caller has them in order), within a wave, and past 1024 requests, where the last ones are little.
-SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room) {
+//
+// Codes with 9 to 16 rows: slots for three CTAs an SM, over-filled by a sixth, and 4 tiles a warp.  Batches of up to one wave, or
+// two where caches are long, are shared by two CTAs a head, the long requests first, since a CTA is slow by itself: 64 requests of 4
+// tokens over up to 8192, 8 kv heads, take 136 us so and 180 unsplit; 24 requests 92 us and 140; over up to 2048 tokens 64
+// requests take 54 unsplit and 58 so.
+SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room, bool many8) {
   const int64_t sms = plan_sms();
   SplitPlan s{};
   s.rows = p->num_q_heads / p->num_kv_heads * max_q <= 8 ? 8 : 16;
@@ -914,12 +921,18 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   }
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
   const int64_t wave = sms * (s.rows == 16 ? 2 : 4) * 7 / 8;
-  const int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
+  int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
+  const bool many16 = many8 && s.rows == 16;
+  if (many16) {
+    const int64_t slots = sms * kManyCtas;
+    n = std::min((tiles + 4 * kWarps - 1) / (4 * kWarps), slots * 7 / 6 / units);
+    if (n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
+  }
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
   const size_t part = static_cast<size_t>(units) * s.rows * (p->head_dim + 4) * sizeof(float);  // of one cluster a row
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
   s.splits = n >= 8 ? static_cast<int>(std::max<int64_t>(1, std::min(n / 8, fit))) * 8 : s.cluster;
-  s.ordered = window == 0 && n < 2 && units > sms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
+  s.ordered = window == 0 && (n < 2 || (many16 && n == 2)) && units > sms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
   const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
   s.bytes = kHeader;
   if (parts > 1) s.bytes += (parts * part + 255) / 256 * 256;
