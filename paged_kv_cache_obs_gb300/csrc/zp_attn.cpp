@@ -180,6 +180,8 @@ zp_status prompt(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int
   a.max_q = max_len;
   a.stall = stall_ns != 0;
   a.limit_ns = a.stall ? stall_ns : kWaitNs;
+  const int most = std::min(max_len, T);
+  if (!a.stall && short_prompts(p, T, B, most)) return short_launch(a, p, most, workspace, reinterpret_cast<cudaStream_t>(stream));
   return tile_rows_launch(a, p, tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, workspace_bytes, true), workspace,
                           reinterpret_cast<cudaStream_t>(stream));
 }
@@ -216,6 +218,7 @@ extern "C" size_t zp_prompt_workspace_size(const zp_params* p, int32_t T, int32_
   if (!p || T < 0 || max_len < 1 || max_len > (1 << 30) || window < 0 || sinks < 0) return 0;
   const PromptRuns r = prompt_runs(p, std::min(max_len, std::max(T, 1)), window);
   if (!sizes_ok(&r.p, B, r.runs)) return 0;
+  // of either form: the test hooks take the tiled one
   return tile_plan(&r.p, T, B, max_len, r.runs, window, sinks, SIZE_MAX, true).bytes;
 }
 
