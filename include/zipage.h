@@ -413,6 +413,8 @@ zp_status zp_rope_apply_axes(const zp_rope_axes* axes, const zp_rows* q, const z
  *   num_blocks      blocks of the pool (num_blocks * block_size <= 2^31 - 1)
  *   block_tables    device int32 [B][max_blocks].  The call writes the entries of blocks whose first token is
  *                   new, and reads those of part-full blocks that get tokens; no others.
+ *                   Where tokens were taken back since (rejected drafts), a block that they had begun counts as
+ *                   new: it gets another id, and the old one is the caller's to hand out again.
  *   token_start     device int32 [B + 1], written: request r owns rows token_start[r] .. token_start[r + 1] - 1.
  *   seq_lens        device int32 [B], written: cached + new.  May be `cached` itself; no other arrays overlap.
  *   positions       device int32 [T] or NULL, written.  Rows behind the last request's: 0.

@@ -5,8 +5,8 @@
 // A prompt of a hundred tokens is one tile for the tensor cores of zp_attn_tile.cuh, whose CTA fills an SM: its loads, products,
 // softmax and stores follow one another, and nothing else is there to fill the gaps.  So here a CTA is small: 4 warps with 16
 // rows each (queries times the heads of a group), 64 tokens of keys and values at a time in 48 KB, warp-level
-// products, and several CTAs on an SM at different stages.  Bound by instructions (2.5 thousand a warp and tile, half of them
-// around the products) and the latency of the chain: load, S, softmax, P V, store.
+// products, and several CTAs on an SM at different stages.  Bound by instructions (some 1600 a warp and tile,
+// half of them around the products) and the latency of the chain: load, S, softmax, P V, store.
 //
 // Masks, weights (P rounded to bf16, sums and maxima fp32) and what a row does not see are as in the tiled kernel.  In a tile
 // that some row does not see whole, values that are not finite would reach it as 0 * inf: such a tile, which the CTA

@@ -12,6 +12,7 @@
 // tokens' cos and sin (one pair per thread, shared by all heads through shared memory) while
 // those are on their way.
 #include <cmath>
+#include <type_traits>
 
 #include "zp_internal.h"
 #include "zp_launch.h"
@@ -35,7 +36,8 @@ struct RopeArgs {
   uint16_t *qo, *ko;
   int64_t q_ts, q_hs, k_ts, k_hs, qo_ts, qo_hs, ko_ts, ko_hs;
   const int32_t* positions;
-  int64_t axis_stride;  // from one axis' positions to the next's
+  int64_t axis_stride;    // from one axis' positions to the next's
+  uint64_t axis_bits[4];  // the pairs' axes, two bits each
   int T, Hq, Hkv, d, rd, inplace_q, inplace_k, tokens;  // tokens: per CTA
   float mscale;
 };
@@ -48,8 +50,9 @@ __device__ __forceinline__ float turn_b(float a, float b, float c, float s) { re
 __device__ __forceinline__ const zp_rope& table_of(const zp_rope& rope) { return rope; }
 __device__ __forceinline__ const zp_rope& table_of(const zp_rope_axes& axes) { return axes.rope; }
 __device__ __forceinline__ int32_t position_of(const zp_rope&, const RopeArgs& a, int t, int) { return a.positions[t]; }
-__device__ __forceinline__ int32_t position_of(const zp_rope_axes& axes, const RopeArgs& a, int t, int pair) {
-  return a.positions[axes.axis[pair] * a.axis_stride + t];
+__device__ __forceinline__ int32_t position_of(const zp_rope_axes&, const RopeArgs& a, int t, int pair) {
+  const uint64_t bits = pair < 64 ? (pair < 32 ? a.axis_bits[0] : a.axis_bits[1]) : (pair < 96 ? a.axis_bits[2] : a.axis_bits[3]);
+  return a.positions[static_cast<int64_t>(bits >> (2 * (pair & 31)) & 3) * a.axis_stride + t];
 }
 
 template <class Handle>
@@ -211,6 +214,10 @@ zp_status apply(const zp_rope* rope, const Handle* handle, const zp_rows* q, con
   }
   a.positions = positions;
   a.axis_stride = axis_stride;
+  if constexpr (std::is_same_v<Handle, zp_rope_axes>) {
+    static_assert(ZP_ROPE_MAX_AXES <= 4, "two bits");
+    for (int i = 0; i < rd / 2; ++i) a.axis_bits[i / 32] |= static_cast<uint64_t>(handle->axis[i]) << (2 * (i % 32));
+  }
   a.T = T;
   a.Hq = Hq;
   a.Hkv = Hkv;

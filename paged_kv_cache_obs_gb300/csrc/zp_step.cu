@@ -12,7 +12,7 @@
 // scan in each warp and one more over the warps' totals), with the part-full blocks' ids and the first free ids on
 // their way meanwhile, and takes its share of the tokens and of the new blocks.  The cluster's barrier stands
 // between the last read of lengths and free_at and the writes, since both may be updated in place.  A row of the
-// step finds its request by halving the chunk's sums in shared memory, once for 4 rows in turn.
+// step finds its request by halving the chunk's sums in shared memory.
 #include <algorithm>
 #include <climits>
 
@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 1024;   // and requests of a chunk
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kFresh = 4096;     // free ids in shared memory: the rows of a large step wait for none (49000 rows 7.5 -> 7.2 us)
 
 struct StepArgs {
   const int32_t *cached, *new_tokens, *first, *free_ids;
@@ -68,9 +69,8 @@ __device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int by) { return __shf
 
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ StepArgs a) {
-  __shared__ int start[kThreads + 1], taken[kThreads + 1], cached[kThreads], first[kThreads], held[kThreads], fresh[kThreads];
+  __shared__ int start[kThreads + 1], taken[kThreads + 1], cached[kThreads], first[kThreads], held[kThreads], fresh[kFresh];
   __shared__ uint64_t sum_t[kWarps], sum_b[kWarps];
-  __shared__ int sm_at;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0, ctas = CLUSTER ? static_cast<int>(cluster_nctarank()) : 1;
   const int all = ctas * kThreads, me = rank * kThreads + tid;
@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   int at = a.free_at ? *a.free_at : 0;
   const bool bad_at = at < 0 || at > a.num_free;
   if (bad_at) at = a.num_free;
-  if (at + tid < a.num_free) fresh[tid] = a.free_ids[at + tid];
+#pragma unroll
+  for (int i = tid; i < kFresh; i += kThreads)
+    if (i < a.num_free - at) fresh[i] = a.free_ids[at + i];
 
   uint64_t tokens_before = 0, blocks_before = 0, tokens_all = 0, blocks_all = 0;
   bool bad = false;
@@ -157,11 +159,12 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     }
     if (!empty && n > 0) {
       // ids of the step's blocks
-      const auto free_id = [&](int j) { return j < kThreads ? fresh[j] : a.free_ids[at + j]; };
+      const auto free_id = [&](int j) { return j < kFresh ? fresh[j] : a.free_ids[at + j]; };
       for (int j = taken[0] + me; j < taken[n]; j += all) {
         const int i = place_of(taken, n, j);
         a.tables[static_cast<int64_t>(base + i) * a.max_blocks + blocks_of(a, cached[i]) + j - taken[i]] = free_id(j);
       }
+#pragma unroll 2
       for (int t = start[0] + me; t < start[n]; t += all) {
         const int i = place_of(start, n, t), k = t - start[i], p = cached[i] + k, j = (p >> a.bshift) - blocks_of(a, cached[i]);
         const int blk = j < 0 ? held[i] : free_id(taken[i] + j);

@@ -142,6 +142,38 @@ def _case(zp, Hq, Hkv, d, lens, window=0, sinks=0, form="rows", qform=None, befo
     return args
 
 
+def _values_case(zp, lens, d, window, sinks, value, bad_at):
+    """Three prompts; the second's keys and values are all `value`, and so are the values of the others at bad_at (row, head, dim)."""
+    Hq, Hkv = 4, 2
+    g = torch.Generator().manual_seed(4)
+    T, (n0, n1, n2) = sum(lens), lens
+    q, k, v = _rows(g, T, Hq, d, "rows", 2.0), _rows(g, T, Hkv, d, "rows"), _rows(g, T, Hkv, d, "rows")
+    k[n0:n0 + n1] = value
+    v[n0:n0 + n1] = value
+    for row, head, dim in bad_at:
+        v[row, head, dim] = value
+    out, p = torch.full((T, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), A._params(Hq, Hkv, d, 16)
+    ws = zp.new_workspace(zp.zp_prompt_workspace_size(p, T, 3, max(lens), window, sinks))
+    zp.zp_prompt_attn(q, k, v, _i32([0, n0, n0 + n1, T]), out, p, ws, max(lens), window=window, sinks=sinks)
+    assert zp.zp_read_error(ws) == 0
+    for lo, hi in ((0, n0), (n0 + n1, T)):
+        n = hi - lo
+        i, t = torch.arange(n, device="cuda")[:, None], torch.arange(n, device="cuda")
+        see = (t <= i) & ((t > i - window) | (t < sinks) | (window == 0))
+        for h in range(Hq):
+            x = v[lo:hi, h // 2].double()
+            bad = ~torch.isfinite(x)
+            hit = see.double() @ bad.double() > 0                        # [n, d]
+            got = out[lo:hi, h].double()
+            assert bool((torch.isfinite(got) == ~hit).all())
+            if math.isinf(value):
+                assert bool((got[hit] == value).all())
+            x = torch.where(bad, torch.zeros_like(x), x)
+            lw = (p["scale"] * (q[lo:hi, h].double() @ k[lo:hi, h // 2].double().T)).masked_fill(~see, -math.inf)
+            w = torch.softmax(lw, -1)
+            _check(got[~hit], (w @ x)[~hit], (w @ x.abs())[~hit])
+
+
 SHAPES = [(32, 8, 128), (28, 4, 128), (8, 8, 64), (16, 2, 64), (8, 4, 128), (3, 1, 128), (16, 1, 128), (10, 1, 64), (11, 1, 64)]
 
 
@@ -216,6 +248,39 @@ def test_few_long_prompts_are_split(zp, lens, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
+def test_short_prompts(zp, Hq, Hkv, d):
+    """Up to 128 tokens: the form in small CTAs."""
+    _case(zp, Hq, Hkv, d, [1, 0, 2, 15, 16, 17, 63, 64, 65, 100, 0, 127, 128, 5], seed=Hq, before=3, behind=5)
+    _case(zp, Hq, Hkv, d, [128], seed=Hq + 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["rows", "fused", "odd", "head-major", "padded"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 1), (16, 17), (40, 5), (64, 64), (65, 3), (100, 200), (128, 2), (7, 70)])
+def test_short_prompts_in_windows_and_strides(zp, form, window, sinks):
+    _case(zp, 4, 2, 128, [100, 5, 70, 128, 1], window, sinks, form=form, seed=1, before=1, behind=3)
+    _case(zp, 7, 1, 64, [33, 127, 64], window, sinks, form=form, seed=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 3)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_values_of_short_prompts_reach_only_the_rows_that_see_them(zp, d, window, sinks, value):
+    _values_case(zp, [100, 20, 128], d, window, sinks, value, ((60, 1, 7), (120 + 2, 0, 9), (120 + 100, 1, 60), (120 + 127, 0, 1)))
+
+
+@pytest.mark.gpu
+def test_short_rows_whose_logits_are_all_minus_infinity_are_nan(zp):
+    q, k = (torch.ones((40, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[20:, 0] = -math.inf
+    out, ws = torch.zeros_like(q), zp.new_workspace(256)
+    zp.zp_prompt_attn(q, k, k, _i32([0, 20, 40]), out, A._params(2, 2, 64, 16), ws, 20)
+    assert bool(torch.isnan(out[20:, 0]).all()) and bool((out[:20] == 1).all()) and bool((out[20:, 1] == 1).all())
+
+
+@pytest.mark.gpu
 def test_many_short_prompts(zp):
     rng = np.random.default_rng(3)
     _case(zp, 8, 2, 64, [int(x) for x in rng.integers(0, 40, 500)], seed=6)
@@ -228,34 +293,7 @@ def test_many_short_prompts(zp):
 def test_values_reach_only_the_rows_that_see_them(zp, window, sinks, value):
     """Bad keys and values of other prompts, of later tokens and of tokens outside the window have no effect; the
     rows that see a bad value get it in that dim."""
-    lens, Hq, Hkv, d = [100, 90, 200], 4, 2, 64
-    g = torch.Generator().manual_seed(4)
-    T = sum(lens)
-    q, k, v = _rows(g, T, Hq, d, "rows", 2.0), _rows(g, T, Hkv, d, "rows"), _rows(g, T, Hkv, d, "rows")
-    k[100:190] = value                       # the whole prompt between the others
-    v[100:190] = value
-    v[60, 1, 7], v[190 + 2, 0, 9], v[190 + 150, 1, 60] = value, value, value
-    out, p = torch.full((T, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), A._params(Hq, Hkv, d, 16)
-    ws = zp.new_workspace(zp.zp_prompt_workspace_size(p, T, 3, 200, window, sinks))
-    zp.zp_prompt_attn(q, k, v, _i32([0, 100, 190, 390]), out, p, ws, 200, window=window, sinks=sinks)
-    assert zp.zp_read_error(ws) == 0
-    for lo, hi in ((0, 100), (190, 390)):
-        want, mass = _exact(q[lo:hi], k[lo:hi], v[lo:hi], window, sinks, p["scale"])
-        n = hi - lo
-        i, t = torch.arange(n, device="cuda")[:, None], torch.arange(n, device="cuda")
-        see = (t <= i) & ((t > i - window) | (t < sinks) | (window == 0))
-        for h in range(Hq):
-            x = v[lo:hi, h // 2].double()
-            bad = ~torch.isfinite(x)
-            hit = see.double() @ bad.double() > 0                        # [n, d]
-            got = out[lo:hi, h].double()
-            assert bool((torch.isfinite(got) == ~hit).all())
-            if math.isinf(value):
-                assert bool((got[hit] == value).all())
-            x = torch.where(bad, torch.zeros_like(x), x)
-            lw = (p["scale"] * (q[lo:hi, h].double() @ k[lo:hi, h // 2].double().T)).masked_fill(~see, -math.inf)
-            w = torch.softmax(lw, -1)
-            _check(got[~hit], (w @ x)[~hit], (w @ x.abs())[~hit])
+    _values_case(zp, [100, 90, 200], 64, window, sinks, value, ((60, 1, 7), (190 + 2, 0, 9), (190 + 150, 1, 60)))
 
 
 @pytest.mark.gpu
