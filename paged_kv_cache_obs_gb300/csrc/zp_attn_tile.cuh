@@ -79,7 +79,7 @@ constexpr int kTurnWarp = 12;         // the first of the four
 constexpr float kLazy = 24.0f, kLazyCodes = 11.0f;
 constexpr float kGain = 15.0f;        // codes: log2 of what weights are multiplied by for f16
 constexpr uint32_t kTmemCols = 512;   // S0 S1 O0 O1, 128 columns each
-constexpr int kFlags = 16;            // items: K's warp is at most 7 ahead of a softmax group (the ring's 3, 2 stages, codes, one)
+constexpr int kFlags = 16;            // items with tiles: K's warp is at most 9 ahead of a softmax group (tiles: 4 listed, 1 brought, 2 stages; 2 of the ring)
 
 // An item: which, and what it walks.
 struct Item {
@@ -128,7 +128,7 @@ struct __align__(1024) TileSmem {
   uint32_t tmem;
   int abort;
   Item items[kItems];
-  int bad[kFlags], odd[kFlags];              // the last item (counted from 1) that a block id or a value marked
+  int bad[kFlags], odd[kFlags];              // the last item (those with tiles, from 1) that a block id or a value marked
   int odd_lo[kFlags], odd_hi[kFlags];        // the first and last tile with such values
   int end;                                   // of what is used
 };
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     if (SRC == Source::kRows && a.kv_tma) prefetch_tensormap(&tv);
     if (Q_TMA) prefetch_tensormap(&tq);
   }
-  // rows of the query tiles that no query fills stay zero
+  // rows of the query tiles that no query has filled start as zeros
   for (int i = tid; i < static_cast<int>(sizeof(s.q) / 16); i += kThreads<SRC>)
     reinterpret_cast<uint4*>(&s.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -785,6 +785,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
   bool bad;
   Raw raw = load_raw<SRC>(a, blockIdx.x, items);
   int count = 0;       // items with work so far
+  int walked = 0;      // those of them that have tiles
   uint32_t tiles = 0;  // KV tiles of the items before
 
   if (warp == kKWarp || warp == kVWarp) {
@@ -807,6 +808,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         continue;
       }
       ++count;
+      walked += w.j0 < w.j1;
       const int32_t* const table = a.tables + static_cast<int64_t>(w.r) * a.max_blocks;
       const auto id_of = [&](int j) {  // block id that the lane loads for tile j
         const int e = j * bpt + lane;
@@ -857,7 +859,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         // an id outside the pool: the item's rows are not written, and block 0 is read in its place
         const bool out = SRC != Source::kRows && (id < 0 || id >= a.num_blocks);
         if (SRC != Source::kRows && __any_sync(0xffffffffu, out) && lane == 0) {
-          *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) = count;
+          *reinterpret_cast<volatile int*>(&s.bad[walked % kFlags]) = walked;
           atomicCAS(a.err, 0, ZP_ERR_BAD_TABLE);
         }
         // blocks past the list's end have a coordinate past the tensor's: they come as zeros
@@ -958,7 +960,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       const Raw now = raw;
       raw = load_raw<SRC>(a, next_item(item), items);
       if (!take_item<SRC>(a, item, nx, now, w, bad)) continue;
-      ++count;
+      walked += w.j0 < w.j1;
       for (int j = w.j0; j < w.j1; ++j) {
         if (!mixed_tile(w, j)) continue;
         const uint32_t st = (tiles + static_cast<uint32_t>(j - w.j0)) % kStages;
@@ -966,8 +968,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         if (!go) break;
         seen_mixed ^= 1u << st;
         if (look_over<D, kCodes<SRC>>(a, w, j, s.v[st][0], lane) && lane == 0) {
-          const int f = count % kFlags;
-          if (s.odd[f] != count) s.odd[f] = count, s.odd_lo[f] = j;
+          const int f = walked % kFlags;
+          if (s.odd[f] != walked) s.odd[f] = walked, s.odd_lo[f] = j;
           s.odd_hi[f] = j;
         }
         fence_proxy_async_smem();
@@ -1114,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
   } else {
     if constexpr (kCodes<SRC>) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    int count = 0;  // items so far
+    int count = 0, walked = 0;  // items so far, and those with tiles
     const int t = warp >> 2, row = tid & 127;
     const int qi = row / a.G, gi = row - qi * a.G;
     const int i = t * qpt + qi;  // query of the item
@@ -1132,10 +1134,14 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       if (w.r < 0) break;
       ++count;
       float gain = 1.0f;  // of the row's logits, where its queries were turned
+      // Also a group without rows waits for the item's queries, which come when both groups are done with those before: what it
+      // arrives at below belongs to this item then, however many it has no part in.
+      if (kCodes<SRC> || (PARTS && t == 1 && !w.two)) {
+        ok = __all_sync(0xffffffffu, wait(&s.q_full, (count - 1) & 1, abort));
+        if (!ok) break;
+      }
       if constexpr (kCodes<SRC>) {
         if (t == 0 || w.two) {
-          ok = __all_sync(0xffffffffu, wait(&s.q_full, (count - 1) & 1, abort));
-          if (!ok) break;
           gain = turn_queries<D>(s.q[t][0], row);
           fence_proxy_async_smem();
         }
@@ -1250,8 +1256,9 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
       }
       const bool have = qi < qpt && i < w.queries;
       const Sink to_row = sink_of<D>(a, w, i, gi, have);
-      const bool marked = *reinterpret_cast<volatile int*>(&s.bad[count % kFlags]) == count;
-      const bool odd = *reinterpret_cast<volatile int*>(&s.odd[count % kFlags]) == count;
+      walked += !empty;
+      const bool marked = !empty && *reinterpret_cast<volatile int*>(&s.bad[walked % kFlags]) == walked;
+      const bool odd = !empty && *reinterpret_cast<volatile int*>(&s.odd[walked % kFlags]) == walked;
       const bool write = have && !marked;
       if (to_row.part && (write || marked || empty)) {
         to_row.part[D] = marked ? NAN : m;  // a maximum is never NaN: marks a part with a bad block id
@@ -1327,7 +1334,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&s.o_empty[t]);
         if (odd && !marked) {
           __syncwarp();  // the rows as written
-          const volatile int* const lo = &s.odd_lo[count % kFlags], *const hi = &s.odd_hi[count % kFlags];
+          const volatile int* const lo = &s.odd_lo[walked % kFlags], *const hi = &s.odd_hi[walked % kFlags];
           add_odd_values<D, SRC>(a, s.items[(count - 1) % kItems], *lo, *hi, t, warp & 3, lane);
         }
       }

@@ -496,6 +496,44 @@ def test_captured_and_replayed(zp, new):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,b", [(16, 8, 128, 16), (28, 4, 64, 32)])
+def test_many_requests_of_one_query_tile(zp, Hq, Hkv, d, b):
+    """CTAs take several items one after another of which one softmax group has no part; here and there one has two tiles."""
+    rng = np.random.default_rng(d)
+    tile = 128 // (Hq // Hkv)
+    for two in (0.0, 0.3):
+        new = [int(rng.integers(1, tile + 1)) + (tile if rng.random() < two else 0) for _ in range(120)]
+        _case(zp, Hq, Hkv, d, b, rng.integers(0, 300, 120).tolist(), new, seed=b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,d,b", [(4, 64, 16), (7, 128, 32)])
+def test_split_requests_of_one_query_tile(zp, G, d, b):
+    """100 items of up to 46 tiles are cut into 3 parts, of which CTAs take two or more; those of short caches have no tiles."""
+    rng = np.random.default_rng(G)
+    tile = 128 // G
+    cached = [int(rng.integers(4000, 5800)) if r % 3 else int(rng.integers(0, 200)) for r in range(50)]
+    args = _case(zp, 2 * G, 2, d, b, cached, [int(rng.integers(17, tile + 1)) for _ in cached[:-1]] + [17], seed=G)
+    assert args[9].numel() > 256 + 2 * args[3].numel() * 4
+
+
+@pytest.mark.gpu
+def test_bad_blocks_between_parts_without_tiles(zp):
+    """A wide table cuts requests of one tile into parts that mostly have none: the warps that bring tiles run far ahead, and what
+    they note of bad blocks stays with its request."""
+    B, new, wide = 153, 20, 50000
+    bad = tuple(r for r in range(B) if r % 3)
+
+    def edit(t):
+        w = np.zeros((B, wide), dtype=np.int32)
+        w[:, :t.shape[1]] = t
+        for r in bad:
+            w[r, 1] = -1 if r % 2 else 10 ** 6
+        return w
+    _case(zp, 4, 1, 64, 16, [12] * B, [new] * B, seed=3, tables_edit=edit, expect=zp.ZP_ERR_BAD_TABLE, skip=bad, ws_bytes=32 * B * new * 4 * 68 * 4 + 256)
+
+
+@pytest.mark.gpu
 def test_random_calls(zp):
     rng = np.random.default_rng(21)
     for i in range(60):

@@ -248,6 +248,13 @@ def test_few_long_prompts_are_split(zp, lens, window):
 
 
 @pytest.mark.gpu
+def test_split_prompts_of_one_query_tile(zp):
+    """100 items are cut into 3 parts, and some CTAs take two in a row of which one softmax group has no part: the long prompts'
+    last 100 queries, and a short prompt."""
+    _case(zp, 1, 1, 64, [4964, 4964, 100, 128, 70], seed=1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
 def test_short_prompts(zp, Hq, Hkv, d):
     """Up to 128 tokens: the form in small CTAs."""
