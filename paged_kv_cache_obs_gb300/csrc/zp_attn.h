@@ -68,7 +68,7 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
                    bool rounds = false);
 
 // Launch the tiled kernel (rows above kMaxSplitRows, and prompts), and the one that joins the parts: over the bf16 pool, the
-// 8-bit pool, or rows of packed prompts (whose a.b is the run of tokens that a copy brings: 32 or 128).
+// 8-bit pool, or rows of packed prompts (whose a.b is the run of tokens that a copy brings: 16 or 128).
 zp_status tile_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
 zp_status tile8_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
 // Packed prompts of up to 128 tokens, in small CTAs.
