@@ -71,7 +71,7 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
 // 8-bit pool, or rows of packed prompts (whose a.b is the run of tokens that a copy brings: 16 or 128).
 zp_status tile_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
 zp_status tile8_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);
-// Packed prompts of up to 128 tokens, in small CTAs.
+// Packed prompts of up to 128 tokens (256 with 64-wide heads), in small CTAs.
 bool short_prompts(const zp_params* p, int T, int B, int max_len);
 zp_status short_launch(AttnArgs a, const zp_params* p, int max_len, void* workspace, cudaStream_t st);
 zp_status tile_rows_launch(const AttnArgs& a, const zp_params* p, const TilePlan& plan, void* workspace, cudaStream_t st);

@@ -5,8 +5,9 @@
 // A prompt of a hundred tokens is one tile for the tensor cores of zp_attn_tile.cuh, whose CTA fills an SM: its loads, products,
 // softmax and stores follow one another, and nothing else is there to fill the gaps.  So here a CTA is small: 4 warps with 16
 // rows each (queries times the heads of a group), 64 tokens of keys and values at a time in 48 KB, warp-level
-// products, and several CTAs on an SM at different stages.  Bound by instructions (some 1600 a warp and tile,
-// half of them around the products) and the latency of the chain: load, S, softmax, P V, store.
+// products, and four CTAs on an SM at different stages.  Bound by instructions (1670 a warp and tile were counted, 0.45 issued a
+// cycle and scheduler, before masks, branches and the queries' addresses were made fewer: 64 prompts of 1 to 127 tokens, 32 heads on 8,
+// 36 -> 31 us; with three CTAs an SM 34) and the latency of the chain: load, S, softmax, P V, store.
 //
 // Masks, weights (P rounded to bf16, sums and maxima fp32) and what a row does not see are as in the tiled kernel.  In a tile
 // that some row does not see whole, values that are not finite would reach it as 0 * inf: such a tile, which the CTA
@@ -76,7 +77,7 @@ __device__ __forceinline__ void load_tile(const Pieces<D>& p, uint32_t to, const
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 3) short_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) short_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kTile = 64 * D * 2;
   __shared__ __align__(128) uint8_t sm[3 * kTile];
   const uint32_t sq = smem_u32(sm), sk = sq + kTile, sv = sk + kTile;
@@ -110,10 +111,21 @@ __global__ void __launch_bounds__(kThreads, 3) short_kernel(const __grid_constan
   int t0 = next_tile(-kKeys);
   {
     const uint16_t* const rows = a.q + static_cast<int64_t>(q0 + i0) * a.q_ts + static_cast<int64_t>(h * a.G) * a.q_hs;
+    if (Pieces<D>::kPer % a.G == 0) {  // a fixed step from piece to piece
+      const int i = mine.row * by_g >> 16, by = Pieces<D>::kPer * by_g >> 16;
+      const uint16_t* x = rows + i * a.q_ts + (mine.row - i * a.G) * a.q_hs + mine.ch * 8;
+      const int64_t step = by * a.q_ts;
 #pragma unroll
-    for (int u = 0; u < Pieces<D>::N; ++u) {
-      const int row = mine.row + u * Pieces<D>::kPer, i = row * by_g >> 16;
-      load_piece<WIDE>(sq + mine.at + u * Pieces<D>::kStep, rows + i * a.q_ts + (row - i * a.G) * a.q_hs + mine.ch * 8, i < queries, a.q);
+      for (int u = 0; u < Pieces<D>::N; ++u) {
+        load_piece<WIDE>(sq + mine.at + u * Pieces<D>::kStep, x, i + u * by < queries, a.q);
+        x += step;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < Pieces<D>::N; ++u) {
+        const int row = mine.row + u * Pieces<D>::kPer, i = row * by_g >> 16;
+        load_piece<WIDE>(sq + mine.at + u * Pieces<D>::kStep, rows + i * a.q_ts + (row - i * a.G) * a.q_hs + mine.ch * 8, i < queries, a.q);
+      }
     }
     if (WIDE) copies_end();
   }
@@ -149,17 +161,21 @@ __global__ void __launch_bounds__(kThreads, 3) short_kernel(const __grid_constan
     float s[kKeys / 8][4];
 #pragma unroll
     for (int x = 0; x < kKeys / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+    // two groups at a time, with the second's logits masked where no row sees it: a branch for each group and 16 dims cost more
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t qa[4];
-      ldmatrix_x4(qat + off_a[ks & 3] + (ks >> 2) * 128, qa);
+    for (int y = 0; y < kKeys / 32; ++y) {
+      if (2 * y >= groups) continue;
 #pragma unroll
-      for (int x = 0; x < kKeys / 16; ++x) {
-        if (x >= groups) continue;
-        uint32_t kb[4];  // keys 16 x .. + 7 and + 8 .. + 15, dims 16 ks .. + 7 and + 8 .. + 15
-        ldmatrix_x4(kat + off_k[ks & 3] + (ks >> 2) * 128 + x * (16 * D * 2), kb);
-        mma_16816_bf16(s[2 * x], qa, kb[0], kb[1]);
-        mma_16816_bf16(s[2 * x + 1], qa, kb[2], kb[3]);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t qa[4];
+        ldmatrix_x4(qat + off_a[ks & 3] + (ks >> 2) * 128, qa);
+#pragma unroll
+        for (int x = 2 * y; x < 2 * y + 2; ++x) {
+          uint32_t kb[4];  // keys 16 x .. + 7 and + 8 .. + 15, dims 16 ks .. + 7 and + 8 .. + 15
+          ldmatrix_x4(kat + off_k[ks & 3] + (ks >> 2) * 128 + x * (16 * D * 2), kb);
+          mma_16816_bf16(s[2 * x], qa, kb[0], kb[1]);
+          mma_16816_bf16(s[2 * x + 1], qa, kb[2], kb[3]);
+        }
       }
     }
     // softmax; the tile's maximum joins the row's
@@ -168,14 +184,21 @@ __global__ void __launch_bounds__(kThreads, 3) short_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         // columns up to `hi`, and above `lo` or below `sink`
-        const int hi = pos[e] - t0 - 2 * c, lo = a.window == 0 ? -1 : hi - a.window, sink = a.sinks - t0 - 2 * c;
+        const int hi = pos[e] - t0 - 2 * c, lo = hi - a.window, sink = a.sinks - t0 - 2 * c;
 #pragma unroll
         for (int x = 0; x < kKeys / 8; ++x) {
-          if (x / 2 >= groups) continue;
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            if (x * 8 + f > hi) s[x][2 * e + f] = -INFINITY;
+          }
+        }
+        if (a.window == 0) continue;
+#pragma unroll
+        for (int x = 0; x < kKeys / 8; ++x) {
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int col = x * 8 + f;
-            if (col > hi || (col <= lo && col >= sink)) s[x][2 * e + f] = -INFINITY;
+            if (col <= lo && col >= sink) s[x][2 * e + f] = -INFINITY;
           }
         }
       }
@@ -312,13 +335,14 @@ __global__ void __launch_bounds__(kThreads, 3) short_kernel(const __grid_constan
 
 }  // namespace
 
-// Where this form is the faster one.  64 prompts, 32 heads on 8, d 128: of 1 to 32 tokens 10.5 us and 24.6 in the tiled form, of 1 to 127 tokens
-// 36 and 43, of 96 tokens 46 and 48, of 128 tokens 64 and 51; one prompt of 128 tokens (64 CTAs) 6.6 us and 8.6.  The prompts'
-// mean length is the call's.
+// Where this form is the faster one: prompts of up to 128 tokens, 256 with 64-wide heads, whose mean length is three quarters of that or
+// less, or which leave the SMs' slots unfilled.  64 prompts, 32 heads on 8, d 128: of 1 to 32 tokens 11 us and 23 in the tiled form, of 1 to
+// 127 tokens 31 and 41, of 96 tokens 40 and 44, of 112 tokens 48 and 46, of 128 tokens 56 and 47; one prompt of 128 tokens 6.5 us and 8.4.
+// With d 64, 64 prompts, 16 heads on 2: of 128 tokens 19 us and 23, of 200 tokens 35 and 38, of 256 tokens 50 and 46.
 bool short_prompts(const zp_params* p, int T, int B, int max_len) {
-  const int64_t per = kRows / (p->num_q_heads / p->num_kv_heads);
+  const int64_t most = p->head_dim == 64 ? 256 : 128, per = kRows / (p->num_q_heads / p->num_kv_heads);
   const int64_t ctas = (max_len + per - 1) / per * p->num_kv_heads * B;
-  return max_len <= 128 && (T <= 96 * static_cast<int64_t>(B) || ctas <= 3 * plan_sms());
+  return max_len <= most && (4 * static_cast<int64_t>(T) <= 3 * most * B || ctas <= 3 * plan_sms());
 }
 
 zp_status short_launch(AttnArgs a, const zp_params* p, int max_len, void* workspace, cudaStream_t st) {

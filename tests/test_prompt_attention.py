@@ -203,6 +203,7 @@ def test_windows(zp, window, sinks):
 def test_strides(zp, form, window, sinks):
     _case(zp, 4, 2, 128, [130, 5, 70], window, sinks, form=form, seed=1, before=1, behind=3)
     _case(zp, 3, 1, 64, [200, 33], window, sinks, form=form, seed=2)
+    _case(zp, 2, 1, 64, [300, 33], window, sinks, form=form, seed=5, behind=2)
     # queries of one form with keys and values of another
     _case(zp, 4, 2, 64, [130, 5, 70], window, sinks, form=form, qform="rows", seed=3)
     _case(zp, 4, 2, 64, [130, 5, 70], window, sinks, form="rows", qform=form, seed=4)
@@ -279,6 +280,22 @@ def test_values_of_short_prompts_reach_only_the_rows_that_see_them(zp, d, window
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("form", ["rows", "odd"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 1), (16, 17), (64, 64), (65, 3), (100, 200), (130, 5), (200, 1), (7, 70), (255, 2), (3, 190)])
+def test_narrow_heads_of_up_to_256_tokens(zp, form, window, sinks):
+    """64-wide heads take the form in small CTAs up to 256 tokens: several tiles, of which a window leaves some out."""
+    _case(zp, 4, 2, 64, [200, 5, 129, 1, 256, 193], window, sinks, form=form, seed=window, before=1, behind=3)
+    _case(zp, 7, 1, 64, [255, 64, 192], window, sinks, form=form, seed=sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_values_of_narrow_heads_reach_only_the_rows_that_see_them(zp, window, sinks, value):
+    _values_case(zp, [200, 30, 256], 64, window, sinks, value, ((60, 1, 7), (150, 0, 33), (230 + 2, 0, 9), (230 + 140, 1, 60), (230 + 255, 0, 1)))
+
+
+@pytest.mark.gpu
 def test_short_rows_whose_logits_are_all_minus_infinity_are_nan(zp):
     q, k = (torch.ones((40, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     q[20:, 0] = -math.inf
@@ -301,18 +318,21 @@ def test_values_reach_only_the_rows_that_see_them(zp, window, sinks, value):
     """Bad keys and values of other prompts, of later tokens and of tokens outside the window have no effect; the
     rows that see a bad value get it in that dim."""
     _values_case(zp, [100, 90, 200], 64, window, sinks, value, ((60, 1, 7), (190 + 2, 0, 9), (190 + 150, 1, 60)))
+    _values_case(zp, [100, 90, 300], 64, window, sinks, value, ((60, 1, 7), (190 + 2, 0, 9), (190 + 250, 1, 60)))
+    _values_case(zp, [100, 90, 200], 128, window, sinks, value, ((60, 1, 7), (190 + 2, 0, 90), (190 + 150, 1, 60)))
 
 
 @pytest.mark.gpu
-def test_odd_values_of_rows_at_odd_addresses(zp):
+@pytest.mark.parametrize("n,d", [(140, 64), (300, 64), (140, 128)])
+def test_odd_values_of_rows_at_odd_addresses(zp, n, d):
     """The same where keys and values are loaded value by value: the prompt's end stands inside of a run."""
     g = torch.Generator().manual_seed(8)
-    q, k, v = _rows(g, 140, 2, 64, "rows"), _rows(g, 140, 1, 64, "odd"), _rows(g, 140, 1, 64, "odd")
-    v[130, 0, 3] = math.inf
-    out, p, ws = torch.zeros_like(q), A._params(2, 1, 64, 16), zp.new_workspace(256)
-    zp.zp_prompt_attn(q, k, v, _i32([0, 140]), out, p, ws, 140)
+    q, k, v = _rows(g, n, 2, d, "rows"), _rows(g, n, 1, d, "odd"), _rows(g, n, 1, d, "odd")
+    v[n - 10, 0, 3] = math.inf
+    out, p, ws = torch.zeros_like(q), A._params(2, 1, d, 16), zp.new_workspace(256)
+    zp.zp_prompt_attn(q, k, v, _i32([0, n]), out, p, ws, n)
     assert zp.zp_read_error(ws) == 0
-    assert bool(torch.isinf(out[130:, :, 3]).all()) and int((~torch.isfinite(out)).sum()) == 20
+    assert bool(torch.isinf(out[n - 10:, :, 3]).all()) and int((~torch.isfinite(out)).sum()) == 20
 
 
 @pytest.mark.gpu
