@@ -571,9 +571,10 @@ size_t zp_prompt_workspace_size(const zp_params* params, int32_t T, int32_t B, i
 /* zp_paged_window_attn over the 8-bit pool: attention of a chunk of new tokens (drafts, chunked prefill, a question
  * about a document in the cache), whose codes are already in the pool.  Arguments, masks and errors are
  * zp_paged_window_attn's.
- * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn.  Above:
+ * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn (weights times V scales to 11 bits
+ * down to 2^-18 of the row's largest).  Above:
  *   - keys are taken as they are; values are exact where their scale is a power of two, not below 2^-15 of the
- *     largest of the 128 tokens that are walked together, and within 2^-11 of themselves (2^-25 of that scale) otherwise;
+ *     largest of the 128 tokens that are walked together, and within 2^-10 of themselves (2^-25 of that scale) otherwise;
  *   - weights times V scales keep 11 bits down to 2^-18 of the row's largest, and 2^-29 of it is the last that counts; sums of
  *     weights are fp32;
  *   - V scales that a row sees are within 2^100 of one another; below 2^-104 they count as that, and above 2^104 values

@@ -10,9 +10,10 @@ import torch
 import test_cache_attention as A
 from oracle import serving_oracle as S
 
-# How far weights are held (f16: half a step is 2^-12 of the value, counted as 2^-11).  In the form for many rows values of
-# scales that are not powers of two are rounded too, scale and product: 2^-12 each.
-FEW, MANY = 2.0 ** -11, 2.0 ** -11 + 2.0 ** -11
+# How far weights are held: f16, half a step is 2^-11 of the value.  In the form for many rows values of scales that are not powers
+# of two are rounded too, the block's scale over the tile's and its product with the code: 2^-11 each, so p (1 + e1) v (1 + e2) (1 + e3)
+# is off by 3 * 2^-11 and terms of 2^-22.
+FEW, MANY = 2.0 ** -11, 3 * 2.0 ** -11
 
 
 @pytest.fixture(scope="module")
