@@ -38,7 +38,7 @@
 // softmax groups as they come.  P is f16, in units of 2^-15 of a reference 11 (in log2) above the largest weight times
 // scale: 11 bits down to 2^-18 of it, 2^-29 of it is the last that counts; sums of weights are fp32 throughout.
 // 4 requests of 2048 new tokens over 0 to 6144, 32 heads on 8: 532 us, 1030 TFLOP/s over the pairs that are seen.  The tensor core
-// works 41 % of the time: the softmax of a tile takes 2.3 times as long beside the warps that turn codes (without them
+// works 49 % of the time: the softmax of a tile takes 2.3 times as long beside the warps that turn codes (without them
 // the call takes 396 us), for issue slots and instruction fetches that they share.
 //
 // Measured: 4 requests of 2048 new tokens, 32 heads on 8, d 128, a window of 2048: 191 us, 1270 TFLOP/s
