@@ -560,7 +560,8 @@ size_t zp_paged_window_workspace_size(const zp_params* params, int32_t T, int32_
  *   params        num_q_heads, num_kv_heads, head_dim and scale are used.
  *   workspace     >= zp_prompt_workspace_size() bytes, 256-byte aligned.
  * A bad token_start: that prompt is not written, ZP_ERR_BAD_TABLE; ZP_ERR_TIMEOUT, weights and what a row does not
- * see as for zp_paged_window_attn's form for many rows.  Rows of k and v at other than 16-byte boundaries or
+ * see as for zp_paged_window_attn's form for many rows.  Which kernel takes a call follows from its sizes, so a row's last bit
+ * may depend on the batch.  Rows of k and v at other than 16-byte boundaries or
  * strides are loaded value by value, at a tenth of the speed.  head_dim 64 or 128, up to 16 query heads per kv head. */
 zp_status zp_prompt_attn(const zp_rows* q, const zp_rows* k, const zp_rows* v, const int32_t* token_start, int32_t T,
                          int32_t B, int32_t max_len, int32_t window, int32_t sinks, const zp_rows* out,

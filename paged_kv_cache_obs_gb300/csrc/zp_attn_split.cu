@@ -263,6 +263,7 @@ __device__ __forceinline__ int acc_at(int row, int ch) {
 // MANY: requests may have more than one query (which the bf16 form always allows).  Codes with 16 rows: three CTAs on the SM,
 // as a warp issues every fifth cycle at most (64 requests of 4 tokens over up to 8192, in clusters of 2: 136 us, 164 with two).
 constexpr int kManyCtas = 3;
+constexpr int kCtaTiles = 40;  // what a CTA costs beside its tiles, in tiles
 template <bool FP8, int D, int NT, bool MANY>
 __global__ void __launch_bounds__(kThreads, FP8 && MANY && NT == 2 ? kManyCtas : Shape<FP8, D, NT>::CTAS) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<FP8, D, NT>;
@@ -905,10 +906,12 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // rows have nearly equal work (64 requests with a window of 1024: 44.0 us as they come, 43.4 us if
 // the caller has them in order), within a wave, and past 1024 requests, where the last ones are little.
 //
-// Codes with 9 to 16 rows: slots for three CTAs an SM, over-filled by a sixth, and 4 tiles a warp.  Batches of up to one wave, or
-// two where caches are long, are shared by two CTAs a head, the long requests first, since a CTA is slow by itself: 64 requests of 4
-// tokens over up to 8192, 8 kv heads, take 136 us so and 180 unsplit; 24 requests 92 us and 140; over up to 2048 tokens 64
-// requests take 54 unsplit and 58 so.
+// Codes with 9 to 16 rows: slots for three CTAs an SM, over-filled by a sixth, and 4 tiles a warp.  Where that gives fewer than 8 CTAs a
+// head, as many as make the call shortest, the long requests first: half of the longest CTA's tiles stand alone at the end, and each
+// CTA costs kCtaTiles of a slot's time; more than 2 only within three waves.  Requests of 4 tokens, 8 kv heads of 128: 24 over up to
+// 8192 tokens take 62 us with the 4 CTAs that it takes and 87 with 2 as they come, 12 over up to 60000 228 us with 8 and 283 with 4; 64 over
+// up to 8192 134 us with 2, 149 with 4, 180 with one; 40 over up to 30000 348 us with 8 and 301 with 4; 64 over up to 2048 51 us
+// unsplit and 58 with 2.
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room, bool many8) {
   const int64_t sms = plan_sms();
   SplitPlan s{};
@@ -925,14 +928,24 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   const bool many16 = many8 && s.rows == 16;
   if (many16) {
     const int64_t slots = sms * kManyCtas;
-    n = std::min((tiles + 4 * kWarps - 1) / (4 * kWarps), slots * 7 / 6 / units);
-    if (n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
+    const int64_t most = (tiles + 4 * kWarps - 1) / (4 * kWarps);
+    n = std::min(most, slots * 7 / 6 / units);
+    if (window > 0) {
+      if (n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
+    } else if (n < 8) {
+      int64_t best = INT64_MAX;
+      for (int64_t x = 1; x <= std::min<int64_t>(most, 8) && (x <= 2 || units * x <= 3 * slots); x *= 2) {
+        const int64_t cost = tiles * slots / x + 2 * kCtaTiles * units * x;  // in halves of a tile, times the slots
+        if (cost < best) best = cost, n = x;
+      }
+    }
   }
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
   const size_t part = static_cast<size_t>(units) * s.rows * (p->head_dim + 4) * sizeof(float);  // of one cluster a row
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
   s.splits = n >= 8 ? static_cast<int>(std::max<int64_t>(1, std::min(n / 8, fit))) * 8 : s.cluster;
-  s.ordered = window == 0 && (n < 2 || (many16 && n == 2)) && units > sms * (s.rows == 16 ? 2 : 4) && B <= kMaxOrdered;
+  s.ordered = window == 0 && B <= kMaxOrdered &&
+              (many16 ? n < 8 && units * n > sms * kManyCtas : n < 2 && units > sms * (s.rows == 16 ? 2 : 4));
   const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
   s.bytes = kHeader;
   if (parts > 1) s.bytes += (parts * part + 255) / 256 * 256;
