@@ -263,7 +263,7 @@ __device__ __forceinline__ int acc_at(int row, int ch) {
 // MANY: requests may have more than one query (which the bf16 form always allows).  Codes with 16 rows: three CTAs on the SM,
 // as a warp issues every fifth cycle at most (64 requests of 4 tokens over up to 8192, in clusters of 2: 136 us, 164 with two).
 constexpr int kManyCtas = 3;
-constexpr int kCtaTiles = 40;  // what a CTA costs beside its tiles, in tiles
+constexpr int kCtaTiles = 50;  // what a CTA costs beside its tiles, in tiles
 template <bool FP8, int D, int NT, bool MANY>
 __global__ void __launch_bounds__(kThreads, FP8 && MANY && NT == 2 ? kManyCtas : Shape<FP8, D, NT>::CTAS) split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<FP8, D, NT>;
@@ -906,12 +906,13 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // rows have nearly equal work (64 requests with a window of 1024: 44.0 us as they come, 43.4 us if
 // the caller has them in order), within a wave, and past 1024 requests, where the last ones are little.
 //
-// Codes with 9 to 16 rows: slots for three CTAs an SM, over-filled by a sixth, and 4 tiles a warp.  Where that gives fewer than 8 CTAs a
-// head, as many as make the call shortest, the long requests first: half of the longest CTA's tiles stand alone at the end, and each
-// CTA costs kCtaTiles of a slot's time; more than 2 only within three waves.  Requests of 4 tokens, 8 kv heads of 128: 24 over up to
-// 8192 tokens take 62 us with the 4 CTAs that it takes and 87 with 2 as they come, 12 over up to 60000 228 us with 8 and 283 with 4; 64 over
-// up to 8192 134 us with 2, 149 with 4, 180 with one; 40 over up to 30000 348 us with 8 and 301 with 4; 64 over up to 2048 51 us
-// unsplit and 58 with 2.
+// Codes and requests of several queries, 9 to 16 rows: slots for three CTAs an SM, over-filled by a sixth, and 4 tiles a warp.  Where that, or
+// the rule above for 8 rows, gives fewer than 8 CTAs a head, as many or more as make the call shortest, the long requests first: half of the
+// longest CTA's tiles stand alone at the end, and each CTA costs kCtaTiles of a slot's time; more than 2 only within three waves.  With 8 kv heads of 128 and 16
+// rows, requests of 4 tokens: 24 over up to 8192 tokens take 62 us with the 4 CTAs that it takes and 87 with 2 as they come, 12 over up to
+// 60000 228 us with 8 and 283 with 4; 64 over up to 8192 134 us with 2, 149 with 4, 180 with one; 40 over up to 30000 348 us
+// with 8 and 301 with 4; 64 over up to 2048 51 us unsplit and 58 with 2.  8 rows, requests of 3 tokens: 64 over up to 8192 100 us with
+// 2 and 138 with one, 40 over up to 30000 209 us with 4 and 440 with one, 200 over up to 8192 244 us with one and 258 with 2.
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room, bool many8) {
   const int64_t sms = plan_sms();
   SplitPlan s{};
@@ -925,19 +926,16 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * p->num_kv_heads);
   const int64_t wave = sms * (s.rows == 16 ? 2 : 4) * 7 / 8;
   int64_t n = std::min((tiles + 2 * kWarps - 1) / (2 * kWarps), wave / units);
-  const bool many16 = many8 && s.rows == 16;
-  if (many16) {
-    const int64_t slots = sms * kManyCtas;
-    const int64_t most = (tiles + 4 * kWarps - 1) / (4 * kWarps);
+  const int64_t slots = sms * (s.rows == 16 ? kManyCtas : 4), most = (tiles + 4 * kWarps - 1) / (4 * kWarps);  // codes
+  if (many8 && s.rows == 16) {
     n = std::min(most, slots * 7 / 6 / units);
-    if (window > 0) {
-      if (n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
-    } else if (n < 8) {
-      int64_t best = INT64_MAX;
-      for (int64_t x = 1; x <= std::min<int64_t>(most, 8) && (x <= 2 || units * x <= 3 * slots); x *= 2) {
-        const int64_t cost = tiles * slots / x + 2 * kCtaTiles * units * x;  // in halves of a tile, times the slots
-        if (cost < best) best = cost, n = x;
-      }
+    if (window > 0 && n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
+  }
+  if (many8 && window == 0 && n < 8) {
+    int64_t best = INT64_MAX;
+    for (int64_t x = n >= 4 ? 4 : n >= 2 ? 2 : 1; x == 1 || (x <= std::min<int64_t>(most, 8) && (x <= 2 || units * x <= 3 * slots)); x *= 2) {
+      const int64_t cost = tiles * slots / x + 2 * kCtaTiles * units * x;  // in halves of a tile, times the slots
+      if (cost < best) best = cost, n = x;
     }
   }
   s.cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
@@ -945,7 +943,7 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   const int64_t fit = room > kHeader ? static_cast<int64_t>(std::min<size_t>((room - kHeader) / part, INT_MAX)) : 0;
   s.splits = n >= 8 ? static_cast<int>(std::max<int64_t>(1, std::min(n / 8, fit))) * 8 : s.cluster;
   s.ordered = window == 0 && B <= kMaxOrdered &&
-              (many16 ? n < 8 && units * n > sms * kManyCtas : n < 2 && units > sms * (s.rows == 16 ? 2 : 4));
+              (many8 ? n < 8 && units * n > slots : n < 2 && units > sms * (s.rows == 16 ? 2 : 4));
   const int parts = s.splits / s.cluster;  // does not fall as tiles grow, so a window never needs more
   s.bytes = kHeader;
   if (parts > 1) s.bytes += (parts * part + 255) / 256 * 256;
