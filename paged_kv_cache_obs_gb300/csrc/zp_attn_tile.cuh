@@ -104,7 +104,7 @@ struct ListedTile {
   int z[8];               // of each block: the pool's (layer, block), or past its end
   uint16_t k[8], v[8];    // for each 16 tokens: what codes are multiplied by, in f16
   float k_rest[8];        // and what K's logits are besides, where k_odd
-  float k_scale, v_log, v_inv;  // of the whole tile: K's scale; V's, a power of two: its log2, and 2^-kGain over it
+  float k_scale, v_log, v_inv;  // of the whole tile: K's scale; V's, a power of two: its log2 (-inf: all values are 0), and 2^-kGain over it
   int row;                // of K in a block
   int what;               // V's: kPlainTile, ...
   int k_odd;
@@ -799,7 +799,6 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
     int q_loads = 0;              // items whose queries were
     uint64_t* last[kStages] = {};  // barrier of each stage's last tile, and how often each was used
     uint32_t used_full = 0, used_mixed = 0, last_parity = 0;  // bits by stage
-    int v_exp = 0;                 // codes: log2 of V's scale of the tile
     for (int item = blockIdx.x; go && item < items; item = next_item(item)) {
       const Raw now = raw;
       raw = load_raw<SRC>(a, next_item(item), items);
@@ -881,7 +880,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
           // least the largest, from 2^-104 to 2^104 (sums of weights are divided by it).
           const float k_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(k_scale))));
           const uint32_t v_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v_scale)));
-          if (v_bits != 0) v_exp = min(max(static_cast<int>(v_bits >> 23) - 127 + ((v_bits & 0x7FFFFFu) != 0), -104), 104);  // values of 0: as before
+          const int v_exp = v_bits == 0 ? 0 : min(max(static_cast<int>(v_bits >> 23) - 127 + ((v_bits & 0x7FFFFFu) != 0), -104), 104);
           const float k_all = k_top > 0.0f ? k_top : 1.0f, k_of = k_scale / k_all;
           const float v_of = v_scale * __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
           const bool odd = __any_sync(0xffffffffu, k_of != 0.0f && ((__float_as_uint(k_of) & 0x7FFFFFu) != 0 || fabsf(k_of) < 0x1p-15f));
@@ -896,7 +895,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
           }
           if (lane == 0) {
             e.k_scale = k_all;
-            e.v_log = static_cast<float>(v_exp);
+            e.v_log = v_bits == 0 ? -INFINITY : static_cast<float>(v_exp);
             e.v_inv = __uint_as_float(static_cast<uint32_t>(127 - v_exp - static_cast<int>(kGain)) << 23);
             e.row = w.h * a.b;
             e.what = mixed_tile(w, j) ? kMixedTile : kPlainTile;
@@ -1203,6 +1202,13 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
         const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (kCodes<SRC> && v_log == -INFINITY) {
+          // Values of 0 count in the sum of weights alone, so any power of two may stand for their scale: the row's own, that
+          // which leaves its reference where it is, or the least where it has none yet.  (One of the item, or of what the CTA had
+          // before, set references that the row's other values were lost beside.)
+          v_log = fmaxf(fminf(floorf(m - kLazyCodes - all * sl2), 104.0f), -104.0f);
+          v_inv = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(v_log) - static_cast<int>(kGain)) << 23);
+        }
         const float top = kCodes<SRC> ? fmaf(all, sl2, v_log) : all * a.sl2;
         if (__any_sync(0xffffffffu, top > m)) {
           const float mn = fmaxf(m, top + (kCodes<SRC> ? kLazyCodes : kLazy)), corr = m == -INFINITY ? 0.0f : ex2(m - mn);

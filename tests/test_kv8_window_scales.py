@@ -1,0 +1,173 @@
+"""Scales of the 8-bit pool in zp_kv8_window_attn: values of 0, scales far from one another, factors of the logits that leave fp32;
+against 64 bits and, for scales that are powers of two, to the bits that weights are held to."""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import test_cache_attention as A
+from oracle import serving_oracle as S
+
+F16 = 2.0 ** -11        # half a step of the weights, relative to them
+
+
+@pytest.fixture(scope="module")
+def zp():
+    from paged_kv_cache_obs_gb300 import build
+    if not os.path.exists(build.LIB):
+        build.build()
+    from paged_kv_cache_obs_gb300 import zipage
+    return zipage
+
+
+def _i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32).cuda()
+
+
+def _codes(rng, shape):
+    return S.e4m3_encode(np.clip(rng.standard_normal(shape) * 64, -448, 448))
+
+
+def _attend(zp, codes, scales, q, new, lens, tables, p, window=0, sinks=0):
+    """Outputs of one call over layer 0 (a second call gives the same bits)."""
+    T, B, mq = q.shape[0], len(lens), max(new)
+    ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, T, B, mq, tables.shape[1], window, sinks))
+    start = _i32(np.concatenate([[0], np.cumsum(new)]))
+    outs = [torch.full_like(q, 7.0) for _ in range(2)]
+    for out in outs:
+        zp.zp_kv8_window_attn(codes, scales, 0, q, start, tables, _i32(lens), out, p, ws, window, sinks, mq)
+    assert zp.zp_read_error(ws) == 0 and torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+    return outs[0]
+
+
+def _walked(scale, i0, n, L, window, sinks, G, b):
+    """For queries i0 .. of an item and the V scales of a request's blocks: the largest of the 128 tokens that are walked together with
+    each token, as a power of two at or above it (2^-104 at least), [L]."""
+    first = max(0, L - n + i0 - window + 1) if window else 0
+    last = min(n, i0 + 2 * (128 // G)) - 1 + L - n
+    lo = first // b
+    listed = list(range(min(-(-min(sinks, L) // b), lo))) + list(range(lo, last // b + 1))
+    out = np.full(-(-L // b), 2.0 ** -104)
+    for i in range(0, len(listed), 128 // b):
+        part = listed[i:i + 128 // b]
+        out[part] = max(2.0 ** -104, 2.0 ** np.ceil(np.log2(max(float(abs(scale[part]).max()), 2.0 ** -104))))
+    return torch.from_numpy(np.repeat(out, b)[:L].copy()).cuda()
+
+
+def _check(codes, scales, table, q, got, L, window, sinks, p, where, tiled=True):
+    """One request's rows against 64 bits: the output's rounding; weights to half a step of f16, and what fp32 sums add; and
+    weights times the largest V scale S_t of the 128 tokens walked together, W_t, which end at 2^-29 of the row's largest W: each token
+    below is off by as much of its value over S_t."""
+    n, Hq, d = q.shape
+    Hkv, b = p["num_kv_heads"], p["block_size"]
+    G = Hq // Hkv
+    pos, t = torch.arange(L - n, L, device="cuda")[:, None], torch.arange(L, device="cuda")
+    see = (t <= pos) & ((t > pos - window) | (t < sinks) | (window == 0))
+    ids = table[:-(-L // b)].long()
+    worst = 0.0
+    for h in range(Hkv):
+        k, v = ((codes[ids, i, h].view(torch.float8_e4m3fn).double() * scales[ids, i, h].double()[:, None, None]).reshape(-1, d)[:L] for i in (0, 1))
+        v_scale = scales[ids, 1, h].cpu().numpy().astype(np.float64)
+        for g in range(h * G, (h + 1) * G):
+            w = torch.softmax((p["scale"] * (q[:, g].double() @ k.T)).masked_fill(~see, -torch.inf), -1)
+            want, mass = w @ v, w @ v.abs()
+            tol = 2.0 ** -8 * want.abs() + (F16 + 2.0 ** -14) * mass + 1e-38
+            step = 2 * (128 // G) if tiled else n
+            for i0 in range(0, n, step):
+                rows = slice(i0, i0 + step)
+                top = _walked(v_scale, i0, n, L, window, sinks, G, b)
+                tol[rows] += 2.0 ** -29 * (w[rows] * top).amax(-1, keepdim=True) * (see[rows].double() @ (v.abs() / top[:, None]))
+            err = (got[:, g].double() - want).abs()
+            assert bool((err <= tol).all()), (where, h, g, float((err / tol).max()))
+            worst = max(worst, float((err / tol).max()))
+    return worst
+
+
+# ------------------------------------------------------------------ values of 0 ---------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exp", [-8, -30, -60])
+@pytest.mark.parametrize("d,b,zeros", [(128, 16, 128), (64, 32, 256), (64, 16, 128), (128, 32, 300)])
+def test_values_of_zero_first(zp, d, b, zeros, exp):
+    """Tokens whose values are 0 (scale 0, as the library writes it) come first, then values of 2^exp."""
+    rng = np.random.default_rng(zeros)
+    Hq, Hkv, new, L = 4, 2, 70, 700
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, Hkv, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))
+    scales[0, :, 1] = 2.0 ** exp
+    scales[0, tables[0, :zeros // b], 1] = 0
+    codes[0, tables[0, :zeros // b], 1] = 0
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p = A._params(Hq, Hkv, d, b)
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(), torch.from_numpy(tables).cuda()
+    for window, sinks in ((0, 0), (500, 20)):
+        got = _attend(zp, c, s, q, [new], [L], dt, p, window, sinks)
+        _check(c[0], s[0], dt[0], q, got, L, window, sinks, p, (exp, window))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exp", [-8, -30, -60])
+def test_values_of_zero_first_behind_a_request_of_large_ones(zp, exp):
+    """CTAs take a request with scales of 2^20 and then one that begins with values of 0: its rows are those of a call by itself."""
+    rng = np.random.default_rng(7)
+    B, d, b, new, L = 330, 64, 16, 20, 300
+    per = -(-L // b)
+    codes = torch.from_numpy(_codes(rng, (1, B * per, 2, 1, b, d))).cuda()
+    scales = torch.full((1, B * per, 2, 1), 2.0 ** -6, device="cuda")
+    tables = torch.from_numpy(rng.permutation(B * per).reshape(B, per).astype(np.int32)).cuda()
+    last = list(range(B // 2, B))
+    scales[0, tables[:B // 2].long().flatten(), 1] = 2.0 ** 20
+    scales[0, tables[last].long().flatten(), 1] = 2.0 ** exp
+    scales[0, tables[last, :8].long().flatten(), 1] = 0.0
+    q = torch.from_numpy(rng.standard_normal((B * new, 2, d)) * 2).to(torch.bfloat16).cuda()
+    p = A._params(2, 1, d, b)
+    got = _attend(zp, codes, scales, q, [new] * B, [L] * B, tables, p)
+    for r in [0, 5] + last[::9] + [B - 1]:
+        rows = slice(r * new, (r + 1) * new)
+        _check(codes[0], scales[0], tables[r], q[rows], got[rows], L, 0, 0, p, r)
+        alone = _attend(zp, codes, scales, q[rows].contiguous(), [new], [L], tables[r:r + 1], p)
+        assert torch.equal(alone, got[rows])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,b", [(128, 32), (64, 16)])
+@pytest.mark.parametrize("exp", [-8, -30, -60])
+def test_values_of_zero_first_for_some_rows(zp, d, b, exp):
+    """A window: the first rows see values of 2^20, the others begin with values of 0 and go on with 2^exp."""
+    rng = np.random.default_rng(b)
+    Hq, new, L, window = 2, 240, 520, 140
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, 1, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, 1))
+    # the item's list starts at the window of position 280: its tiles of 128 tokens are 128 .. 255, 256 .. 383 and so on
+    scales[0, tables[0, :256 // b], 1] = 2.0 ** 20
+    scales[0, tables[0, 256 // b:384 // b], 1] = 0
+    scales[0, tables[0, 384 // b:], 1] = 2.0 ** exp
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p = A._params(Hq, 1, d, b)
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(), torch.from_numpy(tables).cuda()
+    got = _attend(zp, c, s, q, [new], [L], dt, p, window)
+    _check(c[0], s[0], dt[0], q, got, L, window, 0, p, exp)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [4, 60])
+def test_values_of_zero_alone(zp, new):
+    """All of a row's values are 0; and values of 0 behind others count in the sum of weights alone."""
+    rng = np.random.default_rng(new)
+    Hq, d, b, L = 4, 128, 16, 600
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, 1, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, 1))
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p, c, dt = A._params(Hq, 1, d, b), torch.from_numpy(codes).cuda(), torch.from_numpy(tables).cuda()
+    scales[0, :, 1] = 0
+    s = torch.from_numpy(scales.astype(np.float32)).cuda()
+    assert bool((_attend(zp, c, s, q, [new], [L], dt, p) == 0).all())
+    for large in (2.0 ** -90, 1.0, 2.0 ** 90):
+        scales[0, tables[0, :8], 1] = large
+        s = torch.from_numpy(scales.astype(np.float32)).cuda()
+        got = _attend(zp, c, s, q, [new], [L], dt, p)
+        _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, large, tiled=4 * new > 16)
