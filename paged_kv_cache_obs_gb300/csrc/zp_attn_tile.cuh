@@ -54,6 +54,7 @@
 #include "zp_attn.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cstddef>
 #include <type_traits>
@@ -1174,7 +1175,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
           if (!ok) break;
           ++scale_tile;
           const ListedTile& e = s.list[slot];
-          sl2 *= e.k_scale * gain;
+          // a normal number: 0 (queries of 0 beside small keys) or infinity would make NaN of what a row does not see, or of logits of 0
+          sl2 = fminf(fmaxf(sl2 * (e.k_scale * gain), FLT_MIN), FLT_MAX);
           v_log = e.v_log;
           v_inv = e.v_inv;
           if (e.k_odd) {

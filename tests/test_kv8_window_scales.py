@@ -171,3 +171,46 @@ def test_values_of_zero_alone(zp, new):
         s = torch.from_numpy(scales.astype(np.float32)).cuda()
         got = _attend(zp, c, s, q, [new], [L], dt, p)
         _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, large, tiled=4 * new > 16)
+
+
+# ------------------------------------------------------------------ factors of the logits -----
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [3, 20, 150])
+@pytest.mark.parametrize("d,b", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -100, 2.0 ** -126])
+def test_queries_of_zero_and_small_keys(zp, d, b, new, size):
+    """Logits of 0, or as good as: rows are the means of what they see, however small the keys' scales are."""
+    rng = np.random.default_rng(new)
+    Hq, Hkv, L = 4, 2, 400 + new
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, Hkv, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))
+    q = (torch.from_numpy(rng.standard_normal((new, Hq, d))).double() * size).to(torch.bfloat16).cuda()
+    p = A._params(Hq, Hkv, d, b)
+    c, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(tables).cuda()
+    for k_scale in (2.0 ** -20, 2.0 ** -24, 2.0 ** -60, 2.0 ** -126):
+        scales[0, :, 0] = k_scale
+        s = torch.from_numpy(scales.astype(np.float32)).cuda()
+        for window, sinks in ((0, 0), (150, 20)):
+            got = _attend(zp, c, s, q, [new], [L], dt, p, window, sinks)
+            _check(c[0], s[0], dt[0], q, got, L, window, sinks, p, (size, k_scale, window), tiled=2 * new > 16)
+
+
+@pytest.mark.gpu
+def test_queries_and_keys_whose_factor_is_beyond_fp32(zp):
+    """Queries of 2^110 where the keys are 0: logits are 0, not 0 times infinity."""
+    rng = np.random.default_rng(3)
+    d, b, new, L = 128, 16, 40, 300
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, 1, b, d))
+    codes[0, :, 0, :, :, :64] = 0
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, 1))
+    scales[0, :, 0] = 2.0 ** 60
+    q = torch.zeros((new, 4, d))
+    q[:, :, :64] = torch.from_numpy(rng.standard_normal((new, 4, 64))) * 2.0 ** 110
+    q = q.to(torch.bfloat16).cuda()
+    p = A._params(4, 1, d, b)
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(), torch.from_numpy(tables).cuda()
+    got = _attend(zp, c, s, q, [new], [L], dt, p)
+    _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, "large")
