@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
         const int i = place_of(taken, n, j);
         a.tables[static_cast<int64_t>(base + i) * a.max_blocks + blocks_of(a, cached[i]) + j - taken[i]] = free_id(j);
       }
+      // unsigned: what comes behind the last row may pass 2^31
 #pragma unroll 2
-      for (int t = start[0] + me; t < start[n]; t += all) {
-        const int i = place_of(start, n, t), k = t - start[i], p = cached[i] + k, j = (p >> a.bshift) - blocks_of(a, cached[i]);
+      for (uint32_t u = static_cast<uint32_t>(start[0]) + static_cast<uint32_t>(me); u < static_cast<uint32_t>(start[n]); u += static_cast<uint32_t>(all)) {
+        const int t = static_cast<int>(u), i = place_of(start, n, t), k = t - start[i], p = cached[i] + k, j = (p >> a.bshift) - blocks_of(a, cached[i]);
         const int blk = j < 0 ? held[i] : free_id(taken[i] + j);
         const bool out = blk < 0 || blk >= a.num_blocks;
         bad |= out;
