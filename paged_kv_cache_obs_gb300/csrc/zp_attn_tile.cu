@@ -27,12 +27,19 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
   } else {
     // As many as make the longest CTA's share shortest, in tiles: a part costs about 3 beside its own, and where there are
     // several 2 more for its sums.  64 items of up to 783 tiles take 547 us with 7 splits (3 parts a CTA) and 753 with 2 (one each).
-    int64_t best = INT64_MAX;
-    for (int64_t n = 1; n <= std::min<int64_t>(most_splits, 32); ++n) {
+    // Where items fill the SMs by themselves, the fewest that come within 5 % of it: lengths are at most the table's width, and
+    // every further part's sums are written and read for the last wave's rounding alone (4 x 2048 tokens over up to 8192, 1024 items:
+    // 529 us unsplit; with the 4 parts that a table for 65536 or more tokens gave, 848 us and a workspace of 554 MB).
+    const int64_t most_parts = std::min<int64_t>(most_splits, 32);
+    const auto cost = [&](int64_t n) {
       const int64_t parts = (std::max<int64_t>(items, 1) * n + plan.ctas - 1) / plan.ctas;  // of a CTA
-      const int64_t cost = parts * ((tiles + n - 1) / n + (n > 1 ? 5 : 3));
-      if (cost < best) best = cost, plan.splits = static_cast<int>(n);
-    }
+      return parts * ((tiles + n - 1) / n + (n > 1 ? 5 : 3));
+    };
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= most_parts; ++n)
+      if (cost(n) < best) best = cost(n), plan.splits = static_cast<int>(n);
+    if (items >= plan.ctas)
+      for (plan.splits = 1; 20 * cost(plan.splits) > 21 * best;) ++plan.splits;
   }
   plan.nx = static_cast<int>(std::min<int64_t>(nx, INT_MAX));
   plan.items = nx * heads * plan.splits;
