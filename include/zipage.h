@@ -414,7 +414,8 @@ zp_status zp_rope_apply_axes(const zp_rope_axes* axes, const zp_rows* q, const z
  *   block_tables    device int32 [B][max_blocks].  The call writes the entries of blocks whose first token is
  *                   new, and reads those of part-full blocks that get tokens; no others.
  *                   Where tokens were taken back since (rejected drafts), a block that they had begun counts as
- *                   new: it gets another id, and the old one is the caller's to hand out again.
+ *                   new: it gets another id, and the old one is the caller's to hand out again
+ *                   (zp_step_slots_held uses it).
  *   token_start     device int32 [B + 1], written: request r owns rows token_start[r] .. token_start[r + 1] - 1.
  *   seq_lens        device int32 [B], written: cached + new.  May be `cached` itself; no other arrays overlap.
  *   positions       device int32 [T] or NULL, written.  Rows behind the last request's: 0.
@@ -433,6 +434,19 @@ zp_status zp_step_slots(const int32_t* cached, const int32_t* new_tokens, const 
                         int32_t* block_tables, int32_t max_blocks, int32_t* token_start, int32_t* seq_lens,
                         int32_t* positions, int32_t* slots, int32_t T, const zp_params* params, void* workspace,
                         size_t workspace_bytes, zp_stream stream);
+
+/* The same where tokens are taken back between steps (rejected drafts, cached[r] lowered): blocks that they had begun stay
+ * the request's, and its next tokens go there.
+ *   held_blocks     device int32 [B] or NULL (as zp_step_slots): how many entries of request r's table hold blocks, at least
+ *                   those of its cached tokens.  The call reads entries of those blocks that get tokens, takes free ids
+ *                   for the blocks behind them alone, and advances held_blocks[r] by those.  Blocks that are given back lower it.
+ * A request whose held_blocks is below its cached tokens' blocks or above max_blocks takes part without tokens,
+ * ZP_ERR_BAD_TABLE.  A step that does not fit leaves held_blocks as they are. */
+zp_status zp_step_slots_held(const int32_t* cached, const int32_t* new_tokens, const int32_t* first_pos, int32_t* held_blocks,
+                             int32_t B, const int32_t* free_ids, int32_t num_free, int32_t* free_at, int64_t num_blocks,
+                             int32_t* block_tables, int32_t max_blocks, int32_t* token_start, int32_t* seq_lens,
+                             int32_t* positions, int32_t* slots, int32_t T, const zp_params* params, void* workspace,
+                             size_t workspace_bytes, zp_stream stream);
 
 /* New keys and values of one layer into the bf16 pool, bit for bit.
  *   k, v            rows [T][num_kv_heads][head_dim]

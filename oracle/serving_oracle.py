@@ -74,30 +74,39 @@ def rope_axes(x, positions, rotary_dim, theta, sections, layout, interleaved, sc
 # ------------------------------------------------------------------ a step's slots -----------
 
 
-def step_slots(cached, new, free, tables, b, T, num_blocks, first=None, free_at=0):
-    """(tables, token_start, seq_lens, positions, slots, free_at, error) of a step, a token at a time; error is None,
-    "table" or "blocks"."""
+def step_slots(cached, new, free, tables, b, T, num_blocks, first=None, free_at=0, held=None):
+    """(tables, token_start, seq_lens, positions, slots, free_at, error) of a step, a token at a time, and the blocks held after it
+    where they are given; error is None, "table" or "blocks"."""
     B, capacity = len(cached), tables.shape[1] * b
-    had, add, error = [], [], None
+    had, add, have, error = [], [], [], None
     for r in range(B):
         c, n = int(cached[r]), int(new[r])
         good = 0 <= c <= capacity
         if not good or n < 0 or c + n > capacity:
             error, n = "table", 0
-        had.append(c if good else 0)
+        c = c if good else 0
+        h = -(-c // b)
+        if held is not None:
+            if not h <= held[r] <= tables.shape[1]:
+                error, n = "table", 0
+            h = int(held[r])
+        had.append(c)
         add.append(n)
-    need = sum(-(-(c + n) // b) - -(-c // b) for c, n in zip(had, add))
+        have.append(h)
+    need = sum(max(0, -(-(c + n) // b) - h) for c, n, h in zip(had, add, have) if n)
+    after = () if held is None else (have,)
     if not 0 <= free_at <= len(free) or sum(add) > T or need > len(free) - free_at:
         if error is None:
             error = "table" if not 0 <= free_at <= len(free) or sum(add) > T else "blocks"
-        return tables, [0] * (B + 1), had, [0] * T, [-1] * T, free_at, error
+        return (tables, [0] * (B + 1), had, [0] * T, [-1] * T, free_at, error) + after
     tables, start, positions, slots = tables.copy(), [0], [], []
     for r in range(B):
         for i in range(add[r]):
             p = had[r] + i
-            if p % b == 0:
+            if p // b == have[r]:
                 tables[r, p // b] = free[free_at]
                 free_at += 1
+                have[r] += 1
             block = int(tables[r, p // b])
             inside = 0 <= block < num_blocks
             if not inside:
@@ -106,7 +115,7 @@ def step_slots(cached, new, free, tables, b, T, num_blocks, first=None, free_at=
             positions.append((had[r] if first is None else int(first[r])) + i)
         start.append(len(slots))
     rest = T - len(slots)
-    return tables, start, [c + n for c, n in zip(had, add)], positions + [0] * rest, slots + [-1] * rest, free_at, error
+    return (tables, start, [c + n for c, n in zip(had, add)], positions + [0] * rest, slots + [-1] * rest, free_at, error) + after
 
 
 # ------------------------------------------------------------------ 8-bit cache --------------

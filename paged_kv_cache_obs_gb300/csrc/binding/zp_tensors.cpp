@@ -28,7 +28,7 @@ struct Library {
   decltype(&zp_kv8_decode_attn) kv8_decode_attn;
   decltype(&zp_paged_window_attn) paged_window_attn;
   decltype(&zp_rope_apply_axes) rope_apply_axes;
-  decltype(&zp_step_slots) step_slots;
+  decltype(&zp_step_slots_held) step_slots_held;
   decltype(&zp_kv_append) kv_append;
   decltype(&zp_prompt_attn) prompt_attn;
   decltype(&zp_kv8_window_attn) kv8_window_attn;
@@ -183,8 +183,8 @@ PyObject* rope_apply_axes(PyObject* const* a) {
 }
 
 // cached, new_tokens, first_pos, free_ids, free_at, num_blocks, block_tables, token_start, seq_lens, positions, slots, params,
-// workspace, stream
-PyObject* step_slots(PyObject* const* a) {
+// workspace, stream, held_blocks
+PyObject* step_slots_held(PyObject* const* a) {
   const zp_params& p = *address<const zp_params>(a[11]);
   const int dev = device_of(tensor(a[10]));
   const int32_t B = count(a[0], "cached [requests]"), T = count(a[10], "slots [tokens]"), free = count(a[3], "free block ids");
@@ -194,14 +194,14 @@ PyObject* step_slots(PyObject* const* a) {
   int32_t max_blocks;
   const int32_t* const tables = table(a[6], dev, B, max_blocks);
   const int32_t *const start = entries(a[7], dev, static_cast<int64_t>(B) + 1), *const lens = entries(a[8], dev, B);
-  const int32_t *const pos = optional(a[9], T), *const slots = entries(a[10], dev, T);
+  const int32_t *const pos = optional(a[9], T), *const slots = entries(a[10], dev, T), *const held = optional(a[14], B);
   const int64_t blocks = i64(a[5]);
   size_t bytes;
   void* const ws = workspace(a[12], dev, bytes);
   const zp_stream st = stream(a[13], dev);
   const auto out = [](const int32_t* x) { return const_cast<int32_t*>(x); };
   return call([&] {
-    return lib.step_slots(cached, more, first, B, ids, free, out(at), blocks, out(tables), max_blocks, out(start), out(lens), out(pos),
+    return lib.step_slots_held(cached, more, first, out(held), B, ids, free, out(at), blocks, out(tables), max_blocks, out(start), out(lens), out(pos),
                           out(slots), T, &p, ws, bytes, st);
   });
 }
@@ -353,7 +353,7 @@ PyObject* bind(PyObject* const* a) {
   lib.kv8_decode_attn = reinterpret_cast<decltype(lib.kv8_decode_attn)>(address<void>(a[4]));
   lib.paged_window_attn = reinterpret_cast<decltype(lib.paged_window_attn)>(address<void>(a[5]));
   lib.rope_apply_axes = reinterpret_cast<decltype(lib.rope_apply_axes)>(address<void>(a[6]));
-  lib.step_slots = reinterpret_cast<decltype(lib.step_slots)>(address<void>(a[7]));
+  lib.step_slots_held = reinterpret_cast<decltype(lib.step_slots_held)>(address<void>(a[7]));
   lib.kv_append = reinterpret_cast<decltype(lib.kv_append)>(address<void>(a[8]));
   lib.prompt_attn = reinterpret_cast<decltype(lib.prompt_attn)>(address<void>(a[9]));
   lib.kv8_window_attn = reinterpret_cast<decltype(lib.kv8_window_attn)>(address<void>(a[10]));
@@ -391,7 +391,7 @@ PyMethodDef methods[] = {def<bind, 11>("bind"),
                          def<kv8_decode_attn, 12>("kv8_decode_attn"),
                          def<paged_window_attn, 13>("paged_window_attn"),
                          def<rope_apply_axes, 7>("rope_apply_axes"),
-                         def<step_slots, 14>("step_slots"),
+                         def<step_slots_held, 15>("step_slots_held"),
                          def<kv_append, 8>("kv_append"),
                          def<prompt_attn, 11>("prompt_attn"),
                          def<kv8_window_attn, 14>("kv8_window_attn"),

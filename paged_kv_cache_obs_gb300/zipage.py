@@ -48,7 +48,7 @@ class _Tensors:
     become attributes here."""
 
     _ENTRIES = ("rope_apply", "kv8_append", "kv8_pack_blocks", "kv8_unpack_blocks", "kv8_decode_attn", "paged_window_attn",
-                "rope_apply_axes", "step_slots", "kv_append", "prompt_attn", "kv8_window_attn")
+                "rope_apply_axes", "step_slots_held", "kv_append", "prompt_attn", "kv8_window_attn")
 
     def __getattr__(self, name):
         if name not in self._ENTRIES:
@@ -169,6 +169,8 @@ _sig("zp_rope_axes_init", _I32, [ctypes.POINTER(zp_rope_config), ctypes.POINTER(
 _sig("zp_rope_apply_axes", _I32, [ctypes.POINTER(zp_rope_axes), _ROWS, _ROWS, _I32, _ROWS, _ROWS, _I32, _P, _I64, _I32, _P])
 _sig("zp_step_slots", _I32, [_P, _P, _P, _I32, _P, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _I32, ctypes.POINTER(zp_params),
                              _P, _SZ, _P])
+_sig("zp_step_slots_held", _I32, [_P, _P, _P, _P, _I32, _P, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _I32, ctypes.POINTER(zp_params),
+                                  _P, _SZ, _P])
 _sig("zp_kv_append", _I32, [ctypes.POINTER(zp_kv_pool), _I32, _ROWS, _ROWS, _P, _I32, ctypes.POINTER(zp_params), _P, _SZ, _P])
 _sig("zp_kv8_append", _I32, [ctypes.POINTER(zp_kv8_pool), _I32, _ROWS, _ROWS, _I32, _P, _P, _I32, _P, _I32,
                              ctypes.POINTER(zp_params), _P, _SZ, _P])
@@ -446,14 +448,15 @@ def zp_rope_apply_axes(axes: zp_rope_axes, q, k, positions, q_out=None, k_out=No
 
 
 def zp_step_slots(cached, new_tokens, free_ids, block_tables, token_start, seq_lens, slots, params, workspace, num_blocks: int,
-                  positions=None, first_pos=None, free_at=None, stream=None):
+                  positions=None, first_pos=None, free_at=None, stream=None, held_blocks=None):
     """The blocks, slots and positions of a step from its requests' lengths, all device int32: reads cached [B],
     new_tokens [B], free_ids [n] (from free_at [1] on, which advances) and first_pos [B]; writes token_start [B + 1],
     seq_lens [B] (may be cached), slots [T], positions [T] and the new entries of block_tables [B, max_blocks].
-    num_blocks: blocks of the pool (see include/zipage.h)."""
+    num_blocks: blocks of the pool.  held_blocks [B]: how many blocks each table holds, read and advanced, so that those of
+    drafts that were taken back are used again (zp_step_slots_held; see include/zipage.h)."""
     p = _params(params)
-    st = _t.step_slots(cached, new_tokens, first_pos, free_ids, free_at, num_blocks, block_tables, token_start, seq_lens, positions, slots,
-                       _addr(p), workspace, _raw(stream))
+    st = _t.step_slots_held(cached, new_tokens, first_pos, free_ids, free_at, num_blocks, block_tables, token_start, seq_lens, positions, slots,
+                            _addr(p), workspace, _raw(stream), held_blocks)
     if st:
         _check("zp_step_slots", st)
 
