@@ -465,7 +465,7 @@ zp_status zp_kv_append(const zp_kv_pool* pool, int32_t layer, const zp_rows* k, 
  * block of zeros).  With such a scale dividing by it is exact, so a code is off by E4M3's own
  * rounding only, reading back to bf16 is exact, and a scale that grows later keeps every code
  * that stays in E4M3's normal range.  Values that are not finite are stored as E4M3's NaN.
- * zp_kv8_unpack_blocks and zp_kv8_decode_attn take any finite scales. */
+ * zp_kv8_unpack_blocks and zp_kv8_decode_attn take any finite scales, zp_kv8_window_attn those that it names. */
 typedef struct zp_kv8_pool {
   void* codes;            /* device, 16-byte aligned */
   float* scales;          /* device [num_layers][num_blocks][2][num_kv_heads] */
@@ -586,14 +586,16 @@ size_t zp_prompt_workspace_size(const zp_params* params, int32_t T, int32_t B, i
 /* zp_paged_window_attn over the 8-bit pool: attention of a chunk of new tokens (drafts, chunked prefill, a question
  * about a document in the cache), whose codes are already in the pool.  Arguments, masks and errors are
  * zp_paged_window_attn's.
- * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn (weights times V scales to 11 bits
- * down to 2^-18 of the row's largest).  Above:
+ * Scales are finite, and V scales other than 0 of the blocks that a request's new tokens see are within 2^100 of one another.
+ * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn (weights to 11 bits down to 2^-18 of the
+ * row's largest, whatever their V scales).  Above:
  *   - keys are taken as they are; values are exact where their scale is a power of two, not below 2^-15 of the
  *     largest of the 128 tokens that are walked together, and within 2^-10 of themselves (2^-25 of that scale) otherwise;
- *   - weights times V scales keep 11 bits down to 2^-18 of the row's largest, and 2^-29 of it is the last that counts; sums of
- *     weights are fp32;
- *   - V scales that a row sees are within 2^100 of one another; below 2^-104 they count as that, and above 2^104 values
- *     may overflow. */
+ *   - a weight times the largest V scale of those 128 tokens (as a power of two) keeps 11 bits down to 2^-18 of the row's
+ *     largest such product, and 2^-29 of it is the last that counts: a row whose largest weight stands beside V scales 2^15 times
+ *     its own has 15 powers of two less for the others.  Sums of weights are fp32;
+ *   - V scales below 2^-104 count as that (values of 0, with scales of 0, in the sum of weights alone), and above 2^104 values may
+ *     overflow. */
 zp_status zp_kv8_window_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* q_start,
                              int32_t T, int32_t max_q, const int32_t* block_tables, const int32_t* seq_lens,
                              int32_t B, int32_t max_blocks, int32_t window, int32_t sinks, const zp_rows* out,

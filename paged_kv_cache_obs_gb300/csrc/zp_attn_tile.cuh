@@ -35,8 +35,9 @@
 // Over the 8-bit pool four more warps bring the codes and turn them into f16, which holds them exactly, times what their
 // blocks' scales are of the tile's (a power of two of them, as the library writes scales, is exact): the tile's K scale joins
 // the logits', its V scale the exponent of the weights.  Queries are brought to f16 by a power of two for each row, by the
-// softmax groups as they come.  P is f16, in units of 2^-15 of a reference 11 (in log2) above the largest weight times
-// scale: 11 bits down to 2^-18 of it, 2^-29 of it is the last that counts; sums of weights are fp32 throughout.
+// softmax groups as they come.  P is f16, in units of 2^-15 of a reference 11 (in log2) above the largest weight times its tile's V
+// scale (which may be that of another block): 11 bits down to 2^-18 of it, 2^-29 of it is the last that counts; sums of weights
+// are fp32 throughout.
 // 4 requests of 2048 new tokens over 0 to 6144, 32 heads on 8: 532 us, 1030 TFLOP/s over the pairs that are seen.  The tensor core
 // works 49 % of the time: the softmax of a tile takes 2.3 times as long beside the warps that turn codes (without them
 // the call takes 396 us), for issue slots and instruction fetches that they share.
@@ -72,7 +73,7 @@ constexpr int kKWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kVWarp = 11;
 // Where keys and values come from: blocks of the bf16 pool, rows of packed prompts, blocks of the 8-bit pool.
 enum class Source { kPaged, kRows, kPaged8 };
 template <Source SRC>
-constexpr bool kCodes = SRC == Source::kPaged8;  // which a group of four warps turns into bf16
+constexpr bool kCodes = SRC == Source::kPaged8;  // which a group of four warps turns into f16
 // Two softmax groups, a group of the other roles, and the one that turns codes.
 template <Source SRC>
 constexpr int kThreads = kCodes<SRC> ? 512 : 384;

@@ -1,5 +1,5 @@
 """Scales of the 8-bit pool in zp_kv8_window_attn: values of 0, scales far from one another, factors of the logits that leave fp32;
-against 64 bits and, for scales that are powers of two, to the bits that weights are held to."""
+against 64 bits, for scales that are powers of two, to the bits that weights are held to."""
 import os
 
 import numpy as np
@@ -214,3 +214,94 @@ def test_queries_and_keys_whose_factor_is_beyond_fp32(zp):
     c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(), torch.from_numpy(tables).cuda()
     got = _attend(zp, c, s, q, [new], [L], dt, p)
     _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, "large")
+
+
+# ------------------------------------------------------------------ what weights are held to --
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,b", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("less", [0, 6, 11, 15])
+def test_a_peak_among_values_of_a_smaller_scale(zp, d, b, less):
+    """The token with the largest weight stands in a block whose V scale is 2^-less of its neighbours', before 4000 tokens of weights
+    e^-20 of it."""
+    new, L = 20, 4096
+    NB = L // b
+    p = A._params(1, 1, d, b, scale=0.125)
+    rng = np.random.default_rng(less)
+    codes = np.zeros((1, NB, 2, 1, b, d), dtype=np.uint8)
+    codes[0, :, 1] = _codes(rng, (NB, 1, b, d))
+    codes[0, :, 0, 0, :, 0] = S.e4m3_encode(np.array(-20.0))
+    codes[0, 1, 0, 0, 3, 0] = 0                        # logits: 8 * -20 / 8, and 0
+    scales = np.ones((1, NB, 2, 1), dtype=np.float32)
+    scales[0, 1, 1] = 2.0 ** -less
+    q = torch.zeros((new, 1, d), dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 8.0
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), _i32(np.arange(NB)[None])
+    got = _attend(zp, c, s, q, [new], [L], dt, p)
+    _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, less)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,b", [(32, 8, 128, 16), (28, 4, 128, 32), (8, 8, 64, 16), (16, 2, 64, 32), (16, 1, 128, 16), (3, 1, 64, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5)])
+def test_chunks_to_the_weights_rounding(zp, Hq, Hkv, d, b, window, sinks):
+    rng = np.random.default_rng(Hq)
+    new, cached = [40, 129, 300, 17], [0, 260, 31, 1500]
+    lens = [c + n for c, n in zip(cached, new)]
+    tables, NB = A._tables(rng, lens, b)
+    codes = torch.from_numpy(_codes(rng, (1, NB, 2, Hkv, b, d))).cuda()
+    scales = torch.from_numpy((2.0 ** rng.integers(-12, -4, (1, NB, 2, Hkv))).astype(np.float32)).cuda()
+    q = torch.from_numpy(rng.standard_normal((sum(new), Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p, dt = A._params(Hq, Hkv, d, b), torch.from_numpy(tables).cuda()
+    got = _attend(zp, codes, scales, q, new, lens, dt, p, window, sinks)
+    lo = 0
+    for r, n in enumerate(new):
+        _check(codes[0], scales[0], dt[r], q[lo:lo + n], got[lo:lo + n], lens[r], window, sinks, p, r)
+        lo += n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,b", [(128, 16), (128, 32), (64, 16), (64, 32)])
+def test_every_code_and_packed_blocks_to_the_weights_rounding(zp, d, b):
+    """All codes that are numbers; and blocks that the library packed, with the scales that it writes."""
+    rng = np.random.default_rng(d + b)
+    Hq, Hkv, new, L = 4, 2, 200, 900
+    tables, NB = A._tables(rng, [L], b)
+    p, dt = A._params(Hq, Hkv, d, b), torch.from_numpy(tables).cuda()
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) / 4).to(torch.bfloat16).cuda()
+    codes = torch.from_numpy((rng.integers(0, 0x7F, (1, NB, 2, Hkv, b, d)) + 0x80 * rng.integers(0, 2, (1, NB, 2, Hkv, b, d))).astype(np.uint8)).cuda()
+    scales = torch.from_numpy((2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))).astype(np.float32)).cuda()
+    pool = (torch.randn((1, NB, 2, Hkv, b, d), device="cuda") * 2.0 ** torch.randint(-6, 3, (1, NB, 2, Hkv, 1, 1), device="cuda")).to(torch.bfloat16)
+    pool[0, int(tables[0, 1])] = 0
+    ids, ws = torch.arange(NB, dtype=torch.int32, device="cuda"), zp.new_workspace(256)
+    packed, written = torch.zeros_like(codes), torch.zeros_like(scales)
+    zp.zp_kv8_pack_blocks(pool, ids, packed, written, ids, p, ws)
+    for c, s in ((codes, scales), (packed, written)):
+        for window, sinks in ((0, 0), (150, 20)):
+            got = _attend(zp, c, s, q, [new], [L], dt, p, window, sinks)
+            _check(c[0], s[0], dt[0], q, got, L, window, sinks, p, window)
+
+
+@pytest.mark.gpu
+def test_captured_drafts_to_the_weights_rounding(zp):
+    """16 rows a head, the most that the form for few rows takes, captured and replayed over caches that grow."""
+    rng = np.random.default_rng(1)
+    Hq, Hkv, d, b, B, new = 8, 2, 128, 16, 5, 4
+    tables, NB = A._tables(rng, [700] * B, b)
+    codes = torch.from_numpy(_codes(rng, (1, NB, 2, Hkv, b, d))).cuda()
+    scales = torch.from_numpy((2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))).astype(np.float32)).cuda()
+    q = torch.from_numpy(rng.standard_normal((B * new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p, dt, out = A._params(Hq, Hkv, d, b), torch.from_numpy(tables).cuda(), torch.empty_like(q)
+    lens, start = _i32([4] * B), _i32(np.arange(B + 1) * new)
+    ws = zp.new_workspace(zp.zp_kv8_window_workspace_size(p, B * new, B, new, tables.shape[1], 0, 0))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        zp.zp_kv8_window_attn(codes, scales, 0, q, start, dt, lens, out, p, ws, 0, 0, new)
+    for L in ([4, 5, 20, 300, 699], [700, 17, 33, 64, 4]):
+        lens.copy_(_i32(L))
+        graph.replay()
+        for r in range(B):
+            rows = slice(r * new, (r + 1) * new)
+            _check(codes[0], scales[0], dt[r], q[rows], out[rows], L[r], 0, 0, p, r, tiled=False)
+    assert zp.zp_read_error(ws) == 0
