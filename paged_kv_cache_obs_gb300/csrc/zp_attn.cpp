@@ -144,8 +144,8 @@ zp_status kv8_window(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, c
 }
 
 // Prompts walk their rows in runs of tokens as requests walk blocks.  A run is what one copy brings: a whole tile of
-// 128 tokens, or 16 where a window starts and first tokens end inside of tiles (8 prompts of 500 to 4001 tokens, a window of 1024: 241 us so, 249
-// with 32, 277 with 128).
+// 128 tokens, or 16 where a window starts and first tokens end inside of tiles (8 prompts of 500 to 4001 tokens, a window of 1024: 241 to 250 us
+// with 16, which loads the fewest tokens that no row sees, and with 32; 264 to 282 with 128).
 struct PromptRuns {
   zp_params p;
   int32_t runs;  // of the longest prompt

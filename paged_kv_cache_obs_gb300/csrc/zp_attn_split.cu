@@ -913,6 +913,12 @@ cudaError_t dispatch(const CUtensorMap& tm, const AttnArgs& a, int d, const Spli
 // 60000 228 us with 8 and 283 with 4; 64 over up to 8192 134 us with 2, 149 with 4, 180 with one; 40 over up to 30000 348 us
 // with 8 and 301 with 4; 64 over up to 2048 51 us unsplit and 58 with 2.  8 rows, requests of 3 tokens: 64 over up to 8192 100 us with
 // 2 and 138 with one, 40 over up to 30000 209 us with 4 and 440 with one, 200 over up to 8192 244 us with one and 258 with 2.
+// kCtaTiles is one number for all head sizes and rows: over 48 calls (head sizes 64 and 128, 4 to 16 rows, 2 to 8 kv heads, 8 to 160 requests) 25
+// in its place was up to 16 % faster and up to 35 % slower, 100 up to 19 % faster and up to 47 % slower.
+//
+// The same with a window, whose rows have nearly equal work: two CTAs a head where the second wave is at most half full, so that it
+// takes half the time, and the window is long enough for two CTAs' latencies.  512 heads (456 slots) of 16 rows and windows of 4096
+// tokens 151 us so and 169 with one, 640 heads 163 and 179; 880 heads 217 and 197, 360 heads and windows of 1024 42 and 33, 512 heads 62 and 58.
 SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int window, int sinks, size_t room, bool many8) {
   const int64_t sms = plan_sms();
   SplitPlan s{};
@@ -929,7 +935,7 @@ SplitPlan split_plan(const zp_params* p, int B, int max_q, int max_blocks, int w
   const int64_t slots = sms * (s.rows == 16 ? kManyCtas : 4), most = (tiles + 4 * kWarps - 1) / (4 * kWarps);  // codes
   if (many8 && s.rows == 16) {
     n = std::min(most, slots * 7 / 6 / units);
-    if (window > 0 && n < 2 && tiles >= 8 * kWarps && (units <= slots || (units <= 2 * slots && tiles >= 256))) n = 2;
+    if (window > 0 && n < 2 && units > slots && 2 * units <= 3 * slots && tiles >= 256) n = 2;
   }
   if (many8 && window == 0 && n < 8) {
     int64_t best = INT64_MAX;
