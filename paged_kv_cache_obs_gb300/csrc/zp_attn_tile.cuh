@@ -1226,7 +1226,13 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
               tmem_st32(to + c * 32, o);
             }
           }
-          l *= corr;
+          if constexpr (kCodes<SRC>) {
+            // in two steps: behind values of 0 the reference may rise by 2^208, and what they count has to stay
+            const float half = m == -INFINITY ? 0.0f : ex2(0.5f * (m - mn));
+            l = l * half * half;
+          } else {
+            l *= corr;
+          }
           m = mn;
         }
         const uint64_t ref = pair2((m == -INFINITY ? 0.0f : -m) + (kCodes<SRC> ? v_log + kGain : 0.0f));
@@ -1401,7 +1407,12 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
     float4 y = *reinterpret_cast<const float4*>(p + k * step + lane * 4);
     if (ml.x == -INFINITY && ml.y == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // a part that saw nothing: its sums may be unset
     const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
-    l = fmaf(ml.y, c, l);
+    if (c == 0.0f) {  // values of 0 alone in one part, large ones in another: they count in the sum of weights
+      const float half = ex2(0.5f * (ml.x - M));
+      l = fmaf(ml.y * half, half, l);
+    } else {
+      l = fmaf(ml.y, c, l);
+    }
     v[0] = fmaf(y.x, c, v[0]);
     v[1] = fmaf(y.y, c, v[1]);
     v[2] = fmaf(y.z, c, v[2]);

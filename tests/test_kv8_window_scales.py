@@ -78,6 +78,9 @@ def _check(codes, scales, table, q, got, L, window, sinks, p, where, tiled=True)
                 rows = slice(i0, i0 + step)
                 top = _walked(v_scale, i0, n, L, window, sinks, G, b)
                 tol[rows] += 2.0 ** -29 * (w[rows] * top).amax(-1, keepdim=True) * (see[rows].double() @ (v.abs() / top[:, None]))
+                if tiled:   # values whose scale is below 2^-15 of those walked with them: 2^-25 of that scale
+                    small = torch.from_numpy(np.repeat(np.abs(v_scale), b)[:L]).cuda() < 2.0 ** -15 * top
+                    tol[rows] += 2.0 ** -25 * (w[rows] @ (top * small))[:, None]
             err = (got[:, g].double() - want).abs()
             assert bool((err <= tol).all()), (where, h, g, float((err / tol).max()))
             worst = max(worst, float((err / tol).max()))
@@ -171,6 +174,28 @@ def test_values_of_zero_alone(zp, new):
         s = torch.from_numpy(scales.astype(np.float32)).cuda()
         got = _attend(zp, c, s, q, [new], [L], dt, p)
         _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, large, tiled=4 * new > 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exp", [27, 60, 100])
+@pytest.mark.parametrize("d,b,zeros", [(128, 16, 128), (64, 32, 256), (64, 16, 300), (128, 32, 5000)])
+def test_values_of_zero_before_large_ones(zp, d, b, zeros, exp):
+    """Values of 0 count in the sum of weights also where those behind them are larger by more than fp32's range; the last case is cut
+    into parts, of which the first ones see values of 0 alone."""
+    rng = np.random.default_rng(zeros)
+    Hq, Hkv, new, L = 4, 2, 40, zeros + 400
+    tables, NB = A._tables(rng, [L], b)
+    codes = _codes(rng, (1, NB, 2, Hkv, b, d))
+    scales = 2.0 ** rng.integers(-8, -4, (1, NB, 2, Hkv))
+    scales[0, :, 1] = 2.0 ** exp
+    scales[0, tables[0, :zeros // b], 1] = 0
+    q = torch.from_numpy(rng.standard_normal((new, Hq, d)) * 2).to(torch.bfloat16).cuda()
+    p = A._params(Hq, Hkv, d, b)
+    c, s, dt = torch.from_numpy(codes).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(), torch.from_numpy(tables).cuda()
+    if zeros == 5000:
+        assert zp.zp_kv8_window_workspace_size(p, new, 1, new, tables.shape[1], 0, 0) > 256 + 4 * new * Hq * (d + 4)
+    got = _attend(zp, c, s, q, [new], [L], dt, p)
+    _check(c[0], s[0], dt[0], q, got, L, 0, 0, p, exp)
 
 
 # ------------------------------------------------------------------ factors of the logits -----
@@ -305,3 +330,31 @@ def test_captured_drafts_to_the_weights_rounding(zp):
             rows = slice(r * new, (r + 1) * new)
             _check(codes[0], scales[0], dt[r], q[rows], out[rows], L[r], 0, 0, p, r, tiled=False)
     assert zp.zp_read_error(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(24))
+def test_random_scales(zp, seed):
+    """Requests whose V scales are 0 here and there, for whole tiles, and of different sizes from one 128 tokens to the next."""
+    rng = np.random.default_rng(seed)
+    Hkv, G, d, b = int(rng.integers(1, 3)), int(rng.integers(1, 9)), int(rng.choice([64, 128])), int(rng.choice([16, 32]))
+    B, top = int(rng.integers(1, 5)), int(rng.choice([3, 60, 300]))
+    new = [int(x) for x in rng.integers(1, top + 1, B)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, rng.choice([100, 1500]), B))]
+    window, sinks = int(rng.choice([0, rng.integers(1, 600)])), int(rng.choice([0, rng.integers(1, 200)]))
+    tables, NB = A._tables(rng, lens, b)
+    codes = torch.from_numpy(_codes(rng, (1, NB, 2, Hkv, b, d))).cuda()
+    scales = 2.0 ** rng.integers(-12, -4, (1, NB, 2, Hkv))
+    for r, L in enumerate(lens):
+        far = rng.integers(-40, 40, -(-L // 128))
+        for i in range(-(-L // b)):
+            off = rng.integers(-14, 1, Hkv) + far[i * b // 128] - 6
+            scales[0, tables[r, i], 1] = np.where((far[i * b // 128] % 3 == 0) | (rng.random(Hkv) < 0.2), 0.0, 2.0 ** off)
+    scales = torch.from_numpy(scales.astype(np.float32)).cuda()
+    q = torch.from_numpy(rng.standard_normal((sum(new), G * Hkv, d)) * rng.choice([0.0, 0.5, 3.0])).to(torch.bfloat16).cuda()
+    p, dt = A._params(G * Hkv, Hkv, d, b), torch.from_numpy(tables).cuda()
+    got = _attend(zp, codes, scales, q, new, lens, dt, p, window, sinks)
+    lo = 0
+    for r, n in enumerate(new):
+        _check(codes[0], scales[0], dt[r], q[lo:lo + n], got[lo:lo + n], lens[r], window, sinks, p, r, tiled=G * max(new) > 16)
+        lo += n
