@@ -590,7 +590,8 @@ size_t zp_prompt_workspace_size(const zp_params* params, int32_t T, int32_t B, i
  * Where head groups times max_q is 16 or less, everything is held as by zp_kv8_decode_attn (weights to 11 bits down to 2^-18 of the
  * row's largest, whatever their V scales).  Above:
  *   - keys are taken as they are; values are exact where their scale is a power of two, not below 2^-15 of the
- *     largest of the 128 tokens that are walked together, and within 2^-10 of themselves (2^-25 of that scale) otherwise;
+ *     largest of the 128 tokens that are walked together, and otherwise within 2^-10 of themselves and 2^-25 of the largest
+ *     value at that scale (448 times it);
  *   - a weight times the largest V scale of those 128 tokens (as a power of two) keeps 11 bits down to 2^-18 of the row's
  *     largest such product, and 2^-29 of it is the last that counts: a row whose largest weight stands beside V scales 2^15 times
  *     its own has 15 powers of two less for the others.  Sums of weights are fp32;

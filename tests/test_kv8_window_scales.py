@@ -56,9 +56,10 @@ def _walked(scale, i0, n, L, window, sinks, G, b):
 
 
 def _check(codes, scales, table, q, got, L, window, sinks, p, where, tiled=True):
-    """One request's rows against 64 bits: the output's rounding; weights to half a step of f16, and what fp32 sums add; and
-    weights times the largest V scale S_t of the 128 tokens walked together, W_t, which end at 2^-29 of the row's largest W: each token
-    below is off by as much of its value over S_t."""
+    """One request's rows against 64 bits: the output's rounding; weights to half a step of f16, and what fp32 sums add; and what is below
+    f16's range.  Few rows: weights end at 2^-29 of the row's largest.  Tiled: weights times the largest V scale S_t of the 128 tokens
+    walked together, W_t, end at 2^-29 of the row's largest W, each off by as much of its value over S_t; and f16 holds scale / S_t and
+    its product with a code, which end at 2^-25 each: a value of a scale below 2^-15 S_t is off by 2^-25 S_t (|code| + 1)."""
     n, Hq, d = q.shape
     Hkv, b = p["num_kv_heads"], p["block_size"]
     G = Hq // Hkv
@@ -73,14 +74,16 @@ def _check(codes, scales, table, q, got, L, window, sinks, p, where, tiled=True)
             w = torch.softmax((p["scale"] * (q[:, g].double() @ k.T)).masked_fill(~see, -torch.inf), -1)
             want, mass = w @ v, w @ v.abs()
             tol = 2.0 ** -8 * want.abs() + (F16 + 2.0 ** -14) * mass + 1e-38
-            step = 2 * (128 // G) if tiled else n
-            for i0 in range(0, n, step):
+            if not tiled:
+                tol += 2.0 ** -29 * w.amax(-1, keepdim=True) * (see.double() @ v.abs())
+            step = 2 * (128 // G)
+            for i0 in range(0, n if tiled else 0, step):
                 rows = slice(i0, i0 + step)
-                top = _walked(v_scale, i0, n, L, window, sinks, G, b)
-                tol[rows] += 2.0 ** -29 * (w[rows] * top).amax(-1, keepdim=True) * (see[rows].double() @ (v.abs() / top[:, None]))
-                if tiled:   # values whose scale is below 2^-15 of those walked with them: 2^-25 of that scale
-                    small = torch.from_numpy(np.repeat(np.abs(v_scale), b)[:L]).cuda() < 2.0 ** -15 * top
-                    tol[rows] += 2.0 ** -25 * (w[rows] @ (top * small))[:, None]
+                top = _walked(v_scale, i0, n, L, window, sinks, G, b)[:, None]
+                tol[rows] += 2.0 ** -29 * (w[rows] * top.T).amax(-1, keepdim=True) * (see[rows].double() @ (v.abs() / top))
+                scale = torch.from_numpy(np.repeat(np.abs(v_scale), b)[:L]).cuda()[:, None]
+                code = torch.where(scale > 0, v.abs() / scale, 0.0)
+                tol[rows] += 2.0 ** -25 * (w[rows] @ ((scale < 2.0 ** -15 * top) * top * (code + (code > 0))))
             err = (got[:, g].double() - want).abs()
             assert bool((err <= tol).all()), (where, h, g, float((err / tol).max()))
             worst = max(worst, float((err / tol).max()))
