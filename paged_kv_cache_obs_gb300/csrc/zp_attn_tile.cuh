@@ -38,7 +38,7 @@
 // softmax groups as they come.  P is f16, in units of 2^-15 of a reference 11 (in log2) above the largest weight times its tile's V
 // scale (which may be that of another block): 11 bits down to 2^-18 of it, 2^-29 of it is the last that counts; sums of weights
 // are fp32 throughout.
-// 4 requests of 2048 new tokens over 0 to 6144, 32 heads on 8: 532 us, 1030 TFLOP/s over the pairs that are seen.  The tensor core
+// 4 requests of 2048 new tokens over 0 to 6144, 32 heads on 8: 539 us, 1020 TFLOP/s over the pairs that are seen.  The tensor core
 // works 49 % of the time: the softmax of a tile takes 2.3 times as long beside the warps that turn codes (without them
 // the call takes 396 us), for issue slots and instruction fetches that they share.
 //
@@ -577,7 +577,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Turns a quarter of a tile (32 tokens) from codes into f16(code * factor), a factor for each 16 tokens, in the place and
 // order that a bf16 tile has (one warp).  `refill` starts the next copy into the codes' place: every lane has used its loads.
 // What bounds it is how fast one warp gets its instructions beside the softmax groups (8 cycles each), so it is a short loop
-// over 8 tokens at a time, whose code stays at hand: 2048-token chunks of 4 requests over 0 to 6144 tokens take 532 us so, 622
+// over 8 tokens at a time, whose code stays at hand: 2048-token chunks of 4 requests over 0 to 6144 tokens took 532 us so, 622
 // unrolled, and took 740 with values turned into bf16 by 6 integer steps a pair in place of a conversion and a product.
 template <int D, class Refill>
 __device__ __forceinline__ void turn_quarter(uint32_t codes, uint32_t tile, const uint16_t* factors, int quarter, int lane, const Refill& refill) {
@@ -776,7 +776,8 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1) tile_kernel(const __grid_con
   // Registers follow the roles: 2 x 128 x 208 + 128 x 88 of the 384 x 168 that the launch gave.  With 200 the
   // softmax groups spill inside their loop (2048-token chunks 210 us, 200 us with 208).  With codes to turn:
   // 2 x 128 x 192 + 2 x 128 x 64 of 512 x 128 (200 with 48 for those that turn them, or 192 with 80 and 48, took 589 us where
-  // this takes 532: 2048-token chunks of 4 requests over 0 to 6144 tokens).
+  // this took 532: 2048-token chunks of 4 requests over 0 to 6144 tokens).  The roles of 64 registers spill 144 to 152 bytes a thread with
+  // D 128 and 92 with 64, and nothing with 96.
   if (kCodes<SRC> && warp >= kTurnWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if constexpr (kCodes<SRC>) turn_codes<D>(s, tm, a, warp - kTurnWarp, lane, abort);
