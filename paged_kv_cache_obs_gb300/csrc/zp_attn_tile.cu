@@ -29,7 +29,8 @@ TilePlan tile_plan(const zp_params* p, int T, int B, int max_q, int max_blocks, 
     // several 2 more for its sums.  64 items of up to 783 tiles take 547 us with 7 splits (3 parts a CTA) and 753 with 2 (one each).
     // Where items fill the SMs by themselves, the fewest that come within 5 % of it: lengths are at most the table's width, and
     // every further part's sums are written and read for the last wave's rounding alone (4 x 2048 tokens over up to 8192, 1024 items:
-    // 529 us unsplit; with the 4 parts that a table for 65536 or more tokens gave, 848 us and a workspace of 554 MB).
+    // 529 us unsplit; with the 4 parts that a table for 65536 or more tokens gave, 848 us and a workspace of 554 MB).  Where lengths are the
+    // table's width it can cost a little: 200 items of up to 64 tiles 222 us in 2 parts, 214 in 3.
     const int64_t most_parts = std::min<int64_t>(most_splits, 32);
     const auto cost = [&](int64_t n) {
       const int64_t parts = (std::max<int64_t>(items, 1) * n + plan.ctas - 1) / plan.ctas;  // of a CTA
