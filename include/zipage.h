@@ -523,7 +523,8 @@ zp_status zp_kv8_unpack_blocks(const zp_kv8_pool* kv8, const int32_t* src_ids, c
  *   workspace     >= zp_kv8_decode_workspace_size() bytes, 256-byte aligned.
  * A bad seq_len or block id: that row (request and kv head) is not written, ZP_ERR_BAD_TABLE.
  * ZP_ERR_TIMEOUT (a wait inside the kernel gave up) as for zp_compress: the output is undefined.
- * Table entries of blocks that are not visible may hold anything.  head_dim 64 or 128, block_size
+ * Table entries of blocks that are not visible may hold anything.  A query's largest value times params.scale and a visible K
+ * scale stays below 2^127 (logits of 0 beside it would be NaN).  head_dim 64 or 128, block_size
  * 16 or 32, up to 16 query heads per kv head. */
 zp_status zp_kv8_decode_attn(const zp_kv8_pool* pool, int32_t layer, const zp_rows* q, const int32_t* block_tables,
                              const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t window, int32_t sinks,
